@@ -350,7 +350,7 @@ def _verify(s):
     fixed = torch.where(total[:, None] > 0, fixed, alone)
     run_sum = fixed.cumsum(1)
     total = run_sum[:, -1]
-    u24 = s["u24"].long()[rows, accepted]
+    u24 = s["u24"].long()[:, d]   # the draw's own number: those before it decided on the drafts
     goal = (u24 * (total >> 24) + ((u24 * (total & 0xffffff) + 0xffffff) >> 24)).clamp(min=1)
     token = torch.where(total > 0, torch.searchsorted(run_sum, goal[:, None])[:, 0], -1)
     step1 = torch.arange(d + 1, device=DEV)
@@ -445,7 +445,7 @@ def _exact_verify(case, s):
             fixed = torch.round(row.double() * 2.0 ** 40).cpu().numpy().astype("int64")
         sums = fixed.cumsum()
         total = int(sums[-1])
-        goal = max(1, -(-u24[b][k] * total // (1 << 24)))
+        goal = max(1, -(-u24[b][case["drafts"]] * total // (1 << 24)))
         token = int(sums.searchsorted(goal)) if total else -1
         accepted.append(k)
         tokens.append(drafts[b][:k] + [token] + [-1] * (case["drafts"] - k))

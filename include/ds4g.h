@@ -40,6 +40,11 @@
  *    bf16 tensors hold raw bfloat16 bits; the embedding table is IEEE binary16.
  *  - Errors leave the session unchanged unless stated otherwise; DS4G_ECUDA
  *    reports a failed launch or CUDA call, after which the session is undefined.
+ *  - The operators on device buffers (ds4g_sample*, ds4g_paged_*, ds4g_probs,
+ *    ds4g_verify_draft) run on the stream they are given, which belongs to the
+ *    current device, and keep nothing between calls.  The last three groups do not
+ *    synchronise and can be captured into a CUDA graph.  Calls that may overlap in
+ *    time need workspaces of their own.
  */
 #ifndef DS4G_H
 #define DS4G_H
@@ -412,6 +417,132 @@ int32_t ds4g_sample_u_min_p(const float *logits, int n_vocab, float temperature,
  * Synchronises `cuda_stream`. */
 int32_t ds4g_sample_static(const float *logits, int n_vocab, float temperature, float top_p,
                            uint64_t *rng_state, void *cuda_stream);
+
+/* ---------------------------------------------------------------- paged K/V cache
+ *
+ * Several sequences in one K/V cache ([P3] 阶段四 4.2 appends each token's K, after
+ * RoPE, and V to the cache and attends over it; here the cache of many sequences is
+ * cut into pages, so that they grow without moving).  Position p of a sequence lies
+ * in the page its table names at p / page_size, slot p % page_size.  A session's own
+ * cache (ds4g_session_kv) is the case of pages that follow one another. */
+
+/* The cache of one layer.  Element d of head h of slot s of page g is at
+ * k[g * page_stride + s * slot_stride + h * head_stride + d] (v alike); strides in
+ * elements, each a multiple of 16 bytes, the pointers 16-byte aligned.  head_dim: a
+ * multiple of 8, at most 256. */
+typedef struct {
+    void *k, *v;
+    int64_t page_stride, slot_stride, head_stride;
+    int n_pages;
+    int page_size;
+    int n_kv_heads;
+    int head_dim;
+    int dtype; /* DS4G_BF16 or DS4G_F32 */
+} ds4g_paged_kv;
+
+/* The sequences of a call (device arrays).  Sequence b has length[b] tokens, its
+ * newest ones, the call's new tokens, among them: n_b = start[b + 1] - start[b] of
+ * them (at most max_new), rows start[b] .. of the call's token arrays, at positions
+ * length[b] - n_b .. length[b] - 1.  start NULL: one token each, row b.  A table
+ * entry outside [0, n_pages) is a page that is not there (nothing is stored to it and
+ * its keys are left out), and so is everything at or past width * page_size.  Rows at or
+ * past start[n_seqs] are left as they are.  start[0] is 0, start does not fall, and
+ * start[n_seqs] <= n_tokens. */
+typedef struct {
+    const int32_t *table;  /* [n_seqs][table_stride], width entries used */
+    const int32_t *length; /* [n_seqs] */
+    const int32_t *start;  /* [n_seqs + 1] or NULL */
+    int n_seqs;
+    int n_tokens; /* rows of the token arrays; n_seqs when start is NULL */
+    int max_new;  /* most new tokens of one sequence: 1 when start is NULL */
+    int width;
+    int table_stride;
+} ds4g_paged_batch;
+
+/* Rotation table: cs[(p * rot_dim / 2 + i) * 2] = cos and + 1 = sin of the angle of pair
+ * (2i, 2i+1) at position p < n_pos (device, f32, 16-byte aligned).  The first rot_dim
+ * dims of a head turn (even, at most head_dim); the rest pass through. */
+typedef struct {
+    const float *cs;
+    int n_pos;
+    int rot_dim;
+} ds4g_rope;
+
+/* Fill a rotation table: angle p * base^(-2i/rot_dim), computed in FP64 and stored
+ * as FP32 (as the sessions' own tables).  cs: device, n_pos * rot_dim floats. */
+int ds4g_rope_fill(float *cs, int n_pos, int rot_dim, float base, void *cuda_stream);
+
+/* Store the new tokens' K and V rows into their pages, the keys rotated by their
+ * positions on the way, rounded once (to nearest even) to the cache's type; with q
+ * also rotate the queries into q_out (the same type; q_out == q is allowed with equal
+ * strides, other overlaps are not).  k, v: [n_tokens][n_kv_heads][head_dim], q:
+ * [n_tokens][n_heads][head_dim], each with its own token stride in elements (a
+ * multiple of 16 bytes; heads and dims adjacent); dtype: their type, DS4G_BF16 or
+ * DS4G_F32.  rope NULL: no rotation.  q NULL: keys and values only.  A token whose
+ * position is outside the table or its page not there stores no K and V; one before
+ * position 0, or at or past n_pos, stores none either and leaves its q_out row as it
+ * was.  Two tokens of one
+ * call must not share a slot.  One launch. */
+int ds4g_paged_append(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, const ds4g_rope *rope, const void *q, int64_t q_stride,
+                      void *q_out, int64_t q_out_stride, int n_heads, int dtype, void *cuda_stream);
+
+/* Workspace bytes of ds4g_paged_attention (host arithmetic on the sizes alone); 0 on a
+ * bad argument. */
+size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch, int n_heads);
+
+/* Attention of every sequence's new tokens over its cached positions (the new tokens'
+ * rows already appended): token at position p attends to the positions max(0, p -
+ * window + 1) .. p (window <= 0: 0 .. p), out = sum_j softmax_j(scale q . k_j) v_j, query
+ * heads h * n_heads / n_kv_heads .. sharing K/V head h.  scale 0: 1 / sqrt(head_dim).
+ * A masked or missing key adds nothing, whatever its K and V hold; a token without any key
+ * gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
+ * (multiples of 16 bytes, 16-byte aligned); dtype: their type.  q and out must not
+ * overlap.  max_new <= 128.
+ * BF16 queries over a BF16 cache with head_dim 64 or 128, pages of a multiple of 8 slots
+ * and at most 128 query heads per K/V head run on the tensor cores, the probabilities
+ * rounded to BF16 for the product with V (FP32 sums); every other case runs in FP32.
+ * The work is cut over the keys of all sequences by their lengths on the device, and
+ * parts of one sequence are joined by a second launch in a fixed order: the same call gives the
+ * same bits, but a sequence's last bits may depend on the others of its call.
+ * workspace: device, >= ds4g_paged_attention_workspace_bytes, 256-byte aligned. */
+int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
+                         void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
+                         void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* ---------------------------------------------------------------- drafted tokens */
+
+/* Probabilities that ds4g_sample draws from (without top-p), one row of logits each:
+ * p = softmax(logits / temperature); temperature <= 0: 1 at the largest logit (the lowest
+ * id on ties), 0 elsewhere.  A NaN logit counts as -inf; if the largest is +inf, the ids
+ * that have it share the whole; a row of -inf alone gives zeros.  logits, probs: device
+ * f32 [n_rows][n_vocab] with row strides in elements; probs == logits is allowed with
+ * equal strides.  n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */
+int ds4g_probs(const float *logits, int64_t logits_stride, int n_rows, int n_vocab, float temperature, float *probs,
+               int64_t probs_stride, void *cuda_stream);
+
+/* Verify drafted tokens ([P3] 阶段四 4.3 draws one token; here a draft's tokens are kept
+ * while the target would have drawn them, so that the output is distributed as the
+ * target's own draws).  For sequence b with n = n_drafts[b] drafts (NULL: max_drafts;
+ * clamped to [0, max_drafts]): draft i is accepted while u_i * q_i(d_i) < p_i(d_i), u_i =
+ * u24[b][i] / 2^24.  The token after the k accepted ones is drawn with the last number, u =
+ * u24[b][max_drafts] / 2^24 (one that decided on a draft would not be independent of it):
+ * from the weights max(p_k - q_k, 0) if draft k was rejected (p_k where these are all zero),
+ * from p_n if k = n.  As in ds4g_sample the weights are rounded to 2^-40 and summed exactly: the
+ * first token, in vocabulary order, at which the running sum reaches max(1, ceil(u *
+ * total)).  q NULL: drafts without probabilities (each draft's own probability is 1: it is
+ * accepted while u_i < p_i(d_i), and its weight is 0 when it was rejected).
+ * p: device f32 [n_seqs][max_drafts + 1][n_vocab], q: [n_seqs][max_drafts][n_vocab], with
+ * strides of a sequence and of a position in elements; a value below 0 or NaN counts as 0,
+ * one above 1 as 1.  drafts: int32 [n_seqs][max_drafts] (an id outside the vocabulary is
+ * rejected); u24: uint32 [n_seqs][max_drafts + 1] (the low 24 bits).
+ * accepted: int32 [n_seqs], k; tokens: int32 [n_seqs][max_drafts + 1]: the accepted
+ * drafts, the drawn token (-1 if p_k has no weight), then -1.  max_drafts in [0, 64];
+ * n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */
+int ds4g_verify_draft(const float *p, int64_t p_seq_stride, int64_t p_stride, const float *q, int64_t q_seq_stride,
+                      int64_t q_stride, const int32_t *drafts, const int32_t *n_drafts, const uint32_t *u24,
+                      int n_seqs, int max_drafts, int n_vocab, int32_t *accepted, int32_t *tokens,
+                      void *cuda_stream);
 
 const char *ds4g_strerror(int code);
 

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "prefill_tc.h"
 
 using namespace ds4g;
@@ -173,6 +174,13 @@ __global__ void k_rope_table(float2 *t, int n_ctx, int half, double base)
     }
 }
 
+cudaError_t rope_table(float2 *t, int n_pos, int half, double base, cudaStream_t st)
+{
+    k_rope_table<<<256, 256, 0, st>>>(t, n_pos, half, base);
+    ++launch_count();
+    return cudaGetLastError();
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? DS4G_OK : DS4G_ECUDA; }
 
 // xorshift64* (Vigna 2016): shifts 12, 25, 27; output multiplied by the published constant.
@@ -200,6 +208,11 @@ StepArgs step_base(ds4g_session *s)
 }
 
 }  // namespace
+
+cudaError_t ds4g::rope_fill(float2 *t, int n_pos, int half, double base, cudaStream_t st)
+{
+    return rope_table(t, n_pos, half, base, st);
+}
 
 extern "C" {
 
@@ -357,9 +370,7 @@ int ds4g_session_create(ds4g_model *m, int n_ctx, void *dev_mem, size_t bytes, v
                                 cudaMemcpyHostToDevice, s->st);
     if (!e) e = cudaStreamSynchronize(s->st);  // the host tables above are read by the copies
     if (!e) {
-        k_rope_table<<<256, 256, 0, s->st>>>(s->rope, n_ctx, d.HD / 2, (double)m->cfg.rope_base);
-        ++launch_count();
-        e = cudaGetLastError();
+        e = rope_table(s->rope, n_ctx, d.HD / 2, (double)m->cfg.rope_base, s->st);
     }
     if (e) { delete s; return DS4G_ECUDA; }
     *out = s;

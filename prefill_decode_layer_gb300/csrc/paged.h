@@ -1,0 +1,77 @@
+// Operators on a paged K/V cache, probabilities and draft verification: arguments
+// and host-side entry points of their kernel files (internal to the library).
+#pragma once
+
+#include "common.cuh"
+
+namespace ds4g {
+
+// A cache's pages, copied into kernel arguments (strides in elements).
+struct PagedKV {
+    const void *k, *v;
+    long long page_stride, slot_stride, head_stride;
+    int n_pages, page_size, n_kv_heads, head_dim;
+};
+
+// The sequences of a call, copied into kernel arguments.
+struct PagedSeqs {
+    const int *table, *length, *start;
+    int n_seqs, n_tokens, max_new, width, table_stride;
+};
+
+struct AppendArgs {
+    PagedKV kv;
+    PagedSeqs s;
+    const void *k, *v, *q;
+    void *q_out;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    const float *cs;   // null: no rotation
+    int n_pos, rot_dim;
+    int n_heads;       // 0: no queries
+};
+cudaError_t paged_append(const AppendArgs &a, int in_dtype, int kv_dtype, cudaStream_t st, int nsm);
+
+struct AttnArgs {
+    PagedKV kv;
+    PagedSeqs s;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    int group;         // query heads per K/V head
+    int rows;          // query rows of a row tile: (token, head of the group) pairs
+    float scale_log2;  // scale * log2(e)
+    int window;        // 0: no window
+    char *ws;          // records, then parts (PartLayout)
+};
+// Whether the tensor-core form covers the call (paged_attn_tc.cu).
+bool paged_attn_tc_ok(const PagedKV &kv, int group, int q_dtype, int kv_dtype);
+// Query rows per tile of the tensor-core form: whole tokens, at most 128 rows.
+int paged_attn_tc_rows(int group, int max_new);
+cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm);
+// Shared by the two forms (paged_attn.cu): CTAs of a launch over units of kt keys, whether
+// its items can be split, and the join of the tensor-core form's parts.
+int paged_attn_grid(const AttnArgs &a, int kt, int most);
+bool paged_attn_splits(const AttnArgs &a, int kt);
+cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st);
+size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype);
+cudaError_t paged_attention(const AttnArgs &a, int q_dtype, int kv_dtype, cudaStream_t st, int nsm);
+
+cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,
+                       long long os, cudaStream_t st);
+
+struct VerifyArgs {
+    const float *p, *q;
+    long long ps, pstride, qs, qstride;
+    const int *drafts, *n_drafts;
+    const unsigned *u24;
+    int max_drafts, n;
+    int *accepted, *tokens;
+};
+cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st);
+// Largest vocabulary of probs_rows and verify_rows.
+constexpr int kMaxRowVocab = 1 << 20;
+
+// api.cu's RoPE table fill: [n_pos][half] (cos, sin), angles in FP64.
+cudaError_t rope_fill(float2 *t, int n_pos, int half, double base, cudaStream_t st);
+
+}  // namespace ds4g

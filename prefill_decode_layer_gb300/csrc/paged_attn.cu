@@ -1,0 +1,423 @@
+// Attention of the newest tokens of many sequences over a paged K/V cache: page "ds4.c
+// 学习笔记 -- 端到端推理流程", 阶段四 4.2 (the layer step's attention of one token over
+// its cached keys), with grouped heads, several new tokens, an optional window and a
+// cache cut into pages.  This file holds the FP32 form, the join of split items and
+// the host side; paged_attn_tc.cu holds the tensor-core form.
+//
+// out_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = 2^(s (q_r . k_j) - m_r),  s = scale log2 e,
+// over the keys j visible to row r; m_r is the running maximum (online softmax), so
+// that K and V are read once.
+//
+// FP32 form (k_paged_attn): for FP32 queries or caches and for head sizes and page sizes
+// the tensor-core form does not take.  Lanes are split into groups of LPK that own D dims
+// each, and every group is a stream of its own through the CTA's keys: it loads KB keys'
+// K and V straight into registers (coalesced 16-byte loads, no shared memory), forms the
+// dot products of up to 8 query rows by shuffles, and keeps its rows' output in
+// registers.  The streams of an item are merged through shared memory when it ends.
+#include "paged_sched.cuh"
+
+namespace ds4g {
+
+static constexpr int kPaThreads = 256;
+static constexpr int kPaKeys = 64;    // keys of a unit
+static constexpr int kPaRows = kAttnRowsSimt;
+
+// D consecutive elements as floats (D 4 or 8; 8- or 16-byte loads of BF16, 16-byte of FP32).
+template <typename T, int D> struct Load;
+template <> struct Load<float, 4> {
+    static __device__ __forceinline__ void run(const float *p, float (&x)[4])
+    {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    }
+};
+template <> struct Load<float, 8> {
+    static __device__ __forceinline__ void run(const float *p, float (&x)[8])
+    {
+        const float4 v = *reinterpret_cast<const float4 *>(p), w = *reinterpret_cast<const float4 *>(p + 4);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+    }
+};
+template <> struct Load<bf16, 4> {
+    static __device__ __forceinline__ void run(const bf16 *p, float (&x)[4])
+    {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x[0] = __uint_as_float(v.x << 16);
+        x[1] = __uint_as_float(v.x & 0xffff0000u);
+        x[2] = __uint_as_float(v.y << 16);
+        x[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+};
+template <> struct Load<bf16, 8> {
+    static __device__ __forceinline__ void run(const bf16 *p, float (&x)[8])
+    {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <typename T> __device__ __forceinline__ void store_out(T *p, float v);
+template <> __device__ __forceinline__ void store_out<float>(float *p, float v) { *p = v; }
+template <> __device__ __forceinline__ void store_out<bf16>(bf16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Finite stand-in of a maximum over no key, for the exponents.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Dynamic shared memory: [streams][kPaRows] maxima and sums, then [streams][kPaRows][head_dim].
+template <int LPK> struct PaStreams { static constexpr int n = kPaThreads / LPK; };
+
+template <typename TQ, typename TKV, int LPK, int D, int KB>
+__global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant__ AttnArgs a)
+{
+    constexpr int S = PaStreams<LPK>::n;
+    extern __shared__ float sm[];
+    __shared__ PagedCursor s_cur;
+    __shared__ PagedItem s_item;
+    __shared__ long long s_scratch[kPaThreads / 32];
+    const PartLayout lay(kAttnMaxCtas, kPaRows, a.kv.head_dim);
+    PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) split->valid = 0;
+    paged_cursor<kPaThreads>(a, kPaKeys, &s_cur, s_scratch);
+    PagedCursor cur = s_cur;
+    SeqWork w;
+    w.units = -1;
+
+    const int hd = a.kv.head_dim;
+    const int stream = threadIdx.x / LPK, sub = threadIdx.x % LPK;
+    const int d0 = sub * D;
+    const bool own = d0 < hd;   // head_dim is a multiple of 8: whole vectors of D
+    float *s_m = sm, *s_l = sm + S * kPaRows, *s_o = sm + 2 * S * kPaRows;
+    const TKV *kc = static_cast<const TKV *>(a.kv.k), *vc = static_cast<const TKV *>(a.kv.v);
+    const TQ *qp = static_cast<const TQ *>(a.q);
+    TQ *out = static_cast<TQ *>(a.out);
+
+    while (true) {
+        if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, w, split, s_item);
+        __syncthreads();
+        if (!s_item.more) return;
+        const PagedItem it = s_item;
+        const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
+        // the rows' queries, scaled, and the last key each sees
+        float q[kPaRows][D], o[kPaRows][D], m[kPaRows], l[kPaRows];
+        int last[kPaRows];
+#pragma unroll
+        for (int r = 0; r < kPaRows; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            last[r] = -1;
+#pragma unroll
+            for (int e = 0; e < D; ++e) q[r][e] = o[r][e] = 0.f;
+            if (r < it.n_rows) {
+                const int row = it.row0 + r, t = row / a.group, h = row - t * a.group;
+                last[r] = max(it.pos0 + t, -1);   // before position 0: no key
+                if (own)
+                    Load<TQ, D>::run(qp + (long long)(it.token + t) * a.q_stride + (it.head * a.group + h) * hd + d0,
+                                     q[r]);
+#pragma unroll
+                for (int e = 0; e < D; ++e) q[r][e] *= a.scale_log2;
+            }
+        }
+        const int k0 = max(it.lo, it.t0 * kPaKeys), k1 = min(it.hi, it.t1 * kPaKeys);
+        // every row sees keys [all_lo, all_hi]
+        const int win = a.window > 0 ? a.window : 0x7fffffff;
+        const int t_first = it.row0 / a.group, t_last = (it.row0 + it.n_rows - 1) / a.group;
+        const int all_hi = it.pos0 + t_first;
+        const int all_lo = a.window > 0 ? it.pos0 + t_last - a.window + 1 : 0;
+        for (int j0 = k0 + stream * KB; j0 < k1; j0 += S * KB) {
+            float k[KB][D], v[KB][D];
+            bool there[KB];
+            bool all = it.n_rows == kPaRows && j0 >= all_lo && j0 + KB - 1 <= all_hi;
+#pragma unroll
+            for (int u = 0; u < KB; ++u) {
+                const int j = j0 + u;
+                const int page = j < k1 ? key_page(a, table, j) : -1;
+                there[u] = page >= 0;
+                all = all && there[u];
+#pragma unroll
+                for (int e = 0; e < D; ++e) k[u][e] = v[u][e] = 0.f;
+                if (there[u] && own) {
+                    const long long at = page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
+                                         it.head * a.kv.head_stride + d0;
+                    Load<TKV, D>::run(kc + at, k[u]);
+                    Load<TKV, D>::run(vc + at, v[u]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kPaRows; ++r) {
+                if (r >= it.n_rows) break;
+                float s[KB];
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    s[u] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < D; ++e) s[u] = fmaf(q[r][e], k[u][e], s[u]);
+                }
+                const unsigned lanes = LPK == 32 ? 0xffffffffu
+                                                 : ((1u << (LPK & 31)) - 1u) << ((threadIdx.x & 31) / LPK * LPK);
+#pragma unroll
+                for (int x = LPK / 2; x > 0; x >>= 1)
+#pragma unroll
+                    for (int u = 0; u < KB; ++u) s[u] += __shfl_xor_sync(lanes, s[u], x);
+                float mx = m[r];
+                bool see[KB];
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    const int j = j0 + u;
+                    see[u] = all || (there[u] && j <= last[r] && j > last[r] - win);
+                    if (see[u]) mx = fmaxf(mx, s[u]);
+                }
+                const float ref = finite_max(mx), f = exp2f(m[r] - ref);   // m = -inf: 0
+                m[r] = mx;
+                l[r] *= f;
+#pragma unroll
+                for (int e = 0; e < D; ++e) o[r][e] *= f;
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    if (!see[u]) continue;   // a masked key adds nothing, whatever its V holds
+                    const float p = exp2f(s[u] - ref);
+                    l[r] += p;
+#pragma unroll
+                    for (int e = 0; e < D; ++e) o[r][e] = fmaf(p, v[u][e], o[r][e]);
+                }
+            }
+        }
+        // ---- merge the streams: rows' maxima and sums, then their outputs, in stream order
+#pragma unroll
+        for (int r = 0; r < kPaRows; ++r) {
+            if (r >= it.n_rows) break;
+            if (sub == 0) {
+                s_m[stream * kPaRows + r] = m[r];
+                s_l[stream * kPaRows + r] = l[r];
+            }
+            if (own) {
+#pragma unroll
+                for (int e = 0; e < D; ++e) s_o[(stream * kPaRows + r) * hd + d0 + e] = o[r][e];
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < it.n_rows * hd; i += kPaThreads) {
+            const int r = i / hd, d = i - r * hd;
+            float mx = -INFINITY;
+            for (int s = 0; s < S; ++s) mx = fmaxf(mx, s_m[s * kPaRows + r]);
+            const float ref = finite_max(mx);
+            float acc = 0.f, sum = 0.f;
+            for (int s = 0; s < S; ++s) {
+                const float f = exp2f(s_m[s * kPaRows + r] - ref);
+                sum = fmaf(f, s_l[s * kPaRows + r], sum);
+                acc = fmaf(f, s_o[(s * kPaRows + r) * hd + d], acc);
+            }
+            if (it.part < 0) {
+                const int row = it.row0 + r, t = row / a.group, h = row - t * a.group;
+                store_out<TQ>(out + (long long)(it.token + t) * a.out_stride + (it.head * a.group + h) * hd + d,
+                              sum == 0.f ? 0.f : acc / sum);
+            } else {
+                const size_t at = (size_t)it.part * kPaRows + r;
+                float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + at * 2;
+                if (d == 0) {
+                    ml[0] = mx;
+                    ml[1] = sum;
+                }
+                reinterpret_cast<float *>(a.ws + lay.o)[at * hd + d] = acc;
+            }
+        }
+        __syncthreads();   // s_item and the merge buffers are rewritten
+    }
+}
+
+// ------------------------------------------------------------------ join
+
+// One row of a split item per CTA and turn: warp w adds the parts w, w + 8, .. of the row, the
+// eight partial sums are added in order.  Bound: latency (a few KB to a few MB of
+// parts from L2); eight warps keep eight parts' loads in flight.
+static constexpr int kJoinThreads = 256;
+static constexpr int kJoinWarps = kJoinThreads / 32;
+
+template <typename T, int ROWS, int CTAS, int HDL>   // HDL: dims per lane
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ AttnArgs a, int ctas)
+{
+    __shared__ short s_cta[CTAS];
+    __shared__ int s_first[CTAS + 1];   // rows before the i-th split item
+    __shared__ int s_n;
+    __shared__ float s_o[kJoinWarps][32 * HDL], s_ml[kJoinWarps][2];
+    const int hd = a.kv.head_dim;
+    const int stride = ROWS > 0 ? ROWS : a.rows;
+    const PartLayout lay(CTAS, stride, hd);
+    const PagedSplit *split = reinterpret_cast<const PagedSplit *>(a.ws + lay.split);
+    const float *ml = reinterpret_cast<const float *>(a.ws + lay.ml);
+    const float *po = reinterpret_cast<const float *>(a.ws + lay.o);
+    T *out = static_cast<T *>(a.out);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        int n = 0, rows = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + lane;
+            int nr = c < ctas && split[c].valid ? split[c].n_rows : 0;
+            const unsigned has = __ballot_sync(0xffffffffu, nr > 0);
+            int incl = nr;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (nr > 0) {
+                const int i = n + __popc(has & ((1u << lane) - 1u));
+                s_cta[i] = (short)c;
+                s_first[i] = rows + incl - nr;
+            }
+            n += __popc(has);
+            rows += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            s_n = n;
+            s_first[n] = rows;
+        }
+    }
+    __syncthreads();
+    const int n = s_n, jobs = s_first[n];
+    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
+        int lo = 0, hi = n;   // the last i with s_first[i] <= job
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_first[mid] <= job) lo = mid;
+            else hi = mid;
+        }
+        const int r = job - s_first[lo], c = s_cta[lo];
+        const PagedSplit sp = split[c];
+        const int parts = sp.last_cta - c + 1;
+        // part i: the CTA's own tail, then the head parts of the CTAs after it
+        auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride + r; };
+        float mx = -INFINITY;
+        for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i) * 2]);
+        mx = warp_max(mx);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float acc[HDL], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < HDL; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kJoinWarps) {
+            const size_t s = slot(i);
+            const float f = exp2f(ml[s * 2] - ref);
+            sum = fmaf(f, ml[s * 2 + 1], sum);
+#pragma unroll
+            for (int e = 0; e < HDL; ++e) {
+                const int d = lane + 32 * e;
+                if (d < hd) acc[e] = fmaf(f, po[s * hd + d], acc[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < HDL; ++e) s_o[warp][lane + 32 * e] = acc[e];
+        if (lane == 0) s_ml[warp][0] = sum;
+        __syncthreads();
+        for (int d = threadIdx.x; d < hd; d += kJoinThreads) {
+            float v = 0.f, t = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                v += s_o[w][d];
+                t += s_ml[w][0];
+            }
+            const int row = sp.row0 + r, tk = row / a.group, h = row - tk * a.group;
+            store_out<T>(out + (long long)(sp.token + tk) * a.out_stride + (sp.head * a.group + h) * hd + d,
+                         t == 0.f ? 0.f : v / t);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype)
+{
+    size_t n = PartLayout(kAttnMaxCtas, kAttnRowsSimt, kv.head_dim).total;
+    if (paged_attn_tc_ok(kv, group, DS4G_BF16, kv_dtype)) {
+        const size_t t = PartLayout(kAttnMaxCtasTc, paged_attn_tc_rows(group, max_new), kv.head_dim).total;
+        n = t > n ? t : n;
+    }
+    return n;
+}
+
+template <typename T, int ROWS, int CTAS>
+static cudaError_t join(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
+{
+    const int grid = 2 * nsm;
+    if (a.kv.head_dim <= 64) return launch_pdl(k_paged_join<T, ROWS, CTAS, 2>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
+    if (a.kv.head_dim <= 128)
+        return launch_pdl(k_paged_join<T, ROWS, CTAS, 4>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
+    return launch_pdl(k_paged_join<T, ROWS, CTAS, 8>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
+}
+cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
+{
+    return join<bf16, 0, kAttnMaxCtasTc>(a, ctas, nsm, st);
+}
+
+// Most units a call can have, by the sizes the host knows.
+static long long most_units(const AttnArgs &a, int kt)
+{
+    long long keys = (long long)a.s.width * a.kv.page_size;
+    if (a.window > 0) {
+        const long long seen = (long long)a.window + a.s.max_new - 1;   // may begin inside a unit
+        keys = seen + kt - 1 < keys ? seen + kt - 1 : keys;
+    }
+    const long long tiles = keys > 0 ? (keys + kt - 1) / kt : 1;
+    const long long row_tiles = ((long long)a.s.max_new * a.group + a.rows - 1) / a.rows;
+    return (long long)a.s.n_seqs * a.kv.n_kv_heads * row_tiles * tiles;
+}
+int paged_attn_grid(const AttnArgs &a, int kt, int most)
+{
+    const long long u = most_units(a, kt);
+    return (int)(u < most ? u : most);
+}
+// Whether an item can be split between CTAs: not when every item is one unit.
+bool paged_attn_splits(const AttnArgs &a, int kt)
+{
+    return most_units(a, kt) > (long long)a.s.n_seqs * a.kv.n_kv_heads *
+                                   (((long long)a.s.max_new * a.group + a.rows - 1) / a.rows);
+}
+
+template <typename TQ, typename TKV, int LPK, int D, int KB>
+static cudaError_t simt(const AttnArgs &a, int nsm, cudaStream_t st)
+{
+    auto kernel = k_paged_attn<TQ, TKV, LPK, D, KB>;
+    const size_t smem = (size_t)PaStreams<LPK>::n * kPaRows * (2 + a.kv.head_dim) * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e) return e;
+    }
+    const int most = 2 * nsm < kAttnMaxCtas ? 2 * nsm : kAttnMaxCtas;
+    const int grid = paged_attn_grid(a, kPaKeys, most);
+    cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kPaThreads), smem, st, a);
+    if (!e && paged_attn_splits(a, kPaKeys)) e = join<TQ, kAttnRowsSimt, kAttnMaxCtas>(a, grid, nsm, st);
+    return e;
+}
+template <typename TQ, typename TKV> static cudaError_t simt_dim(const AttnArgs &a, int nsm, cudaStream_t st)
+{
+    if (a.kv.head_dim <= 32) return simt<TQ, TKV, 8, 4, 4>(a, nsm, st);
+    if (a.kv.head_dim <= 64) return simt<TQ, TKV, 16, 4, 4>(a, nsm, st);
+    if (a.kv.head_dim <= 128) return simt<TQ, TKV, 32, 4, 4>(a, nsm, st);
+    return simt<TQ, TKV, 32, 8, 2>(a, nsm, st);
+}
+
+cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaStream_t st, int nsm)
+{
+    if (in.s.n_seqs == 0 || in.s.n_tokens == 0) return cudaSuccess;
+    AttnArgs a = in;
+    if (paged_attn_tc_ok(a.kv, a.group, q_dtype, kv_dtype)) {
+        a.rows = paged_attn_tc_rows(a.group, a.s.max_new);
+        return paged_attn_tc(a, st, nsm);
+    }
+    a.rows = kAttnRowsSimt;
+    if (q_dtype == DS4G_F32)
+        return kv_dtype == DS4G_F32 ? simt_dim<float, float>(a, nsm, st) : simt_dim<float, bf16>(a, nsm, st);
+    return kv_dtype == DS4G_F32 ? simt_dim<bf16, float>(a, nsm, st) : simt_dim<bf16, bf16>(a, nsm, st);
+}
+
+}  // namespace ds4g

@@ -1,0 +1,188 @@
+// Division of paged attention's work among the CTAs of a launch, on the device.
+//
+// An item is one row tile of one sequence and K/V head: up to `rows` query rows
+// (row r of a sequence: new token r / group, head r % group of the K/V head's group),
+// all of them over the sequence's keys [lo, hi).  A unit is kt keys of an item.  With U
+// units in all, CTA c of G takes units [c U / G, (c + 1) U / G), items in the order
+// (sequence, K/V head, row tile), so that ragged lengths still give every CTA the same
+// number of units.  An item that lies in one CTA is written to the output; a CTA's share
+// of an item that others share goes to the workspace as a part (row maxima, row sums,
+// unnormalised rows), and k_paged_join adds the parts in CTA order.  A CTA has at most
+// two parts: of the item it begins in (slot 2c) and of the one it ends in (slot 2c + 1).
+#pragma once
+
+#include "paged.h"
+
+namespace ds4g {
+
+// Most CTAs of the two forms (the workspace holds two parts for each).
+constexpr int kAttnMaxCtas = 320;      // FP32 form: two CTAs per SM
+constexpr int kAttnMaxCtasTc = 160;    // tensor-core form: one
+constexpr int kAttnRowsSimt = 8;       // query rows of an FP32 row tile
+
+struct PagedItem {
+    int seq, head;          // sequence, K/V head
+    int token;              // row of the token arrays of the sequence's first new token
+    int n_new;              // its new tokens (at most max_new)
+    int pos0;               // position of its first new token
+    int row0, n_rows;       // query rows of the tile
+    int lo, hi;             // the sequence's keys
+    int t0, t1;             // this CTA's key tiles of the item
+    int part;               // slot of the workspace, or -1: the whole item is here
+    int more;               // 0: no item (the CTA is done)
+};
+
+// What the join needs of an item that begins in CTA c and ends in a later one.
+struct PagedSplit {
+    int valid, last_cta, seq, head, token, row0, n_rows, pad;
+};
+
+struct PartLayout {
+    size_t split, ml, o, total;   // byte offsets of [ctas] records, [2 ctas][rows][2], [2 ctas][rows][head_dim]
+    __host__ __device__ PartLayout(int ctas, int rows, int head_dim)
+    {
+        split = 0;
+        ml = ((size_t)ctas * sizeof(PagedSplit) + 255) & ~(size_t)255;
+        o = (ml + (size_t)2 * ctas * rows * 2 * 4 + 255) & ~(size_t)255;
+        total = o + (size_t)2 * ctas * rows * head_dim * 4;
+    }
+};
+
+// A sequence's keys, new tokens and units.
+struct SeqWork {
+    int token, n_new, pos0, lo, hi, tiles, row_tiles;
+    long long units;
+};
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
+{
+    SeqWork w;
+    int first = b, n = 1;
+    if (a.s.start) {
+        first = a.s.start[b];
+        n = a.s.start[b + 1] - first;
+    }
+    // no row outside the token arrays, whatever start holds
+    if (first < 0 || first > a.s.n_tokens) n = 0;
+    n = min(min(n, a.s.max_new), a.s.n_tokens - first);
+    n = max(n, 0);
+    const int cap = a.s.width * a.kv.page_size;   // fits: checked by the host
+    const int len = max(a.s.length[b], 0);
+    w.token = first;
+    w.n_new = n;
+    w.pos0 = len - n;
+    w.hi = min(len, cap);
+    w.lo = a.window > 0 ? min(max(w.pos0 - a.window + 1, 0), w.hi) : 0;
+    const int t = w.hi > w.lo ? (w.hi + kt - 1) / kt - w.lo / kt : 1;   // one empty unit still writes zeros
+    w.tiles = t;
+    w.row_tiles = (n * a.group + a.rows - 1) / a.rows;
+    w.units = (long long)a.kv.n_kv_heads * w.row_tiles * t;
+    return w;
+}
+
+// Where a CTA's units begin; found once by all its threads.
+struct PagedCursor {
+    long long total;        // units of the launch
+    long long at, end;      // this CTA's remaining units
+    long long local;        // unit `at` within sequence seq
+    int seq, ctas;          // ctas: those that have units
+};
+
+// All NT threads of the CTA (a multiple of 32); the result is in *cur (shared memory) after
+// it returns.  scratch: NT / 32 shared 64-bit words.
+template <int NT>
+__device__ __forceinline__ void paged_cursor(const AttnArgs &a, int kt, PagedCursor *cur, long long *scratch)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.s.n_seqs + NT - 1) / NT;
+    const int b0 = min(tid * per, a.s.n_seqs), b1 = min(b0 + per, a.s.n_seqs);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_work(a, b, kt).units;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long base = 0, total = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) base += scratch[w];
+        total += scratch[w];
+    }
+    const int g = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+    const long long c = blockIdx.x;
+    const long long u0 = c < g ? c * total / g : total, u1 = c < g ? (c + 1) * total / g : total;
+    if (tid == 0) {   // (a CTA without units: nobody below sets the rest)
+        cur->total = total;
+        cur->at = u0;
+        cur->end = u1;
+        cur->ctas = g;
+        cur->seq = a.s.n_seqs;
+        cur->local = 0;
+    }
+    __syncthreads();
+    long long s = base + incl - mine;   // units before this thread's sequences
+    if (u0 < u1 && s <= u0 && u0 < s + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const long long n = seq_work(a, b, kt).units;
+            if (u0 < s + n) {
+                cur->seq = b;
+                cur->local = u0 - s;
+                break;
+            }
+            s += n;
+        }
+    }
+    __syncthreads();
+}
+
+// The CTA's next item, one thread.  `w` and `cur` are the caller's copies, kept
+// between calls; w.units < 0 before the first.  Writes the CTA's split record.
+__device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, SeqWork &w, PagedSplit *split,
+                                           PagedItem &it)
+{
+    it.more = cur.at < cur.end;
+    if (!it.more) return;
+    if (w.units < 0) w = seq_work(a, cur.seq, kt);
+    while (cur.local >= w.units) {   // ends: cur.at < total
+        cur.local -= w.units;
+        w = seq_work(a, ++cur.seq, kt);
+    }
+    const long long item = cur.local / w.tiles;
+    const int x = (int)(cur.local - item * w.tiles);
+    const long long left = cur.end - cur.at;
+    const int take = (int)min((long long)(w.tiles - x), left);
+    const int tile0 = w.lo / kt;
+    it.seq = cur.seq;
+    it.head = (int)(item / w.row_tiles);
+    it.token = w.token;
+    it.n_new = w.n_new;
+    it.pos0 = w.pos0;
+    it.row0 = (int)(item % w.row_tiles) * a.rows;
+    it.n_rows = min(a.rows, w.n_new * a.group - it.row0);
+    it.lo = w.lo;
+    it.hi = w.hi;
+    it.t0 = tile0 + x;
+    it.t1 = tile0 + x + take;
+    const bool begins = x == 0, ends = x + take == w.tiles;
+    it.part = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
+    if (begins && !ends) {
+        // the CTA of the item's last unit e: the largest c with c total / ctas <= e
+        const unsigned long long e = (unsigned long long)(cur.at + w.tiles - 1);
+        PagedSplit r = {1, (int)(((e + 1) * (unsigned long long)cur.ctas - 1) / (unsigned long long)cur.total),
+                        it.seq, it.head, it.token, it.row0, it.n_rows, 0};
+        *split = r;
+    }
+    cur.at += take;
+    cur.local += take;
+}
+
+// Page of key j of sequence b, or -1.
+__device__ __forceinline__ int key_page(const AttnArgs &a, const int *table_row, int j)
+{
+    const int p = table_row[j / a.kv.page_size];
+    return p >= 0 && p < a.kv.n_pages ? p : -1;
+}
+
+}  // namespace ds4g

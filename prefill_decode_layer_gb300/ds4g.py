@@ -61,7 +61,7 @@ def lib():
             raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                               "(there is no fallback implementation)")
         L = C.CDLL(LIB_PATH)
-        vp, i32, sz = C.c_void_p, C.c_int, C.c_size_t
+        vp, i32, i64, sz = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
         sig = {
             "ds4g_model_create": ([vp, vp, vp], i32),
             "ds4g_model_destroy": ([vp], None),
@@ -100,6 +100,12 @@ def lib():
             "ds4g_sample_min_p": ([vp, i32, C.c_float, C.c_float, C.c_float, vp, vp, sz, vp], C.c_int32),
             "ds4g_sample_u_min_p": ([vp, i32, C.c_float, C.c_float, C.c_float, C.c_uint32, vp, sz, vp],
                                     C.c_int32),
+            "ds4g_rope_fill": ([vp, i32, i32, C.c_float, vp], i32),
+            "ds4g_paged_append": ([vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp], i32),
+            "ds4g_paged_attention_workspace_bytes": ([vp, vp, i32], sz),
+            "ds4g_paged_attention": ([vp, vp, vp, i64, vp, i64, i32, i32, C.c_float, i32, vp, sz, vp], i32),
+            "ds4g_probs": ([vp, i64, i32, i32, C.c_float, vp, i64, vp], i32),
+            "ds4g_verify_draft": ([vp, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp], i32),
             "ds4g_strerror": ([i32], C.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -369,3 +375,184 @@ def sample_u(logits: torch.Tensor, temperature: float, top_p: float, u24: int,
     return lib().ds4g_sample_u(logits.data_ptr(), logits.numel(), float(temperature),
                                float(top_p), int(u24), workspace.data_ptr(), workspace.numel(),
                                _stream_ptr(stream))
+
+
+# ---------------------------------------------------------------- operators on device buffers
+
+class PagedKVStruct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("slot_stride", C.c_int64), ("head_stride", C.c_int64), ("n_pages", C.c_int),
+                ("page_size", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("dtype", C.c_int)]
+
+
+class PagedBatchStruct(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("length", C.c_void_p), ("start", C.c_void_p),
+                ("n_seqs", C.c_int), ("n_tokens", C.c_int), ("max_new", C.c_int),
+                ("width", C.c_int), ("table_stride", C.c_int)]
+
+
+class RopeStruct(C.Structure):
+    _fields_ = [("cs", C.c_void_p), ("n_pos", C.c_int), ("rot_dim", C.c_int)]
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise Ds4gError(EINVAL, what)
+
+
+def _call(name: str, device, stream, *args) -> None:
+    """One call of the library on `device`, on `stream` (None: that device's current
+    stream)."""
+    f = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, _stream_ptr(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, _stream_ptr(stream))
+    if rc < 0:
+        raise Ds4gError(rc, name)
+
+
+class PagedKV:
+    """The paged K/V cache of one layer (ds4g_paged_kv): k and v [n_pages][page_size]
+    [n_kv_heads][head_dim], of equal strides, the last dimension adjacent."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1 and
+                 k.dtype == v.dtype and k.dtype in _DTYPES and k.device == v.device, "PagedKV")
+        self.k, self.v, self.device = k, v, k.device
+        n, p, h, d = k.shape
+        self.n_kv_heads, self.head_dim = h, d
+        self.struct = PagedKVStruct(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
+                                    n, p, h, d, _DTYPES[k.dtype])
+        self.ref = C.addressof(self.struct)
+
+
+class PagedBatch:
+    """The sequences of a call (ds4g_paged_batch): int32 device tensors table [n_seqs]
+    [width], length [n_seqs] and start [n_seqs + 1] (None: one new token each).  The
+    tensors are kept, and read by each call as they then are; max_new bounds a sequence's
+    new tokens.  A batch has one owner thread, as a session has."""
+
+    def __init__(self, table: torch.Tensor, length: torch.Tensor, start: torch.Tensor | None = None,
+                 max_new: int = 1):
+        n = length.numel()
+        _require(table.dim() == 2 and table.shape[0] == n and table.dtype == torch.int32 and
+                 (table.shape[1] <= 1 or table.stride(1) == 1) and length.dtype == torch.int32 and
+                 length.is_contiguous() and table.device == length.device, "PagedBatch")
+        _require(start is None or (start.dtype == torch.int32 and start.numel() == n + 1 and
+                                   start.is_contiguous() and start.device == length.device), "PagedBatch")
+        self.table, self.length, self.start, self.device = table, length, start, length.device
+        width = table.shape[1]
+        self.struct = PagedBatchStruct(table.data_ptr(), length.data_ptr(),
+                                       start.data_ptr() if start is not None else None, n, n, max_new,
+                                       width, max(table.stride(0), width) if n > 1 else width)
+        self.ref = C.addressof(self.struct)
+
+
+class Rope:
+    """Rotation table (ds4g_rope): cs [n_pos][rot_dim / 2][2] f32, (cos, sin) of every pair."""
+
+    def __init__(self, cs: torch.Tensor):
+        _require(cs.dim() == 3 and cs.shape[2] == 2 and cs.dtype == torch.float32 and cs.is_contiguous(), "Rope")
+        self.cs, self.device = cs, cs.device
+        self.struct = RopeStruct(cs.data_ptr(), cs.shape[0], 2 * cs.shape[1])
+        self.ref = C.addressof(self.struct)
+
+    @classmethod
+    def fill(cls, n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda", stream=None) -> "Rope":
+        """A table filled by ds4g_rope_fill."""
+        cs = torch.empty(n_pos, rot_dim // 2, 2, dtype=torch.float32, device=device)
+        _call("ds4g_rope_fill", cs.device, stream, cs.data_ptr(), n_pos, rot_dim, float(base))
+        return cls(cs)
+
+
+def _rows(t: torch.Tensor, batch: PagedBatch, heads: int | None, dim: int, dtype) -> bool:
+    """t is a token tensor [n_tokens][heads][dim] of `dtype`, heads and dims adjacent."""
+    s = t.shape
+    return (len(s) == 3 and s[0] == batch.struct.n_tokens and s[2] == dim and (heads is None or s[1] == heads) and
+            t.dtype == dtype and t.stride(2) == 1 and t.stride(1) == dim and t.device == batch.device)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def paged_append(kv: PagedKV, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor, rope: Rope | None = None,
+                 q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None) -> None:
+    """ds4g_paged_append: k, v [n_tokens][n_kv_heads][head_dim] into the cache's pages, the
+    keys rotated by `rope`; q [n_tokens][n_heads][head_dim] rotated into q_out (which may
+    be q)."""
+    if batch.start is not None:
+        batch.struct.n_tokens = k.shape[0]
+    h, d, dt = kv.n_kv_heads, kv.head_dim, k.dtype
+    _require(dt in _DTYPES and kv.device == batch.device and _rows(k, batch, h, d, dt) and _rows(v, batch, h, d, dt) and
+             (rope is None or rope.device == batch.device) and (q is None) == (q_out is None), "paged_append")
+    if q is None:
+        _call("ds4g_paged_append", batch.device, stream, kv.ref, batch.ref, k.data_ptr(), _row_stride(k),
+              v.data_ptr(), _row_stride(v), rope.ref if rope is not None else None, None, 0, None, 0, 0, _DTYPES[dt])
+        return
+    _require(_rows(q, batch, None, d, dt) and _rows(q_out, batch, q.shape[1], d, dt), "paged_append")
+    _call("ds4g_paged_append", batch.device, stream, kv.ref, batch.ref, k.data_ptr(), _row_stride(k), v.data_ptr(),
+          _row_stride(v), rope.ref if rope is not None else None, q.data_ptr(), _row_stride(q), q_out.data_ptr(),
+          _row_stride(q_out), q.shape[1], _DTYPES[dt])
+
+
+def paged_attention_workspace_bytes(kv: PagedKV, batch: PagedBatch, n_heads: int) -> int:
+    return lib().ds4g_paged_attention_workspace_bytes(kv.ref, batch.ref, n_heads)
+
+
+def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                    scale: float = 0.0, window: int = 0, stream=None) -> None:
+    """ds4g_paged_attention: q and out [n_tokens][n_heads][head_dim]; scale 0: 1 /
+    sqrt(head_dim); window 0: every position up to the token's own."""
+    if batch.start is not None:
+        batch.struct.n_tokens = q.shape[0]
+    d, dt, heads = kv.head_dim, q.dtype, q.shape[1]
+    _require(dt in _DTYPES and kv.device == batch.device and _rows(q, batch, None, d, dt) and
+             _rows(out, batch, heads, d, dt) and workspace.device == batch.device, "paged_attention")
+    _call("ds4g_paged_attention", batch.device, stream, kv.ref, batch.ref, q.data_ptr(), _row_stride(q),
+          out.data_ptr(), _row_stride(out), heads, _DTYPES[dt], scale, window, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+
+
+def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:
+    """ds4g_probs: rows of f32 logits [n_rows][n_vocab] to probabilities (out may be logits)."""
+    _require(logits.dim() == 2 and logits.shape == out.shape and logits.dtype == out.dtype == torch.float32 and
+             logits.device == out.device and (logits.shape[1] <= 1 or logits.stride(1) == out.stride(1) == 1), "probs")
+    n, v = logits.shape
+    _call("ds4g_probs", logits.device, stream, logits.data_ptr(), logits.stride(0) if n > 1 else v, n, v,
+          float(temperature), out.data_ptr(), out.stride(0) if n > 1 else v)
+
+
+def verify_draft(p: torch.Tensor, q: torch.Tensor | None, drafts: torch.Tensor, u24: torch.Tensor,
+                 accepted: torch.Tensor, tokens: torch.Tensor, n_drafts: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """ds4g_verify_draft: p [n_seqs][max_drafts + 1][n_vocab] and q [n_seqs][max_drafts][n_vocab]
+    (or None) f32; drafts [n_seqs][max_drafts], u24 [n_seqs][max_drafts + 1], accepted [n_seqs], tokens
+    [n_seqs][max_drafts + 1] and n_drafts [n_seqs] (or None) int32."""
+    _require(p.dim() == 3 and drafts.dim() == 2, "verify_draft")
+    (b, d1, v), d, i32 = p.shape, drafts.shape[1], torch.int32
+
+    def ints(t, *shape):
+        return t.dtype == i32 and t.shape == shape and t.is_contiguous() and t.device == p.device
+
+    _require(p.dtype == torch.float32 and (v <= 1 or p.stride(2) == 1) and d1 == d + 1 and ints(drafts, b, d) and
+             ints(u24, b, d1) and ints(accepted, b) and ints(tokens, b, d1) and
+             (n_drafts is None or ints(n_drafts, b)), "verify_draft")
+    _require(q is None or (q.dtype == torch.float32 and q.shape == (b, d, v) and (v <= 1 or q.stride(2) == 1) and
+                           q.device == p.device), "verify_draft")
+
+    def strides(t, rows):   # of a sequence and of a position; a dimension of one element has any stride
+        pos = t.stride(1) if rows > 1 else v
+        return (t.stride(0) if b > 1 else max(v, rows * pos)), pos
+
+    ps, pp = strides(p, d1)
+    qs, qp = strides(q, d) if q is not None else (0, 0)
+    _call("ds4g_verify_draft", p.device, stream, p.data_ptr(), ps, pp, q.data_ptr() if q is not None else None, qs, qp,
+          drafts.data_ptr(), n_drafts.data_ptr() if n_drafts is not None else None, u24.data_ptr(), b, d, v,
+          accepted.data_ptr(), tokens.data_ptr())

@@ -494,7 +494,7 @@ size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_
 /* Attention of every sequence's new tokens over its cached positions (the new tokens'
  * rows already appended): token at position p attends to the positions max(0, p -
  * window + 1) .. p (window <= 0: 0 .. p), out = sum_j softmax_j(scale q . k_j) v_j, query
- * heads h * n_heads / n_kv_heads .. sharing K/V head h.  scale 0: 1 / sqrt(head_dim).
+ * heads h * n_heads / n_kv_heads .. sharing K/V head h.  scale > 0, or 0: 1 / sqrt(head_dim).
  * A masked or missing key adds nothing, whatever its K and V hold; a token without any key
  * gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
  * (multiples of 16 bytes, 16-byte aligned); dtype: their type.  q and out must not
@@ -509,6 +509,11 @@ size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_
 int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
                          void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
                          void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* Synchronise the stream and report how the last ds4g_paged_attention on this workspace
+ * ended: DS4G_OK, or DS4G_ETIMEOUT if a bounded device-side wait gave up (its output is then
+ * invalid). */
+int ds4g_paged_attention_status(const void *workspace, void *cuda_stream);
 
 /* ---------------------------------------------------------------- drafted tokens */
 

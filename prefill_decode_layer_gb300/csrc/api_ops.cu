@@ -109,7 +109,7 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
                          void *workspace, size_t workspace_bytes, void *stream)
 {
     if (!kv_ok(kv) || !batch_ok(batch, kv) || !dtype_ok(dtype) || !heads_ok(kv, n_heads)) return DS4G_EINVAL;
-    if (scale != scale || scale - scale != 0.f) return DS4G_EINVAL;   // NaN or infinite
+    if (!(scale >= 0.f) || scale - scale != 0.f) return DS4G_EINVAL;   // negative, NaN or infinite
     if (batch->n_tokens == 0 || batch->n_seqs == 0) return DS4G_OK;
     if (batch->max_new > kMaxNew) return DS4G_EINVAL;
     const int64_t row = (int64_t)n_heads * kv->head_dim;
@@ -123,6 +123,14 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
     AttnArgs a = {kv_of(*kv), seqs_of(*batch), q, out, q_stride, out_stride, n_heads / kv->n_kv_heads, 0,
                   (float)((double)sc * 1.4426950408889634), window > 0 ? window : 0, static_cast<char *>(workspace)};
     return status_of(paged_attention(a, dtype, kv->dtype, static_cast<cudaStream_t>(stream), nsm));
+}
+
+int ds4g_paged_attention_status(const void *workspace, void *stream)
+{
+    if (!workspace || ((uintptr_t)workspace & 255u)) return DS4G_EINVAL;
+    int status = DS4G_OK;
+    const cudaError_t e = paged_attn_status(workspace, static_cast<cudaStream_t>(stream), &status);
+    return e ? DS4G_ECUDA : status;
 }
 
 int ds4g_probs(const float *logits, int64_t logits_stride, int n_rows, int n_vocab, float temperature, float *probs,

@@ -54,6 +54,8 @@ int paged_attn_grid(const AttnArgs &a, int kt, int most);
 bool paged_attn_splits(const AttnArgs &a, int kt);
 cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st);
 size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype);
+// DS4G_OK or DS4G_ETIMEOUT of the last call that used the workspace (synchronises st).
+cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status);
 cudaError_t paged_attention(const AttnArgs &a, int q_dtype, int kv_dtype, cudaStream_t st, int nsm);
 
 cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,

@@ -84,7 +84,11 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
     PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x == 0) split->valid = 0;
+    if (threadIdx.x == 0) {
+        split->valid = 0;
+        split->status = DS4G_OK;
+        split->ctas = gridDim.x;
+    }
     paged_cursor<kPaThreads>(a, kPaKeys, &s_cur, s_scratch);
     PagedCursor cur = s_cur;
     SeqWork w;
@@ -343,6 +347,19 @@ size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dty
         n = t > n ? t : n;
     }
     return n;
+}
+
+cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status)
+{
+    PagedSplit rec[kAttnMaxCtas];
+    static_assert(sizeof(rec) <= 16384, "on the host's stack");
+    // (the workspace holds at least this many bytes: PartLayout of the FP32 form)
+    cudaError_t e = cudaMemcpyAsync(rec, ws, sizeof(rec), cudaMemcpyDeviceToHost, st);
+    if (!e) e = cudaStreamSynchronize(st);
+    *status = DS4G_OK;
+    for (int c = 0; !e && c < rec[0].ctas && c < kAttnMaxCtas; ++c)
+        if (rec[c].status != DS4G_OK) *status = DS4G_ETIMEOUT;
+    return e;
 }
 
 template <typename T, int ROWS, int CTAS>

@@ -1,6 +1,642 @@
+// Tensor-core form of the paged attention (tcgen05 MMAs with TMEM accumulators, TMA tiles
+// of the cache's pages): page "ds4.c 学习笔记 -- 端到端推理流程", 阶段四 4.2. The
+// mathematics and the division of the work are paged_attn.cu's and paged_sched.cuh's; this
+// form takes BF16 queries over a BF16 cache, head_dim 64 or 128.
+//
+// A unit is 128 keys of an item; the item's up to 128 query rows (new token, head of the
+// K/V head's group) are the MMA's M side, also where there are fewer: at one new token the
+// bound is the cache's bytes (128 keys of 128 dims are 64 KB, 1.46 us of an SM's share of
+// the HBM bandwidth, against 0.57 us of padded MMA work).  Per unit:
+//   S = Q K^T    M 128 x N 128 keys, from shared memory into TMEM;
+//   softmax      a thread owns a row: it reads its 128 scores from TMEM, masks them, and
+//                writes P = 2^(s c - m) as BF16 over them (the row sums stay FP32 and
+//                unrounded; P's rounding, 2^-9 of a weight on average, is the price of the
+//                BF16 tensor cores).  m is the row's running maximum, but moved only when a
+//                tile exceeds it by 2^8: the rescale of O is then rare;
+//   O += P V     A = P straight from TMEM, V read MN-major from its TMA tile.
+// Units alternate between two streams, each with its own S/P and O columns and its own
+// four softmax warps, which are independent attentions over every other unit: the MMAs of
+// one overlap the softmax of the other.  When the item ends both streams' O lie in the
+// same TMEM lanes, so that merging them is a thread's own arithmetic.
+//
+// Masked places: rows of V outside the sequence's keys are zeroed in shared memory where a
+// 16-key MMA step contains them; pages that are not there are read as zeros (a page
+// coordinate out of bounds) and masked by a bit per 8 keys.  A key that only some rows
+// see (several new tokens, or a window's edge) must not reach the others as 0 * NaN: what
+// is not finite in its V row is replaced by 0 and added to the rows that see it when
+// the item ends.
+//
+// Roles (320 threads, one CTA per SM): warps 0-3 and 4-7 softmax and output of streams 0
+// and 1; warp 8 the items, the page look-ups and the TMA copies; warp 9 lane 0 the
+// MMAs.  Every wait is bounded; a CTA that gives up says so in its record, drains its copies
+// and MMAs, frees its TMEM and returns.
+#include <cuda.h>
+
 #include "paged_sched.cuh"
+#include "sm100.cuh"
+#include "tc_gemm.cuh"
+
 namespace ds4g {
-bool paged_attn_tc_ok(const PagedKV &, int, int, int) { return false; }
-int paged_attn_tc_rows(int group, int max_new) { return 128 / group * group; }
-cudaError_t paged_attn_tc(const AttnArgs &, cudaStream_t, int) { return cudaErrorNotSupported; }
+
+static constexpr int kTcKeys = 128;                    // keys of a unit
+static constexpr int kTcSoft = 256;                    // softmax threads
+static constexpr int kTcThreads = kTcSoft + 64;
+static constexpr int kTcTma = kTcSoft / 32, kTcMma = kTcTma + 1;   // their warps
+static constexpr int kTcMaxSlots = 8;
+static constexpr int kTcItems = 4;                     // items ahead of the softmax at most
+static constexpr uint32_t kTcHalf = kTcKeys * 128;     // bytes of 64 dims of a K or V tile
+static constexpr int kTcSmem = 227 * 1024;
+
+struct TcMisc {
+    uint64_t full[kTcMaxSlots], empty[kTcMaxSlots];    // K/V tiles of the ring
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];         // of a stream
+    uint64_t o_done, o_free;                           // O complete; O read by the softmax threads
+    uint64_t item_full[kTcItems], item_empty[kTcItems];
+    uint64_t done;
+    PagedItem item[kTcItems];
+    PagedCursor cur;
+    long long scratch[kTcThreads / 32];
+    uint32_t there[8];                                 // of unit u % 8: a bit per 8 keys whose page is there
+    uint32_t tmem;
+    int abort_flag;
+    int poison[2];                                     // of item i % 2: a partly seen V row is not finite
+    float2 ml[2][128];                                 // [stream][row] maximum (log2 units) and sum
+};
+static_assert(sizeof(TcMisc) <= 3072, "shared memory beside the tiles");
+
+struct TcGeometry {
+    int rows;        // query rows of an item's tile, all loaded by one box
+    int q_half;      // bytes of 64 dims of the query tile
+    int slots;
+    int box;         // slots of a page in one copy: gcd(page_size, 128)
+    int toks;        // tokens of the query box
+};
+
+bool paged_attn_tc_ok(const PagedKV &kv, int group, int q_dtype, int kv_dtype)
+{
+    return q_dtype == DS4G_BF16 && kv_dtype == DS4G_BF16 && (kv.head_dim == 64 || kv.head_dim == 128) &&
+           kv.page_size % 8 == 0 && group <= 128;
 }
+
+int paged_attn_tc_rows(int group, int max_new)
+{
+    const int toks = 128 / group;
+    return group * (toks < max_new ? toks : max_new);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_paged_attn_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a,
+                    const __grid_constant__ TcGeometry geo)
+{
+    constexpr int H = HD / 64;                         // 64-dim boxes of a row
+    constexpr uint32_t kTile = H * kTcHalf;            // bytes of a K or V tile
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t qbytes = (uint32_t)H * geo.q_half;  // one of two query buffers
+    unsigned char *ring = sm + 2 * qbytes;
+    TcMisc &x = *reinterpret_cast<TcMisc *>(ring + (uint32_t)geo.slots * kTile);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PartLayout lay(kAttnMaxCtasTc, a.rows, HD);
+    PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < geo.slots; ++i) {
+            mbar_init(&x.full[i], 1);
+            mbar_init(&x.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&x.q_full[i], 1);
+            mbar_init(&x.q_empty[i], 1);
+            mbar_init(&x.s_full[i], 1);
+            mbar_init(&x.p_full[i], 4);
+            mbar_init(&x.pv_done[i], 1);
+        }
+        mbar_init(&x.o_done, 1);
+        mbar_init(&x.o_free, kTcSoft / 32);
+        for (int i = 0; i < kTcItems; ++i) {
+            mbar_init(&x.item_full[i], 1);
+            mbar_init(&x.item_empty[i], 1 + kTcSoft / 32);
+        }
+        mbar_init(&x.done, 1);
+        x.abort_flag = 0;
+        x.poison[0] = x.poison[1] = 0;
+        mbar_fence_init();
+    }
+    if (warp == kTcMma) tmem_alloc(&x.tmem, 512);
+    if (threadIdx.x == kTcTma * 32) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        split->valid = 0;
+        split->status = DS4G_OK;
+        split->ctas = gridDim.x;
+    }
+    paged_cursor<kTcThreads>(a, kTcKeys, &x.cur, x.scratch);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = x.tmem;
+    volatile int *ab = &x.abort_flag;
+    auto give_up = [&]() {
+        x.abort_flag = 1;
+        split->status = DS4G_ETIMEOUT;
+    };
+    // stream s: scores (then P) at column 128 s, O at 256 + 128 s
+    auto ring_slot = [&](unsigned idx) { return idx % (unsigned)geo.slots; };
+    auto ring_phase = [&](unsigned idx) { return idx / (unsigned)geo.slots & 1u; };
+
+    if (warp == kTcTma) {
+        // ---------------- items, page look-ups, copies
+        PagedCursor cur = x.cur;
+        SeqWork w;
+        w.units = -1;
+        auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
+        };
+        const int boxes = kTcKeys / geo.box, per_page = a.kv.page_size;
+        unsigned idx = 0;    // tiles loaded
+        unsigned nq = 0;     // query tiles loaded
+        bool ok = true;
+        for (unsigned i = 0; ok; ++i) {
+            if (!warp_wait(&x.item_empty[i % kTcItems], (i / kTcItems & 1u) ^ 1u)) {
+                ok = false;
+                break;
+            }
+            PagedItem &it = x.item[i % kTcItems];
+            if (lane == 0) {
+                paged_next(a, kTcKeys, cur, w, split, it);
+                mbar_arrive(&x.item_full[i % kTcItems]);
+            }
+            __syncwarp();
+            if (!it.more) break;
+            if (!warp_wait(&x.q_empty[i & 1], (i >> 1 & 1u) ^ 1u)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                mbar_expect_tx(&x.q_full[i & 1], (uint32_t)(H * a.group * geo.toks * 128));
+                for (int h = 0; h < H; ++h)
+                    tma_load_3d(sm + (i & 1) * qbytes + h * geo.q_half, &qmap, h * 64, it.head * a.group,
+                                it.token + it.row0 / a.group, &x.q_full[i & 1]);
+                ++nq;
+            }
+            const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
+            const int lo = it.lo, hi = it.hi, head = it.head, t1 = it.t1;
+            for (int t = it.t0; ok && t < t1; ++t) {
+                // lane i: the i-th box of the tile
+                const int j = t * kTcKeys + lane * geo.box;
+                const bool load = lane < boxes && j < hi && j + geo.box > lo;
+                int page = -1, slot = 0;
+                if (load) {
+                    page = key_page(a, table, j);
+                    slot = j % per_page;
+                }
+                const uint32_t bits = load && page >= 0 ? ((1u << (geo.box >> 3)) - 1u) << (lane * (geo.box >> 3)) : 0u;
+                const uint32_t there = __reduce_or_sync(0xffffffffu, bits);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * geo.box * 128 * H;
+                if (page < 0) page = a.kv.n_pages;   // out of bounds: read as zeros
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++idx) {
+                    const unsigned sl = ring_slot(idx);
+                    if (!warp_wait(&x.empty[sl], ring_phase(idx) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (kv == 0) x.there[idx / 2 % 8] = there;
+                        mbar_expect_tx(&x.full[sl], bytes);
+                    }
+                    __syncwarp();
+                    if (load) {
+                        unsigned char *dst = ring + sl * kTile + lane * geo.box * 128;
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            tma_load_4d(dst + h * kTcHalf, kv == 0 ? &kmap : &vmap, h * 64, slot, head, page,
+                                        &x.full[sl]);
+                    }
+                }
+            }
+        }
+        if (!ok) give_up();
+        // nothing may be in flight when the CTA exits
+        volatile int never = 0;
+        for (unsigned k = idx > (unsigned)geo.slots ? idx - geo.slots : 0; k < idx; ++k)
+            mbar_wait(&x.full[ring_slot(k)], ring_phase(k), &never);
+        if (lane == 0)
+            for (unsigned k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait(&x.q_full[k & 1], k >> 1 & 1u, &never);
+    } else if (warp == kTcMma) {
+        // ---------------- MMAs.  The next unit's scores (of the other stream, or of this one
+        // once its P is used) and the oldest unit's P V are issued as their inputs arrive.
+        if (lane == 0) {
+            const uint32_t sbase = smem_u32(sm), rbase = smem_u32(ring);
+            const uint32_t id_s = idesc_bf16_f32(128, kTcKeys), id_o = idesc_bf16_f32_bmn(128, HD);
+            unsigned s_item = 0, p_item = 0, su = 0, pu = 0;   // items begun, units issued, of the two
+            int s_left = 0, p_tile = 0, p_end = 0, p_lo = 0, p_hi = 0, p_k = 0;
+            bool s_have = false, s_q = false, s_over = false, p_have = false, ok = true;
+            bool fresh[2] = {true, true};   // no MMA of the item has written the stream's O
+            long long since = clock64();
+            for (unsigned polls = 1;; ++polls) {
+                bool moved = false;
+                if (!s_over && !s_have && mbar_test(&x.item_full[s_item % kTcItems], s_item / kTcItems & 1u)) {
+                    const PagedItem &it = x.item[s_item % kTcItems];
+                    if (it.more) {
+                        s_left = it.t1 - it.t0;
+                        s_have = true;
+                        s_q = false;
+                    } else {
+                        s_over = true;
+                    }
+                    moved = true;
+                }
+                if (s_have && su - pu < 2) {
+                    if (!s_q) s_q = mbar_test(&x.q_full[s_item & 1], s_item >> 1 & 1u);
+                    const unsigned sl = ring_slot(2 * su);
+                    if (s_q && mbar_test(&x.full[sl], ring_phase(2 * su))) {
+                        tc_fence_after();
+                        const uint32_t qb = sbase + (s_item & 1) * qbytes, kb = rbase + sl * kTile;
+#pragma unroll
+                        for (int ks = 0; ks < HD / 16; ++ks)
+                            tc_mma_bf16(tmem + (su & 1) * 128,
+                                        sdesc_kmajor_sw128(qb + (uint32_t)(ks >> 2) * geo.q_half + (ks & 3) * 32),
+                                        sdesc_kmajor_sw128(kb + (uint32_t)(ks >> 2) * kTcHalf + (ks & 3) * 32), id_s,
+                                        ks > 0);
+                        tc_commit(&x.s_full[su & 1]);
+                        tc_commit(&x.empty[sl]);
+                        ++su;
+                        if (--s_left == 0) {
+                            tc_commit(&x.q_empty[s_item & 1]);
+                            s_have = false;
+                            ++s_item;
+                        }
+                        moved = true;
+                    }
+                }
+                if (pu < su) {
+                    if (!p_have) {   // its scores were issued, so the item is there
+                        const PagedItem &it = x.item[p_item % kTcItems];
+                        p_tile = it.t0;
+                        p_end = it.t1;
+                        p_lo = it.lo;
+                        p_hi = it.hi;
+                        p_k = 0;
+                        p_have = true;
+                        fresh[0] = fresh[1] = true;
+                    }
+                    const unsigned s = pu & 1, sl = ring_slot(2 * pu + 1);
+                    if (mbar_test(&x.p_full[s], pu >> 1 & 1u) && mbar_test(&x.full[sl], ring_phase(2 * pu + 1)) &&
+                        (p_k >= 2 || p_item == 0 || mbar_test(&x.o_free, (p_item - 1) & 1u))) {
+                        tc_fence_after();
+                        const int base = p_tile * kTcKeys;
+                        const int k0 = (max(p_lo - base, 0)) / 16, k1 = (min(p_hi - base, kTcKeys) + 15) / 16;
+                        const bool add = s ? !fresh[1] : !fresh[0];
+                        if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
+                        for (int ks = k0; ks < k1; ++ks)
+                            tc_mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + (uint32_t)ks * 8,
+                                           sdesc_mnmajor_sw128(rbase + sl * kTile + (uint32_t)ks * 2048, kTcHalf, 1024),
+                                           id_o, add || ks > k0);
+                        tc_commit(&x.empty[sl]);
+                        tc_commit(&x.pv_done[s]);
+                        ++pu;
+                        ++p_k;
+                        if (++p_tile == p_end) {
+                            tc_commit(&x.o_done);
+                            mbar_arrive(&x.item_empty[p_item % kTcItems]);
+                            p_have = false;
+                            ++p_item;
+                        }
+                        moved = true;
+                    }
+                }
+                if (s_over && pu == su) break;
+                if (moved) {
+                    since = clock64();
+                } else if ((polls & 255u) == 0 && (*ab || clock64() - since > kWaitCycles)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) give_up();
+            volatile int never = 0;
+            tc_commit(&x.done);
+            mbar_wait(&x.done, 0, &never);
+        }
+    } else {
+        // ---------------- softmax and output: stream s, row r = TMEM lane
+        const int s = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
+        const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+        const uint32_t t_s = tmem + lanes + s * 128, t_o = tmem + lanes + 256;
+        const float c = a.scale_log2;
+        bf16 *out = static_cast<bf16 *>(a.out);
+        const int win = a.window > 0 ? a.window : 0x7fffffff;
+        auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
+        };
+        // barrier of the softmax threads that also tells each of them whether any failed
+        auto soft_sync_any = [&](bool fail) -> bool {
+            uint32_t any;
+            asm volatile(
+                "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, 1, %2, q;\n"
+                " selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(any)
+                : "r"((uint32_t)fail), "n"(kTcSoft)
+                : "memory");
+            return any != 0;
+        };
+        unsigned u0 = 0;   // the CTA's units before this item
+        for (unsigned i = 0;; ++i) {
+            bool ok = warp_wait(&x.item_full[i % kTcItems], i / kTcItems & 1u);
+            if (soft_sync_any(!ok)) {
+                give_up();
+                break;
+            }
+            const PagedItem it = x.item[i % kTcItems];
+            if (!it.more) break;
+            const int units = it.t1 - it.t0;
+            const bool active = 32 * wq < it.n_rows;   // the warp has rows
+            const int row = it.row0 + r, tok = row / a.group, hd = row - tok * a.group;
+            const bool mine = r < it.n_rows;
+            const int pos = mine ? it.pos0 + tok : -1;          // -1: sees no key
+            const int see_lo = max(it.lo, pos - win + 1), see_hi = min(pos, it.hi - 1);
+            // keys that some rows of the tile see and others do not
+            const int pos_a = it.pos0 + it.row0 / a.group, pos_b = it.pos0 + (it.row0 + it.n_rows - 1) / a.group;
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int k = (int)((s ^ u0) & 1u); k < units; k += 2) {
+                const unsigned u = u0 + k, nth = u >> 1;
+                const int base = (it.t0 + k) * kTcKeys;
+                ok = ok && warp_wait(&x.s_full[s], nth & 1u);
+                if (ok && active) {
+                    tc_fence_after();
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32_async(t_s + 32 * q, v[q]);
+                    tmem_wait_ld();
+                    const uint32_t there = *const_cast<volatile uint32_t *>(&x.there[u % 8]);
+                    const int c0 = see_lo - base, c1 = see_hi - base;   // the row's keys, in columns
+                    const bool whole = __all_sync(0xffffffffu, (c0 <= 0 && c1 >= kTcKeys - 1) || !mine) && there == 0xffffu;
+                    float mx = -INFINITY;
+                    if (whole) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[q][e]));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int col = 32 * q + e;
+                                const bool in = col >= c0 && col <= c1 && (there >> (col >> 3) & 1u);
+                                if (!in) v[q][e] = 0xff800000u;   // -inf: its weight is 0
+                                mx = fmaxf(mx, __uint_as_float(v[q][e]));
+                            }
+                    }
+                    const float top = mx * c;   // c > 0
+                    if (first) {
+                        m = top;
+                        first = false;
+                    } else {
+                        const bool move = top > m + 8.f;   // (also from -inf)
+                        if (__any_sync(0xffffffffu, move && mine)) {
+                            const float f = move ? exp2f(m - top) : 1.f;   // m = -inf: 0, and O is 0
+                            if (move) m = top;
+                            l *= f;
+                            ok = warp_wait(&x.pv_done[s], (nth - 1) & 1u);   // O of the unit before
+                            tc_fence_after();
+                            if (ok) {
+#pragma unroll
+                                for (int q = 0; q < HD / 32; ++q) {
+                                    uint32_t o[32];
+                                    tmem_ld32_async(t_o + s * 128 + 32 * q, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st32(t_o + s * 128 + 32 * q, o);
+                                }
+                            }
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : m;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float p0, p1;
+                            const float y0 = fmaf(__uint_as_float(v[q][2 * e]), c, -off);
+                            const float y1 = fmaf(__uint_as_float(v[q][2 * e + 1]), c, -off);
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
+                            sum += p0 + p1;
+                            const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+                            p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                        }
+                        tmem_st16(t_s + 16 * q, p);
+                    }
+                    l += sum;
+                    tmem_wait_st();
+                }
+                // ---- V rows of the tile that no row, or not every row, may take as they are
+                const int end = min(it.hi - base, kTcKeys);
+                const int beg = max(it.lo - base, 0);
+                const bool edge = ((beg | end) & 15) != 0 && end > beg;
+                // columns only some rows see: (pos_a, pos_b], and (pos_a - win, pos_b - win]
+                const int h0 = max(pos_a + 1 - base, beg), h1 = min(pos_b + 1 - base, end);
+                const int g0 = a.window > 0 ? max(pos_a - win + 1 - base, beg) : 0;
+                const int g1 = a.window > 0 ? min(pos_b - win + 1 - base, end) : 0;
+                if (ok && (edge || h0 < h1 || g0 < g1)) {
+                    const unsigned vi = 2 * u + 1;
+                    unsigned char *vt = ring + ring_slot(vi) * kTile;
+                    ok = warp_wait(&x.full[ring_slot(vi)], ring_phase(vi));
+                    if (ok) {
+                        const int t = threadIdx.x & 127;
+                        auto chunk = [&](int key, int d16) {   // 16 bytes of dims 8 d16 .. of a V row
+                            return reinterpret_cast<uint4 *>(vt + (uint32_t)(d16 >> 3) * kTcHalf + (uint32_t)key * 128 +
+                                                             (uint32_t)(((d16 & 7) ^ (key & 7)) * 16));
+                        };
+                        if (edge) {
+                            const int b0 = beg & ~15, e1 = (end + 15) & ~15, n0 = beg - b0, n = n0 + e1 - end;
+                            for (int y = t; y < n * (HD / 8); y += 128) {
+                                const int z = y / (HD / 8);
+                                *chunk(z < n0 ? b0 + z : end + z - n0, y % (HD / 8)) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        auto finite_only = [&](int f0, int f1) {
+                            for (int y = t; y < (f1 - f0) * (HD / 8); y += 128) {
+                                uint4 *at = chunk(f0 + y / (HD / 8), y % (HD / 8));
+                                uint4 w4 = *at;
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&w4);
+                                bool bad = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & 0x7f80u) == 0x7f80u) {
+                                        w[e] &= 0xffff0000u;
+                                        bad = true;
+                                    }
+                                    if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+                                        w[e] &= 0xffffu;
+                                        bad = true;
+                                    }
+                                }
+                                if (bad) {
+                                    *at = w4;
+                                    x.poison[i & 1] = 1;
+                                }
+                            }
+                        };
+                        if (h0 < h1) finite_only(h0, h1);
+                        if (g0 < g1) finite_only(g0, g1);
+                        fence_proxy_async_smem();   // before the MMA reads the tile
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&x.p_full[s]);
+            }
+            // ---- the item's rows: both streams' O, this warp's half of the dims
+            x.ml[s][r] = make_float2(first ? -INFINITY : m, l);
+            ok = ok && warp_wait(&x.o_done, i & 1u);
+            if (soft_sync_any(!ok)) {
+                give_up();
+                break;
+            }
+            const float2 a0 = x.ml[0][r], a1 = x.ml[1][r];
+            const bool poison = *const_cast<volatile int *>(&x.poison[i & 1]) != 0;
+            if (threadIdx.x == 0) x.poison[(i + 1) & 1] = 0;
+            asm volatile("bar.sync 1, %0;" ::"n"(kTcSoft) : "memory");   // ml may be rewritten
+            if (active) {
+                tc_fence_after();
+                // the units that have a key: an MMA wrote the O of their streams
+                const int ka = max(it.lo / kTcKeys - it.t0, 0);
+                const int kb = it.hi > it.lo ? min((it.hi + kTcKeys - 1) / kTcKeys - it.t0, units) : 0;
+                const bool has0 = kb - ka >= 2 || (kb - ka == 1 && ((u0 + ka) & 1u) == 0);
+                const bool has1 = kb - ka >= 2 || (kb - ka == 1 && ((u0 + ka) & 1u) == 1);
+                const float mm = fmaxf(a0.x, a1.x), ref = mm == -INFINITY ? 0.f : mm;
+                const float f0 = exp2f(a0.x - ref), f1 = exp2f(a1.x - ref);
+                const float sum = f0 * a0.y + f1 * a1.y;
+                const bool part = it.part >= 0;
+                const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                const size_t at = (size_t)it.part * a.rows + r;
+                if (part && mine && s == 0) {
+                    float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + at * 2;
+                    ml[0] = mm;
+                    ml[1] = sum;
+                }
+#pragma unroll
+                for (int q = 0; q < HD / 64; ++q) {
+                    const int d = s * (HD / 2) + 32 * q;
+                    uint32_t o0[32], o1[32];
+                    tmem_ld32_async(t_o + d, o0);
+                    tmem_ld32_async(t_o + 128 + d, o1);
+                    tmem_wait_ld();
+                    float o[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        o[e] = 0.f;
+                        if (has0) o[e] = f0 * __uint_as_float(o0[e]);
+                        if (has1) o[e] = fmaf(f1, __uint_as_float(o1[e]), o[e]);
+                    }
+                    if (poison && mine) {
+                        // what was taken out of the V rows that this row sees and others do not
+                        const int w0 = it.t0 * kTcKeys, w1 = it.t1 * kTcKeys;
+                        auto add = [&](int j0, int j1) {
+                            for (int j = max(j0, max(see_lo, w0)); j < min(j1, min(see_hi + 1, w1)); ++j) {
+                                const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
+                                if (page < 0) continue;
+                                const bf16 *vr = static_cast<const bf16 *>(a.kv.v) + page * a.kv.page_stride +
+                                                 (j % a.kv.page_size) * a.kv.slot_stride + it.head * a.kv.head_stride + d;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float vv = __bfloat162float(vr[e]);
+                                    if (!isfinite(vv)) o[e] += vv;
+                                }
+                            }
+                        };
+                        add(pos_a + 1, pos_b + 1);
+                        // a key of both ranges is added once
+                        if (a.window > 0) add(pos_a - win + 1, min(pos_b - win + 1, pos_a + 1));
+                    }
+                    if (mine) {
+                        if (part) {
+                            float *po = reinterpret_cast<float *>(a.ws + lay.o) + at * HD + d;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<float4 *>(po + 4 * e) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        } else {
+                            bf16 *dst = out + (long long)(it.token + tok) * a.out_stride +
+                                        (it.head * a.group + hd) * HD + d;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    w[y] = pack_bf16x2(__float2bfloat16_rn(o[8 * e + 2 * y] * inv),
+                                                       __float2bfloat16_rn(o[8 * e + 2 * y + 1] * inv));
+                                *reinterpret_cast<uint4 *>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&x.o_free);
+                mbar_arrive(&x.item_empty[i % kTcItems]);
+            }
+            u0 += units;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kTcMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm)
+{
+    const int hd = a.kv.head_dim, halves = hd / 64;
+    TcGeometry g;
+    g.rows = a.rows;
+    g.toks = a.rows / a.group;
+    g.q_half = (a.rows + 7) / 8 * 8 * 128;
+    g.box = gcd(a.kv.page_size, kTcKeys);
+    const int tile = halves * (int)kTcHalf, qbytes = 2 * halves * g.q_half;
+    g.slots = (kTcSmem - (int)sizeof(TcMisc) - qbytes) / tile;
+    if (g.slots > kTcMaxSlots) g.slots = kTcMaxSlots;
+    const int smem = qbytes + g.slots * tile + (int)sizeof(TcMisc);
+
+    CUtensorMap qm, km, vm;
+    const int n_heads = a.group * a.kv.n_kv_heads;
+    const long long qd[3] = {hd, n_heads, a.s.n_tokens}, qs[2] = {hd, a.q_stride};
+    const int qb[3] = {64, a.group, g.toks};
+    cudaError_t e = tc::make_map_bf16_nd(&qm, a.q, 3, qd, qs, qb);
+    const long long cd[4] = {hd, a.kv.page_size, a.kv.n_kv_heads, a.kv.n_pages};
+    const long long cs[3] = {a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
+    const int cb[4] = {64, g.box, 1, 1};
+    if (!e) e = tc::make_map_bf16_nd(&km, a.kv.k, 4, cd, cs, cb);
+    if (!e) e = tc::make_map_bf16_nd(&vm, a.kv.v, 4, cd, cs, cb);
+    if (e) return e;
+    const int grid = paged_attn_grid(a, kTcKeys, nsm < kAttnMaxCtasTc ? nsm : kAttnMaxCtasTc);
+    auto kernel = hd == 64 ? k_paged_attn_tc<64> : k_paged_attn_tc<128>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (!e) e = launch_pdl(kernel, dim3(grid), dim3(kTcThreads), (size_t)smem, st, qm, km, vm, a, g);
+    if (!e && paged_attn_splits(a, kTcKeys)) e = paged_join_tc(a, grid, nsm, st);
+    return e;
+}
+
+}  // namespace ds4g

@@ -26,15 +26,18 @@ struct PagedItem {
     int n_new;              // its new tokens (at most max_new)
     int pos0;               // position of its first new token
     int row0, n_rows;       // query rows of the tile
-    int lo, hi;             // the sequence's keys
+    int lo, hi;             // keys that some row of the tile sees: [lo, hi)
     int t0, t1;             // this CTA's key tiles of the item
     int part;               // slot of the workspace, or -1: the whole item is here
     int more;               // 0: no item (the CTA is done)
 };
 
-// What the join needs of an item that begins in CTA c and ends in a later one.
+// CTA c's record: what the join needs of an item that begins in it and ends in a later one,
+// and how the CTA ended.
 struct PagedSplit {
-    int valid, last_cta, seq, head, token, row0, n_rows, pad;
+    int valid, last_cta, seq, head, token, row0, n_rows;
+    int status;             // DS4G_OK, or DS4G_ETIMEOUT: a bounded wait gave up
+    int ctas;               // CTAs of the launch
 };
 
 struct PartLayout {
@@ -161,8 +164,9 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     it.pos0 = w.pos0;
     it.row0 = (int)(item % w.row_tiles) * a.rows;
     it.n_rows = min(a.rows, w.n_new * a.group - it.row0);
-    it.lo = w.lo;
-    it.hi = w.hi;
+    const int pos_b = w.pos0 + (it.row0 + it.n_rows - 1) / a.group;
+    it.hi = min(w.hi, pos_b + 1);
+    it.lo = a.window > 0 ? max(w.lo, w.pos0 + it.row0 / a.group - a.window + 1) : w.lo;
     it.t0 = tile0 + x;
     it.t1 = tile0 + x + take;
     const bool begins = x == 0, ends = x + take == w.tiles;
@@ -170,9 +174,13 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     if (begins && !ends) {
         // the CTA of the item's last unit e: the largest c with c total / ctas <= e
         const unsigned long long e = (unsigned long long)(cur.at + w.tiles - 1);
-        PagedSplit r = {1, (int)(((e + 1) * (unsigned long long)cur.ctas - 1) / (unsigned long long)cur.total),
-                        it.seq, it.head, it.token, it.row0, it.n_rows, 0};
-        *split = r;
+        split->valid = 1;
+        split->last_cta = (int)(((e + 1) * (unsigned long long)cur.ctas - 1) / (unsigned long long)cur.total);
+        split->seq = it.seq;
+        split->head = it.head;
+        split->token = it.token;
+        split->row0 = it.row0;
+        split->n_rows = it.n_rows;
     }
     cur.at += take;
     cur.local += take;

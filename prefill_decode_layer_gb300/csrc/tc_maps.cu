@@ -41,5 +41,24 @@ cudaError_t make_map_bf16(CUtensorMap *m, const void *base, int rows, int cols, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_map_bf16_nd(CUtensorMap *m, const void *base, int rank, const long long *dims,
+                             const long long *strides, const int *box)
+{
+    auto fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t d[4], s[3];
+    cuuint32_t b[4];
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        b[i] = (cuuint32_t)box[i];
+        if (i > 0) s[i - 1] = (cuuint64_t)strides[i - 1] * 2;
+    }
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, s, b, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace tc
 }  // namespace ds4g

@@ -104,6 +104,7 @@ def lib():
             "ds4g_paged_append": ([vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp], i32),
             "ds4g_paged_attention_workspace_bytes": ([vp, vp, i32], sz),
             "ds4g_paged_attention": ([vp, vp, vp, i64, vp, i64, i32, i32, C.c_float, i32, vp, sz, vp], i32),
+            "ds4g_paged_attention_status": ([vp, vp], i32),
             "ds4g_probs": ([vp, i64, i32, i32, C.c_float, vp, i64, vp], i32),
             "ds4g_verify_draft": ([vp, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp], i32),
             "ds4g_strerror": ([i32], C.c_char_p),
@@ -518,6 +519,13 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.
     _call("ds4g_paged_attention", batch.device, stream, kv.ref, batch.ref, q.data_ptr(), _row_stride(q),
           out.data_ptr(), _row_stride(out), heads, _DTYPES[dt], scale, window, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
+
+
+def paged_attention_status(workspace: torch.Tensor, stream=None) -> int:
+    """ds4g_paged_attention_status: OK or ETIMEOUT of the workspace's last call (synchronises)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(workspace.device)
+    return lib().ds4g_paged_attention_status(workspace.data_ptr(), stream.cuda_stream)
 
 
 def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:

@@ -128,6 +128,7 @@ def attend(p, q, window=0, scale=0.0, start=True, max_new=None, out=None, ws=Non
         ws = torch.full((pdl.paged_attention_workspace_bytes(kv, batch, q.shape[1]),), 255, dtype=torch.uint8,
                         device="cuda")
     pdl.paged_attention(kv, batch, q, out, ws, scale=scale, window=window)
+    assert pdl.paged_attention_status(ws) == 0
     return out
 
 

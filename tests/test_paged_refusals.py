@@ -74,10 +74,11 @@ def test_attention_refuses(lib):
     assert need > 0
     assert attention(lib, None, b) == EINVAL and attention(lib, kv, None) == EINVAL
     for bad in (dict(q=None), dict(q=8), dict(out=None), dict(out=4100), dict(qs=511), dict(os=64), dict(heads=0),
-                dict(heads=7), dict(dtype=9), dict(scale=float("nan")), dict(scale=float("inf")), dict(ws=None),
+                dict(heads=7), dict(dtype=9), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-1.0), dict(ws=None),
                 dict(ws=4096 + 128)):
         assert attention(lib, kv, b, **bad) == EINVAL, bad
     assert attention(lib, kv, b, n=need - 1) == ESIZE
+    assert lib.ds4g_paged_attention_status(None, None) == EINVAL
     assert attention(lib, kv, structs(max_new=129)[1]) == EINVAL
     assert lib.ds4g_paged_attention_workspace_bytes(C.byref(kv), C.byref(b), 7) == 0
     assert attention(lib, kv, structs(n_seqs=0, n_tokens=0)[1]) == OK

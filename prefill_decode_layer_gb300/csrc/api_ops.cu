@@ -121,7 +121,7 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
     if (!nsm) return DS4G_ECUDA;
     const float sc = scale != 0.f ? scale : 1.f / sqrtf((float)kv->head_dim);
     AttnArgs a = {kv_of(*kv), seqs_of(*batch), q, out, q_stride, out_stride, n_heads / kv->n_kv_heads, 0,
-                  (float)((double)sc * 1.4426950408889634), window > 0 ? window : 0, static_cast<char *>(workspace)};
+                  (float)((double)sc * 1.4426950408889634), window > 0 ? window : 0, 0, static_cast<char *>(workspace)};
     return status_of(paged_attention(a, dtype, kv->dtype, static_cast<cudaStream_t>(stream), nsm));
 }
 

@@ -41,17 +41,17 @@ struct AttnArgs {
     int rows;          // query rows of a row tile: (token, head of the group) pairs
     float scale_log2;  // scale * log2(e)
     int window;        // 0: no window
+    int whole;         // items are not cut between CTAs
     char *ws;          // records, then parts (PartLayout)
 };
 // Whether the tensor-core form covers the call (paged_attn_tc.cu).
 bool paged_attn_tc_ok(const PagedKV &kv, int group, int q_dtype, int kv_dtype);
 // Query rows per tile of the tensor-core form: whole tokens, at most 128 rows.
 int paged_attn_tc_rows(int group, int max_new);
-cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm);
-// Shared by the two forms (paged_attn.cu): CTAs of a launch over units of kt keys, whether
-// its items can be split, and the join of the tensor-core form's parts.
-int paged_attn_grid(const AttnArgs &a, int kt, int most);
-bool paged_attn_splits(const AttnArgs &a, int kt);
+cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm);
+// Shared by the two forms (paged_attn.cu): CTAs of a launch over units of kt keys (and
+// a.whole), and the join of the tensor-core form's parts.
+int paged_attn_grid(AttnArgs &a, int kt, int most);
 cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st);
 size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype);
 // DS4G_OK or DS4G_ETIMEOUT of the last call that used the workspace (synchronises st).

@@ -238,19 +238,48 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
 
 // ------------------------------------------------------------------ join
 
-// One row of a split item per CTA and turn: warp w adds the parts w, w + 8, .. of the row, the
-// eight partial sums are added in order.  Bound: latency (a few KB to a few MB of
-// parts from L2); eight warps keep eight parts' loads in flight.
+// Rows of split items: out = sum_i f_i o_i / sum_i f_i l_i over the row's parts i, f_i = 2^(m_i -
+// max m).  A row of few parts is one warp's, eight rows a CTA; one of many parts (a long
+// sequence alone) is a CTA's, warp w adding the parts w, w + 8, .. and the eight partial sums
+// then added in order.  Bound: latency (KBs to a few MB of parts from L2).
 static constexpr int kJoinThreads = 256;
 static constexpr int kJoinWarps = kJoinThreads / 32;
+static constexpr int kJoinFew = 16;   // parts that one warp adds by itself
 
-template <typename T, int ROWS, int CTAS, int HDL>   // HDL: dims per lane
+// V consecutive floats, 4 V bytes aligned (V 2, 4 or 8).
+template <int V> __device__ __forceinline__ void ld_part(const float *p, float (&x)[V])
+{
+    if constexpr (V == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x; x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + i);
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void st_row(T *p, const float (&x)[V])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) *reinterpret_cast<float2 *>(p + i) = make_float2(x[i], x[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            *reinterpret_cast<uint32_t *>(p + i) =
+                pack_bf16x2(__float2bfloat16_rn(x[i]), __float2bfloat16_rn(x[i + 1]));
+    }
+}
+
+template <typename T, int ROWS, int CTAS, int V>   // V: adjacent dims per lane
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ AttnArgs a, int ctas)
 {
     __shared__ short s_cta[CTAS];
-    __shared__ int s_first[CTAS + 1];   // rows before the i-th split item
+    __shared__ int s_first[CTAS + 1];   // jobs before the i-th split item
     __shared__ int s_n;
-    __shared__ float s_o[kJoinWarps][32 * HDL], s_ml[kJoinWarps][2];
+    __shared__ float s_o[kJoinWarps][32 * V], s_l[kJoinWarps];
     const int hd = a.kv.head_dim;
     const int stride = ROWS > 0 ? ROWS : a.rows;
     const PartLayout lay(CTAS, stride, hd);
@@ -259,31 +288,42 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     const float *po = reinterpret_cast<const float *>(a.ws + lay.o);
     T *out = static_cast<T *>(a.out);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int d = lane * V;
     pdl_wait();
     pdl_trigger();
     if (warp == 0) {
-        int n = 0, rows = 0;
-        for (int c0 = 0; c0 < ctas; c0 += 32) {
-            const int c = c0 + lane;
-            int nr = c < ctas && split[c].valid ? split[c].n_rows : 0;
-            const unsigned has = __ballot_sync(0xffffffffu, nr > 0);
-            int incl = nr;
+        int nr[(CTAS + 31) / 32];   // all loads first: one trip to L2
+#pragma unroll
+        for (int k = 0; k < (CTAS + 31) / 32; ++k) {
+            const int c = 32 * k + lane;
+            nr[k] = 0;
+            if (c < ctas) {
+                const PagedSplit r = split[c];
+                if (r.valid) nr[k] = r.last_cta - c < kJoinFew ? (r.n_rows + kJoinWarps - 1) / kJoinWarps : r.n_rows;
+            }
+        }
+        int n = 0, jobs = 0;
+#pragma unroll
+        for (int k = 0; k < (CTAS + 31) / 32; ++k) {
+            const unsigned has = __ballot_sync(0xffffffffu, nr[k] > 0);
+            if (!has) continue;
+            int incl = nr[k];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            if (nr > 0) {
+            if (nr[k] > 0) {
                 const int i = n + __popc(has & ((1u << lane) - 1u));
-                s_cta[i] = (short)c;
-                s_first[i] = rows + incl - nr;
+                s_cta[i] = (short)(32 * k + lane);
+                s_first[i] = jobs + incl - nr[k];
             }
             n += __popc(has);
-            rows += __shfl_sync(0xffffffffu, incl, 31);
+            jobs += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) {
             s_n = n;
-            s_first[n] = rows;
+            s_first[n] = jobs;
         }
     }
     __syncthreads();
@@ -295,45 +335,62 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
             if (s_first[mid] <= job) lo = mid;
             else hi = mid;
         }
-        const int r = job - s_first[lo], c = s_cta[lo];
+        const int c = s_cta[lo];
         const PagedSplit sp = split[c];
         const int parts = sp.last_cta - c + 1;
+        const bool few = parts <= kJoinFew;
+        const int r = few ? (job - s_first[lo]) * kJoinWarps + warp : job - s_first[lo];
+        const int p0 = few ? 0 : warp, step = few ? 1 : kJoinWarps;
+        const bool live = r < sp.n_rows;
         // part i: the CTA's own tail, then the head parts of the CTAs after it
         auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride + r; };
-        float mx = -INFINITY;
-        for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i) * 2]);
-        mx = warp_max(mx);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float acc[HDL], sum = 0.f;
+        float acc[V], sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < HDL; ++e) acc[e] = 0.f;
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        if (live) {
+            float mx = -INFINITY;
+            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i) * 2]);
+            mx = warp_max(mx);
+            const float ref = finite_max(mx);
 #pragma unroll 4
-        for (int i = warp; i < parts; i += kJoinWarps) {
-            const size_t s = slot(i);
-            const float f = exp2f(ml[s * 2] - ref);
-            sum = fmaf(f, ml[s * 2 + 1], sum);
+            for (int i = p0; i < parts; i += step) {
+                const size_t s = slot(i);
+                const float2 m2 = *reinterpret_cast<const float2 *>(ml + s * 2);
+                const float f = exp2f(m2.x - ref);
+                sum = fmaf(f, m2.y, sum);
+                if (d < hd) {
+                    float x[V];
+                    ld_part<V>(po + s * hd + d, x);
 #pragma unroll
-            for (int e = 0; e < HDL; ++e) {
-                const int d = lane + 32 * e;
-                if (d < hd) acc[e] = fmaf(f, po[s * hd + d], acc[e]);
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(f, x[e], acc[e]);
+                }
             }
         }
+        if (!few) {
 #pragma unroll
-        for (int e = 0; e < HDL; ++e) s_o[warp][lane + 32 * e] = acc[e];
-        if (lane == 0) s_ml[warp][0] = sum;
-        __syncthreads();
-        for (int d = threadIdx.x; d < hd; d += kJoinThreads) {
-            float v = 0.f, t = 0.f;
+            for (int e = 0; e < V; ++e) s_o[warp][d + e] = acc[e];
+            if (lane == 0) s_l[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+                sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                v += s_o[w][d];
-                t += s_ml[w][0];
+                for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    sum += s_l[w];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] += s_o[w][d + e];
+                }
             }
+            __syncthreads();
+        }
+        if (live && d < hd && (few || warp == 0)) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int row = sp.row0 + r, tk = row / a.group, h = row - tk * a.group;
-            store_out<T>(out + (long long)(sp.token + tk) * a.out_stride + (sp.head * a.group + h) * hd + d,
-                         t == 0.f ? 0.f : v / t);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= inv;
+            st_row<T, V>(out + (long long)(sp.token + tk) * a.out_stride + (sp.head * a.group + h) * hd + d, acc);
         }
-        __syncthreads();
     }
 }
 
@@ -365,7 +422,7 @@ cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status)
 template <typename T, int ROWS, int CTAS>
 static cudaError_t join(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
 {
-    const int grid = 2 * nsm;
+    const int grid = 4 * nsm;
     if (a.kv.head_dim <= 64) return launch_pdl(k_paged_join<T, ROWS, CTAS, 2>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
     if (a.kv.head_dim <= 128)
         return launch_pdl(k_paged_join<T, ROWS, CTAS, 4>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
@@ -376,32 +433,30 @@ cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
     return join<bf16, 0, kAttnMaxCtasTc>(a, ctas, nsm, st);
 }
 
-// Most units a call can have, by the sizes the host knows.
-static long long most_units(const AttnArgs &a, int kt)
+// Most items of a call and most units of an item, by the sizes the host knows.
+static long long most_items(const AttnArgs &a)
+{
+    return (long long)a.s.n_seqs * a.kv.n_kv_heads * (((long long)a.s.max_new * a.group + a.rows - 1) / a.rows);
+}
+static long long most_tiles(const AttnArgs &a, int kt)
 {
     long long keys = (long long)a.s.width * a.kv.page_size;
     if (a.window > 0) {
         const long long seen = (long long)a.window + a.s.max_new - 1;   // may begin inside a unit
         keys = seen + kt - 1 < keys ? seen + kt - 1 : keys;
     }
-    const long long tiles = keys > 0 ? (keys + kt - 1) / kt : 1;
-    const long long row_tiles = ((long long)a.s.max_new * a.group + a.rows - 1) / a.rows;
-    return (long long)a.s.n_seqs * a.kv.n_kv_heads * row_tiles * tiles;
+    return keys > 0 ? (keys + kt - 1) / kt : 1;
 }
-int paged_attn_grid(const AttnArgs &a, int kt, int most)
+int paged_attn_grid(AttnArgs &a, int kt, int most)
 {
-    const long long u = most_units(a, kt);
+    const long long tiles = most_tiles(a, kt);
+    a.whole = tiles <= 2;
+    const long long u = most_items(a) * (a.whole ? 1 : tiles);
     return (int)(u < most ? u : most);
-}
-// Whether an item can be split between CTAs: not when every item is one unit.
-bool paged_attn_splits(const AttnArgs &a, int kt)
-{
-    return most_units(a, kt) > (long long)a.s.n_seqs * a.kv.n_kv_heads *
-                                   (((long long)a.s.max_new * a.group + a.rows - 1) / a.rows);
 }
 
 template <typename TQ, typename TKV, int LPK, int D, int KB>
-static cudaError_t simt(const AttnArgs &a, int nsm, cudaStream_t st)
+static cudaError_t simt(AttnArgs &a, int nsm, cudaStream_t st)
 {
     auto kernel = k_paged_attn<TQ, TKV, LPK, D, KB>;
     const size_t smem = (size_t)PaStreams<LPK>::n * kPaRows * (2 + a.kv.head_dim) * 4;
@@ -412,10 +467,10 @@ static cudaError_t simt(const AttnArgs &a, int nsm, cudaStream_t st)
     const int most = 2 * nsm < kAttnMaxCtas ? 2 * nsm : kAttnMaxCtas;
     const int grid = paged_attn_grid(a, kPaKeys, most);
     cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kPaThreads), smem, st, a);
-    if (!e && paged_attn_splits(a, kPaKeys)) e = join<TQ, kAttnRowsSimt, kAttnMaxCtas>(a, grid, nsm, st);
+    if (!e && !a.whole) e = join<TQ, kAttnRowsSimt, kAttnMaxCtas>(a, grid, nsm, st);
     return e;
 }
-template <typename TQ, typename TKV> static cudaError_t simt_dim(const AttnArgs &a, int nsm, cudaStream_t st)
+template <typename TQ, typename TKV> static cudaError_t simt_dim(AttnArgs &a, int nsm, cudaStream_t st)
 {
     if (a.kv.head_dim <= 32) return simt<TQ, TKV, 8, 4, 4>(a, nsm, st);
     if (a.kv.head_dim <= 64) return simt<TQ, TKV, 16, 4, 4>(a, nsm, st);

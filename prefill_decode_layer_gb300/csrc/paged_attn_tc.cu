@@ -44,7 +44,6 @@ static constexpr int kTcThreads = kTcSoft + 64;
 static constexpr int kTcTma = kTcSoft / 32, kTcMma = kTcTma + 1;   // their warps
 static constexpr int kTcMaxSlots = 8;
 static constexpr int kTcItems = 4;                     // items ahead of the softmax at most
-static constexpr uint32_t kTcHalf = kTcKeys * 128;     // bytes of 64 dims of a K or V tile
 static constexpr int kTcSmem = 227 * 1024;
 
 struct TcMisc {
@@ -71,12 +70,27 @@ struct TcGeometry {
     int slots;
     int box;         // slots of a page in one copy: gcd(page_size, 128)
     int toks;        // tokens of the query box
+    // coordinates of (page, head) in the cache's tensor map: 64-dim block head * block, index
+    // page * page_mul + head * head_mul; `none` is an index out of bounds
+    int block, page_mul, head_mul, none;
 };
+
+// The tensor map of a cache has five dimensions: 64 dims, 8 slots, the 64-dim blocks, the
+// groups of 8 slots of a page, and the pages.  A copy then brings a page's rows as
+// [8-slot group][64-dim block][8 rows of 128 bytes], whose 8-row groups lie evenly over
+// all pages of a tile, and one copy suffices for both 64-dim halves.  Heads join the
+// 64-dim blocks where they are adjacent, else the pages (heads outside the slots).
+static bool heads_adjacent(const PagedKV &kv) { return kv.n_kv_heads == 1 || kv.head_stride == kv.head_dim; }
+static bool heads_divide_pages(const PagedKV &kv)
+{
+    return kv.page_stride % kv.head_stride == 0 &&
+           (kv.page_stride / kv.head_stride) * (kv.n_pages - 1) + kv.n_kv_heads < 0x7fffffff;
+}
 
 bool paged_attn_tc_ok(const PagedKV &kv, int group, int q_dtype, int kv_dtype)
 {
     return q_dtype == DS4G_BF16 && kv_dtype == DS4G_BF16 && (kv.head_dim == 64 || kv.head_dim == 128) &&
-           kv.page_size % 8 == 0 && group <= 128;
+           kv.page_size % 8 == 0 && group <= 128 && (heads_adjacent(kv) || heads_divide_pages(kv));
 }
 
 int paged_attn_tc_rows(int group, int max_new)
@@ -92,7 +106,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const __grid_constant__ TcGeometry geo)
 {
     constexpr int H = HD / 64;                         // 64-dim boxes of a row
-    constexpr uint32_t kTile = H * kTcHalf;            // bytes of a K or V tile
+    constexpr uint32_t kTile = H * kTcKeys * 128;      // bytes of a K or V tile
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t qbytes = (uint32_t)H * geo.q_half;  // one of two query buffers
     unsigned char *ring = sm + 2 * qbytes;
@@ -200,7 +214,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t bits = load && page >= 0 ? ((1u << (geo.box >> 3)) - 1u) << (lane * (geo.box >> 3)) : 0u;
                 const uint32_t there = __reduce_or_sync(0xffffffffu, bits);
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * geo.box * 128 * H;
-                if (page < 0) page = a.kv.n_pages;   // out of bounds: read as zeros
+                // a page that is not there: out of bounds, read as zeros
+                const int at = page < 0 ? geo.none : page * geo.page_mul + head * geo.head_mul;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++idx) {
                     const unsigned sl = ring_slot(idx);
@@ -213,13 +228,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         mbar_expect_tx(&x.full[sl], bytes);
                     }
                     __syncwarp();
-                    if (load) {
-                        unsigned char *dst = ring + sl * kTile + lane * geo.box * 128;
-#pragma unroll
-                        for (int h = 0; h < H; ++h)
-                            tma_load_4d(dst + h * kTcHalf, kv == 0 ? &kmap : &vmap, h * 64, slot, head, page,
-                                        &x.full[sl]);
-                    }
+                    if (load)
+                        tma_load_5d(ring + sl * kTile + lane * geo.box * 128 * H, kv == 0 ? &kmap : &vmap, 0, 0,
+                                    head * geo.block, slot >> 3, at, &x.full[sl]);
                 }
             }
         }
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int ks = 0; ks < HD / 16; ++ks)
                             tc_mma_bf16(tmem + (su & 1) * 128,
                                         sdesc_kmajor_sw128(qb + (uint32_t)(ks >> 2) * geo.q_half + (ks & 3) * 32),
-                                        sdesc_kmajor_sw128(kb + (uint32_t)(ks >> 2) * kTcHalf + (ks & 3) * 32), id_s,
+                                        sdesc_kmajor_sw128(kb + (uint32_t)(ks >> 2) * 1024 + (ks & 3) * 32, H * 1024), id_s,
                                         ks > 0);
                         tc_commit(&x.s_full[su & 1]);
                         tc_commit(&x.empty[sl]);
@@ -298,7 +309,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
                         for (int ks = k0; ks < k1; ++ks)
                             tc_mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + (uint32_t)ks * 8,
-                                           sdesc_mnmajor_sw128(rbase + sl * kTile + (uint32_t)ks * 2048, kTcHalf, 1024),
+                                           sdesc_mnmajor_sw128(rbase + sl * kTile + (uint32_t)ks * (2 * H * 1024), 1024,
+                                                               H * 1024),
                                            id_o, add || ks > k0);
                         tc_commit(&x.empty[sl]);
                         tc_commit(&x.pv_done[s]);
@@ -373,30 +385,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = ok && warp_wait(&x.s_full[s], nth & 1u);
                 if (ok && active) {
                     tc_fence_after();
-                    uint32_t v[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32_async(t_s + 32 * q, v[q]);
-                    tmem_wait_ld();
+                    // The scores are read in halves, twice the second one, so that a thread
+                    // holds 64 of them: columns 64-127 for the maximum, 0-63 for the maximum and
+                    // the weights, 64-127 again (P of 0-63 covers columns 0-31 only).
+                    uint32_t v[2][32];
                     const uint32_t there = *const_cast<volatile uint32_t *>(&x.there[u % 8]);
                     const int c0 = see_lo - base, c1 = see_hi - base;   // the row's keys, in columns
                     const bool whole = __all_sync(0xffffffffu, (c0 <= 0 && c1 >= kTcKeys - 1) || !mine) && there == 0xffffu;
-                    float mx = -INFINITY;
-                    if (whole) {
+                    auto load = [&](int h) {
+                        tmem_ld32_async(t_s + 64 * h, v[0]);
+                        tmem_ld32_async(t_s + 64 * h + 32, v[1]);
+                        tmem_wait_ld32(v[0]);
+                        tmem_wait_ld32(v[1]);
+                        if (!whole) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[q][e]));
-                    } else {
+                                for (int e = 0; e < 32; ++e) {
+                                    const int col = 64 * h + 32 * q + e;
+                                    const bool in = col >= c0 && col <= c1 && (there >> (col >> 3) & 1u);
+                                    if (!in) v[q][e] = 0xff800000u;   // -inf: its weight is 0
+                                }
+                        }
+                    };
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                    for (int h = 1; h >= 0; --h) {
+                        load(h);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int col = 32 * q + e;
-                                const bool in = col >= c0 && col <= c1 && (there >> (col >> 3) & 1u);
-                                if (!in) v[q][e] = 0xff800000u;   // -inf: its weight is 0
-                                mx = fmaxf(mx, __uint_as_float(v[q][e]));
-                            }
+                        for (int e = 0; e < 32; ++e)
+                            mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(__uint_as_float(v[0][e]), __uint_as_float(v[1][e])));
                     }
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     const float top = mx * c;   // c > 0
                     if (first) {
                         m = top;
@@ -414,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 for (int q = 0; q < HD / 32; ++q) {
                                     uint32_t o[32];
                                     tmem_ld32_async(t_o + s * 128 + 32 * q, o);
-                                    tmem_wait_ld();
+                                    tmem_wait_ld32(o);
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                                     tmem_st32(t_o + s * 128 + 32 * q, o);
@@ -423,24 +443,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     const float off = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t p[16];
+                    for (int h = 0; h < 2; ++h) {
+                        if (h) load(1);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float p0, p1;
-                            const float y0 = fmaf(__uint_as_float(v[q][2 * e]), c, -off);
-                            const float y1 = fmaf(__uint_as_float(v[q][2 * e + 1]), c, -off);
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
-                            sum += p0 + p1;
-                            const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
-                            p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float p0, p1;
+                                const float y0 = fmaf(__uint_as_float(v[q][2 * e]), c, -off);
+                                const float y1 = fmaf(__uint_as_float(v[q][2 * e + 1]), c, -off);
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
+                                sum[e & 1] += p0;
+                                sum[2 + (e & 1)] += p1;
+                                const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+                                p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                            }
+                            tmem_st16(t_s + 32 * h + 16 * q, p);
                         }
-                        tmem_st16(t_s + 16 * q, p);
                     }
-                    l += sum;
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
                 }
                 // ---- V rows of the tile that no row, or not every row, may take as they are
@@ -458,7 +483,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (ok) {
                         const int t = threadIdx.x & 127;
                         auto chunk = [&](int key, int d16) {   // 16 bytes of dims 8 d16 .. of a V row
-                            return reinterpret_cast<uint4 *>(vt + (uint32_t)(d16 >> 3) * kTcHalf + (uint32_t)key * 128 +
+                            return reinterpret_cast<uint4 *>(vt + (uint32_t)(key >> 3) * (H * 1024) +
+                                                             (uint32_t)(d16 >> 3) * 1024 + (uint32_t)(key & 7) * 128 +
                                                              (uint32_t)(((d16 & 7) ^ (key & 7)) * 16));
                         };
                         if (edge) {
@@ -535,7 +561,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     uint32_t o0[32], o1[32];
                     tmem_ld32_async(t_o + d, o0);
                     tmem_ld32_async(t_o + 128 + d, o1);
-                    tmem_wait_ld();
+                    tmem_wait_ld32(o0);
+                    tmem_wait_ld32(o1);
                     float o[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -607,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm)
+cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm)
 {
     const int hd = a.kv.head_dim, halves = hd / 64;
     TcGeometry g;
@@ -615,7 +642,7 @@ cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm)
     g.toks = a.rows / a.group;
     g.q_half = (a.rows + 7) / 8 * 8 * 128;
     g.box = gcd(a.kv.page_size, kTcKeys);
-    const int tile = halves * (int)kTcHalf, qbytes = 2 * halves * g.q_half;
+    const int tile = halves * kTcKeys * 128, qbytes = 2 * halves * g.q_half;
     g.slots = (kTcSmem - (int)sizeof(TcMisc) - qbytes) / tile;
     if (g.slots > kTcMaxSlots) g.slots = kTcMaxSlots;
     const int smem = qbytes + g.slots * tile + (int)sizeof(TcMisc);
@@ -625,17 +652,24 @@ cudaError_t paged_attn_tc(const AttnArgs &a, cudaStream_t st, int nsm)
     const long long qd[3] = {hd, n_heads, a.s.n_tokens}, qs[2] = {hd, a.q_stride};
     const int qb[3] = {64, a.group, g.toks};
     cudaError_t e = tc::make_map_bf16_nd(&qm, a.q, 3, qd, qs, qb);
-    const long long cd[4] = {hd, a.kv.page_size, a.kv.n_kv_heads, a.kv.n_pages};
-    const long long cs[3] = {a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
-    const int cb[4] = {64, g.box, 1, 1};
-    if (!e) e = tc::make_map_bf16_nd(&km, a.kv.k, 4, cd, cs, cb);
-    if (!e) e = tc::make_map_bf16_nd(&vm, a.kv.v, 4, cd, cs, cb);
+    const bool adj = heads_adjacent(a.kv);
+    const long long per = adj ? 1 : a.kv.page_stride / a.kv.head_stride;
+    const long long n_at = adj ? a.kv.n_pages : per * (a.kv.n_pages - 1) + a.kv.n_kv_heads;
+    g.block = adj ? halves : 0;
+    g.page_mul = (int)per;
+    g.head_mul = adj ? 0 : 1;
+    g.none = (int)n_at;
+    const long long cd[5] = {64, 8, adj ? halves * a.kv.n_kv_heads : halves, a.kv.page_size / 8, n_at};
+    const long long cs[4] = {a.kv.slot_stride, 64, 8 * a.kv.slot_stride, adj ? a.kv.page_stride : a.kv.head_stride};
+    const int cb[5] = {64, 8, halves, g.box / 8, 1};
+    if (!e) e = tc::make_map_bf16_nd(&km, a.kv.k, 5, cd, cs, cb);
+    if (!e) e = tc::make_map_bf16_nd(&vm, a.kv.v, 5, cd, cs, cb);
     if (e) return e;
     const int grid = paged_attn_grid(a, kTcKeys, nsm < kAttnMaxCtasTc ? nsm : kAttnMaxCtasTc);
     auto kernel = hd == 64 ? k_paged_attn_tc<64> : k_paged_attn_tc<128>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (!e) e = launch_pdl(kernel, dim3(grid), dim3(kTcThreads), (size_t)smem, st, qm, km, vm, a, g);
-    if (!e && paged_attn_splits(a, kTcKeys)) e = paged_join_tc(a, grid, nsm, st);
+    if (!e && !a.whole) e = paged_join_tc(a, grid, nsm, st);
     return e;
 }
 

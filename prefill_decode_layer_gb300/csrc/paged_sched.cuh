@@ -9,6 +9,9 @@
 // of an item that others share goes to the workspace as a part (row maxima, row sums,
 // unnormalised rows), and k_paged_join adds the parts in CTA order.  A CTA has at most
 // two parts: of the item it begins in (slot 2c) and of the one it ends in (slot 2c + 1).
+// Where no item can have more than two units (a short window or table), items are not cut
+// and the unit of the division is the item: a second launch for the join would cost more than
+// the second unit.
 #pragma once
 
 #include "paged.h"
@@ -78,7 +81,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
     const int t = w.hi > w.lo ? (w.hi + kt - 1) / kt - w.lo / kt : 1;   // one empty unit still writes zeros
     w.tiles = t;
     w.row_tiles = (n * a.group + a.rows - 1) / a.rows;
-    w.units = (long long)a.kv.n_kv_heads * w.row_tiles * t;
+    w.units = (long long)a.kv.n_kv_heads * w.row_tiles * (a.whole ? 1 : t);
     return w;
 }
 
@@ -152,10 +155,10 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
         cur.local -= w.units;
         w = seq_work(a, ++cur.seq, kt);
     }
-    const long long item = cur.local / w.tiles;
-    const int x = (int)(cur.local - item * w.tiles);
+    const long long item = a.whole ? cur.local : cur.local / w.tiles;
+    const int x = a.whole ? 0 : (int)(cur.local - item * w.tiles);
     const long long left = cur.end - cur.at;
-    const int take = (int)min((long long)(w.tiles - x), left);
+    const int take = a.whole ? w.tiles : (int)min((long long)(w.tiles - x), left);
     const int tile0 = w.lo / kt;
     it.seq = cur.seq;
     it.head = (int)(item / w.row_tiles);
@@ -182,8 +185,8 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
         split->row0 = it.row0;
         split->n_rows = it.n_rows;
     }
-    cur.at += take;
-    cur.local += take;
+    cur.at += a.whole ? 1 : take;
+    cur.local += a.whole ? 1 : take;
 }
 
 // Page of key j of sequence b, or -1.

@@ -127,7 +127,7 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
         "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-// The same of a box of a 3-D and of a 4-D map.
+// The same of a box of a 3-D and of a 5-D map.
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar)
 {
     asm volatile(
@@ -136,12 +136,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, 
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar)
+__device__ __forceinline__ void tma_load_5d(void *dst, const void *tmap, int x, int y, int z, int w, int v,
+                                            uint64_t *bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
         : "memory");
 }
 // The 2-D copy into this CTA's shared memory, with the completion signalled on the
@@ -227,13 +228,14 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // 128-byte swizzle: rows of 128 bytes (64 bf16 of K), 8-row groups 1024 bytes apart
 // (the stride-dimension offset); the leading-dimension offset is unused for this
 // layout.  `saddr` is the tile's shared address (1024-byte aligned for the swizzle
-// pattern; a K offset inside the 128-byte row is added to the start address).
-__device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr)
+// pattern; a K offset inside the 128-byte row is added to the start address).  sbo: the
+// distance of the 8-row groups where they are not adjacent.
+__device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr, uint32_t sbo = 1024)
 {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);   // start address
     d |= (uint64_t)1 << 16;                      // leading-dimension byte offset (16 B, unused)
-    d |= (uint64_t)(1024 >> 4) << 32;            // stride-dimension byte offset: 8 rows x 128 B
+    d |= (uint64_t)(sbo >> 4) << 32;             // stride-dimension byte offset: 8 rows x 128 B
     d |= (uint64_t)1 << 46;                      // descriptor version for tcgen05
     d |= (uint64_t)2 << 61;                      // swizzle: 128 bytes
     return d;
@@ -320,7 +322,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 columns as tmem_ld32, without the wait: the registers are valid after tmem_wait_ld.
+// 32 columns as tmem_ld32, without the wait: the registers are valid after tmem_wait_ld32 of
+// them (which names them, so that no use moves before it).
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile(
@@ -334,7 +337,18 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
 // 16 or 32 registers of this warp's 32 lanes into consecutive 32-bit TMEM columns (complete
 // after tmem_wait_st).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])

@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(GA ? THREADS_GA : THREADS, 1)
 // in boxes of 64 columns x box_rows rows with the 128-byte swizzle; rows beyond
 // `rows` read as zeros.
 cudaError_t make_map_bf16(CUtensorMap *m, const void *base, int rows, int cols, int ld, int box_rows);
-// The same of a BF16 array of up to four dimensions (innermost first, its elements
+// The same of a BF16 array of up to five dimensions (innermost first, its elements
 // adjacent; strides of the others in elements), read in boxes of box[0] = 64 elements.
 cudaError_t make_map_bf16_nd(CUtensorMap *m, const void *base, int rank, const long long *dims,
                              const long long *strides, const int *box);

@@ -46,9 +46,9 @@ cudaError_t make_map_bf16_nd(CUtensorMap *m, const void *base, int rank, const l
 {
     auto fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
-    cuuint64_t d[4], s[3];
-    cuuint32_t b[4];
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5];
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = (cuuint64_t)dims[i];
         b[i] = (cuuint32_t)box[i];

@@ -91,9 +91,6 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
     }
     paged_cursor<kPaThreads>(a, kPaKeys, &s_cur, s_scratch);
     PagedCursor cur = s_cur;
-    SeqWork w;
-    w.units = -1;
-
     const int hd = a.kv.head_dim;
     const int stream = threadIdx.x / LPK, sub = threadIdx.x % LPK;
     const int d0 = sub * D;
@@ -104,7 +101,7 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
     TQ *out = static_cast<TQ *>(a.out);
 
     while (true) {
-        if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, w, split, s_item);
+        if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, split, s_item);
         __syncthreads();
         if (!s_item.more) return;
         const PagedItem it = s_item;
@@ -132,9 +129,8 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
         const int k0 = max(it.lo, it.t0 * kPaKeys), k1 = min(it.hi, it.t1 * kPaKeys);
         // every row sees keys [all_lo, all_hi]
         const int win = a.window > 0 ? a.window : 0x7fffffff;
-        const int t_first = it.row0 / a.group, t_last = (it.row0 + it.n_rows - 1) / a.group;
-        const int all_hi = it.pos0 + t_first;
-        const int all_lo = a.window > 0 ? it.pos0 + t_last - a.window + 1 : 0;
+        const int all_hi = it.pos0 + it.tok_a;
+        const int all_lo = a.window > 0 ? it.pos0 + it.tok_b - a.window + 1 : 0;
         for (int j0 = k0 + stream * KB; j0 < k1; j0 += S * KB) {
             float k[KB][D], v[KB][D];
             bool there[KB];

@@ -31,6 +31,7 @@
 // MMAs.  Every wait is bounded; a CTA that gives up says so in its record, drains its copies
 // and MMAs, frees its TMEM and returns.
 #include <cuda.h>
+#include <stddef.h>
 
 #include "paged_sched.cuh"
 #include "sm100.cuh"
@@ -115,27 +116,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const PartLayout lay(kAttnMaxCtasTc, a.rows, HD);
     PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < geo.slots; ++i) {
-            mbar_init(&x.full[i], 1);
-            mbar_init(&x.empty[i], 1);
+    {   // one barrier per thread
+        uint64_t *bars = x.full;
+        constexpr int n = offsetof(TcMisc, item) / 8;
+        const int i = threadIdx.x;
+        if (i < n) {
+            int count = 1;
+            if (bars + i == &x.p_full[0] || bars + i == &x.p_full[1]) count = 4;
+            else if (bars + i == &x.o_free) count = kTcSoft / 32;
+            else if (bars + i >= x.item_empty && bars + i < x.item_empty + kTcItems) count = 1 + kTcSoft / 32;
+            mbar_init(bars + i, count);
+        } else if (i == n) {
+            x.abort_flag = 0;
+            x.poison[0] = x.poison[1] = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&x.q_full[i], 1);
-            mbar_init(&x.q_empty[i], 1);
-            mbar_init(&x.s_full[i], 1);
-            mbar_init(&x.p_full[i], 4);
-            mbar_init(&x.pv_done[i], 1);
-        }
-        mbar_init(&x.o_done, 1);
-        mbar_init(&x.o_free, kTcSoft / 32);
-        for (int i = 0; i < kTcItems; ++i) {
-            mbar_init(&x.item_full[i], 1);
-            mbar_init(&x.item_empty[i], 1 + kTcSoft / 32);
-        }
-        mbar_init(&x.done, 1);
-        x.abort_flag = 0;
-        x.poison[0] = x.poison[1] = 0;
         mbar_fence_init();
     }
     if (warp == kTcMma) tmem_alloc(&x.tmem, 512);
@@ -168,8 +162,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kTcTma) {
         // ---------------- items, page look-ups, copies
         PagedCursor cur = x.cur;
-        SeqWork w;
-        w.units = -1;
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
         };
@@ -184,7 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             PagedItem &it = x.item[i % kTcItems];
             if (lane == 0) {
-                paged_next(a, kTcKeys, cur, w, split, it);
+                paged_next(a, kTcKeys, cur, split, it);
                 mbar_arrive(&x.item_full[i % kTcItems]);
             }
             __syncwarp();
@@ -197,7 +189,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_expect_tx(&x.q_full[i & 1], (uint32_t)(H * a.group * geo.toks * 128));
                 for (int h = 0; h < H; ++h)
                     tma_load_3d(sm + (i & 1) * qbytes + h * geo.q_half, &qmap, h * 64, it.head * a.group,
-                                it.token + it.row0 / a.group, &x.q_full[i & 1]);
+                                it.token + it.tok_a, &x.q_full[i & 1]);
                 ++nq;
             }
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
@@ -376,7 +368,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int pos = mine ? it.pos0 + tok : -1;          // -1: sees no key
             const int see_lo = max(it.lo, pos - win + 1), see_hi = min(pos, it.hi - 1);
             // keys that some rows of the tile see and others do not
-            const int pos_a = it.pos0 + it.row0 / a.group, pos_b = it.pos0 + (it.row0 + it.n_rows - 1) / a.group;
+            const int pos_a = it.pos0 + it.tok_a, pos_b = it.pos0 + it.tok_b;
             float m = -INFINITY, l = 0.f;
             bool first = true;
             for (int k = (int)((s ^ u0) & 1u); k < units; k += 2) {
@@ -385,36 +377,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = ok && warp_wait(&x.s_full[s], nth & 1u);
                 if (ok && active) {
                     tc_fence_after();
-                    // The scores are read in halves, twice the second one, so that a thread
-                    // holds 64 of them: columns 64-127 for the maximum, 0-63 for the maximum and
-                    // the weights, 64-127 again (P of 0-63 covers columns 0-31 only).
-                    uint32_t v[2][32];
+                    // 32 scores at a time, read once for the maximum and again for the weights (P
+                    // of columns 32 q .. covers columns 16 q .., which are read by then).  Loops
+                    // that are not unrolled: the instructions of a fully unrolled unit took
+                    // longer to fetch, in a short call, than to run.
+                    uint32_t v[32];
                     const uint32_t there = *const_cast<volatile uint32_t *>(&x.there[u % 8]);
                     const int c0 = see_lo - base, c1 = see_hi - base;   // the row's keys, in columns
                     const bool whole = __all_sync(0xffffffffu, (c0 <= 0 && c1 >= kTcKeys - 1) || !mine) && there == 0xffffu;
-                    auto load = [&](int h) {
-                        tmem_ld32_async(t_s + 64 * h, v[0]);
-                        tmem_ld32_async(t_s + 64 * h + 32, v[1]);
-                        tmem_wait_ld32(v[0]);
-                        tmem_wait_ld32(v[1]);
+                    auto load = [&](int q) {
+                        tmem_ld32_async(t_s + 32 * q, v);
+                        tmem_wait_ld32(v);
                         if (!whole) {
+                            // the row's keys among these 32: bits c0 .. c1, and 8 for every page bit
+                            const int f = max(c0 - 32 * q, 0), t = min(c1 - 32 * q, 31);
+                            uint32_t in = t >= f ? (0xffffffffu >> (31 - t)) & (0xffffffffu << f) : 0u;
+                            const uint32_t pg = there >> (4 * q) & 15u;
+                            in &= (pg & 1u) * 0xffu | (pg >> 1 & 1u) * 0xff00u | (pg >> 2 & 1u) * 0xff0000u |
+                                  (pg >> 3) * 0xff000000u;
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int col = 64 * h + 32 * q + e;
-                                    const bool in = col >= c0 && col <= c1 && (there >> (col >> 3) & 1u);
-                                    if (!in) v[q][e] = 0xff800000u;   // -inf: its weight is 0
-                                }
+                            for (int e = 0; e < 32; ++e)
+                                if (!(in >> e & 1u)) v[e] = 0xff800000u;   // -inf: its weight is 0
                         }
                     };
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        load(q);
 #pragma unroll
-                    for (int h = 1; h >= 0; --h) {
-                        load(h);
+                        for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(__uint_as_float(v[0][e]), __uint_as_float(v[1][e])));
+                            for (int y = 0; y < 4; ++y)
+                                mx4[y] = fmaxf(fmaxf(mx4[y], __uint_as_float(v[e + y])), __uint_as_float(v[e + y + 4]));
                     }
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     const float top = mx * c;   // c > 0
@@ -430,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             ok = warp_wait(&x.pv_done[s], (nth - 1) & 1u);   // O of the unit before
                             tc_fence_after();
                             if (ok) {
-#pragma unroll
+#pragma unroll 1
                                 for (int q = 0; q < HD / 32; ++q) {
                                     uint32_t o[32];
                                     tmem_ld32_async(t_o + s * 128 + 32 * q, o);
@@ -444,26 +438,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     const float off = m == -INFINITY ? 0.f : m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        load(q);
+                        uint32_t p[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h) load(1);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float p0, p1;
-                                const float y0 = fmaf(__uint_as_float(v[q][2 * e]), c, -off);
-                                const float y1 = fmaf(__uint_as_float(v[q][2 * e + 1]), c, -off);
-                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
-                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
-                                sum[e & 1] += p0;
-                                sum[2 + (e & 1)] += p1;
-                                const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
-                                p[e] = *reinterpret_cast<const uint32_t *>(&pk);
-                            }
-                            tmem_st16(t_s + 32 * h + 16 * q, p);
+                        for (int e = 0; e < 16; ++e) {
+                            float p0, p1;
+                            const float y0 = fmaf(__uint_as_float(v[2 * e]), c, -off);
+                            const float y1 = fmaf(__uint_as_float(v[2 * e + 1]), c, -off);
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
+                            sum[e & 1] += p0;
+                            sum[2 + (e & 1)] += p1;
+                            const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+                            p[e] = *reinterpret_cast<const uint32_t *>(&pk);
                         }
+                        tmem_st16(t_s + 16 * q, p);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_wait_st();
@@ -489,12 +480,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         };
                         if (edge) {
                             const int b0 = beg & ~15, e1 = (end + 15) & ~15, n0 = beg - b0, n = n0 + e1 - end;
+#pragma unroll 1
                             for (int y = t; y < n * (HD / 8); y += 128) {
                                 const int z = y / (HD / 8);
                                 *chunk(z < n0 ? b0 + z : end + z - n0, y % (HD / 8)) = make_uint4(0u, 0u, 0u, 0u);
                             }
                         }
                         auto finite_only = [&](int f0, int f1) {
+#pragma unroll 1
                             for (int y = t; y < (f1 - f0) * (HD / 8); y += 128) {
                                 uint4 *at = chunk(f0 + y / (HD / 8), y % (HD / 8));
                                 uint4 w4 = *at;
@@ -555,7 +548,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ml[0] = mm;
                     ml[1] = sum;
                 }
-#pragma unroll
+                float *po = reinterpret_cast<float *>(a.ws + lay.o) + at * HD;
+                bf16 *dst = out + (long long)(it.token + tok) * a.out_stride + (it.head * a.group + hd) * HD;
+#pragma unroll 1
                 for (int q = 0; q < HD / 64; ++q) {
                     const int d = s * (HD / 2) + 32 * q;
                     uint32_t o0[32], o1[32];
@@ -566,51 +561,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     float o[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        o[e] = 0.f;
-                        if (has0) o[e] = f0 * __uint_as_float(o0[e]);
+                        o[e] = has0 ? f0 * __uint_as_float(o0[e]) : 0.f;
                         if (has1) o[e] = fmaf(f1, __uint_as_float(o1[e]), o[e]);
                     }
-                    if (poison && mine) {
-                        // what was taken out of the V rows that this row sees and others do not
-                        const int w0 = it.t0 * kTcKeys, w1 = it.t1 * kTcKeys;
-                        auto add = [&](int j0, int j1) {
-                            for (int j = max(j0, max(see_lo, w0)); j < min(j1, min(see_hi + 1, w1)); ++j) {
-                                const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
-                                if (page < 0) continue;
-                                const bf16 *vr = static_cast<const bf16 *>(a.kv.v) + page * a.kv.page_stride +
-                                                 (j % a.kv.page_size) * a.kv.slot_stride + it.head * a.kv.head_stride + d;
+                    if (mine && part) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float vv = __bfloat162float(vr[e]);
-                                    if (!isfinite(vv)) o[e] += vv;
-                                }
-                            }
-                        };
-                        add(pos_a + 1, pos_b + 1);
-                        // a key of both ranges is added once
-                        if (a.window > 0) add(pos_a - win + 1, min(pos_b - win + 1, pos_a + 1));
-                    }
-                    if (mine) {
-                        if (part) {
-                            float *po = reinterpret_cast<float *>(a.ws + lay.o) + at * HD + d;
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4 *>(po + d + 4 * e) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else if (mine) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<float4 *>(po + 4 * e) =
-                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        } else {
-                            bf16 *dst = out + (long long)(it.token + tok) * a.out_stride +
-                                        (it.head * a.group + hd) * HD + d;
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    w[y] = pack_bf16x2(__float2bfloat16_rn(o[8 * e + 2 * y] * inv),
-                                                       __float2bfloat16_rn(o[8 * e + 2 * y + 1] * inv));
-                                *reinterpret_cast<uint4 *>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = pack_bf16x2(__float2bfloat16_rn(o[8 * e + 2 * y] * inv),
+                                                   __float2bfloat16_rn(o[8 * e + 2 * y + 1] * inv));
+                            *reinterpret_cast<uint4 *>(dst + d + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
+                }
+                if (poison && mine) {
+                    // what was taken out of the V rows that this row sees and others do not: an
+                    // infinity or a NaN is added to what was just stored
+                    auto add = [&](int j0, int j1) {
+                        const int f = max(j0, max(see_lo, it.t0 * kTcKeys)), t = min(j1, min(see_hi + 1, it.t1 * kTcKeys));
+#pragma unroll 1
+                        for (int j = f; j < t; ++j) {
+                            const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
+                            if (page < 0) continue;
+                            const bf16 *vr = static_cast<const bf16 *>(a.kv.v) + page * a.kv.page_stride +
+                                             (j % a.kv.page_size) * a.kv.slot_stride + it.head * a.kv.head_stride;
+#pragma unroll 1
+                            for (int d = s * (HD / 2); d < (s + 1) * (HD / 2); ++d) {
+                                const float vv = __bfloat162float(vr[d]);
+                                if (isfinite(vv)) continue;
+                                if (part) po[d] += vv;
+                                else dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + vv);
+                            }
+                        }
+                    };
+                    add(pos_a + 1, pos_b + 1);
+                    // a key of both ranges is added once
+                    if (a.window > 0) add(pos_a - win + 1, min(pos_b - win + 1, pos_a + 1));
                 }
             }
             tc_fence_before();

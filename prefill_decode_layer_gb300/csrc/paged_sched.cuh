@@ -29,6 +29,7 @@ struct PagedItem {
     int n_new;              // its new tokens (at most max_new)
     int pos0;               // position of its first new token
     int row0, n_rows;       // query rows of the tile
+    int tok_a, tok_b;       // the new tokens (of the sequence) of its first and last row
     int lo, hi;             // keys that some row of the tile sees: [lo, hi)
     int t0, t1;             // this CTA's key tiles of the item
     int part;               // slot of the workspace, or -1: the whole item is here
@@ -57,11 +58,12 @@ struct PartLayout {
 // A sequence's keys, new tokens and units.
 struct SeqWork {
     int token, n_new, pos0, lo, hi, tiles, row_tiles;
-    long long units;
+    int units;   // fits: checked by the host
 };
 __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
 {
     SeqWork w;
+    const int length = a.s.length[b];
     int first = b, n = 1;
     if (a.s.start) {
         first = a.s.start[b];
@@ -72,7 +74,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
     n = min(min(n, a.s.max_new), a.s.n_tokens - first);
     n = max(n, 0);
     const int cap = a.s.width * a.kv.page_size;   // fits: checked by the host
-    const int len = max(a.s.length[b], 0);
+    const int len = max(length, 0);
     w.token = first;
     w.n_new = n;
     w.pos0 = len - n;
@@ -80,8 +82,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
     w.lo = a.window > 0 ? min(max(w.pos0 - a.window + 1, 0), w.hi) : 0;
     const int t = w.hi > w.lo ? (w.hi + kt - 1) / kt - w.lo / kt : 1;   // one empty unit still writes zeros
     w.tiles = t;
-    w.row_tiles = (n * a.group + a.rows - 1) / a.rows;
-    w.units = (long long)a.kv.n_kv_heads * w.row_tiles * (a.whole ? 1 : t);
+    w.row_tiles = a.rows >= a.s.max_new * a.group ? min(n, 1) : (n * a.group + a.rows - 1) / a.rows;
+    w.units = a.kv.n_kv_heads * w.row_tiles * (a.whole ? 1 : t);
     return w;
 }
 
@@ -89,9 +91,18 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
 struct PagedCursor {
     long long total;        // units of the launch
     long long at, end;      // this CTA's remaining units
-    long long local;        // unit `at` within sequence seq
+    int local;              // unit `at` within sequence seq
     int seq, ctas;          // ctas: those that have units
+    SeqWork w;              // of sequence seq
 };
+
+// floor(c total / g) for c <= g (the quotient of 32-bit numbers where that is enough: a
+// 64-bit division is a hundred instructions on the way to the first copy)
+__device__ __forceinline__ long long share(long long total, int c, int g)
+{
+    if (total < (1ll << 22)) return (unsigned)total * (unsigned)c / (unsigned)g;   // c <= 512
+    return total * c / g;
+}
 
 // All NT threads of the CTA (a multiple of 32); the result is in *cur (shared memory) after
 // it returns.  scratch: NT / 32 shared 64-bit words.
@@ -102,7 +113,12 @@ __device__ __forceinline__ void paged_cursor(const AttnArgs &a, int kt, PagedCur
     const int per = (a.s.n_seqs + NT - 1) / NT;
     const int b0 = min(tid * per, a.s.n_seqs), b1 = min(b0 + per, a.s.n_seqs);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_work(a, b, kt).units;
+    SeqWork w;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        w = seq_work(a, b, kt);
+        mine += w.units;
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -112,64 +128,65 @@ __device__ __forceinline__ void paged_cursor(const AttnArgs &a, int kt, PagedCur
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     long long base = 0, total = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) base += scratch[w];
-        total += scratch[w];
+#pragma unroll
+    for (int k = 0; k < NT / 32; ++k) {
+        const long long v = scratch[k];
+        if (k < warp) base += v;
+        total += v;
     }
-    const int g = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
-    const long long c = blockIdx.x;
-    const long long u0 = c < g ? c * total / g : total, u1 = c < g ? (c + 1) * total / g : total;
-    if (tid == 0) {   // (a CTA without units: nobody below sets the rest)
+    const int g = total < (long long)gridDim.x ? (int)total : (int)gridDim.x, c = (int)blockIdx.x;
+    const long long u0 = c < g ? share(total, c, g) : total, u1 = c < g ? share(total, c + 1, g) : total;
+    if (tid == 0) {
         cur->total = total;
         cur->at = u0;
         cur->end = u1;
         cur->ctas = g;
-        cur->seq = a.s.n_seqs;
-        cur->local = 0;
     }
-    __syncthreads();
     long long s = base + incl - mine;   // units before this thread's sequences
     if (u0 < u1 && s <= u0 && u0 < s + mine) {
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const long long n = seq_work(a, b, kt).units;
-            if (u0 < s + n) {
+            if (per > 1) w = seq_work(a, b, kt);
+            if (u0 < s + w.units) {
                 cur->seq = b;
-                cur->local = u0 - s;
+                cur->local = (int)(u0 - s);
+                cur->w = w;
                 break;
             }
-            s += n;
+            s += w.units;
         }
     }
     __syncthreads();
 }
 
-// The CTA's next item, one thread.  `w` and `cur` are the caller's copies, kept
-// between calls; w.units < 0 before the first.  Writes the CTA's split record.
-__device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, SeqWork &w, PagedSplit *split,
-                                           PagedItem &it)
+// The CTA's next item, one thread.  `cur` is the caller's copy, kept between calls.  Writes
+// the CTA's split record.
+__device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, PagedSplit *split, PagedItem &it)
 {
     it.more = cur.at < cur.end;
     if (!it.more) return;
-    if (w.units < 0) w = seq_work(a, cur.seq, kt);
+    SeqWork &w = cur.w;
     while (cur.local >= w.units) {   // ends: cur.at < total
         cur.local -= w.units;
         w = seq_work(a, ++cur.seq, kt);
     }
-    const long long item = a.whole ? cur.local : cur.local / w.tiles;
-    const int x = a.whole ? 0 : (int)(cur.local - item * w.tiles);
+    const int item = a.whole ? cur.local : cur.local / w.tiles;
+    const int x = a.whole ? 0 : cur.local - item * w.tiles;
     const long long left = cur.end - cur.at;
     const int take = a.whole ? w.tiles : (int)min((long long)(w.tiles - x), left);
     const int tile0 = w.lo / kt;
     it.seq = cur.seq;
-    it.head = (int)(item / w.row_tiles);
+    it.head = w.row_tiles == 1 ? item : item / w.row_tiles;
     it.token = w.token;
     it.n_new = w.n_new;
     it.pos0 = w.pos0;
-    it.row0 = (int)(item % w.row_tiles) * a.rows;
+    it.row0 = (item - it.head * w.row_tiles) * a.rows;
     it.n_rows = min(a.rows, w.n_new * a.group - it.row0);
-    const int pos_b = w.pos0 + (it.row0 + it.n_rows - 1) / a.group;
-    it.hi = min(w.hi, pos_b + 1);
-    it.lo = a.window > 0 ? max(w.lo, w.pos0 + it.row0 / a.group - a.window + 1) : w.lo;
+    const int tok_a = it.row0 / a.group, tok_b = (it.row0 + it.n_rows - 1) / a.group;
+    it.hi = min(w.hi, w.pos0 + tok_b + 1);
+    it.lo = a.window > 0 ? max(w.lo, w.pos0 + tok_a - a.window + 1) : w.lo;
+    it.tok_a = tok_a;
+    it.tok_b = tok_b;
     it.t0 = tile0 + x;
     it.t1 = tile0 + x + take;
     const bool begins = x == 0, ends = x + take == w.tiles;

@@ -156,8 +156,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         split->status = DS4G_ETIMEOUT;
     };
     // stream s: scores (then P) at column 128 s, O at 256 + 128 s
-    auto ring_slot = [&](unsigned idx) { return idx % (unsigned)geo.slots; };
-    auto ring_phase = [&](unsigned idx) { return idx / (unsigned)geo.slots & 1u; };
+    // a place in the ring: tile idx lies in slot idx % slots, in the phase (idx / slots) % 2 of its
+    // barriers (kept up to date: a division at every poll cost more than the MMAs)
+    struct Place {
+        unsigned slot, phase;
+    };
+    const unsigned slots = (unsigned)geo.slots;
+    auto ahead = [&](Place &p, unsigned by) {   // by <= slots
+        p.slot += by;
+        if (p.slot >= slots) {
+            p.slot -= slots;
+            p.phase ^= 1u;
+        }
+    };
+    // The ring holds the tiles in the order of their use, K0 K1 V0 K2 V1 K3 V2 .. (V of a unit is
+    // needed a softmax after its K): K V K V kept two slots waiting through each softmax, and
+    // the next K came late (2600 cycles a unit for 1400 of HBM time).
+    const Place k_first = {0, 0}, v_first = {2, 0};                              // tiles 0 and 2
+    auto k_next = [&](Place &p, unsigned u) { ahead(p, u == 0 ? 1 : 2); };       // from unit u's
+    auto v_next = [&](Place &p) { ahead(p, 2); };
 
     if (warp == kTcTma) {
         // ---------------- items, page look-ups, copies
@@ -166,9 +183,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
         };
         const int boxes = kTcKeys / geo.box, per_page = a.kv.page_size;
-        unsigned idx = 0;    // tiles loaded
+        unsigned u = 0;      // units whose K is loaded
         unsigned nq = 0;     // query tiles loaded
+        int used = -1;       // lane i: the phase of the last load into ring slot i
+        Place kp = k_first, vp = v_first;
         bool ok = true;
+        // this lane's box of a unit (the lane-th of its tile)
+        struct Box {
+            int block, slot8, at;
+            bool load;
+            uint32_t bytes;   // of the whole tile
+        };
+        auto copy = [&](const Place &p, const CUtensorMap *map, const Box &b) {
+            const unsigned sl = p.slot;
+            if (!warp_wait(&x.empty[sl], p.phase ^ 1u)) return false;
+            if (lane == 0) mbar_expect_tx(&x.full[sl], b.bytes);
+            if (lane == (int)sl) used = (int)p.phase;
+            __syncwarp();
+            if (b.load)
+                tma_load_5d(ring + sl * kTile + lane * geo.box * 128 * H, map, 0, 0, b.block, b.slot8, b.at, &x.full[sl]);
+            return true;
+        };
+        Box prev = {};       // of unit u - 1, whose V follows this unit's K
         for (unsigned i = 0; ok; ++i) {
             if (!warp_wait(&x.item_empty[i % kTcItems], (i / kTcItems & 1u) ^ 1u)) {
                 ok = false;
@@ -190,47 +226,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int h = 0; h < H; ++h)
                     tma_load_3d(sm + (i & 1) * qbytes + h * geo.q_half, &qmap, h * 64, it.head * a.group,
                                 it.token + it.tok_a, &x.q_full[i & 1]);
-                ++nq;
             }
+            ++nq;
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
             const int lo = it.lo, hi = it.hi, head = it.head, t1 = it.t1;
-            for (int t = it.t0; ok && t < t1; ++t) {
-                // lane i: the i-th box of the tile
+            for (int t = it.t0; ok && t < t1; ++t, ++u) {
                 const int j = t * kTcKeys + lane * geo.box;
-                const bool load = lane < boxes && j < hi && j + geo.box > lo;
+                Box b;
+                b.load = lane < boxes && j < hi && j + geo.box > lo;
                 int page = -1, slot = 0;
-                if (load) {
-                    page = key_page(a, table, j);
-                    slot = j % per_page;
+                if (b.load) {
+                    const int p = j / per_page;
+                    slot = j - p * per_page;
+                    page = table[p];
+                    if (page >= a.kv.n_pages) page = -1;
                 }
-                const uint32_t bits = load && page >= 0 ? ((1u << (geo.box >> 3)) - 1u) << (lane * (geo.box >> 3)) : 0u;
+                const uint32_t bits = b.load && page >= 0 ? ((1u << (geo.box >> 3)) - 1u) << (lane * (geo.box >> 3)) : 0u;
                 const uint32_t there = __reduce_or_sync(0xffffffffu, bits);
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * geo.box * 128 * H;
+                b.bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, b.load)) * geo.box * 128 * H;
+                b.block = head * geo.block;
+                b.slot8 = slot >> 3;
                 // a page that is not there: out of bounds, read as zeros
-                const int at = page < 0 ? geo.none : page * geo.page_mul + head * geo.head_mul;
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++idx) {
-                    const unsigned sl = ring_slot(idx);
-                    if (!warp_wait(&x.empty[sl], ring_phase(idx) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        if (kv == 0) x.there[idx / 2 % 8] = there;
-                        mbar_expect_tx(&x.full[sl], bytes);
-                    }
-                    __syncwarp();
-                    if (load)
-                        tma_load_5d(ring + sl * kTile + lane * geo.box * 128 * H, kv == 0 ? &kmap : &vmap, 0, 0,
-                                    head * geo.block, slot >> 3, at, &x.full[sl]);
+                b.at = page < 0 ? geo.none : page * geo.page_mul + head * geo.head_mul;
+                if (lane == 0) x.there[u % 8] = there;   // read once the scores are there
+                ok = copy(kp, &kmap, b);
+                k_next(kp, u);
+                if (ok && u > 0) {
+                    ok = copy(vp, &vmap, prev);
+                    v_next(vp);
                 }
+                prev = b;
             }
         }
+        if (ok && u > 0) ok = copy(vp, &vmap, prev);
         if (!ok) give_up();
         // nothing may be in flight when the CTA exits
         volatile int never = 0;
-        for (unsigned k = idx > (unsigned)geo.slots ? idx - geo.slots : 0; k < idx; ++k)
-            mbar_wait(&x.full[ring_slot(k)], ring_phase(k), &never);
+        if (used >= 0) mbar_wait(&x.full[lane], (uint32_t)used, &never);
         if (lane == 0)
             for (unsigned k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait(&x.q_full[k & 1], k >> 1 & 1u, &never);
     } else if (warp == kTcMma) {
@@ -243,6 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int s_left = 0, p_tile = 0, p_end = 0, p_lo = 0, p_hi = 0, p_k = 0;
             bool s_have = false, s_q = false, s_over = false, p_have = false, ok = true;
             bool fresh[2] = {true, true};   // no MMA of the item has written the stream's O
+            Place kp = k_first, vp = v_first;
             long long since = clock64();
             for (unsigned polls = 1;; ++polls) {
                 bool moved = false;
@@ -259,18 +292,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (s_have && su - pu < 2) {
                     if (!s_q) s_q = mbar_test(&x.q_full[s_item & 1], s_item >> 1 & 1u);
-                    const unsigned sl = ring_slot(2 * su);
-                    if (s_q && mbar_test(&x.full[sl], ring_phase(2 * su))) {
+                    const unsigned sl = kp.slot;
+                    if (s_q && mbar_test(&x.full[sl], kp.phase)) {
                         tc_fence_after();
                         const uint32_t qb = sbase + (s_item & 1) * qbytes, kb = rbase + sl * kTile;
+                        const uint64_t qd = sdesc_kmajor_sw128(qb), kd = sdesc_kmajor_sw128(kb, H * 1024);
 #pragma unroll
                         for (int ks = 0; ks < HD / 16; ++ks)
                             tc_mma_bf16(tmem + (su & 1) * 128,
-                                        sdesc_kmajor_sw128(qb + (uint32_t)(ks >> 2) * geo.q_half + (ks & 3) * 32),
-                                        sdesc_kmajor_sw128(kb + (uint32_t)(ks >> 2) * 1024 + (ks & 3) * 32, H * 1024), id_s,
-                                        ks > 0);
+                                        qd + (uint64_t)(((uint32_t)(ks >> 2) * geo.q_half + (ks & 3) * 32) >> 4),
+                                        kd + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 32 >> 4), id_s, ks > 0);
                         tc_commit(&x.s_full[su & 1]);
                         tc_commit(&x.empty[sl]);
+                        k_next(kp, su);
                         ++su;
                         if (--s_left == 0) {
                             tc_commit(&x.q_empty[s_item & 1]);
@@ -291,21 +325,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         p_have = true;
                         fresh[0] = fresh[1] = true;
                     }
-                    const unsigned s = pu & 1, sl = ring_slot(2 * pu + 1);
-                    if (mbar_test(&x.p_full[s], pu >> 1 & 1u) && mbar_test(&x.full[sl], ring_phase(2 * pu + 1)) &&
+                    const unsigned s = pu & 1, sl = vp.slot;
+                    if (mbar_test(&x.p_full[s], pu >> 1 & 1u) && mbar_test(&x.full[sl], vp.phase) &&
                         (p_k >= 2 || p_item == 0 || mbar_test(&x.o_free, (p_item - 1) & 1u))) {
                         tc_fence_after();
                         const int base = p_tile * kTcKeys;
                         const int k0 = (max(p_lo - base, 0)) / 16, k1 = (min(p_hi - base, kTcKeys) + 15) / 16;
                         const bool add = s ? !fresh[1] : !fresh[0];
                         if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
-                        for (int ks = k0; ks < k1; ++ks)
-                            tc_mma_bf16_ta(tmem + 256 + s * 128, tmem + s * 128 + (uint32_t)ks * 8,
-                                           sdesc_mnmajor_sw128(rbase + sl * kTile + (uint32_t)ks * (2 * H * 1024), 1024,
-                                                               H * 1024),
-                                           id_o, add || ks > k0);
+                        const uint64_t vd = sdesc_mnmajor_sw128(rbase + sl * kTile, 1024, H * 1024);
+                        const uint32_t po = tmem + s * 128, oo = tmem + 256 + s * 128;
+#pragma unroll
+                        for (int ks = 0; ks < kTcKeys / 16; ++ks)   // 16 keys are 2 H KB of the tile
+                            if (ks >= k0 && ks < k1)
+                                tc_mma_bf16_ta(oo, po + (uint32_t)ks * 8, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), id_o,
+                                               add || ks > k0);
                         tc_commit(&x.empty[sl]);
                         tc_commit(&x.pv_done[s]);
+                        v_next(vp);
                         ++pu;
                         ++p_k;
                         if (++p_tile == p_end) {
@@ -353,6 +390,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             return any != 0;
         };
         unsigned u0 = 0;   // the CTA's units before this item
+        Place vp = v_first;   // of this stream's next unit
+        if (s) v_next(vp);
         for (unsigned i = 0;; ++i) {
             bool ok = warp_wait(&x.item_full[i % kTcItems], i / kTcItems & 1u);
             if (soft_sync_any(!ok)) {
@@ -468,9 +507,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int g0 = a.window > 0 ? max(pos_a - win + 1 - base, beg) : 0;
                 const int g1 = a.window > 0 ? min(pos_b - win + 1 - base, end) : 0;
                 if (ok && (edge || h0 < h1 || g0 < g1)) {
-                    const unsigned vi = 2 * u + 1;
-                    unsigned char *vt = ring + ring_slot(vi) * kTile;
-                    ok = warp_wait(&x.full[ring_slot(vi)], ring_phase(vi));
+                    unsigned char *vt = ring + vp.slot * kTile;
+                    ok = warp_wait(&x.full[vp.slot], vp.phase);
                     if (ok) {
                         const int t = threadIdx.x & 127;
                         auto chunk = [&](int key, int d16) {   // 16 bytes of dims 8 d16 .. of a V row
@@ -515,6 +553,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         fence_proxy_async_smem();   // before the MMA reads the tile
                     }
                 }
+                v_next(vp);
+                v_next(vp);
                 tc_fence_before();
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(&x.p_full[s]);

@@ -50,7 +50,7 @@ static constexpr int kTcSmem = 227 * 1024;
 struct TcMisc {
     uint64_t full[kTcMaxSlots], empty[kTcMaxSlots];    // K/V tiles of the ring
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2];         // of a stream
+    uint64_t s_full[2], p_full[2];                     // of a stream
     uint64_t o_done, o_free;                           // O complete; O read by the softmax threads
     uint64_t item_full[kTcItems], item_empty[kTcItems];
     uint64_t done;
@@ -266,101 +266,86 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0)
             for (unsigned k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait(&x.q_full[k & 1], k >> 1 & 1u, &never);
     } else if (warp == kTcMma) {
-        // ---------------- MMAs.  The next unit's scores (of the other stream, or of this one
-        // once its P is used) and the oldest unit's P V are issued as their inputs arrive.
+        // ---------------- MMAs: S0 S1, then P V of each unit and the S of the unit after the next,
+        // the order in which the tiles arrive
         if (lane == 0) {
             const uint32_t sbase = smem_u32(sm), rbase = smem_u32(ring);
             const uint32_t id_s = idesc_bf16_f32(128, kTcKeys), id_o = idesc_bf16_f32_bmn(128, HD);
             unsigned s_item = 0, p_item = 0, su = 0, pu = 0;   // items begun, units issued, of the two
-            int s_left = 0, p_tile = 0, p_end = 0, p_lo = 0, p_hi = 0, p_k = 0;
-            bool s_have = false, s_q = false, s_over = false, p_have = false, ok = true;
-            bool fresh[2] = {true, true};   // no MMA of the item has written the stream's O
+            int s_left = 0;
+            bool s_over = false, ok = true;
             Place kp = k_first, vp = v_first;
-            long long since = clock64();
-            for (unsigned polls = 1;; ++polls) {
-                bool moved = false;
-                if (!s_over && !s_have && mbar_test(&x.item_full[s_item % kTcItems], s_item / kTcItems & 1u)) {
+            auto next_s = [&]() {   // the next unit's scores, if there is one; false: gave up
+                if (s_over) return true;
+                if (s_left == 0) {
+                    if (!mbar_wait(&x.item_full[s_item % kTcItems], s_item / kTcItems & 1u, ab)) return false;
                     const PagedItem &it = x.item[s_item % kTcItems];
-                    if (it.more) {
-                        s_left = it.t1 - it.t0;
-                        s_have = true;
-                        s_q = false;
-                    } else {
+                    if (!it.more) {
                         s_over = true;
+                        return true;
                     }
-                    moved = true;
+                    s_left = it.t1 - it.t0;
+                    if (!mbar_wait(&x.q_full[s_item & 1], s_item >> 1 & 1u, ab)) return false;
                 }
-                if (s_have && su - pu < 2) {
-                    if (!s_q) s_q = mbar_test(&x.q_full[s_item & 1], s_item >> 1 & 1u);
-                    const unsigned sl = kp.slot;
-                    if (s_q && mbar_test(&x.full[sl], kp.phase)) {
-                        tc_fence_after();
-                        const uint32_t qb = sbase + (s_item & 1) * qbytes, kb = rbase + sl * kTile;
-                        const uint64_t qd = sdesc_kmajor_sw128(qb), kd = sdesc_kmajor_sw128(kb, H * 1024);
+                if (!mbar_wait(&x.full[kp.slot], kp.phase, ab)) return false;
+                tc_fence_after();
+                const uint64_t qd = sdesc_kmajor_sw128(sbase + (s_item & 1) * qbytes);
+                const uint64_t kd = sdesc_kmajor_sw128(rbase + kp.slot * kTile, H * 1024);
+                const uint32_t qh = (uint32_t)geo.q_half >> 4, acc = tmem + (su & 1) * 128;
 #pragma unroll
-                        for (int ks = 0; ks < HD / 16; ++ks)
-                            tc_mma_bf16(tmem + (su & 1) * 128,
-                                        qd + (uint64_t)(((uint32_t)(ks >> 2) * geo.q_half + (ks & 3) * 32) >> 4),
-                                        kd + (uint64_t)((ks >> 2) * 1024 + (ks & 3) * 32 >> 4), id_s, ks > 0);
-                        tc_commit(&x.s_full[su & 1]);
-                        tc_commit(&x.empty[sl]);
-                        k_next(kp, su);
-                        ++su;
-                        if (--s_left == 0) {
-                            tc_commit(&x.q_empty[s_item & 1]);
-                            s_have = false;
-                            ++s_item;
-                        }
-                        moved = true;
-                    }
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    tc_mma_bf16(acc, qd + (uint64_t)((ks >> 2) * qh + (ks & 3) * 2),
+                                kd + (uint64_t)((ks >> 2) * 64 + (ks & 3) * 2), id_s, ks > 0);
+                // (also: P V of the unit before the last is complete, so that its stream may rescale O)
+                tc_commit(&x.s_full[su & 1]);
+                tc_commit(&x.empty[kp.slot]);
+                k_next(kp, su);
+                ++su;
+                if (--s_left == 0) {
+                    tc_commit(&x.q_empty[s_item & 1]);
+                    ++s_item;
                 }
-                if (pu < su) {
-                    if (!p_have) {   // its scores were issued, so the item is there
-                        const PagedItem &it = x.item[p_item % kTcItems];
-                        p_tile = it.t0;
-                        p_end = it.t1;
-                        p_lo = it.lo;
-                        p_hi = it.hi;
-                        p_k = 0;
-                        p_have = true;
-                        fresh[0] = fresh[1] = true;
-                    }
-                    const unsigned s = pu & 1, sl = vp.slot;
-                    if (mbar_test(&x.p_full[s], pu >> 1 & 1u) && mbar_test(&x.full[sl], vp.phase) &&
-                        (p_k >= 2 || p_item == 0 || mbar_test(&x.o_free, (p_item - 1) & 1u))) {
-                        tc_fence_after();
-                        const int base = p_tile * kTcKeys;
-                        const int k0 = (max(p_lo - base, 0)) / 16, k1 = (min(p_hi - base, kTcKeys) + 15) / 16;
-                        const bool add = s ? !fresh[1] : !fresh[0];
-                        if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
-                        const uint64_t vd = sdesc_mnmajor_sw128(rbase + sl * kTile, 1024, H * 1024);
-                        const uint32_t po = tmem + s * 128, oo = tmem + 256 + s * 128;
+                return true;
+            };
+            int p_tile = 0, p_end = 0, p_lo = 0, p_hi = 0, p_k = 0;
+            bool fresh[2] = {true, true};   // no MMA of the item has written the stream's O
+            ok = next_s() && next_s();
+            while (ok && pu < su) {
+                if (p_tile == p_end) {   // its scores were issued, so the item is there
+                    const PagedItem &it = x.item[p_item % kTcItems];
+                    p_tile = it.t0;
+                    p_end = it.t1;
+                    p_lo = it.lo;
+                    p_hi = it.hi;
+                    p_k = 0;
+                    fresh[0] = fresh[1] = true;
+                }
+                const unsigned s = pu & 1;
+                ok = (p_k >= 2 || p_item == 0 || mbar_wait(&x.o_free, (p_item - 1) & 1u, ab)) &&
+                     mbar_wait(&x.full[vp.slot], vp.phase, ab) && mbar_wait(&x.p_full[s], pu >> 1 & 1u, ab);
+                if (!ok) break;
+                tc_fence_after();
+                const int base = p_tile * kTcKeys;
+                const int k0 = (max(p_lo - base, 0)) / 16, k1 = (min(p_hi - base, kTcKeys) + 15) / 16;
+                const bool add = s ? !fresh[1] : !fresh[0];
+                if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
+                const uint64_t vd = sdesc_mnmajor_sw128(rbase + vp.slot * kTile, 1024, H * 1024);
+                const uint32_t po = tmem + s * 128, oo = tmem + 256 + s * 128;
 #pragma unroll
-                        for (int ks = 0; ks < kTcKeys / 16; ++ks)   // 16 keys are 2 H KB of the tile
-                            if (ks >= k0 && ks < k1)
-                                tc_mma_bf16_ta(oo, po + (uint32_t)ks * 8, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), id_o,
-                                               add || ks > k0);
-                        tc_commit(&x.empty[sl]);
-                        tc_commit(&x.pv_done[s]);
-                        v_next(vp);
-                        ++pu;
-                        ++p_k;
-                        if (++p_tile == p_end) {
-                            tc_commit(&x.o_done);
-                            mbar_arrive(&x.item_empty[p_item % kTcItems]);
-                            p_have = false;
-                            ++p_item;
-                        }
-                        moved = true;
-                    }
+                for (int ks = 0; ks < kTcKeys / 16; ++ks)   // 16 keys are 2 H KB of the tile
+                    if (ks >= k0 && ks < k1)
+                        tc_mma_bf16_ta(oo, po + (uint32_t)ks * 8, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), id_o,
+                                       add || ks > k0);
+                tc_commit(&x.empty[vp.slot]);
+                v_next(vp);
+                ++pu;
+                ++p_k;
+                if (++p_tile == p_end) {
+                    tc_commit(&x.o_done);
+                    mbar_arrive(&x.item_empty[p_item % kTcItems]);
+                    ++p_item;
                 }
-                if (s_over && pu == su) break;
-                if (moved) {
-                    since = clock64();
-                } else if ((polls & 255u) == 0 && (*ab || clock64() - since > kWaitCycles)) {
-                    ok = false;
-                    break;
-                }
+                ok = next_s();
             }
             if (!ok) give_up();
             volatile int never = 0;
@@ -460,18 +445,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const float f = move ? exp2f(m - top) : 1.f;   // m = -inf: 0, and O is 0
                             if (move) m = top;
                             l *= f;
-                            ok = warp_wait(&x.pv_done[s], (nth - 1) & 1u);   // O of the unit before
-                            tc_fence_after();
-                            if (ok) {
+                            // (O of the stream's unit before is complete: its MMAs precede this S)
 #pragma unroll 1
-                                for (int q = 0; q < HD / 32; ++q) {
-                                    uint32_t o[32];
-                                    tmem_ld32_async(t_o + s * 128 + 32 * q, o);
-                                    tmem_wait_ld32(o);
+                            for (int q = 0; q < HD / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_ld32_async(t_o + s * 128 + 32 * q, o);
+                                tmem_wait_ld32(o);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(t_o + s * 128 + 32 * q, o);
-                                }
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(t_o + s * 128 + 32 * q, o);
                             }
                         }
                     }

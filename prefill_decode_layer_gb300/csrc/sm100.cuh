@@ -53,18 +53,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *b, uint32_t parity)
         : "memory");
     return ok != 0;
 }
-// The same without the hardware's suspended wait: answers at once.
-__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // Bounded wait for the phase of `parity` to complete; false if it gave up or the
 // CTA is aborting.  The bound uses the SM cycle counter, read once per 256 polls.
 __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag)

@@ -1,6 +1,8 @@
 // C ABI of the operators on device buffers beside the sampler's (include/ds4g.h): the
 // paged K/V cache, rows of probabilities and draft verification.  Validation here, work
 // in the kernel files; nothing is kept between calls.
+#include <atomic>
+
 #include "paged.h"
 
 using namespace ds4g;
@@ -42,11 +44,17 @@ PagedSeqs seqs_of(const ds4g_paged_batch &b)
     return {b.table, b.length, b.start, b.n_seqs, b.n_tokens, b.max_new, b.width, b.table_stride};
 }
 
-// SMs of the current device; 0 if there is none.
+// SMs of the current device; 0 if there is none.  (Asked for once per device: a constant of
+// the device, not of a call.)
 int sm_count()
 {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) return 0;
+    if (cudaGetDevice(&dev)) return 0;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (n = known[dev].load(std::memory_order_relaxed))) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) return 0;
+    if (keep) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

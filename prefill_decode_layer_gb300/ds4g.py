@@ -405,15 +405,22 @@ def _require(ok: bool, what: str) -> None:
         raise Ds4gError(EINVAL, what)
 
 
-def _call(name: str, device, stream, *args) -> None:
-    """One call of the library on `device`, on `stream` (None: that device's current
-    stream)."""
-    f = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, _stream_ptr(stream))
+# The current stream's handle without building a Stream object (3 us of a small call's 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, index: int, stream, *args) -> None:
+    """One call of the library on CUDA device `index`, on `stream` (None: that device's
+    current stream)."""
+    _require(index >= 0, name)
+    f = getattr(_lib or lib(), name)
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = f(*args, st)
     else:
-        with torch.cuda.device(device):
-            rc = f(*args, _stream_ptr(stream))
+        with torch.cuda.device(index):
+            rc = f(*args, st)
     if rc < 0:
         raise Ds4gError(rc, name)
 
@@ -425,7 +432,7 @@ class PagedKV:
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1 and
                  k.dtype == v.dtype and k.dtype in _DTYPES and k.device == v.device, "PagedKV")
-        self.k, self.v, self.device = k, v, k.device
+        self.k, self.v, self.index = k, v, k.get_device()
         n, p, h, d = k.shape
         self.n_kv_heads, self.head_dim = h, d
         self.struct = PagedKVStruct(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
@@ -447,7 +454,7 @@ class PagedBatch:
                  length.is_contiguous() and table.device == length.device, "PagedBatch")
         _require(start is None or (start.dtype == torch.int32 and start.numel() == n + 1 and
                                    start.is_contiguous() and start.device == length.device), "PagedBatch")
-        self.table, self.length, self.start, self.device = table, length, start, length.device
+        self.table, self.length, self.start, self.index = table, length, start, length.get_device()
         width = table.shape[1]
         self.struct = PagedBatchStruct(table.data_ptr(), length.data_ptr(),
                                        start.data_ptr() if start is not None else None, n, n, max_new,
@@ -460,7 +467,7 @@ class Rope:
 
     def __init__(self, cs: torch.Tensor):
         _require(cs.dim() == 3 and cs.shape[2] == 2 and cs.dtype == torch.float32 and cs.is_contiguous(), "Rope")
-        self.cs, self.device = cs, cs.device
+        self.cs, self.index = cs, cs.get_device()
         self.struct = RopeStruct(cs.data_ptr(), cs.shape[0], 2 * cs.shape[1])
         self.ref = C.addressof(self.struct)
 
@@ -468,19 +475,25 @@ class Rope:
     def fill(cls, n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda", stream=None) -> "Rope":
         """A table filled by ds4g_rope_fill."""
         cs = torch.empty(n_pos, rot_dim // 2, 2, dtype=torch.float32, device=device)
-        _call("ds4g_rope_fill", cs.device, stream, cs.data_ptr(), n_pos, rot_dim, float(base))
+        _call("ds4g_rope_fill", cs.get_device(), stream, cs.data_ptr(), n_pos, rot_dim, float(base))
         return cls(cs)
 
 
-def _rows(t: torch.Tensor, batch: PagedBatch, heads: int | None, dim: int, dtype) -> bool:
-    """t is a token tensor [n_tokens][heads][dim] of `dtype`, heads and dims adjacent."""
-    s = t.shape
-    return (len(s) == 3 and s[0] == batch.struct.n_tokens and s[2] == dim and (heads is None or s[1] == heads) and
-            t.dtype == dtype and t.stride(2) == 1 and t.stride(1) == dim and t.device == batch.device)
+def _rows(t: torch.Tensor, n: int, heads: int, dim: int, dtype, index: int, what: str) -> int:
+    """Token stride of t, a token tensor [n][heads][dim] of `dtype`, heads and dims adjacent."""
+    if t.shape == (n, heads, dim) and t.dtype is dtype and t.get_device() == index:
+        s = t.stride()
+        if s[2] == 1 and (s[1] == dim or heads == 1):
+            return s[0] if n > 1 else heads * dim
+    raise Ds4gError(EINVAL, what)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _tokens(batch: PagedBatch, t: torch.Tensor) -> int:
+    """Rows of a call's token tensors: as many as there are sequences without starts, else t's."""
+    if batch.start is None:
+        return batch.struct.n_tokens
+    batch.struct.n_tokens = n = t.shape[0]
+    return n
 
 
 def paged_append(kv: PagedKV, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor, rope: Rope | None = None,
@@ -488,19 +501,20 @@ def paged_append(kv: PagedKV, batch: PagedBatch, k: torch.Tensor, v: torch.Tenso
     """ds4g_paged_append: k, v [n_tokens][n_kv_heads][head_dim] into the cache's pages, the
     keys rotated by `rope`; q [n_tokens][n_heads][head_dim] rotated into q_out (which may
     be q)."""
-    if batch.start is not None:
-        batch.struct.n_tokens = k.shape[0]
-    h, d, dt = kv.n_kv_heads, kv.head_dim, k.dtype
-    _require(dt in _DTYPES and kv.device == batch.device and _rows(k, batch, h, d, dt) and _rows(v, batch, h, d, dt) and
-             (rope is None or rope.device == batch.device) and (q is None) == (q_out is None), "paged_append")
+    n, h, d, dt, index, what = _tokens(batch, k), kv.n_kv_heads, kv.head_dim, k.dtype, batch.index, "paged_append"
+    _require(dt in _DTYPES and kv.index == index and (rope is None or rope.index == index) and
+             (q is None) == (q_out is None), what)
+    ks, vs = _rows(k, n, h, d, dt, index, what), _rows(v, n, h, d, dt, index, what)
+    rp = rope.ref if rope is not None else None
     if q is None:
-        _call("ds4g_paged_append", batch.device, stream, kv.ref, batch.ref, k.data_ptr(), _row_stride(k),
-              v.data_ptr(), _row_stride(v), rope.ref if rope is not None else None, None, 0, None, 0, 0, _DTYPES[dt])
+        _call("ds4g_paged_append", index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, None, 0,
+              None, 0, 0, _DTYPES[dt])
         return
-    _require(_rows(q, batch, None, d, dt) and _rows(q_out, batch, q.shape[1], d, dt), "paged_append")
-    _call("ds4g_paged_append", batch.device, stream, kv.ref, batch.ref, k.data_ptr(), _row_stride(k), v.data_ptr(),
-          _row_stride(v), rope.ref if rope is not None else None, q.data_ptr(), _row_stride(q), q_out.data_ptr(),
-          _row_stride(q_out), q.shape[1], _DTYPES[dt])
+    _require(q.dim() == 3, what)
+    heads = q.shape[1]
+    _call("ds4g_paged_append", index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, q.data_ptr(),
+          _rows(q, n, heads, d, dt, index, what), q_out.data_ptr(), _rows(q_out, n, heads, d, dt, index, what), heads,
+          _DTYPES[dt])
 
 
 def paged_attention_workspace_bytes(kv: PagedKV, batch: PagedBatch, n_heads: int) -> int:
@@ -511,30 +525,31 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.
                     scale: float = 0.0, window: int = 0, stream=None) -> None:
     """ds4g_paged_attention: q and out [n_tokens][n_heads][head_dim]; scale 0: 1 /
     sqrt(head_dim); window 0: every position up to the token's own."""
-    if batch.start is not None:
-        batch.struct.n_tokens = q.shape[0]
-    d, dt, heads = kv.head_dim, q.dtype, q.shape[1]
-    _require(dt in _DTYPES and kv.device == batch.device and _rows(q, batch, None, d, dt) and
-             _rows(out, batch, heads, d, dt) and workspace.device == batch.device, "paged_attention")
-    _call("ds4g_paged_attention", batch.device, stream, kv.ref, batch.ref, q.data_ptr(), _row_stride(q),
-          out.data_ptr(), _row_stride(out), heads, _DTYPES[dt], scale, window, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _require(q.dim() == 3 and q.dtype in _DTYPES and kv.index == batch.index == workspace.get_device(),
+             "paged_attention")
+    n, d, dt, heads, index = _tokens(batch, q), kv.head_dim, q.dtype, q.shape[1], batch.index
+    _call("ds4g_paged_attention", index, stream, kv.ref, batch.ref, q.data_ptr(),
+          _rows(q, n, heads, d, dt, index, "paged_attention"), out.data_ptr(),
+          _rows(out, n, heads, d, dt, index, "paged_attention"), heads, _DTYPES[dt], scale, window,
+          workspace.data_ptr(), workspace.nbytes)
 
 
 def paged_attention_status(workspace: torch.Tensor, stream=None) -> int:
     """ds4g_paged_attention_status: OK or ETIMEOUT of the workspace's last call (synchronises)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(workspace.device)
-    return lib().ds4g_paged_attention_status(workspace.data_ptr(), stream.cuda_stream)
+    index = workspace.get_device()
+    _require(index >= 0, "paged_attention_status")
+    return lib().ds4g_paged_attention_status(workspace.data_ptr(),
+                                             _raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:
     """ds4g_probs: rows of f32 logits [n_rows][n_vocab] to probabilities (out may be logits)."""
-    _require(logits.dim() == 2 and logits.shape == out.shape and logits.dtype == out.dtype == torch.float32 and
-             logits.device == out.device and (logits.shape[1] <= 1 or logits.stride(1) == out.stride(1) == 1), "probs")
-    n, v = logits.shape
-    _call("ds4g_probs", logits.device, stream, logits.data_ptr(), logits.stride(0) if n > 1 else v, n, v,
-          float(temperature), out.data_ptr(), out.stride(0) if n > 1 else v)
+    shape, zs, ps, index = logits.shape, logits.stride(), out.stride(), logits.get_device()
+    _require(len(shape) == 2 and shape == out.shape and logits.dtype is torch.float32 and out.dtype is torch.float32 and
+             index == out.get_device() and (shape[1] <= 1 or zs[1] == ps[1] == 1), "probs")
+    n, v = shape
+    _call("ds4g_probs", index, stream, logits.data_ptr(), zs[0] if n > 1 else v, n, v, float(temperature),
+          out.data_ptr(), ps[0] if n > 1 else v)
 
 
 def verify_draft(p: torch.Tensor, q: torch.Tensor | None, drafts: torch.Tensor, u24: torch.Tensor,
@@ -543,24 +558,28 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor | None, drafts: torch.Tensor, 
     """ds4g_verify_draft: p [n_seqs][max_drafts + 1][n_vocab] and q [n_seqs][max_drafts][n_vocab]
     (or None) f32; drafts [n_seqs][max_drafts], u24 [n_seqs][max_drafts + 1], accepted [n_seqs], tokens
     [n_seqs][max_drafts + 1] and n_drafts [n_seqs] (or None) int32."""
-    _require(p.dim() == 3 and drafts.dim() == 2, "verify_draft")
-    (b, d1, v), d, i32 = p.shape, drafts.shape[1], torch.int32
+    shape, what, index = p.shape, "verify_draft", p.get_device()
+    _require(len(shape) == 3 and p.dtype is torch.float32, what)
+    b, d1, v = shape
+    d = d1 - 1
 
     def ints(t, *shape):
-        return t.dtype == i32 and t.shape == shape and t.is_contiguous() and t.device == p.device
-
-    _require(p.dtype == torch.float32 and (v <= 1 or p.stride(2) == 1) and d1 == d + 1 and ints(drafts, b, d) and
-             ints(u24, b, d1) and ints(accepted, b) and ints(tokens, b, d1) and
-             (n_drafts is None or ints(n_drafts, b)), "verify_draft")
-    _require(q is None or (q.dtype == torch.float32 and q.shape == (b, d, v) and (v <= 1 or q.stride(2) == 1) and
-                           q.device == p.device), "verify_draft")
+        if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == index):
+            raise Ds4gError(EINVAL, what)
+        return t.data_ptr()
 
     def strides(t, rows):   # of a sequence and of a position; a dimension of one element has any stride
-        pos = t.stride(1) if rows > 1 else v
-        return (t.stride(0) if b > 1 else max(v, rows * pos)), pos
+        s = t.stride()
+        _require(v <= 1 or s[2] == 1, what)
+        pos = s[1] if rows > 1 else v
+        return (s[0] if b > 1 else max(v, rows * pos)), pos
 
     ps, pp = strides(p, d1)
-    qs, qp = strides(q, d) if q is not None else (0, 0)
-    _call("ds4g_verify_draft", p.device, stream, p.data_ptr(), ps, pp, q.data_ptr() if q is not None else None, qs, qp,
-          drafts.data_ptr(), n_drafts.data_ptr() if n_drafts is not None else None, u24.data_ptr(), b, d, v,
-          accepted.data_ptr(), tokens.data_ptr())
+    qa, qs, qp = None, 0, 0
+    if q is not None:
+        _require(q.dtype is torch.float32 and q.shape == (b, d, v) and q.get_device() == index, what)
+        qa = q.data_ptr()
+        qs, qp = strides(q, d)
+    _call("ds4g_verify_draft", index, stream, p.data_ptr(), ps, pp, qa, qs, qp, ints(drafts, b, d),
+          ints(n_drafts, b) if n_drafts is not None else None, ints(u24, b, d1), b, d, v, ints(accepted, b),
+          ints(tokens, b, d1))

@@ -152,8 +152,10 @@ int ds4g_probs(const float *logits, int64_t logits_stride, int n_rows, int n_voc
     if (n_rows == 0) return DS4G_OK;
     if (!logits || !probs || logits_stride < n_vocab || probs_stride < n_vocab || n_rows > (1 << 27)) return DS4G_EINVAL;
     if (logits == probs && logits_stride != probs_stride) return DS4G_EINVAL;
+    const int nsm = sm_count();
+    if (!nsm) return DS4G_ECUDA;
     return status_of(probs_rows(logits, logits_stride, n_rows, n_vocab, temperature, probs, probs_stride,
-                                static_cast<cudaStream_t>(stream)));
+                                static_cast<cudaStream_t>(stream), nsm));
 }
 
 int ds4g_verify_draft(const float *p, int64_t p_seq_stride, int64_t p_stride, const float *q, int64_t q_seq_stride,
@@ -170,7 +172,9 @@ int ds4g_verify_draft(const float *p, int64_t p_seq_stride, int64_t p_stride, co
     if (q && (q_stride < n_vocab || q_seq_stride < n_vocab)) return DS4G_EINVAL;
     const VerifyArgs a = {p, q, p_seq_stride, p_stride, q_seq_stride, q_stride, drafts, n_drafts,
                           u24, max_drafts, n_vocab, accepted, tokens};
-    return status_of(verify_rows(a, n_seqs, static_cast<cudaStream_t>(stream)));
+    const int nsm = sm_count();
+    if (!nsm) return DS4G_ECUDA;
+    return status_of(verify_rows(a, n_seqs, static_cast<cudaStream_t>(stream), nsm));
 }
 
 }  // extern "C"

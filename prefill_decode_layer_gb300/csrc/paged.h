@@ -59,7 +59,7 @@ cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status);
 cudaError_t paged_attention(const AttnArgs &a, int q_dtype, int kv_dtype, cudaStream_t st, int nsm);
 
 cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,
-                       long long os, cudaStream_t st);
+                       long long os, cudaStream_t st, int nsm);
 
 struct VerifyArgs {
     const float *p, *q;
@@ -69,7 +69,7 @@ struct VerifyArgs {
     int max_drafts, n;
     int *accepted, *tokens;
 };
-cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st);
+cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st, int nsm);
 // Largest vocabulary of probs_rows and verify_rows.
 constexpr int kMaxRowVocab = 1 << 20;
 

@@ -8,9 +8,10 @@
 // query head turns by the table's (cos, sin) of (p, i) in FP32; every value is rounded
 // once, to nearest even, to the type it is stored in.
 //
-// Bound: bytes (each row read once and written once).  A thread moves 8 elements of
-// one head at a time (16 bytes of BF16, 32 of FP32); the CTA's tokens are looked up
-// first by one warp each, then all threads walk the (token, 8-element vector) pairs.
+// Bound: bytes (each row read once and written once).  A thread owns 8 adjacent dims (16
+// bytes of BF16, 32 of FP32) of one token: it loads their (cos, sin) once and moves that part of
+// one head after another, 128 bytes in flight.  The CTA's tokens are looked up first, by one
+// warp each.
 #include "paged.h"
 
 namespace ds4g {
@@ -18,11 +19,13 @@ namespace ds4g {
 static constexpr int kApThreads = 256;
 static constexpr int kApTokens = 8;   // tokens of a CTA at most: one warp looks up each
 
+// 8 adjacent elements: as loaded, and as floats.
 template <typename T> struct Row8;
 template <> struct Row8<bf16> {
-    static __device__ __forceinline__ void load(const bf16 *p, float (&x)[8])
+    uint4 w;
+    __device__ __forceinline__ void load(const bf16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void floats(float (&x)[8]) const
     {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -40,9 +43,14 @@ template <> struct Row8<bf16> {
     }
 };
 template <> struct Row8<float> {
-    static __device__ __forceinline__ void load(const float *p, float (&x)[8])
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
     {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void floats(float (&x)[8]) const
+    {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
@@ -53,26 +61,20 @@ template <> struct Row8<float> {
     }
 };
 
-// Turn the pairs of dims d .. d + 7 by the row cs of the table (rot_dim / 2 pairs).
-__device__ __forceinline__ void turn8(float (&x)[8], const float *cs, int d, int rot_dim)
+// (cos, sin) of the pairs of dims d .. d + 7 from a row of the table (rot_dim / 2 pairs).
+__device__ __forceinline__ void load_angles(float (&c)[8], const float *cs, int d, int rot_dim)
 {
-    float4 t[2][2];
     if (d + 8 <= rot_dim && (rot_dim & 3) == 0) {   // 16-byte aligned: rows of a multiple of 4 floats
-        const float4 *p = reinterpret_cast<const float4 *>(cs + d);
-        t[0][0] = p[0];
-        t[0][1] = p[1];
-    } else {
-        float c[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = d + 2 * i < rot_dim;
-            c[2 * i] = in ? cs[d + 2 * i] : 1.f;
-            c[2 * i + 1] = in ? cs[d + 2 * i + 1] : 0.f;
-        }
-        t[0][0] = make_float4(c[0], c[1], c[2], c[3]);
-        t[0][1] = make_float4(c[4], c[5], c[6], c[7]);
+        Row8<float> r;
+        r.load(cs + d);
+        r.floats(c);
+        return;
     }
-    const float c[8] = {t[0][0].x, t[0][0].y, t[0][0].z, t[0][0].w, t[0][1].x, t[0][1].y, t[0][1].z, t[0][1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = d + (i & ~1) < rot_dim ? cs[d + i] : 0.f;
+}
+__device__ __forceinline__ void turn8(float (&x)[8], const float (&c)[8], int d, int rot_dim)
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (d + 2 * i >= rot_dim) break;   // passes through unchanged, whatever it holds
@@ -82,7 +84,10 @@ __device__ __forceinline__ void turn8(float (&x)[8], const float *cs, int d, int
     }
 }
 
-template <typename TI, typename TC>
+// U: heads in flight per thread.  128 bytes of them for many tokens (10k tokens: 91 us; 120 with
+// half), one where every thread has one head anyway: the unrolled form's instructions take
+// longer to fetch than 64 tokens take (5.0 against 3.1 us).
+template <typename TI, typename TC, int U>
 __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_constant__ AppendArgs a, int tokens_per_cta)
 {
     __shared__ long long s_slot[kApTokens];   // element offset of the token's slot, or -1
@@ -127,69 +132,71 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
         }
     }
     __syncthreads();
-    const int hd = a.kv.head_dim, hv = hd >> 3, kvv = a.kv.n_kv_heads * hv;
-    const int per = 2 * kvv + a.n_heads * hv;   // vectors of a token: K, V, then Q
-    const int total = per * min(tokens_per_cta, a.s.n_tokens - t0);
-    const TI *k = static_cast<const TI *>(a.k), *v = static_cast<const TI *>(a.v), *q = static_cast<const TI *>(a.q);
-    TC *kc = static_cast<TC *>(const_cast<void *>(a.kv.k)), *vc = static_cast<TC *>(const_cast<void *>(a.kv.v));
-    TI *qo = static_cast<TI *>(a.q_out);
-    constexpr int U = 4;   // vectors in flight per thread
-    const int stride = gridDim.y * kApThreads;
-    for (int i0 = blockIdx.y * kApThreads + threadIdx.x; i0 < total; i0 += U * stride) {
-        float x[U][8];
-        int tt[U], vec[U];
+    const int hd = a.kv.head_dim, hv = hd >> 3, kvh = a.kv.n_kv_heads;
+    // groups of hv threads; `per` of them share a token
+    const int per = kApThreads / hv / tokens_per_cta, grp = threadIdx.x / hv, d = (threadIdx.x - grp * hv) * 8;
+    const int j = grp / per;
+    if (j >= min(tokens_per_cta, a.s.n_tokens - t0)) return;
+    const int pos = s_pos[j];
+    if (pos < 0) return;
+    const long long slot = s_slot[j], t = t0 + j;
+    const int heads = a.n_heads + 2 * kvh;   // of a token: queries, keys, values
+    const TI *k = static_cast<const TI *>(a.k) + t * a.k_stride + d;
+    const TI *v = static_cast<const TI *>(a.v) + t * a.v_stride + d;
+    const TI *q = static_cast<const TI *>(a.q) + t * a.q_stride + d;
+    TC *kc = static_cast<TC *>(const_cast<void *>(a.kv.k)) + slot + d;
+    TC *vc = static_cast<TC *>(const_cast<void *>(a.kv.v)) + slot + d;
+    TI *qo = static_cast<TI *>(a.q_out) + t * a.q_out_stride + d;
+    const bool turns = a.cs && d < a.rot_dim;
+    float c[8];
+    if (turns) load_angles(c, a.cs + (long long)pos * a.rot_dim, d, a.rot_dim);
+    const int step = per * gridDim.y;
+    for (int h0 = grp - j * per + per * blockIdx.y; h0 < heads; h0 += U * step) {
+        Row8<TI> w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * stride;
-            tt[u] = -1;
-            if (i >= total) continue;
-            const int j = i / per;
-            tt[u] = j;
-            vec[u] = i - j * per;
-            const long long t = t0 + j;
-            const TI *src = vec[u] < kvv       ? k + t * a.k_stride + vec[u] * 8
-                            : vec[u] < 2 * kvv ? v + t * a.v_stride + (vec[u] - kvv) * 8
-                                               : q + t * a.q_stride + (vec[u] - 2 * kvv) * 8;
-            Row8<TI>::load(src, x[u]);
+            const int h = h0 + u * step, kh = h - a.n_heads;
+            if (h < heads) w[u].load(kh < 0 ? q + h * hd : kh < kvh ? k + kh * hd : v + (kh - kvh) * hd);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (tt[u] < 0) continue;
-            const int pos = s_pos[tt[u]];
-            const long long slot = s_slot[tt[u]];
-            if (pos < 0) continue;
-            const int c = vec[u];
-            if (c < 2 * kvv) {
-                if (slot < 0) continue;
-                const int kv = c < kvv ? c : c - kvv, h = kv / hv, d = (kv - h * hv) * 8;
-                if (c < kvv && a.cs && d < a.rot_dim) turn8(x[u], a.cs + (long long)pos * a.rot_dim, d, a.rot_dim);
-                Row8<TC>::store((c < kvv ? kc : vc) + slot + h * a.kv.head_stride + d, x[u]);
-            } else {
-                const int d = (c - 2 * kvv) % hv * 8;
-                if (a.cs && d < a.rot_dim) turn8(x[u], a.cs + (long long)pos * a.rot_dim, d, a.rot_dim);
-                Row8<TI>::store(qo + (t0 + tt[u]) * a.q_out_stride + (c - 2 * kvv) * 8, x[u]);
-            }
+            const int h = h0 + u * step, kh = h - a.n_heads;
+            if (h >= heads) continue;
+            float x[8];
+            w[u].floats(x);
+            if (turns && kh < kvh) turn8(x, c, d, a.rot_dim);
+            if (kh < 0) Row8<TI>::store(qo + h * hd, x);
+            else if (slot >= 0) Row8<TC>::store(kh < kvh ? kc + kh * a.kv.head_stride : vc + (kh - kvh) * a.kv.head_stride, x);
         }
     }
+}
+
+template <typename TI>
+static cudaError_t append_from(const AppendArgs &a, int kv_dtype, dim3 grid, int tpc, int per_thread, cudaStream_t st)
+{
+    constexpr int U = 16 / sizeof(TI);
+    const dim3 block(kApThreads);
+    if (per_thread <= 2)
+        return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<TI, bf16, 1>, grid, block, 0, st, a, tpc)
+                                     : launch_pdl(k_paged_append<TI, float, 1>, grid, block, 0, st, a, tpc);
+    return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<TI, bf16, U>, grid, block, 0, st, a, tpc)
+                                 : launch_pdl(k_paged_append<TI, float, U>, grid, block, 0, st, a, tpc);
 }
 
 cudaError_t paged_append(const AppendArgs &a, int in_dtype, int kv_dtype, cudaStream_t st, int nsm)
 {
     if (a.s.n_tokens == 0) return cudaSuccess;
-    const int per = (2 * a.kv.n_kv_heads + a.n_heads) * (a.kv.head_dim >> 3);
-    // Few tokens: a CTA for each and several for its vectors, so that every SM has work;
-    // many: up to kApTokens a CTA, which share one look-up of positions and pages.
+    const int groups = kApThreads / (a.kv.head_dim >> 3), heads = 2 * a.kv.n_kv_heads + a.n_heads;
+    // Few tokens: a CTA for each and several for its heads, so that every SM has work; many:
+    // up to kApTokens a CTA, whose look-ups of positions and pages run side by side.
     int tpc = 1;
-    while (tpc < kApTokens && a.s.n_tokens / (2 * tpc) >= 16 * nsm) tpc *= 2;
+    while (tpc < kApTokens && a.s.n_tokens / (2 * tpc) >= 4 * nsm) tpc *= 2;
     const int gx = (a.s.n_tokens + tpc - 1) / tpc;
     int gy = 1;
-    while ((long long)gx * gy < 8 * nsm && gy * kApThreads < per * tpc) ++gy;
-    const dim3 grid(gx, gy), block(kApThreads);
-    if (in_dtype == DS4G_BF16)
-        return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<bf16, bf16>, grid, block, 0, st, a, tpc)
-                                     : launch_pdl(k_paged_append<bf16, float>, grid, block, 0, st, a, tpc);
-    return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<float, bf16>, grid, block, 0, st, a, tpc)
-                                 : launch_pdl(k_paged_append<float, float>, grid, block, 0, st, a, tpc);
+    while ((long long)gx * gy < 8 * nsm && gy * groups < heads * tpc) ++gy;
+    const int per_thread = (heads * tpc + groups * gy - 1) / (groups * gy);
+    return in_dtype == DS4G_BF16 ? append_from<bf16>(a, kv_dtype, dim3(gx, gy), tpc, per_thread, st)
+                                 : append_from<float>(a, kv_dtype, dim3(gx, gy), tpc, per_thread, st);
 }
 
 }  // namespace ds4g

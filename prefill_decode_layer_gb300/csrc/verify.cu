@@ -3,13 +3,16 @@
 // sample_full_vocab), for many rows and for tokens that a draft proposed.
 //
 // A row of the vocabulary (0.5 MB at 129280 tokens) is the unit of work and one cluster's:
-// up to 8 CTAs of 512 threads read a contiguous chunk each, so that one row alone
-// already runs on 8 SMs, and combine their maxima and sums through distributed shared
+// 8 CTAs (16 where there are few rows) take a contiguous chunk each, so that one row alone
+// already runs on 8 or 16 SMs, and combine their maxima and sums through distributed shared
 // memory; one launch, no workspace.
 //
-// k_probs: p = 2^((z - max z) log2(e) / T) / sum.  The row stays in registers between
-// the maximum, the sum and the store (32 values per thread, 131072 per cluster; a
-// larger vocabulary is read again), so that it crosses HBM once each way.
+// k_probs: p = 2^((z - max z) log2(e) / T) / sum.  A chunk stays in registers between the
+// maximum, the sum and the store (32 values per thread; what a larger vocabulary has beyond
+// is read again), so that a row crosses HBM once each way.  Clusters walk over the rows, and
+// the next row's chunk is copied into shared memory (a bulk copy) while this one's is computed
+// and stored: without it the memory idled between a row's load and its store (94 us for
+// 320 rows of 129280).
 //
 // k_verify: draft i is accepted while u_i q_i(d_i) < p_i(d_i) (exact: products of two
 // 24-bit numbers in FP64), which every CTA of the cluster evaluates for itself.  The
@@ -17,6 +20,8 @@
 // sampler's do, so that every order of summation gives the same total and the drawn
 // token does not depend on the split: sums of 128 consecutive tokens are kept in shared
 // memory, and only the segment that holds the target R is read a second time.
+#include <atomic>
+
 #include "paged.h"
 #include "sm100.cuh"
 
@@ -26,6 +31,7 @@ static constexpr int kRowThreads = 512;
 static constexpr int kRowWarps = kRowThreads / 32;
 static constexpr int kRowTile = kRowThreads * 4;   // tokens of one round: 4 adjacent ones per thread
 static constexpr int kRowHold = 8;                 // rounds a thread keeps in registers
+static constexpr int kMaxCluster = 16;
 
 __device__ __forceinline__ float ld_cluster_f32(const float *p, uint32_t rank)
 {
@@ -66,162 +72,207 @@ template <bool VEC> __device__ __forceinline__ void row_store4(float *row, int i
     if (i + 3 < n) row[i + 3] = v.w;
 }
 
-// 2^((z - m) c), c = c_hi + c_lo: the rounding errors of the difference and of the
-// product are carried to the result, so that its relative error stays near that of
-// exp2f also where the exponent is large.
+// 2^((z - m) c), c = c_hi + c_lo.  The rounding of the product is carried to the result, so
+// that what is left is that of the difference, 2^-24 of the exponent (a large one belongs to
+// a small result), and of the hardware's 2^x.  Results below 2^-126 are 0, and so are those of
+// -inf and NaN.
 __device__ __forceinline__ float exp_scaled(float z, float m, float c_hi, float c_lo)
 {
-    const float d = z - m;
-    const float y = d * c_hi;
-    if (!(y > -160.f)) return 0.f;   // below the smallest FP32 value (also -inf logits and 0 * -inf)
-    const float t = d - z;
-    const float de = (z - (d - t)) + (-m - t);   // z - m = d + de exactly
-    const float r = fmaf(d, c_hi, -y) + fmaf(d, c_lo, de * c_hi);
-    return exp2f(y) * fmaf(r, 0.693147180559945f, 1.f);
+    const float d = z - m, y = d * c_hi;
+    const float r = fmaf(d, c_lo, fmaf(d, c_hi, -y));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    e *= fmaf(r, 0.693147180559945f, 1.f);
+    return y > -126.f ? e : 0.f;
 }
 
 struct ProbsArgs {
     const float *z;
     float *p;
     long long zs, ps;
-    int n, chunk;
+    int n, chunk, rows;
     float c_hi, c_lo;   // log2(e) / T
     int greedy;
+    int ahead;          // the next row's chunk is copied into shared memory meanwhile
 };
 
+// One row after another: cluster i of the grid takes rows i, i + clusters, ..
 template <bool VEC>
 __global__ void __launch_bounds__(kRowThreads, 2) k_probs(const __grid_constant__ ProbsArgs a)
 {
-    __shared__ float s_red[kRowWarps], s_max, s_sum;
-    __shared__ unsigned long long s_red64[kRowWarps], s_key;
+    extern __shared__ __align__(16) float s_next[];   // the next row's chunk (a.ahead)
+    __shared__ float s_red[kRowWarps], s_max[2], s_sum[2];
+    __shared__ unsigned long long s_red64[kRowWarps], s_key[2];
+    __shared__ uint64_t s_bar;
+    __shared__ int s_abort;
     const uint32_t rank = cluster_rank(), size = cluster_size();
-    const long long row = blockIdx.x / size;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (int)rank * a.chunk, c1 = min(a.n, c0 + a.chunk);
-    const float *z = a.z + row * a.zs;
-    float *p = a.p + row * a.ps;
     const int rounds = c1 > c0 ? (c1 - c0 + kRowTile - 1) / kRowTile : 0;
+    // what a bulk copy brings: whole 16-byte vectors, as many as the registers hold
+    const int bulk = a.ahead && c1 > c0 ? min(c1 - c0, kRowHold * kRowTile) & ~3 : 0;
+    const int clusters = gridDim.x / size;
+    if (threadIdx.x == 0) {
+        mbar_init(&s_bar, 1);
+        mbar_fence_init();
+        s_abort = 0;
+    }
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     auto at = [&](int j) { return c0 + (j * kRowThreads + (int)threadIdx.x) * 4; };
     auto clean = [](float v) { return v != v ? -INFINITY : v; };
-    float4 x[kRowHold];
+    auto fetch = [&](int row) {   // thread 0
+        mbar_expect_tx(&s_bar, (uint32_t)bulk * 4);
+        bulk_g2s(s_next, a.z + row * a.zs + c0, (uint32_t)bulk * 4, &s_bar, policy_evict_first());
+    };
+    int turn = 0;   // rows of this cluster so far
+    for (int row = blockIdx.x / size; row < a.rows; row += clusters, ++turn) {
+        const float *z = a.z + row * a.zs;
+        float *p = a.p + row * a.ps;
+        const int par = turn & 1;   // a row's shared values are read by the others until the next row's exist
+        float4 x[kRowHold];
+        const bool here = bulk && turn > 0;   // this row's chunk was fetched during the last one
+        if (here) {
+            if (!mbar_wait(&s_bar, (turn - 1) & 1u, &s_abort)) s_abort = 1;   // (a failed copy: the row is read below)
 #pragma unroll
-    for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), c1, -INFINITY);
-    float mx = -INFINITY;   // fmaxf takes the number beside a NaN
+            for (int j = 0; j < kRowHold; ++j) {
+                const int i = at(j) - c0;
+                x[j] = i + 3 < bulk && !s_abort ? *reinterpret_cast<const float4 *>(s_next + i)
+                                                : row_load4<VEC>(z, c0 + i, c1, -INFINITY);
+            }
+            __syncthreads();   // the buffer is free
+        } else {
 #pragma unroll
-    for (int j = 0; j < kRowHold; ++j) mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
-    for (int j = kRowHold; j < rounds; ++j) {
-        const float4 v = row_load4<VEC>(z, at(j), c1, -INFINITY);
-        mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
-    }
-    mx = clean(mx);
+            for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), c1, -INFINITY);
+        }
+        if (bulk && threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
+        float mx = -INFINITY;   // fmaxf takes the number beside a NaN
+#pragma unroll
+        for (int j = 0; j < kRowHold; ++j) mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
+        for (int j = kRowHold; j < rounds; ++j) {
+            const float4 v = row_load4<VEC>(z, at(j), c1, -INFINITY);
+            mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+        }
+        mx = clean(mx);
 
-    if (a.greedy) {   // one at the largest logit, lowest id on ties
-        unsigned long long best = 0ull;
-        auto look = [&](float v, int i) {
-            if (i < c1 && clean(v) > -INFINITY) {
-                const unsigned long long k = ((unsigned long long)topk_key(v) << 32) | (0xffffffffu - (unsigned)i);
+        if (a.greedy) {   // one at the largest logit, lowest id on ties
+            unsigned long long best = 0ull;
+            auto look = [&](float v, int i) {
+                if (i < c1 && clean(v) > -INFINITY) {
+                    const unsigned long long k = ((unsigned long long)topk_key(v) << 32) | (0xffffffffu - (unsigned)i);
+                    best = k > best ? k : best;
+                }
+            };
+            auto look4 = [&](const float4 &v, int i) {
+                look(v.x, i); look(v.y, i + 1); look(v.z, i + 2); look(v.w, i + 3);
+            };
+#pragma unroll
+            for (int j = 0; j < kRowHold; ++j) look4(x[j], at(j));
+            for (int j = kRowHold; j < rounds; ++j) look4(row_load4<VEC>(z, at(j), c1, -INFINITY), at(j));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
                 best = k > best ? k : best;
             }
-        };
-        for (int j = 0; j < rounds; ++j) {   // a second read: the chunk is in L2
-            const int i = at(j);
-            const float4 v = row_load4<VEC>(z, i, c1, -INFINITY);
-            look(v.x, i); look(v.y, i + 1); look(v.z, i + 2); look(v.w, i + 3);
+            if (lane == 0) s_red64[warp] = best;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < kRowWarps; ++w) best = s_red64[w] > best ? s_red64[w] : best;
+                s_key[par] = best;
+            }
+            cluster_sync_all();   // (also: in place, every thread has read its part of the row)
+            best = 0ull;
+            for (uint32_t r = 0; r < size; ++r) {
+                const unsigned long long k = ld_cluster_u64(&s_key[par], r);
+                best = k > best ? k : best;
+            }
+            const int win = best ? (int)(0xffffffffu - (unsigned)(best & 0xffffffffull)) : -1;
+            for (int j = 0; j < rounds; ++j) {
+                const int i = at(j);
+                row_store4<VEC>(p, i, c1,
+                                make_float4(i == win ? 1.f : 0.f, i + 1 == win ? 1.f : 0.f, i + 2 == win ? 1.f : 0.f,
+                                            i + 3 == win ? 1.f : 0.f));
+            }
+            continue;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
-            best = k > best ? k : best;
-        }
-        if (lane == 0) s_red64[warp] = best;
+
+        mx = warp_max(mx);
+        if (lane == 0) s_red[warp] = mx;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kRowWarps; ++w) best = s_red64[w] > best ? s_red64[w] : best;
-            s_key = best;
+        if (warp == 0) {
+            mx = warp_max(lane < kRowWarps ? s_red[lane] : -INFINITY);
+            if (lane == 0) s_max[par] = mx;
         }
         cluster_sync_all();
-        best = 0ull;
-        for (uint32_t r = 0; r < size; ++r) {
-            const unsigned long long k = ld_cluster_u64(&s_key, r);
-            best = k > best ? k : best;
-        }
-        cluster_sync_all();   // every CTA has read the others' key (and, in place, the row)
-        const int win = best ? (int)(0xffffffffu - (unsigned)(best & 0xffffffffull)) : -1;
-        for (int j = 0; j < rounds; ++j) {
-            const int i = at(j);
-            row_store4<VEC>(p, i, c1,
-                            make_float4(i == win ? 1.f : 0.f, i + 1 == win ? 1.f : 0.f, i + 2 == win ? 1.f : 0.f,
-                                        i + 3 == win ? 1.f : 0.f));
-        }
-        return;
-    }
-
-    mx = warp_max(mx);
-    if (lane == 0) s_red[warp] = mx;
-    __syncthreads();
-    if (warp == 0) {
-        mx = warp_max(lane < kRowWarps ? s_red[lane] : -INFINITY);
-        if (lane == 0) s_max = mx;
-    }
-    cluster_sync_all();
-    mx = -INFINITY;
-    for (uint32_t r = 0; r < size; ++r) mx = fmaxf(mx, ld_cluster_f32(&s_max, r));
-    const float c_hi = a.c_hi, c_lo = a.c_lo;
-    const bool top_inf = mx == INFINITY, none = mx == -INFINITY;
-    auto weight = [&](float v) {
-        if (none || top_inf) return top_inf && v == mx ? 1.f : 0.f;
-        return exp_scaled(clean(v), mx, c_hi, c_lo);
-    };
-    auto weight4 = [&](const float4 &v) { return make_float4(weight(v.x), weight(v.y), weight(v.z), weight(v.w)); };
-    float sum = 0.f;
+        mx = -INFINITY;
+        for (uint32_t r = 0; r < size; ++r) mx = fmaxf(mx, ld_cluster_f32(&s_max[par], r));
+        const float c_hi = a.c_hi, c_lo = a.c_lo;
+        // an infinite maximum: its ids share the whole; no maximum: every weight is 0
+        const bool top_inf = mx == INFINITY;
+        if (top_inf || mx == -INFINITY) mx = 0.f;
+        auto seen = [&](float v) { return !top_inf ? v : v == INFINITY ? 0.f : -INFINITY; };
+        auto weight4 = [&](float4 v) {
+            if (top_inf) v = make_float4(seen(v.x), seen(v.y), seen(v.z), seen(v.w));
+            return make_float4(exp_scaled(v.x, mx, c_hi, c_lo), exp_scaled(v.y, mx, c_hi, c_lo),
+                               exp_scaled(v.z, mx, c_hi, c_lo), exp_scaled(v.w, mx, c_hi, c_lo));
+        };
+        float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < kRowHold; ++j) {
-        x[j] = weight4(x[j]);
-        sum += (x[j].x + x[j].y) + (x[j].z + x[j].w);
-    }
-    for (int j = kRowHold; j < rounds; ++j) {
-        const float4 v = weight4(row_load4<VEC>(z, at(j), c1, -INFINITY));
-        sum += (v.x + v.y) + (v.z + v.w);
-    }
-    sum = warp_sum(sum);
-    __syncthreads();   // s_red holds the maxima until here
-    if (lane == 0) s_red[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        sum = warp_sum(lane < kRowWarps ? s_red[lane] : 0.f);
-        if (lane == 0) s_sum = sum;
-    }
-    cluster_sync_all();
-    sum = 0.f;
-    for (uint32_t r = 0; r < size; ++r) sum += ld_cluster_f32(&s_sum, r);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    auto store = [&](int j, const float4 &v) {
-        row_store4<VEC>(p, at(j), c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    };
+        for (int j = 0; j < kRowHold; ++j) {
+            x[j] = weight4(x[j]);
+            sum += (x[j].x + x[j].y) + (x[j].z + x[j].w);
+        }
+        for (int j = kRowHold; j < rounds; ++j) {
+            const float4 v = weight4(row_load4<VEC>(z, at(j), c1, -INFINITY));
+            sum += (v.x + v.y) + (v.z + v.w);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) s_red[warp] = sum;   // (the maxima in it were read before the cluster's barrier)
+        __syncthreads();
+        if (warp == 0) {
+            sum = warp_sum(lane < kRowWarps ? s_red[lane] : 0.f);
+            if (lane == 0) s_sum[par] = sum;
+        }
+        cluster_sync_all();
+        sum = 0.f;
+        for (uint32_t r = 0; r < size; ++r) sum += ld_cluster_f32(&s_sum[par], r);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        auto store = [&](int j, const float4 &v) {
+            row_store4<VEC>(p, at(j), c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        };
 #pragma unroll
-    for (int j = 0; j < kRowHold; ++j) store(j, x[j]);
-    for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), c1, -INFINITY)));
+        for (int j = 0; j < kRowHold; ++j) store(j, x[j]);
+        for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), c1, -INFINITY)));
+    }
     cluster_sync_all();   // no CTA leaves while another may still read its shared memory
 }
 
-// CTAs of a row's cluster: as many as keep 2048 tokens each, at most 8 (the portable
-// size), so that a single row's latency is that of an eighth of it.
-static int row_cluster(int n)
+// CTAs of a row's cluster: as many as keep 2048 tokens each, at most 8, or 16 (more than the
+// portable size) for up to `few` rows: one verification of 129280 tokens takes 7.9 us on 16
+// CTAs and 9.5 on 8, nine take 10.4 and 9.7; a row of probabilities is no faster on 16.
+static int row_cluster(int n, int rows, int few)
 {
+    const int most = rows <= few ? kMaxCluster : 8;
     int c = 1;
-    while (c < 8 && n >= 2 * c * kRowTile) c *= 2;
+    while (c < most && n >= 2 * c * kRowTile) c *= 2;
     return c;
 }
 static int row_chunk(int n, int c) { return ((n + c - 1) / c + 3) & ~3; }
 
 template <typename A>
-static cudaError_t launch_rows(void (*kernel)(A), int rows, int cluster, cudaStream_t st, const A &a)
+static cudaError_t launch_rows(void (*kernel)(A), int clusters, int cluster, int threads, size_t smem, cudaStream_t st,
+                               const A &a)
 {
+    cudaError_t e = cudaSuccess;
+    if (cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (!e && smem > 48 * 1024)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows * cluster);
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.gridDim = dim3((unsigned)clusters * cluster);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -236,31 +287,77 @@ static cudaError_t launch_rows(void (*kernel)(A), int rows, int cluster, cudaStr
 
 static bool vec_ok(const void *p, long long s) { return ((uintptr_t)p & 15u) == 0 && (s & 3) == 0; }
 
+// Clusters of c CTAs of k_probs, each with the largest buffer, that the current device holds at
+// once (asked for once per device and size: whole clusters lie in one GPC, so that fewer fit
+// than the SMs alone say).
+static int probs_resident(int c, int nsm)
+{
+    static std::atomic<int> known[64][5];
+    int dev = 0;
+    if (cudaGetDevice(&dev)) return 1;
+    int k = 0;
+    while ((1 << k) < c) ++k;
+    const bool keep = dev >= 0 && dev < 64 && k < 5;
+    if (keep) {
+        const int n = known[dev][k].load(std::memory_order_relaxed);
+        if (n) return n;
+    }
+    const int smem = kRowHold * kRowTile * 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(nsm / c + 1) * c);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)c, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(k_probs<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ||
+        cudaOccupancyMaxActiveClusters(&n, k_probs<true>, &cfg) || n < 1) {
+        cudaGetLastError();
+        n = nsm / c > 0 ? nsm / c : 1;
+    }
+    if (keep) known[dev][k].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,
-                       long long os, cudaStream_t st)
+                       long long os, cudaStream_t st, int nsm)
 {
     if (rows == 0) return cudaSuccess;
-    const int c = row_cluster(n);
-    ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), 0.f, 0.f, temperature <= 0.f};
+    const int c = row_cluster(n, rows, 0);
+    ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), rows, 0.f, 0.f, temperature <= 0.f, 0};
     if (!a.greedy) {
         const double cc = 1.4426950408889634 / (double)temperature;
         a.c_hi = (float)(cc < 3e38 ? cc : 3e38);
         a.c_lo = cc < 3e38 ? (float)(cc - (double)a.c_hi) : 0.f;
     }
     const bool vec = vec_ok(logits, ls) && vec_ok(out, os);
-    return vec ? launch_rows(k_probs<true>, rows, c, st, a) : launch_rows(k_probs<false>, rows, c, st, a);
+    // more rows than the GPU holds clusters take turns
+    const int most = probs_resident(c, nsm), clusters = rows < most ? rows : most;
+    a.ahead = vec && rows > clusters;
+    const int hold = kRowHold * kRowTile;
+    const size_t smem = a.ahead ? (size_t)(a.chunk < hold ? a.chunk : hold) * 4 : 0;
+    return vec ? launch_rows(k_probs<true>, clusters, c, kRowThreads, smem, st, a)
+               : launch_rows(k_probs<false>, clusters, c, kRowThreads, smem, st, a);
 }
 
 // ------------------------------------------------------------------ verification
 
-static constexpr int kVerifySegs = kMaxRowVocab / 8 / kRowTile * kRowWarps;   // 128-token segments of a chunk
+static constexpr int kVerifySegs = kMaxRowVocab / 8 / 128;   // 128-token segments of a chunk
 static constexpr int kMaxDrafts = 64;
 
 __device__ __forceinline__ float unit_prob(float v) { return v > 0.f ? fminf(v, 1.f) : 0.f; }   // NaN: 0
 
-__device__ __forceinline__ unsigned long long weight_q(float w)
+// round(w 2^40) of w in [0, 1] as hi 2^20 + lo (lo <= 2^20): w 2^20 and its fraction are exact, and
+// so the second rounding, to nearest even, is the only one.  (One conversion to a 64-bit
+// integer is the same number on a pipe of a fraction of the rate.)
+__device__ __forceinline__ void weight_q(float w, unsigned &hi, unsigned &lo)
 {
-    return (unsigned long long)__float2ll_rn(w * 1099511627776.f);   // 2^40, exact scaling
+    const float s = w * 1048576.f;
+    hi = (unsigned)s;
+    lo = __float2uint_rn((s - (float)hi) * 1048576.f);
 }
 
 struct VerifyKArgs {
@@ -268,12 +365,15 @@ struct VerifyKArgs {
     int chunk;
 };
 
-template <bool VEC>
-__global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant__ VerifyKArgs args)
+// Threads: 512 for few sequences (a chunk's loads all in flight at once), 256 for many (four CTAs
+// an SM: 64 sequences of 8 CTAs run in one wave).
+template <bool VEC, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant__ VerifyKArgs args)
 {
     __shared__ unsigned long long s_seg[kVerifySegs];
-    __shared__ unsigned long long s_warp[kRowWarps], s_total[2];
+    __shared__ unsigned long long s_warp[NT / 32], s_total[2];
     __shared__ unsigned s_ok[kMaxDrafts / 32];
+    constexpr int kWarps = NT / 32, kTile = NT * 4;
     const VerifyArgs &a = args.a;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int b = blockIdx.x / size;
@@ -312,8 +412,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
 
     // ---- the weights of tokens i .. i + 3 as integers; alone: those of p
     const int c0 = (int)rank * args.chunk, c1 = min(a.n, c0 + args.chunk);
-    const int rounds = c1 > c0 ? (c1 - c0 + kRowTile - 1) / kRowTile : 0;
-    auto weights4 = [&](const float4 &p, const float4 &q, int i, bool alone, unsigned long long (&w)[4]) {
+    const int rounds = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0;
+    auto weights4 = [&](const float4 &p, const float4 &q, int i, bool alone, unsigned (&hi)[4], unsigned (&lo)[4]) {
         const float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -322,7 +422,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
                 v = fmaxf(v - unit_prob(qv[e]), 0.f);
                 if (i + e == gone) v = 0.f;
             }
-            w[e] = weight_q(v);
+            weight_q(v, hi[e], lo[e]);
         }
     };
     const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -336,21 +436,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
             float4 p[4], q[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = c0 + ((j0 + u) * kRowThreads + (int)threadIdx.x) * 4;
+                const int i = c0 + ((j0 + u) * NT + (int)threadIdx.x) * 4;
                 p[u] = j0 + u < rounds ? row_load4<VEC>(prow, i, c1, 0.f) : zero4;
                 q[u] = j0 + u < rounds && with_q ? row_load4<VEC>(qrow, i, c1, 0.f) : zero4;
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (j0 + u >= rounds) break;
-                const int i = c0 + ((j0 + u) * kRowThreads + (int)threadIdx.x) * 4;
-                unsigned long long w[4];
-                weights4(p[u], q[u], i, alone, w);
-                const unsigned long long s = (w[0] + w[1]) + (w[2] + w[3]);   // at most 2^42
-                const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)(s & 0x1fffffull));
-                const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)(s >> 21));
-                const unsigned long long seg = ((unsigned long long)hi << 21) + lo;
-                if (lane == 0) s_seg[(j0 + u) * kRowWarps + warp] = seg;
+                const int i = c0 + ((j0 + u) * NT + (int)threadIdx.x) * 4;
+                unsigned h4[4], l4[4];
+                weights4(p[u], q[u], i, alone, h4, l4);
+                // 128 tokens: both halves stay below 2^28
+                const unsigned lo = __reduce_add_sync(0xffffffffu, (l4[0] + l4[1]) + (l4[2] + l4[3]));
+                const unsigned hi = __reduce_add_sync(0xffffffffu, (h4[0] + h4[1]) + (h4[2] + h4[3]));
+                const unsigned long long seg = ((unsigned long long)hi << 20) + lo;
+                if (lane == 0) s_seg[(j0 + u) * kWarps + warp] = seg;
                 wsum += seg;
             }
         }
@@ -358,7 +458,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
         __syncthreads();
         if (threadIdx.x == 0) {
             unsigned long long t = 0ull;
-            for (int w = 0; w < kRowWarps; ++w) t += s_warp[w];
+            for (int w = 0; w < kWarps; ++w) t += s_warp[w];
             s_total[mode] = t;
         }
         cluster_sync_all();
@@ -390,7 +490,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
 
     // ---- the segment of 128 tokens in which the running sum reaches R, then the token
     unsigned long long need = R - before;
-    const int nseg = rounds * kRowWarps, per = (nseg + 31) / 32;
+    const int nseg = rounds * kWarps, per = (nseg + 31) / 32;
     unsigned long long sum = 0ull;
     for (int i = lane * per; i < min(nseg, (lane + 1) * per); ++i) sum += s_seg[i];
     auto scan = [&](unsigned long long v) {   // inclusive over the lanes
@@ -406,10 +506,13 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
     unsigned long long left = need - __shfl_sync(0xffffffffu, incl - sum, src);
     int seg = src * per;
     while (left > s_seg[seg]) left -= s_seg[seg++];   // ends: the lane's segments reach it
-    const int j = seg / kRowWarps, w0 = seg - j * kRowWarps;
-    const int i = c0 + (j * kRowThreads + w0 * 32 + lane) * 4;
+    const int j = seg / kWarps, w0 = seg - j * kWarps;
+    const int i = c0 + (j * NT + w0 * 32 + lane) * 4;
+    unsigned h4[4], l4[4];
+    weights4(row_load4<VEC>(prow, i, c1, 0.f), qrow && !alone ? row_load4<VEC>(qrow, i, c1, 0.f) : zero4, i, alone, h4, l4);
     unsigned long long w[4];
-    weights4(row_load4<VEC>(prow, i, c1, 0.f), qrow && !alone ? row_load4<VEC>(qrow, i, c1, 0.f) : zero4, i, alone, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = ((unsigned long long)h4[e] << 20) + l4[e];
     sum = (w[0] + w[1]) + (w[2] + w[3]);
     incl = scan(sum);
     const int hit = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;
@@ -421,14 +524,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_verify(const __grid_constant
     }
 }
 
-cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st)
+cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st, int nsm)
 {
     if (n_seqs == 0) return cudaSuccess;
-    const int c = row_cluster(a.n);
+    const int c = row_cluster(a.n, n_seqs, 4);
     const VerifyKArgs ka = {a, row_chunk(a.n, c)};
     bool vec = vec_ok(a.p, a.ps) && vec_ok(a.p, a.pstride);
     if (a.q) vec = vec && vec_ok(a.q, a.qs) && vec_ok(a.q, a.qstride);
-    return vec ? launch_rows(k_verify<true>, n_seqs, c, st, ka) : launch_rows(k_verify<false>, n_seqs, c, st, ka);
+    const bool few = n_seqs * c <= nsm;
+    if (few)
+        return vec ? launch_rows(k_verify<true, 512>, n_seqs, c, 512, 0, st, ka)
+                   : launch_rows(k_verify<false, 512>, n_seqs, c, 512, 0, st, ka);
+    return vec ? launch_rows(k_verify<true, 256>, n_seqs, c, 256, 0, st, ka)
+               : launch_rows(k_verify<false, 256>, n_seqs, c, 256, 0, st, ka);
 }
 
 }  // namespace ds4g

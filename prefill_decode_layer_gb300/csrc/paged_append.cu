@@ -84,9 +84,10 @@ __device__ __forceinline__ void turn8(float (&x)[8], const float (&c)[8], int d,
     }
 }
 
-// U: heads in flight per thread.  128 bytes of them for many tokens (10k tokens: 91 us; 120 with
-// half), one where every thread has one head anyway: the unrolled form's instructions take
-// longer to fetch than 64 tokens take (5.0 against 3.1 us).
+// U: heads in flight per thread, by how many it has.  128 bytes of them for many tokens (10k
+// tokens: 91 us; 120 with half), half of that for some (1000 tokens: 14 us; 18 with 128 bytes
+// and fewer CTAs an SM), one where every thread has one or two anyway: the unrolled forms'
+// instructions take longer to fetch than 64 tokens take (5.0 against 3.0 us).
 template <typename TI, typename TC, int U>
 __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_constant__ AppendArgs a, int tokens_per_cta)
 {
@@ -176,11 +177,13 @@ static cudaError_t append_from(const AppendArgs &a, int kv_dtype, dim3 grid, int
 {
     constexpr int U = 16 / sizeof(TI);
     const dim3 block(kApThreads);
-    if (per_thread <= 2)
-        return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<TI, bf16, 1>, grid, block, 0, st, a, tpc)
-                                     : launch_pdl(k_paged_append<TI, float, 1>, grid, block, 0, st, a, tpc);
-    return kv_dtype == DS4G_BF16 ? launch_pdl(k_paged_append<TI, bf16, U>, grid, block, 0, st, a, tpc)
-                                 : launch_pdl(k_paged_append<TI, float, U>, grid, block, 0, st, a, tpc);
+    auto go = [&](auto to_bf16, auto to_f32) {
+        return kv_dtype == DS4G_BF16 ? launch_pdl(to_bf16, grid, block, 0, st, a, tpc)
+                                     : launch_pdl(to_f32, grid, block, 0, st, a, tpc);
+    };
+    if (per_thread <= 2) return go(k_paged_append<TI, bf16, 1>, k_paged_append<TI, float, 1>);
+    if (per_thread <= U) return go(k_paged_append<TI, bf16, U / 2>, k_paged_append<TI, float, U / 2>);
+    return go(k_paged_append<TI, bf16, U>, k_paged_append<TI, float, U>);
 }
 
 cudaError_t paged_append(const AppendArgs &a, int in_dtype, int kv_dtype, cudaStream_t st, int nsm)

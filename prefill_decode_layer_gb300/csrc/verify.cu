@@ -7,12 +7,15 @@
 // already runs on 8 or 16 SMs, and combine their maxima and sums through distributed shared
 // memory; one launch, no workspace.
 //
-// k_probs: p = 2^((z - max z) log2(e) / T) / sum.  A chunk stays in registers between the
-// maximum, the sum and the store (32 values per thread; what a larger vocabulary has beyond
-// is read again), so that a row crosses HBM once each way.  Clusters walk over the rows, and
-// the next row's chunk is copied into shared memory (a bulk copy) while this one's is computed
-// and stored: without it the memory idled between a row's load and its store (94 us for
-// 320 rows of 129280).
+// k_probs: p = 2^((z - max z) log2(e) / T) / sum.  A CTA's chunk comes into shared memory by a
+// bulk copy and crosses HBM once each way.  Every thread takes 2^((z - m) c) of its values
+// against a maximum m of its own, the (m, sum) pairs are combined over the CTA and then, in
+// one exchange, over the cluster, and each thread scales its values by 2^((m - M) c) / S on the
+// way out.  Three CTAs fit an SM, so that the copies of some overlap the arithmetic of others
+// (with the chunk in registers two fit, and 56 of a GPC's 57 places against 32 of 38: 94 us
+// for 320 rows of 129280).  k_probs_any holds the chunk in registers and reads what a larger
+// vocabulary has beyond again: for rows that are not 16-byte aligned and vocabularies above
+// 131072.
 //
 // k_verify: draft i is accepted while u_i q_i(d_i) < p_i(d_i) (exact: products of two
 // 24-bit numbers in FP64), which every CTA of the cluster evaluates for itself.  The
@@ -93,158 +96,259 @@ struct ProbsArgs {
     int n, chunk, rows;
     float c_hi, c_lo;   // log2(e) / T
     int greedy;
-    int ahead;          // the next row's chunk is copied into shared memory meanwhile
 };
 
-// One row after another: cluster i of the grid takes rows i, i + clusters, ..
-template <bool VEC>
-__global__ void __launch_bounds__(kRowThreads, 2) k_probs(const __grid_constant__ ProbsArgs a)
+// The larger of two argmax candidates (key of the value, then the lower id); 0: none.
+__device__ __forceinline__ unsigned long long arg_key(float v, int i)
 {
-    extern __shared__ __align__(16) float s_next[];   // the next row's chunk (a.ahead)
-    __shared__ float s_red[kRowWarps], s_max[2], s_sum[2];
+    return v > -INFINITY ? ((unsigned long long)topk_key(v) << 32) | (0xffffffffu - (unsigned)i) : 0ull;
+}
+__device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned long long warp_max64(unsigned long long v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max64(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// Values i .. i + 3 of the row that is 1 at id `win`.
+__device__ __forceinline__ float4 one_hot4(int i, int win)
+{
+    return make_float4(i == win ? 1.f : 0.f, i + 1 == win ? 1.f : 0.f, i + 2 == win ? 1.f : 0.f,
+                       i + 3 == win ? 1.f : 0.f);
+}
+__device__ __forceinline__ int key_id(unsigned long long k) { return k ? (int)(0xffffffffu - (unsigned)(k & 0xffffffffull)) : -1; }
+
+// Weight factor of values taken against maximum m once the maximum is M >= m (2^((m - M) c); 1
+// for equal ones, infinite or absent as they may be).
+__device__ __forceinline__ float rebase(float m, float M, float c_hi, float c_lo)
+{
+    return m == M ? 1.f : exp_scaled(m, M, c_hi, c_lo);
+}
+
+// Rows 16-byte aligned, chunks of at most kRowHold rounds: cluster i of the grid takes rows i,
+// i + clusters, ..
+__global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant__ ProbsArgs a)
+{
+    extern __shared__ __align__(16) float s_x[];   // the chunk: logits, then weights
+    __shared__ float2 s_red[kRowWarps], s_ms[2];
     __shared__ unsigned long long s_red64[kRowWarps], s_key[2];
     __shared__ uint64_t s_bar;
-    __shared__ int s_abort;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = (int)rank * a.chunk, c1 = min(a.n, c0 + a.chunk);
-    const int rounds = c1 > c0 ? (c1 - c0 + kRowTile - 1) / kRowTile : 0;
-    // what a bulk copy brings: whole 16-byte vectors, as many as the registers hold
-    const int bulk = a.ahead && c1 > c0 ? min(c1 - c0, kRowHold * kRowTile) & ~3 : 0;
+    const int c0 = (int)rank * a.chunk, len = min(a.n, c0 + a.chunk) - c0;   // (len <= 0: a CTA without tokens)
+    const int bulk = max(len, 0) & ~3;                                       // what the copy brings
     const int clusters = gridDim.x / size;
+    constexpr int kBatch = kRowHold / 2;   // vectors a thread holds at a time
     if (threadIdx.x == 0) {
         mbar_init(&s_bar, 1);
         mbar_fence_init();
-        s_abort = 0;
     }
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    auto at = [&](int j) { return c0 + (j * kRowThreads + (int)threadIdx.x) * 4; };
-    auto clean = [](float v) { return v != v ? -INFINITY : v; };
     auto fetch = [&](int row) {   // thread 0
         mbar_expect_tx(&s_bar, (uint32_t)bulk * 4);
-        bulk_g2s(s_next, a.z + row * a.zs + c0, (uint32_t)bulk * 4, &s_bar, policy_evict_first());
+        if (bulk) bulk_g2s(s_x, a.z + row * a.zs + c0, (uint32_t)bulk * 4, &s_bar, policy_evict_first());
     };
-    int turn = 0;   // rows of this cluster so far
-    for (int row = blockIdx.x / size; row < a.rows; row += clusters, ++turn) {
-        const float *z = a.z + row * a.zs;
-        float *p = a.p + row * a.ps;
-        const int par = turn & 1;   // a row's shared values are read by the others until the next row's exist
-        float4 x[kRowHold];
-        const bool here = bulk && turn > 0;   // this row's chunk was fetched during the last one
-        if (here) {
-            if (!mbar_wait(&s_bar, (turn - 1) & 1u, &s_abort)) s_abort = 1;   // (a failed copy: the row is read below)
-#pragma unroll
-            for (int j = 0; j < kRowHold; ++j) {
-                const int i = at(j) - c0;
-                x[j] = i + 3 < bulk && !s_abort ? *reinterpret_cast<const float4 *>(s_next + i)
-                                                : row_load4<VEC>(z, c0 + i, c1, -INFINITY);
-            }
-            __syncthreads();   // the buffer is free
-        } else {
-#pragma unroll
-            for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), c1, -INFINITY);
-        }
-        if (bulk && threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
-        float mx = -INFINITY;   // fmaxf takes the number beside a NaN
-#pragma unroll
-        for (int j = 0; j < kRowHold; ++j) mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
-        for (int j = kRowHold; j < rounds; ++j) {
-            const float4 v = row_load4<VEC>(z, at(j), c1, -INFINITY);
-            mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
-        }
-        mx = clean(mx);
-
+    int row = blockIdx.x / size;
+    if (threadIdx.x == 0 && row < a.rows) fetch(row);
+    volatile int never = 0;
+    for (int turn = 0; row < a.rows; row += clusters, ++turn) {
+        const float *z = a.z + row * a.zs + c0;
+        float *p = a.p + row * a.ps + c0;
+        const int par = turn & 1;   // a row's shared pair is read by the others until the next row's exists
+        const bool landed = mbar_wait(&s_bar, turn & 1u, &never);   // if the wait gave up, the row becomes NaN
+        auto load4 = [&](int i) {   // the last one to three tokens of a row are not part of the copy
+            return i + 3 < bulk ? *reinterpret_cast<const float4 *>(s_x + i) : row_load4<false>(z, i, len, -INFINITY);
+        };
+        auto at = [&](int j) { return (j * kRowThreads + (int)threadIdx.x) * 4; };
         if (a.greedy) {   // one at the largest logit, lowest id on ties
             unsigned long long best = 0ull;
-            auto look = [&](float v, int i) {
-                if (i < c1 && clean(v) > -INFINITY) {
-                    const unsigned long long k = ((unsigned long long)topk_key(v) << 32) | (0xffffffffu - (unsigned)i);
-                    best = k > best ? k : best;
-                }
-            };
-            auto look4 = [&](const float4 &v, int i) {
-                look(v.x, i); look(v.y, i + 1); look(v.z, i + 2); look(v.w, i + 3);
-            };
 #pragma unroll
-            for (int j = 0; j < kRowHold; ++j) look4(x[j], at(j));
-            for (int j = kRowHold; j < rounds; ++j) look4(row_load4<VEC>(z, at(j), c1, -INFINITY), at(j));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
-                best = k > best ? k : best;
-            }
-            if (lane == 0) s_red64[warp] = best;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int w = 1; w < kRowWarps; ++w) best = s_red64[w] > best ? s_red64[w] : best;
-                s_key[par] = best;
-            }
-            cluster_sync_all();   // (also: in place, every thread has read its part of the row)
-            best = 0ull;
-            for (uint32_t r = 0; r < size; ++r) {
-                const unsigned long long k = ld_cluster_u64(&s_key[par], r);
-                best = k > best ? k : best;
-            }
-            const int win = best ? (int)(0xffffffffu - (unsigned)(best & 0xffffffffull)) : -1;
-            for (int j = 0; j < rounds; ++j) {
+            for (int j = 0; j < kRowHold; ++j) {
                 const int i = at(j);
-                row_store4<VEC>(p, i, c1,
-                                make_float4(i == win ? 1.f : 0.f, i + 1 == win ? 1.f : 0.f, i + 2 == win ? 1.f : 0.f,
-                                            i + 3 == win ? 1.f : 0.f));
+                if (i >= len) break;
+                const float4 v = load4(i);
+                best = max64(best, max64(max64(arg_key(v.x, c0 + i), arg_key(v.y, c0 + i + 1)),
+                                         max64(arg_key(v.z, c0 + i + 2), arg_key(v.w, c0 + i + 3))));
             }
+            best = warp_max64(best);
+            if (lane == 0) s_red64[warp] = best;
+            __syncthreads();   // (also: the buffer is free)
+            if (threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
+            if (warp == 0) {
+                best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
+                if (lane == 0) s_key[par] = best;
+            }
+            cluster_sync_all();   // (in place: every CTA has read its part of the row)
+            best = lane < (int)size ? ld_cluster_u64(&s_key[par], lane) : 0ull;
+            const int win = key_id(warp_max64(best)) - c0;
+#pragma unroll
+            for (int j = 0; j < kRowHold; ++j)
+                if (at(j) < len)
+                    row_store4<true>(p, at(j), len, landed ? one_hot4(at(j), win) : make_float4(NAN, NAN, NAN, NAN));
             continue;
         }
-
-        mx = warp_max(mx);
-        if (lane == 0) s_red[warp] = mx;
+        // ---- weights against the maximum of each batch of the thread
+        float m[2], s[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float4 x[kBatch];
+            float mx = -INFINITY;   // fmaxf takes the number beside a NaN
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = at(b * kBatch + j);
+                x[j] = i < len ? load4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
+            }
+            m[b] = mx;
+            s[b] = 0.f;
+            if (mx == INFINITY) {   // its ids have weight 1, the others none
+                auto is = [](float v) { return v == INFINITY ? 0.f : -INFINITY; };
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) x[j] = make_float4(is(x[j].x), is(x[j].y), is(x[j].z), is(x[j].w));
+                mx = 0.f;
+            } else if (mx == -INFINITY) {
+                mx = 0.f;   // no weight
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = at(b * kBatch + j);
+                const float4 w = make_float4(exp_scaled(x[j].x, mx, a.c_hi, a.c_lo), exp_scaled(x[j].y, mx, a.c_hi, a.c_lo),
+                                             exp_scaled(x[j].z, mx, a.c_hi, a.c_lo), exp_scaled(x[j].w, mx, a.c_hi, a.c_lo));
+                s[b] += (w.x + w.y) + (w.z + w.w);
+                if (i < len) *reinterpret_cast<float4 *>(s_x + i) = w;   // (the buffer holds whole vectors)
+            }
+        }
+        // ---- (maximum, sum) of the CTA, then of the row
+        float M = fmaxf(m[0], m[1]);
+        const float wm = warp_max(M);
+        float ws = warp_sum(s[0] * rebase(m[0], wm, a.c_hi, a.c_lo) + s[1] * rebase(m[1], wm, a.c_hi, a.c_lo));
+        if (lane == 0) s_red[warp] = make_float2(wm, ws);
         __syncthreads();
         if (warp == 0) {
-            mx = warp_max(lane < kRowWarps ? s_red[lane] : -INFINITY);
-            if (lane == 0) s_max[par] = mx;
+            const float2 v = lane < kRowWarps ? s_red[lane] : make_float2(-INFINITY, 0.f);
+            M = warp_max(v.x);
+            ws = warp_sum(v.y * rebase(v.x, M, a.c_hi, a.c_lo));
+            if (lane == 0) s_ms[par] = make_float2(M, ws);
         }
         cluster_sync_all();
-        mx = -INFINITY;
-        for (uint32_t r = 0; r < size; ++r) mx = fmaxf(mx, ld_cluster_f32(&s_max[par], r));
-        const float c_hi = a.c_hi, c_lo = a.c_lo;
-        // an infinite maximum: its ids share the whole; no maximum: every weight is 0
-        const bool top_inf = mx == INFINITY;
-        if (top_inf || mx == -INFINITY) mx = 0.f;
-        auto seen = [&](float v) { return !top_inf ? v : v == INFINITY ? 0.f : -INFINITY; };
-        auto weight4 = [&](float4 v) {
-            if (top_inf) v = make_float4(seen(v.x), seen(v.y), seen(v.z), seen(v.w));
-            return make_float4(exp_scaled(v.x, mx, c_hi, c_lo), exp_scaled(v.y, mx, c_hi, c_lo),
-                               exp_scaled(v.z, mx, c_hi, c_lo), exp_scaled(v.w, mx, c_hi, c_lo));
-        };
-        float sum = 0.f;
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (lane < (int)size) {
+            const unsigned long long w = ld_cluster_u64(reinterpret_cast<const unsigned long long *>(&s_ms[par]), lane);
+            v = make_float2(__uint_as_float((unsigned)w), __uint_as_float((unsigned)(w >> 32)));
+        }
+        M = warp_max(v.x);
+        const float total = warp_sum(v.y * rebase(v.x, M, a.c_hi, a.c_lo));
+        const float inv = !landed ? NAN : total > 0.f ? 1.f / total : 0.f;
+        const float f[2] = {rebase(m[0], M, a.c_hi, a.c_lo) * inv, rebase(m[1], M, a.c_hi, a.c_lo) * inv};
 #pragma unroll
         for (int j = 0; j < kRowHold; ++j) {
-            x[j] = weight4(x[j]);
-            sum += (x[j].x + x[j].y) + (x[j].z + x[j].w);
+            const int i = at(j);
+            if (i >= len) break;
+            const float4 w = *reinterpret_cast<const float4 *>(s_x + i);
+            const float g = f[j / kBatch];
+            row_store4<true>(p, i, len, make_float4(w.x * g, w.y * g, w.z * g, w.w * g));
         }
-        for (int j = kRowHold; j < rounds; ++j) {
-            const float4 v = weight4(row_load4<VEC>(z, at(j), c1, -INFINITY));
-            sum += (v.x + v.y) + (v.z + v.w);
-        }
-        sum = warp_sum(sum);
-        if (lane == 0) s_red[warp] = sum;   // (the maxima in it were read before the cluster's barrier)
+        fence_proxy_async_smem();   // this thread's accesses of the buffer, before the next copy's
         __syncthreads();
-        if (warp == 0) {
-            sum = warp_sum(lane < kRowWarps ? s_red[lane] : 0.f);
-            if (lane == 0) s_sum[par] = sum;
-        }
-        cluster_sync_all();
-        sum = 0.f;
-        for (uint32_t r = 0; r < size; ++r) sum += ld_cluster_f32(&s_sum[par], r);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        auto store = [&](int j, const float4 &v) {
-            row_store4<VEC>(p, at(j), c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        if (threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
+    }
+    cluster_sync_all();   // no CTA leaves while another may still read its shared memory
+}
+
+// Rows of any alignment and any vocabulary, one cluster each.
+template <bool VEC>
+__global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_constant__ ProbsArgs a)
+{
+    __shared__ float s_red[kRowWarps], s_max, s_sum;
+    __shared__ unsigned long long s_red64[kRowWarps], s_key;
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = (int)rank * a.chunk, c1 = min(a.n, c0 + a.chunk);
+    const int rounds = c1 > c0 ? (c1 - c0 + kRowTile - 1) / kRowTile : 0;
+    const long long row = blockIdx.x / size;
+    const float *z = a.z + row * a.zs;
+    float *p = a.p + row * a.ps;
+    pdl_wait();
+    pdl_trigger();
+    auto at = [&](int j) { return c0 + (j * kRowThreads + (int)threadIdx.x) * 4; };
+    float4 x[kRowHold];
+#pragma unroll
+    for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), c1, -INFINITY);
+    if (a.greedy) {
+        unsigned long long best = 0ull;
+        auto look4 = [&](const float4 &v, int i) {   // (absent tokens are -inf)
+            best = max64(best, max64(max64(arg_key(v.x, i), arg_key(v.y, i + 1)),
+                                     max64(arg_key(v.z, i + 2), arg_key(v.w, i + 3))));
         };
 #pragma unroll
-        for (int j = 0; j < kRowHold; ++j) store(j, x[j]);
-        for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), c1, -INFINITY)));
+        for (int j = 0; j < kRowHold; ++j) look4(x[j], at(j));
+        for (int j = kRowHold; j < rounds; ++j) look4(row_load4<VEC>(z, at(j), c1, -INFINITY), at(j));
+        best = warp_max64(best);
+        if (lane == 0) s_red64[warp] = best;
+        __syncthreads();
+        if (warp == 0) {
+            best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
+            if (lane == 0) s_key = best;
+        }
+        cluster_sync_all();   // (in place: every CTA has read its part of the row)
+        const int win = key_id(warp_max64(lane < (int)size ? ld_cluster_u64(&s_key, lane) : 0ull));
+        for (int j = 0; j < rounds; ++j) row_store4<VEC>(p, at(j), c1, one_hot4(at(j), win));
+        cluster_sync_all();   // no CTA leaves while another may still read its shared memory
+        return;
     }
+    float mx = -INFINITY;   // fmaxf takes the number beside a NaN
+#pragma unroll
+    for (int j = 0; j < kRowHold; ++j) mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
+    for (int j = kRowHold; j < rounds; ++j) {
+        const float4 v = row_load4<VEC>(z, at(j), c1, -INFINITY);
+        mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+    }
+    mx = warp_max(mx);
+    if (lane == 0) s_red[warp] = mx;
+    __syncthreads();
+    if (warp == 0) {
+        mx = warp_max(lane < kRowWarps ? s_red[lane] : -INFINITY);
+        if (lane == 0) s_max = mx;
+    }
+    cluster_sync_all();
+    mx = warp_max(lane < (int)size ? ld_cluster_f32(&s_max, lane) : -INFINITY);
+    // an infinite maximum: its ids share the whole; no maximum: every weight is 0
+    const bool top_inf = mx == INFINITY;
+    if (top_inf || mx == -INFINITY) mx = 0.f;
+    auto seen = [&](float v) { return !top_inf ? v : v == INFINITY ? 0.f : -INFINITY; };
+    auto weight4 = [&](float4 v) {
+        if (top_inf) v = make_float4(seen(v.x), seen(v.y), seen(v.z), seen(v.w));
+        return make_float4(exp_scaled(v.x, mx, a.c_hi, a.c_lo), exp_scaled(v.y, mx, a.c_hi, a.c_lo),
+                           exp_scaled(v.z, mx, a.c_hi, a.c_lo), exp_scaled(v.w, mx, a.c_hi, a.c_lo));
+    };
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kRowHold; ++j) {
+        x[j] = weight4(x[j]);
+        sum += (x[j].x + x[j].y) + (x[j].z + x[j].w);
+    }
+    for (int j = kRowHold; j < rounds; ++j) {
+        const float4 v = weight4(row_load4<VEC>(z, at(j), c1, -INFINITY));
+        sum += (v.x + v.y) + (v.z + v.w);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) s_red[warp] = sum;   // (the maxima in it were read before the cluster's barrier)
+    __syncthreads();
+    if (warp == 0) {
+        sum = warp_sum(lane < kRowWarps ? s_red[lane] : 0.f);
+        if (lane == 0) s_sum = sum;
+    }
+    cluster_sync_all();
+    sum = warp_sum(lane < (int)size ? ld_cluster_f32(&s_sum, lane) : 0.f);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    auto store = [&](int j, const float4 &v) {
+        row_store4<VEC>(p, at(j), c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    };
+#pragma unroll
+    for (int j = 0; j < kRowHold; ++j) store(j, x[j]);
+    for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), c1, -INFINITY)));
     cluster_sync_all();   // no CTA leaves while another may still read its shared memory
 }
 
@@ -313,8 +417,8 @@ static int probs_resident(int c, int nsm)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaFuncSetAttribute(k_probs<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ||
-        cudaOccupancyMaxActiveClusters(&n, k_probs<true>, &cfg) || n < 1) {
+    if (cudaFuncSetAttribute(k_probs, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ||
+        cudaOccupancyMaxActiveClusters(&n, k_probs, &cfg) || n < 1) {
         cudaGetLastError();
         n = nsm / c > 0 ? nsm / c : 1;
     }
@@ -327,20 +431,20 @@ cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float
 {
     if (rows == 0) return cudaSuccess;
     const int c = row_cluster(n, rows, 0);
-    ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), rows, 0.f, 0.f, temperature <= 0.f, 0};
+    ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), rows, 0.f, 0.f, temperature <= 0.f};
     if (!a.greedy) {
         const double cc = 1.4426950408889634 / (double)temperature;
         a.c_hi = (float)(cc < 3e38 ? cc : 3e38);
         a.c_lo = cc < 3e38 ? (float)(cc - (double)a.c_hi) : 0.f;
     }
     const bool vec = vec_ok(logits, ls) && vec_ok(out, os);
-    // more rows than the GPU holds clusters take turns
-    const int most = probs_resident(c, nsm), clusters = rows < most ? rows : most;
-    a.ahead = vec && rows > clusters;
-    const int hold = kRowHold * kRowTile;
-    const size_t smem = a.ahead ? (size_t)(a.chunk < hold ? a.chunk : hold) * 4 : 0;
-    return vec ? launch_rows(k_probs<true>, clusters, c, kRowThreads, smem, st, a)
-               : launch_rows(k_probs<false>, clusters, c, kRowThreads, smem, st, a);
+    if (vec && a.chunk <= kRowHold * kRowTile) {
+        // more rows than the GPU holds clusters take turns
+        const int most = probs_resident(c, nsm);
+        return launch_rows(k_probs, rows < most ? rows : most, c, kRowThreads, (size_t)a.chunk * 4, st, a);
+    }
+    return vec ? launch_rows(k_probs_any<true>, rows, c, kRowThreads, 0, st, a)
+               : launch_rows(k_probs_any<false>, rows, c, kRowThreads, 0, st, a);
 }
 
 // ------------------------------------------------------------------ verification

@@ -120,8 +120,8 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
     if (!(scale >= 0.f) || scale - scale != 0.f) return DS4G_EINVAL;   // negative, NaN or infinite
     if (batch->n_tokens == 0 || batch->n_seqs == 0) return DS4G_OK;
     if (batch->max_new > kMaxNew) return DS4G_EINVAL;
-    // units of one sequence are counted in 32 bits (64 keys and 8 query rows a unit at least)
-    if ((double)batch->width * kv->page_size / 64 * ((double)batch->max_new * n_heads / 8 + kv->n_kv_heads) > 2e9)
+    // units of one sequence are counted in 32 bits (64 keys and 4 query rows a unit at least)
+    if ((double)batch->width * kv->page_size / 64 * ((double)batch->max_new * n_heads / 4 + kv->n_kv_heads) > 2e9)
         return DS4G_EINVAL;
     const int64_t row = (int64_t)n_heads * kv->head_dim;
     if (!q || !out || !al16(q) || !al16(out) || !stride_ok(q_stride, row, dtype) || !stride_ok(out_stride, row, dtype))

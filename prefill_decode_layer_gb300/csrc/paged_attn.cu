@@ -11,16 +11,20 @@
 // FP32 form (k_paged_attn): for FP32 queries or caches and for head sizes and page sizes
 // the tensor-core form does not take.  Lanes are split into groups of LPK that own D dims
 // each, and every group is a stream of its own through the CTA's keys: it loads KB keys'
-// K and V straight into registers (coalesced 16-byte loads, no shared memory), forms the
-// dot products of up to 8 query rows by shuffles, and keeps its rows' output in
-// registers.  The streams of an item are merged through shared memory when it ends.
+// K and V straight into registers (coalesced 16-byte loads, no shared memory).  The R x KB dot
+// products of R query rows are summed over the lanes by exchanging halves, so that a lane
+// ends with one of them: R KB - 1 exchanges where summing each over all lanes takes log2(LPK)
+// R KB, and one 2^x a lane.  The weights then go round once (a shuffle each) for O += P V in
+// registers.  The streams of an item are merged when it ends, those of a warp by shuffles, the
+// eight warps through shared memory.  Bound: the cache's bytes at few rows (two CTAs an SM keep
+// 64 KB of loads in flight), the FP32 pipes at many.
 #include "paged_sched.cuh"
 
 namespace ds4g {
 
 static constexpr int kPaThreads = 256;
+static constexpr int kPaWarps = kPaThreads / 32;
 static constexpr int kPaKeys = 64;    // keys of a unit
-static constexpr int kPaRows = kAttnRowsSimt;
 
 // D consecutive elements as floats (D 4 or 8; 8- or 16-byte loads of BF16, 16-byte of FP32).
 template <typename T, int D> struct Load;
@@ -69,18 +73,28 @@ template <> __device__ __forceinline__ void store_out<bf16>(bf16 *p, float v) { 
 // Finite stand-in of a maximum over no key, for the exponents.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Dynamic shared memory: [streams][kPaRows] maxima and sums, then [streams][kPaRows][head_dim].
-template <int LPK> struct PaStreams { static constexpr int n = kPaThreads / LPK; };
-
-template <typename TQ, typename TKV, int LPK, int D, int KB>
-__global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant__ AttnArgs a)
+__device__ __forceinline__ float pa_ex2(float x)   // 2^x (hardware approximation, 2 ulp)
 {
-    constexpr int S = PaStreams<LPK>::n;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Dynamic shared memory: [warps][R] maxima and sums, then [warps][R][head_dim].
+static size_t pa_smem(int rows, int hd) { return (size_t)kPaWarps * rows * (2 + hd) * 4; }
+
+template <typename TQ, typename TKV, int LPK, int D, int R, int KB>
+__global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(const __grid_constant__ AttnArgs a)
+{
+    constexpr int S = kPaThreads / LPK;   // streams
+    constexpr int NV = R * KB;            // dot products of a batch
+    constexpr int REP = LPK / NV;         // lanes that hold the same one
+    static_assert(NV <= LPK, "a lane holds one dot product");
     extern __shared__ float sm[];
     __shared__ PagedCursor s_cur;
     __shared__ PagedItem s_item;
-    __shared__ long long s_scratch[kPaThreads / 32];
-    const PartLayout lay(kAttnMaxCtas, kPaRows, a.kv.head_dim);
+    __shared__ long long s_scratch[kPaWarps];
+    const PartLayout lay(kAttnMaxCtas, kAttnRowsSimt, a.kv.head_dim);
     PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
     pdl_wait();
     pdl_trigger();
@@ -91,14 +105,20 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
     }
     paged_cursor<kPaThreads>(a, kPaKeys, &s_cur, s_scratch);
     PagedCursor cur = s_cur;
-    const int hd = a.kv.head_dim;
+
+    const int hd = a.kv.head_dim, ps = a.kv.page_size;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int stream = threadIdx.x / LPK, sub = threadIdx.x % LPK;
     const int d0 = sub * D;
     const bool own = d0 < hd;   // head_dim is a multiple of 8: whole vectors of D
-    float *s_m = sm, *s_l = sm + S * kPaRows, *s_o = sm + 2 * S * kPaRows;
-    const TKV *kc = static_cast<const TKV *>(a.kv.k), *vc = static_cast<const TKV *>(a.kv.v);
-    const TQ *qp = static_cast<const TQ *>(a.q);
+    const unsigned lanes = LPK == 32 ? 0xffffffffu : ((1u << (LPK & 31)) - 1u) << (lane / LPK * LPK);
+    const int my_row = sub / REP / KB, my_key = sub / REP % KB;   // the dot product this lane ends with
+    const bool one_page = ps % KB == 0;   // a batch's keys lie in one page
+    float *s_m = sm, *s_l = sm + kPaWarps * R, *s_o = sm + 2 * kPaWarps * R;
+    const TKV *kc = static_cast<const TKV *>(a.kv.k) + d0, *vc = static_cast<const TKV *>(a.kv.v) + d0;
+    const TQ *qp = static_cast<const TQ *>(a.q) + d0;
     TQ *out = static_cast<TQ *>(a.out);
+    const int win = a.window > 0 ? a.window : 0x7fffffff;
 
     while (true) {
         if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, split, s_item);
@@ -106,126 +126,172 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_attn(const __grid_constant
         if (!s_item.more) return;
         const PagedItem it = s_item;
         const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
-        // the rows' queries, scaled, and the last key each sees
-        float q[kPaRows][D], o[kPaRows][D], m[kPaRows], l[kPaRows];
-        int last[kPaRows];
+        float q[R][D], o[R][D], m = -INFINITY, l = 0.f;   // m, l: of this lane's row (l: of its keys)
 #pragma unroll
-        for (int r = 0; r < kPaRows; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-            last[r] = -1;
+        for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int e = 0; e < D; ++e) q[r][e] = o[r][e] = 0.f;
-            if (r < it.n_rows) {
+            if (r < it.n_rows && own) {
                 const int row = it.row0 + r, t = row / a.group, h = row - t * a.group;
-                last[r] = max(it.pos0 + t, -1);   // before position 0: no key
-                if (own)
-                    Load<TQ, D>::run(qp + (long long)(it.token + t) * a.q_stride + (it.head * a.group + h) * hd + d0,
-                                     q[r]);
+                Load<TQ, D>::run(qp + (long long)(it.token + t) * a.q_stride + (it.head * a.group + h) * hd, q[r]);
 #pragma unroll
                 for (int e = 0; e < D; ++e) q[r][e] *= a.scale_log2;
             }
         }
+        // the keys this lane's row sees: [see_lo, see_hi]
+        const int pos = my_row < it.n_rows ? it.pos0 + (it.row0 + my_row) / a.group : -1;
         const int k0 = max(it.lo, it.t0 * kPaKeys), k1 = min(it.hi, it.t1 * kPaKeys);
-        // every row sees keys [all_lo, all_hi]
-        const int win = a.window > 0 ? a.window : 0x7fffffff;
-        const int all_hi = it.pos0 + it.tok_a;
-        const int all_lo = a.window > 0 ? it.pos0 + it.tok_b - a.window + 1 : 0;
-        for (int j0 = k0 + stream * KB; j0 < k1; j0 += S * KB) {
-            float k[KB][D], v[KB][D];
-            bool there[KB];
-            bool all = it.n_rows == kPaRows && j0 >= all_lo && j0 + KB - 1 <= all_hi;
-#pragma unroll
-            for (int u = 0; u < KB; ++u) {
-                const int j = j0 + u;
-                const int page = j < k1 ? key_page(a, table, j) : -1;
-                there[u] = page >= 0;
-                all = all && there[u];
-#pragma unroll
-                for (int e = 0; e < D; ++e) k[u][e] = v[u][e] = 0.f;
-                if (there[u] && own) {
-                    const long long at = page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
-                                         it.head * a.kv.head_stride + d0;
-                    Load<TKV, D>::run(kc + at, k[u]);
-                    Load<TKV, D>::run(vc + at, v[u]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < kPaRows; ++r) {
-                if (r >= it.n_rows) break;
-                float s[KB];
-#pragma unroll
-                for (int u = 0; u < KB; ++u) {
-                    s[u] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < D; ++e) s[u] = fmaf(q[r][e], k[u][e], s[u]);
-                }
-                const unsigned lanes = LPK == 32 ? 0xffffffffu
-                                                 : ((1u << (LPK & 31)) - 1u) << ((threadIdx.x & 31) / LPK * LPK);
-#pragma unroll
-                for (int x = LPK / 2; x > 0; x >>= 1)
-#pragma unroll
-                    for (int u = 0; u < KB; ++u) s[u] += __shfl_xor_sync(lanes, s[u], x);
-                float mx = m[r];
-                bool see[KB];
+        const int see_lo = max(max(pos, -1) - win + 1, k0), see_hi = min(pos, k1 - 1);
+        // element offset of key j in its page, or -1: outside the CTA's keys or no page
+        auto place = [&](int j) -> long long {
+            if (j < k0 || j >= k1) return -1;
+            const int pi = j / ps, page = table[pi];
+            if (page < 0 || page >= a.kv.n_pages) return -1;
+            return page * a.kv.page_stride + (j - pi * ps) * a.kv.slot_stride + it.head * a.kv.head_stride;
+        };
+        auto places = [&](int j0, long long (&at)[KB]) {
+            if (one_page) {
+                const int jv = min(max(j0, k0), k1 - 1);   // a key of the batch that is the CTA's, if one is
+                const long long p = j0 < k1 ? place(jv) : -1;
 #pragma unroll
                 for (int u = 0; u < KB; ++u) {
                     const int j = j0 + u;
-                    see[u] = all || (there[u] && j <= last[r] && j > last[r] - win);
-                    if (see[u]) mx = fmaxf(mx, s[u]);
+                    at[u] = p < 0 || j < k0 || j >= k1 ? -1 : p + (j - jv) * a.kv.slot_stride;
                 }
-                const float ref = finite_max(mx), f = exp2f(m[r] - ref);   // m = -inf: 0
-                m[r] = mx;
-                l[r] *= f;
+            } else {
 #pragma unroll
-                for (int e = 0; e < D; ++e) o[r][e] *= f;
+                for (int u = 0; u < KB; ++u) at[u] = place(j0 + u);
+            }
+        };
+        long long at[KB];
+        int j0 = k0 / KB * KB + stream * KB;
+        if (j0 < k1) places(j0, at);
+#pragma unroll 1
+        for (; j0 < k1; j0 += S * KB) {
+            float k[KB][D], v[KB][D];
+            bool there = false;   // of this lane's key
+#pragma unroll
+            for (int u = 0; u < KB; ++u) {
+#pragma unroll
+                for (int e = 0; e < D; ++e) k[u][e] = v[u][e] = 0.f;
+                if (at[u] >= 0 && own) Load<TKV, D>::run(kc + at[u], k[u]);
+                if (u == my_key) there = at[u] >= 0;
+            }
+#pragma unroll
+            for (int u = 0; u < KB; ++u)
+                if (at[u] >= 0 && own) Load<TKV, D>::run(vc + at[u], v[u]);
+            places(j0 + S * KB, at);   // the next batch's pages, while these keys are on their way
+            float s[NV];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int u = 0; u < KB; ++u) {
-                    if (!see[u]) continue;   // a masked key adds nothing, whatever its V holds
-                    const float p = exp2f(s[u] - ref);
-                    l[r] += p;
+                    float x = 0.f;
 #pragma unroll
-                    for (int e = 0; e < D; ++e) o[r][e] = fmaf(p, v[u][e], o[r][e]);
+                    for (int e = 0; e < D; ++e) x = fmaf(q[r][e], k[u][e], x);
+                    s[r * KB + u] = x;
+                }
+            // sums over the lanes: at each step a lane keeps half of its values
+#pragma unroll
+            for (int n = NV / 2, x = LPK / 2; n >= 1; n /= 2, x /= 2) {
+                const bool up = sub & x;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float send = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+                    s[i] = keep + __shfl_xor_sync(lanes, send, x);
                 }
             }
-        }
-        // ---- merge the streams: rows' maxima and sums, then their outputs, in stream order
 #pragma unroll
-        for (int r = 0; r < kPaRows; ++r) {
-            if (r >= it.n_rows) break;
-            if (sub == 0) {
-                s_m[stream * kPaRows + r] = m[r];
-                s_l[stream * kPaRows + r] = l[r];
+            for (int x = REP / 2; x > 0; x >>= 1) s[0] += __shfl_xor_sync(lanes, s[0], x);
+            const int j = j0 + my_key;
+            const bool see = there && j >= see_lo && j <= see_hi;
+            float top = see ? s[0] : -INFINITY;
+#pragma unroll
+            for (int x = REP; x < REP * KB; x *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, x));
+            // the reference moves only when it is exceeded by 2^8 (or was no key's)
+            if (__any_sync(lanes, top > m + 8.f)) {
+                const bool move = top > m + 8.f;
+                const float f = move ? pa_ex2(m - top) : 1.f;   // m = -inf: 0
+                if (move) m = top;
+                l *= f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float fr = __shfl_sync(lanes, f, r * KB * REP, LPK);
+#pragma unroll
+                    for (int e = 0; e < D; ++e) o[r][e] *= fr;
+                }
+            }
+            const float p = see ? pa_ex2(s[0] - finite_max(m)) : 0.f;
+            l += p;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int u = 0; u < KB; ++u) {
+                    const float pr = __shfl_sync(lanes, p, (r * KB + u) * REP, LPK);
+                    if (pr != 0.f) {   // (NaN: yes) a masked key adds nothing, whatever its V holds
+#pragma unroll
+                        for (int e = 0; e < D; ++e) o[r][e] = fmaf(pr, v[u][e], o[r][e]);
+                    }
+                }
+        }
+        // ---- merge the streams of the warp, then the warps, in order
+        __syncwarp();
+#pragma unroll
+        for (int x = REP; x < REP * KB; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+#pragma unroll
+        for (int x = LPK; x < 32; x *= 2) {
+            const float mo = __shfl_xor_sync(0xffffffffu, m, x), lo = __shfl_xor_sync(0xffffffffu, l, x);
+            const float mn = fmaxf(m, mo), ref = finite_max(mn);
+            const float f = pa_ex2(m - ref), fo = pa_ex2(mo - ref);
+            l = l * f + lo * fo;
+            m = mn;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float fr = __shfl_sync(0xffffffffu, f, r * KB * REP, LPK);
+                const float fro = __shfl_sync(0xffffffffu, fo, r * KB * REP, LPK);
+#pragma unroll
+                for (int e = 0; e < D; ++e)
+                    o[r][e] = o[r][e] * fr + __shfl_xor_sync(0xffffffffu, o[r][e], x) * fro;
+            }
+        }
+        if (lane < LPK) {
+            if (sub % (REP * KB) == 0) {
+                s_m[warp * R + my_row] = m;
+                s_l[warp * R + my_row] = l;
             }
             if (own) {
 #pragma unroll
-                for (int e = 0; e < D; ++e) s_o[(stream * kPaRows + r) * hd + d0 + e] = o[r][e];
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < D; ++e) s_o[(warp * R + r) * hd + d0 + e] = o[r][e];
             }
         }
         __syncthreads();
         for (int i = threadIdx.x; i < it.n_rows * hd; i += kPaThreads) {
             const int r = i / hd, d = i - r * hd;
             float mx = -INFINITY;
-            for (int s = 0; s < S; ++s) mx = fmaxf(mx, s_m[s * kPaRows + r]);
+#pragma unroll
+            for (int w = 0; w < kPaWarps; ++w) mx = fmaxf(mx, s_m[w * R + r]);
             const float ref = finite_max(mx);
             float acc = 0.f, sum = 0.f;
-            for (int s = 0; s < S; ++s) {
-                const float f = exp2f(s_m[s * kPaRows + r] - ref);
-                sum = fmaf(f, s_l[s * kPaRows + r], sum);
-                acc = fmaf(f, s_o[(s * kPaRows + r) * hd + d], acc);
+#pragma unroll
+            for (int w = 0; w < kPaWarps; ++w) {
+                const float f = pa_ex2(s_m[w * R + r] - ref);
+                sum = fmaf(f, s_l[w * R + r], sum);
+                acc = fmaf(f, s_o[(w * R + r) * hd + d], acc);
             }
             if (it.part < 0) {
                 const int row = it.row0 + r, t = row / a.group, h = row - t * a.group;
                 store_out<TQ>(out + (long long)(it.token + t) * a.out_stride + (it.head * a.group + h) * hd + d,
                               sum == 0.f ? 0.f : acc / sum);
             } else {
-                const size_t at = (size_t)it.part * kPaRows + r;
-                float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + at * 2;
+                const size_t part = (size_t)it.part * kAttnRowsSimt + r;
+                float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + part * 2;
                 if (d == 0) {
                     ml[0] = mx;
                     ml[1] = sum;
                 }
-                reinterpret_cast<float *>(a.ws + lay.o)[at * hd + d] = acc;
+                reinterpret_cast<float *>(a.ws + lay.o)[part * hd + d] = acc;
             }
         }
         __syncthreads();   // s_item and the merge buffers are rewritten
@@ -451,27 +517,34 @@ int paged_attn_grid(AttnArgs &a, int kt, int most)
     return (int)(u < most ? u : most);
 }
 
-template <typename TQ, typename TKV, int LPK, int D, int KB>
+template <typename TQ, typename TKV, int LPK, int D, int R, int KB>
 static cudaError_t simt(AttnArgs &a, int nsm, cudaStream_t st)
 {
-    auto kernel = k_paged_attn<TQ, TKV, LPK, D, KB>;
-    const size_t smem = (size_t)PaStreams<LPK>::n * kPaRows * (2 + a.kv.head_dim) * 4;
+    auto kernel = k_paged_attn<TQ, TKV, LPK, D, R, KB>;
+    const size_t smem = pa_smem(R, a.kv.head_dim);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e) return e;
     }
-    const int most = 2 * nsm < kAttnMaxCtas ? 2 * nsm : kAttnMaxCtas;
-    const int grid = paged_attn_grid(a, kPaKeys, most);
+    a.rows = R;
+    const int resident = (R * D <= 16 ? 2 : 1) * nsm;
+    const int grid = paged_attn_grid(a, kPaKeys, resident < kAttnMaxCtas ? resident : kAttnMaxCtas);
     cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kPaThreads), smem, st, a);
     if (!e && !a.whole) e = join<TQ, kAttnRowsSimt, kAttnMaxCtas>(a, grid, nsm, st);
     return e;
 }
+// Four query rows a tile where no sequence has more in a K/V head (or the head is wide), else
+// eight.
 template <typename TQ, typename TKV> static cudaError_t simt_dim(AttnArgs &a, int nsm, cudaStream_t st)
 {
-    if (a.kv.head_dim <= 32) return simt<TQ, TKV, 8, 4, 4>(a, nsm, st);
-    if (a.kv.head_dim <= 64) return simt<TQ, TKV, 16, 4, 4>(a, nsm, st);
-    if (a.kv.head_dim <= 128) return simt<TQ, TKV, 32, 4, 4>(a, nsm, st);
-    return simt<TQ, TKV, 32, 8, 2>(a, nsm, st);
+    const bool four = a.group * a.s.max_new <= 4;
+    if (a.kv.head_dim <= 32)
+        return four ? simt<TQ, TKV, 8, 4, 4, 2>(a, nsm, st) : simt<TQ, TKV, 8, 4, 8, 1>(a, nsm, st);
+    if (a.kv.head_dim <= 64)
+        return four ? simt<TQ, TKV, 16, 4, 4, 4>(a, nsm, st) : simt<TQ, TKV, 16, 4, 8, 2>(a, nsm, st);
+    if (a.kv.head_dim <= 128)
+        return four ? simt<TQ, TKV, 32, 4, 4, 4>(a, nsm, st) : simt<TQ, TKV, 32, 4, 8, 4>(a, nsm, st);
+    return simt<TQ, TKV, 32, 8, 4, 4>(a, nsm, st);
 }
 
 cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaStream_t st, int nsm)
@@ -482,7 +555,6 @@ cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaS
         a.rows = paged_attn_tc_rows(a.group, a.s.max_new);
         return paged_attn_tc(a, st, nsm);
     }
-    a.rows = kAttnRowsSimt;
     if (q_dtype == DS4G_F32)
         return kv_dtype == DS4G_F32 ? simt_dim<float, float>(a, nsm, st) : simt_dim<float, bf16>(a, nsm, st);
     return kv_dtype == DS4G_F32 ? simt_dim<bf16, float>(a, nsm, st) : simt_dim<bf16, bf16>(a, nsm, st);

@@ -95,14 +95,9 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
     __shared__ PagedItem s_item;
     __shared__ long long s_scratch[kPaWarps];
     const PartLayout lay(kAttnMaxCtas, kAttnRowsSimt, a.kv.head_dim);
-    PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x == 0) {
-        split->valid = 0;
-        split->status = DS4G_OK;
-        split->ctas = gridDim.x;
-    }
+    paged_begin(a, lay);
     paged_cursor<kPaThreads>(a, kPaKeys, &s_cur, s_scratch);
     PagedCursor cur = s_cur;
 
@@ -121,7 +116,7 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
     const int win = a.window > 0 ? a.window : 0x7fffffff;
 
     while (true) {
-        if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, split, s_item);
+        if (threadIdx.x == 0) paged_next(a, kPaKeys, cur, lay, s_item);
         __syncthreads();
         if (!s_item.more) return;
         const PagedItem it = s_item;
@@ -301,12 +296,13 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
 // ------------------------------------------------------------------ join
 
 // Rows of split items: out = sum_i f_i o_i / sum_i f_i l_i over the row's parts i, f_i = 2^(m_i -
-// max m).  A row of few parts is one warp's, eight rows a CTA; one of many parts (a long
-// sequence alone) is a CTA's, warp w adding the parts w, w + 8, .. and the eight partial sums
-// then added in order.  Bound: latency (KBs to a few MB of parts from L2).
+// max m).  Every warp reads how many rows each CTA's split item has and finds its rows itself.
+// Where items are many, a row has few parts and is one warp's; where they are few (a long
+// sequence alone), a row is a CTA's, warp w adding the parts w, w + 8, .. and the eight partial
+// sums then added in order.  Bound: latency (KBs to a few MB of parts from L2): three
+// loads that wait for one another, the rows' counts, the item's record, its parts.
 static constexpr int kJoinThreads = 256;
 static constexpr int kJoinWarps = kJoinThreads / 32;
-static constexpr int kJoinFew = 16;   // parts that one warp adds by itself
 
 // V consecutive floats, 4 V bytes aligned (V 2, 4 or 8).
 template <int V> __device__ __forceinline__ void ld_part(const float *p, float (&x)[V])
@@ -336,99 +332,80 @@ template <typename T, int V> __device__ __forceinline__ void st_row(T *p, const 
 }
 
 template <typename T, int ROWS, int CTAS, int V>   // V: adjacent dims per lane
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ AttnArgs a, int ctas)
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ AttnArgs a, int wide)
 {
-    __shared__ short s_cta[CTAS];
-    __shared__ int s_first[CTAS + 1];   // jobs before the i-th split item
-    __shared__ int s_n;
     __shared__ float s_o[kJoinWarps][32 * V], s_l[kJoinWarps];
     const int hd = a.kv.head_dim;
     const int stride = ROWS > 0 ? ROWS : a.rows;
     const PartLayout lay(CTAS, stride, hd);
+    const int *n_rows = reinterpret_cast<const int *>(a.ws + lay.n_rows);
     const PagedSplit *split = reinterpret_cast<const PagedSplit *>(a.ws + lay.split);
-    const float *ml = reinterpret_cast<const float *>(a.ws + lay.ml);
+    const float2 *ml = reinterpret_cast<const float2 *>(a.ws + lay.ml);
     const float *po = reinterpret_cast<const float *>(a.ws + lay.o);
     T *out = static_cast<T *>(a.out);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int d = lane * V;
     pdl_wait();
     pdl_trigger();
-    if (warp == 0) {
-        int nr[(CTAS + 31) / 32];   // all loads first: one trip to L2
+    // lane i: rows of the split items of CTAs K i .. K i + K - 1, and the rows before them
+    constexpr int K = CTAS / 32;
+    static_assert(CTAS % 32 == 0 && CTAS <= kAttnMaxCtas, "a lane looks at whole groups");
+    int nr[K], mine = 0;
 #pragma unroll
-        for (int k = 0; k < (CTAS + 31) / 32; ++k) {
-            const int c = 32 * k + lane;
-            nr[k] = 0;
-            if (c < ctas) {
-                const PagedSplit r = split[c];
-                if (r.valid) nr[k] = r.last_cta - c < kJoinFew ? (r.n_rows + kJoinWarps - 1) / kJoinWarps : r.n_rows;
-            }
-        }
-        int n = 0, jobs = 0;
-#pragma unroll
-        for (int k = 0; k < (CTAS + 31) / 32; ++k) {
-            const unsigned has = __ballot_sync(0xffffffffu, nr[k] > 0);
-            if (!has) continue;
-            int incl = nr[k];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (nr[k] > 0) {
-                const int i = n + __popc(has & ((1u << lane) - 1u));
-                s_cta[i] = (short)(32 * k + lane);
-                s_first[i] = jobs + incl - nr[k];
-            }
-            n += __popc(has);
-            jobs += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) {
-            s_n = n;
-            s_first[n] = jobs;
-        }
+    for (int k = 0; k < K; ++k) {
+        nr[k] = n_rows[K * lane + k];
+        mine += nr[k];
     }
-    __syncthreads();
-    const int n = s_n, jobs = s_first[n];
-    for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
-        int lo = 0, hi = n;   // the last i with s_first[i] <= job
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_first[mid] <= job) lo = mid;
-            else hi = mid;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const int rows = __shfl_sync(0xffffffffu, incl, 31);
+    const int first = wide ? blockIdx.x : blockIdx.x * kJoinWarps + warp, step = wide ? gridDim.x : gridDim.x * kJoinWarps;
+    for (int job = first; job < rows; job += step) {
+        // the CTA whose item has row `job`, and the row in the item
+        const int src = __ffs(__ballot_sync(0xffffffffu, job < incl)) - 1;
+        int c = 0, r = job - (incl - mine);
+        if (lane == src) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (c == k && r >= nr[k]) {
+                    r -= nr[k];
+                    c = k + 1;
+                }
+            c += K * lane;
         }
-        const int c = s_cta[lo];
+        c = __shfl_sync(0xffffffffu, c, src);
+        r = __shfl_sync(0xffffffffu, r, src);
         const PagedSplit sp = split[c];
         const int parts = sp.last_cta - c + 1;
-        const bool few = parts <= kJoinFew;
-        const int r = few ? (job - s_first[lo]) * kJoinWarps + warp : job - s_first[lo];
-        const int p0 = few ? 0 : warp, step = few ? 1 : kJoinWarps;
-        const bool live = r < sp.n_rows;
         // part i: the CTA's own tail, then the head parts of the CTAs after it
         auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride + r; };
-        float acc[V], sum = 0.f;
+        float mx = -INFINITY, acc[V], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
-        if (live) {
-            float mx = -INFINITY;
-            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i) * 2]);
-            mx = warp_max(mx);
-            const float ref = finite_max(mx);
+        const float2 m0 = lane < parts ? ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+        mx = m0.x;
+        for (int i = lane + 32; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i)].x);
+        mx = warp_max(mx);
+        const float ref = finite_max(mx);
+        const int w0 = wide ? warp : 0, ws = wide ? kJoinWarps : 1;
 #pragma unroll 4
-            for (int i = p0; i < parts; i += step) {
-                const size_t s = slot(i);
-                const float2 m2 = *reinterpret_cast<const float2 *>(ml + s * 2);
-                const float f = exp2f(m2.x - ref);
-                sum = fmaf(f, m2.y, sum);
-                if (d < hd) {
-                    float x[V];
-                    ld_part<V>(po + s * hd + d, x);
+        for (int i = w0; i < parts; i += ws) {
+            float2 m2 = make_float2(__shfl_sync(0xffffffffu, m0.x, i & 31), __shfl_sync(0xffffffffu, m0.y, i & 31));
+            if (i >= 32) m2 = ml[slot(i)];
+            const float f = pa_ex2(m2.x - ref);
+            sum = fmaf(f, m2.y, sum);
+            if (d < hd) {
+                float x[V];
+                ld_part<V>(po + slot(i) * hd + d, x);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] = fmaf(f, x[e], acc[e]);
-                }
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, x[e], acc[e]);
             }
         }
-        if (!few) {
+        if (wide) {
 #pragma unroll
             for (int e = 0; e < V; ++e) s_o[warp][d + e] = acc[e];
             if (lane == 0) s_l[warp] = sum;
@@ -446,7 +423,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
             }
             __syncthreads();
         }
-        if (live && d < hd && (few || warp == 0)) {
+        if (d < hd && (!wide || warp == 0)) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int row = sp.row0 + r, tk = row / a.group, h = row - tk * a.group;
 #pragma unroll
@@ -470,25 +447,27 @@ size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dty
 
 cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status)
 {
-    PagedSplit rec[kAttnMaxCtas];
-    static_assert(sizeof(rec) <= 16384, "on the host's stack");
-    // (the workspace holds at least this many bytes: PartLayout of the FP32 form)
-    cudaError_t e = cudaMemcpyAsync(rec, ws, sizeof(rec), cudaMemcpyDeviceToHost, st);
+    int word[kAttnMaxCtas];
+    cudaError_t e = cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, st);   // PartLayout::status
     if (!e) e = cudaStreamSynchronize(st);
     *status = DS4G_OK;
-    for (int c = 0; !e && c < rec[0].ctas && c < kAttnMaxCtas; ++c)
-        if (rec[c].status != DS4G_OK) *status = DS4G_ETIMEOUT;
+    for (int c = 0; !e && c < kAttnMaxCtas; ++c)
+        if (word[c] != DS4G_OK) *status = DS4G_ETIMEOUT;
     return e;
 }
 
+static long long most_items(const AttnArgs &a);
+
+// Launches the join behind a grid of `ctas`: one row a CTA where the items are so few that a
+// row has eight parts or more on average.
 template <typename T, int ROWS, int CTAS>
 static cudaError_t join(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
 {
-    const int grid = 4 * nsm;
-    if (a.kv.head_dim <= 64) return launch_pdl(k_paged_join<T, ROWS, CTAS, 2>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
-    if (a.kv.head_dim <= 128)
-        return launch_pdl(k_paged_join<T, ROWS, CTAS, 4>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
-    return launch_pdl(k_paged_join<T, ROWS, CTAS, 8>, dim3(grid), dim3(kJoinThreads), 0, st, a, ctas);
+    const int wide = most_items(a) * 8 <= ctas, grid = 4 * nsm;
+    const dim3 block(kJoinThreads);
+    if (a.kv.head_dim <= 64) return launch_pdl(k_paged_join<T, ROWS, CTAS, 2>, dim3(grid), block, 0, st, a, wide);
+    if (a.kv.head_dim <= 128) return launch_pdl(k_paged_join<T, ROWS, CTAS, 4>, dim3(grid), block, 0, st, a, wide);
+    return launch_pdl(k_paged_join<T, ROWS, CTAS, 8>, dim3(grid), block, 0, st, a, wide);
 }
 cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
 {

@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     TcMisc &x = *reinterpret_cast<TcMisc *>(ring + (uint32_t)geo.slots * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PartLayout lay(kAttnMaxCtasTc, a.rows, HD);
-    PagedSplit *split = reinterpret_cast<PagedSplit *>(a.ws + lay.split) + blockIdx.x;
 
     {   // one barrier per thread
         uint64_t *bars = x.full;
@@ -140,11 +139,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x == 0) {
-        split->valid = 0;
-        split->status = DS4G_OK;
-        split->ctas = gridDim.x;
-    }
+    paged_begin(a, lay);
     paged_cursor<kTcThreads>(a, kTcKeys, &x.cur, x.scratch);
     tc_fence_before();
     __syncthreads();
@@ -153,7 +148,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *ab = &x.abort_flag;
     auto give_up = [&]() {
         x.abort_flag = 1;
-        split->status = DS4G_ETIMEOUT;
+        reinterpret_cast<int *>(a.ws + lay.status)[blockIdx.x] = DS4G_ETIMEOUT;
     };
     // stream s: scores (then P) at column 128 s, O at 256 + 128 s
     // a place in the ring: tile idx lies in slot idx % slots, in the phase (idx / slots) % 2 of its
@@ -212,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             PagedItem &it = x.item[i % kTcItems];
             if (lane == 0) {
-                paged_next(a, kTcKeys, cur, split, it);
+                paged_next(a, kTcKeys, cur, lay, it);
                 mbar_arrive(&x.item_full[i % kTcItems]);
             }
             __syncwarp();

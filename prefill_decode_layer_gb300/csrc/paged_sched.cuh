@@ -19,7 +19,7 @@
 namespace ds4g {
 
 // Most CTAs of the two forms (the workspace holds two parts for each).
-constexpr int kAttnMaxCtas = 320;      // FP32 form: two CTAs per SM
+constexpr int kAttnMaxCtas = 320;      // FP32 form: two CTAs per SM (a multiple of 64)
 constexpr int kAttnMaxCtasTc = 160;    // tensor-core form: one
 constexpr int kAttnRowsSimt = 8;       // query rows of an FP32 row tile
 
@@ -36,24 +36,38 @@ struct PagedItem {
     int more;               // 0: no item (the CTA is done)
 };
 
-// CTA c's record: what the join needs of an item that begins in it and ends in a later one,
-// and how the CTA ended.
-struct PagedSplit {
-    int valid, last_cta, seq, head, token, row0, n_rows;
-    int status;             // DS4G_OK, or DS4G_ETIMEOUT: a bounded wait gave up
-    int ctas;               // CTAs of the launch
+// What the join needs of an item that begins in CTA c and ends in a later one.
+struct __align__(16) PagedSplit {
+    int last_cta, head, token, row0;
 };
 
+// Workspace: per CTA how it ended (DS4G_OK, or DS4G_ETIMEOUT: a bounded wait gave up), the rows of
+// its split item (0: none begins in it) and that item's record; then the parts, [2 ctas][rows][2]
+// maxima and sums and [2 ctas][rows][head_dim] rows.
 struct PartLayout {
-    size_t split, ml, o, total;   // byte offsets of [ctas] records, [2 ctas][rows][2], [2 ctas][rows][head_dim]
+    size_t status, n_rows, split, ml, o, total;   // byte offsets
     __host__ __device__ PartLayout(int ctas, int rows, int head_dim)
     {
-        split = 0;
-        ml = ((size_t)ctas * sizeof(PagedSplit) + 255) & ~(size_t)255;
+        status = 0;
+        n_rows = (size_t)kAttnMaxCtas * 4;
+        split = n_rows + (size_t)kAttnMaxCtas * 4;
+        ml = split + (size_t)kAttnMaxCtas * sizeof(PagedSplit);
         o = (ml + (size_t)2 * ctas * rows * 2 * 4 + 255) & ~(size_t)255;
         total = o + (size_t)2 * ctas * rows * head_dim * 4;
     }
 };
+static_assert(kAttnMaxCtas * 4 % 256 == 0, "the arrays of the workspace are aligned");
+
+// This CTA's words of the workspace at the start of a launch (all threads; words of CTAs that
+// the grid does not have are cleared too).
+__device__ __forceinline__ void paged_begin(const AttnArgs &a, const PartLayout &lay)
+{
+    int *n_rows = reinterpret_cast<int *>(a.ws + lay.n_rows), *status = reinterpret_cast<int *>(a.ws + lay.status);
+    for (int c = blockIdx.x + gridDim.x * threadIdx.x; c < kAttnMaxCtas; c += gridDim.x * blockDim.x) {
+        n_rows[c] = 0;
+        status[c] = DS4G_OK;
+    }
+}
 
 // A sequence's keys, new tokens and units.
 struct SeqWork {
@@ -161,7 +175,7 @@ __device__ __forceinline__ void paged_cursor(const AttnArgs &a, int kt, PagedCur
 
 // The CTA's next item, one thread.  `cur` is the caller's copy, kept between calls.  Writes
 // the CTA's split record.
-__device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, PagedSplit *split, PagedItem &it)
+__device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, const PartLayout &lay, PagedItem &it)
 {
     it.more = cur.at < cur.end;
     if (!it.more) return;
@@ -194,13 +208,10 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     if (begins && !ends) {
         // the CTA of the item's last unit e: the largest c with c total / ctas <= e
         const unsigned long long e = (unsigned long long)(cur.at + w.tiles - 1);
-        split->valid = 1;
-        split->last_cta = (int)(((e + 1) * (unsigned long long)cur.ctas - 1) / (unsigned long long)cur.total);
-        split->seq = it.seq;
-        split->head = it.head;
-        split->token = it.token;
-        split->row0 = it.row0;
-        split->n_rows = it.n_rows;
+        const PagedSplit r = {(int)(((e + 1) * (unsigned long long)cur.ctas - 1) / (unsigned long long)cur.total),
+                              it.head, it.token, it.row0};
+        reinterpret_cast<PagedSplit *>(a.ws + lay.split)[blockIdx.x] = r;
+        reinterpret_cast<int *>(a.ws + lay.n_rows)[blockIdx.x] = it.n_rows;
     }
     cur.at += a.whole ? 1 : take;
     cur.local += a.whole ? 1 : take;

@@ -84,10 +84,10 @@ __device__ __forceinline__ void turn8(float (&x)[8], const float (&c)[8], int d,
     }
 }
 
-// U: heads in flight per thread, by how many it has.  128 bytes of them for many tokens (10k
-// tokens: 91 us; 120 with half), half of that for some (1000 tokens: 14 us; 18 with 128 bytes
-// and fewer CTAs an SM), one where every thread has one or two anyway: the unrolled forms'
-// instructions take longer to fetch than 64 tokens take (5.0 against 3.0 us).
+// U: heads in flight per thread, twice: the next U are loaded before these are stored (10k
+// tokens of 66 heads: 72 us, 88 % of the copy rate).  One where a thread has up to five: more CTAs
+// fit an SM, and the unrolled form's instructions take longer to fetch (1000 tokens: 10.2 us
+// against 14.0).
 template <typename TI, typename TC, int U>
 __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_constant__ AppendArgs a, int tokens_per_cta)
 {
@@ -95,26 +95,47 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
     __shared__ int s_pos[kApTokens];          // its position, or -1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * tokens_per_cta;
+    const int hd = a.kv.head_dim, hv = hd >> 3, kvh = a.kv.n_kv_heads;
+    // groups of hv threads; `per` of them share a token
+    const int per = kApThreads / hv / tokens_per_cta, grp = threadIdx.x / hv, d = (threadIdx.x - grp * hv) * 8;
+    const int j = grp / per;
+    const bool mine = j < min(tokens_per_cta, a.s.n_tokens - t0);
+    const long long t = t0 + j;
+    const int heads = mine ? a.n_heads + 2 * kvh : 0;   // of a token: queries, keys, values
+    const TI *k = static_cast<const TI *>(a.k) + t * a.k_stride + d;
+    const TI *v = static_cast<const TI *>(a.v) + t * a.v_stride + d;
+    const TI *q = static_cast<const TI *>(a.q) + t * a.q_stride + d;
+    const int step = per * gridDim.y;
+    auto load = [&](Row8<TI> (&w)[U], int h0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * step, kh = h - a.n_heads;
+            if (h < heads) w[u].load(kh < 0 ? q + h * hd : kh < kvh ? k + kh * hd : v + (kh - kvh) * hd);
+        }
+    };
     pdl_wait();
     pdl_trigger();
+    int h0 = grp - j * per + per * blockIdx.y;
+    Row8<TI> w[U];
+    load(w, h0);   // on its way while the positions and pages are looked up
     if (warp < tokens_per_cta) {
-        const int t = t0 + warp;
+        const int tk = t0 + warp;
         int pos = -1;
         long long slot = -1;
-        if (t < a.s.n_tokens) {
-            int b = t, first = t, n = 1;
+        if (tk < a.s.n_tokens) {
+            int b = tk, first = tk, n = 1;
             if (a.s.start) {
-                // the sequence of token t: as many sequences end at or before it
+                // the sequence of token tk: as many sequences end at or before it
                 int ended = 0;
-                for (int i = lane; i < a.s.n_seqs; i += 32) ended += a.s.start[i + 1] <= t;
+                for (int i = lane; i < a.s.n_seqs; i += 32) ended += a.s.start[i + 1] <= tk;
                 b = __reduce_add_sync(0xffffffffu, ended);
                 if (b < a.s.n_seqs) {
                     first = a.s.start[b];
                     n = a.s.start[b + 1] - first;
                 }
             }
-            if (b < a.s.n_seqs && t >= first) {
-                const long long p = (long long)a.s.length[b] - n + (t - first);
+            if (b < a.s.n_seqs && tk >= first) {
+                const long long p = (long long)a.s.length[b] - n + (tk - first);
                 if (p >= 0 && p < (long long)a.s.width * a.kv.page_size) {
                     const int page = a.s.table[(long long)b * a.s.table_stride + (int)p / a.kv.page_size];
                     if (page >= 0 && page < a.kv.n_pages)
@@ -133,32 +154,20 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
         }
     }
     __syncthreads();
-    const int hd = a.kv.head_dim, hv = hd >> 3, kvh = a.kv.n_kv_heads;
-    // groups of hv threads; `per` of them share a token
-    const int per = kApThreads / hv / tokens_per_cta, grp = threadIdx.x / hv, d = (threadIdx.x - grp * hv) * 8;
-    const int j = grp / per;
-    if (j >= min(tokens_per_cta, a.s.n_tokens - t0)) return;
+    if (!mine) return;
     const int pos = s_pos[j];
     if (pos < 0) return;
-    const long long slot = s_slot[j], t = t0 + j;
-    const int heads = a.n_heads + 2 * kvh;   // of a token: queries, keys, values
-    const TI *k = static_cast<const TI *>(a.k) + t * a.k_stride + d;
-    const TI *v = static_cast<const TI *>(a.v) + t * a.v_stride + d;
-    const TI *q = static_cast<const TI *>(a.q) + t * a.q_stride + d;
+    const long long slot = s_slot[j];
     TC *kc = static_cast<TC *>(const_cast<void *>(a.kv.k)) + slot + d;
     TC *vc = static_cast<TC *>(const_cast<void *>(a.kv.v)) + slot + d;
     TI *qo = static_cast<TI *>(a.q_out) + t * a.q_out_stride + d;
     const bool turns = a.cs && d < a.rot_dim;
     float c[8];
     if (turns) load_angles(c, a.cs + (long long)pos * a.rot_dim, d, a.rot_dim);
-    const int step = per * gridDim.y;
-    for (int h0 = grp - j * per + per * blockIdx.y; h0 < heads; h0 += U * step) {
-        Row8<TI> w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * step, kh = h - a.n_heads;
-            if (h < heads) w[u].load(kh < 0 ? q + h * hd : kh < kvh ? k + kh * hd : v + (kh - kvh) * hd);
-        }
+#pragma unroll 1
+    for (; h0 < heads; h0 += U * step) {
+        Row8<TI> next[U];
+        if (U > 1) load(next, h0 + U * step);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * step, kh = h - a.n_heads;
@@ -169,20 +178,25 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
             if (kh < 0) Row8<TI>::store(qo + h * hd, x);
             else if (slot >= 0) Row8<TC>::store(kh < kvh ? kc + kh * a.kv.head_stride : vc + (kh - kvh) * a.kv.head_stride, x);
         }
+        if (U == 1) {
+            load(w, h0 + step);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = next[u];
+        }
     }
 }
 
 template <typename TI>
 static cudaError_t append_from(const AppendArgs &a, int kv_dtype, dim3 grid, int tpc, int per_thread, cudaStream_t st)
 {
-    constexpr int U = 16 / sizeof(TI);
+    constexpr int U = 8 / sizeof(TI);
     const dim3 block(kApThreads);
     auto go = [&](auto to_bf16, auto to_f32) {
         return kv_dtype == DS4G_BF16 ? launch_pdl(to_bf16, grid, block, 0, st, a, tpc)
                                      : launch_pdl(to_f32, grid, block, 0, st, a, tpc);
     };
-    if (per_thread <= 2) return go(k_paged_append<TI, bf16, 1>, k_paged_append<TI, float, 1>);
-    if (per_thread <= U) return go(k_paged_append<TI, bf16, U / 2>, k_paged_append<TI, float, U / 2>);
+    if (per_thread <= 5) return go(k_paged_append<TI, bf16, 1>, k_paged_append<TI, float, 1>);
     return go(k_paged_append<TI, bf16, U>, k_paged_append<TI, float, U>);
 }
 

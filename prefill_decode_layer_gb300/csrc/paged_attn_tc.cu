@@ -71,6 +71,7 @@ struct TcGeometry {
     int slots;
     int box;         // slots of a page in one copy: gcd(page_size, 128)
     int toks;        // tokens of the query box
+    int page_shift;  // log2(page_size), or -1
     // coordinates of (page, head) in the cache's tensor map: 64-dim block head * block, index
     // page * page_mul + head * head_mul; `none` is an index out of bounds
     int block, page_mul, head_mul, none;
@@ -140,7 +141,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_wait();
     pdl_trigger();
     paged_begin(a, lay);
-    paged_cursor<kTcThreads>(a, kTcKeys, &x.cur, x.scratch);
+    const bool few = a.s.n_seqs <= 32;   // the copying warp finds the CTA's share by itself
+    if (!few) paged_cursor<kTcThreads>(a, kTcKeys, &x.cur, x.scratch);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -173,7 +175,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp == kTcTma) {
         // ---------------- items, page look-ups, copies
-        PagedCursor cur = x.cur;
+        PagedCursor cur;
+        if (few) paged_cursor_warp(a, kTcKeys, cur);
+        else cur = x.cur;
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
         };
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 b.load = lane < boxes && j < hi && j + geo.box > lo;
                 int page = -1, slot = 0;
                 if (b.load) {
-                    const int p = j / per_page;
+                    const int p = geo.page_shift >= 0 ? j >> geo.page_shift : j / per_page;
                     slot = j - p * per_page;
                     page = table[p];
                     if (page >= a.kv.n_pages) page = -1;
@@ -393,6 +397,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int k = (int)((s ^ u0) & 1u); k < units; k += 2) {
                 const unsigned u = u0 + k, nth = u >> 1;
                 const int base = (it.t0 + k) * kTcKeys;
+                const int end = min(it.hi - base, kTcKeys);   // columns [beg, end) are the item's keys
+                const int beg = max(it.lo - base, 0);
+                const int q0 = beg >> 5, q1 = (end + 31) >> 5;   // the 32-column parts they lie in
                 ok = ok && warp_wait(&x.s_full[s], nth & 1u);
                 if (ok && active) {
                     tc_fence_after();
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     };
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = q0; q < q1; ++q) {
                         load(q);
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float off = m == -INFINITY ? 0.f : m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = q0; q < q1; ++q) {
                         load(q);
                         uint32_t p[16];
 #pragma unroll
@@ -476,8 +483,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tmem_wait_st();
                 }
                 // ---- V rows of the tile that no row, or not every row, may take as they are
-                const int end = min(it.hi - base, kTcKeys);
-                const int beg = max(it.lo - base, 0);
                 const bool edge = ((beg | end) & 15) != 0 && end > beg;
                 // columns only some rows see: (pos_a, pos_b], and (pos_a - win, pos_b - win]
                 const int h0 = max(pos_a + 1 - base, beg), h1 = min(pos_b + 1 - base, end);
@@ -652,6 +657,9 @@ cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm)
     g.toks = a.rows / a.group;
     g.q_half = (a.rows + 7) / 8 * 8 * 128;
     g.box = gcd(a.kv.page_size, kTcKeys);
+    g.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (1 << i == a.kv.page_size) g.page_shift = i;
     const int tile = halves * kTcKeys * 128, qbytes = 2 * halves * g.q_half;
     g.slots = (kTcSmem - (int)sizeof(TcMisc) - qbytes) / tile;
     if (g.slots > kTcMaxSlots) g.slots = kTcMaxSlots;

@@ -173,6 +173,35 @@ __device__ __forceinline__ void paged_cursor(const AttnArgs &a, int kt, PagedCur
     __syncthreads();
 }
 
+// The same by one warp, for up to 32 sequences (one a lane): no barrier of the CTA lies on the way
+// to its first copy.
+__device__ __forceinline__ void paged_cursor_warp(const AttnArgs &a, int kt, PagedCursor &cur)
+{
+    const int lane = threadIdx.x & 31;
+    SeqWork w;
+    w.units = 0;
+    if (lane < a.s.n_seqs) w = seq_work(a, lane, kt);
+    long long incl = w.units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31);
+    const int g = total < (long long)gridDim.x ? (int)total : (int)gridDim.x, c = (int)blockIdx.x;
+    cur.total = total;
+    cur.at = c < g ? share(total, c, g) : total;
+    cur.end = c < g ? share(total, c + 1, g) : total;
+    cur.ctas = g;
+    const unsigned has = __ballot_sync(0xffffffffu, cur.at < incl);
+    const int src = has ? __ffs(has) - 1 : 0;
+    cur.seq = src;
+    cur.local = (int)(cur.at - __shfl_sync(0xffffffffu, incl - w.units, src));
+    int *words = reinterpret_cast<int *>(&w), *to = reinterpret_cast<int *>(&cur.w);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(SeqWork) / 4); ++i) to[i] = __shfl_sync(0xffffffffu, words[i], src);
+}
+
 // The CTA's next item, one thread.  `cur` is the caller's copy, kept between calls.  Writes
 // the CTA's split record.
 __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCursor &cur, const PartLayout &lay, PagedItem &it)
@@ -194,9 +223,11 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     it.token = w.token;
     it.n_new = w.n_new;
     it.pos0 = w.pos0;
-    it.row0 = (item - it.head * w.row_tiles) * a.rows;
+    it.row0 = w.row_tiles == 1 ? 0 : (item - it.head * w.row_tiles) * a.rows;
     it.n_rows = min(a.rows, w.n_new * a.group - it.row0);
-    const int tok_a = it.row0 / a.group, tok_b = (it.row0 + it.n_rows - 1) / a.group;
+    // (one tile: all new tokens, no division)
+    const int tok_a = w.row_tiles == 1 ? 0 : it.row0 / a.group;
+    const int tok_b = w.row_tiles == 1 ? w.n_new - 1 : (it.row0 + it.n_rows - 1) / a.group;
     it.hi = min(w.hi, w.pos0 + tok_b + 1);
     it.lo = a.window > 0 ? max(w.lo, w.pos0 + tok_a - a.window + 1) : w.lo;
     it.tok_a = tok_a;

@@ -499,8 +499,9 @@ size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_
  * gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
  * (multiples of 16 bytes, 16-byte aligned); dtype: their type.  q and out must not
  * overlap.  max_new <= 128.
- * BF16 queries over a BF16 cache with head_dim 64 or 128, pages of a multiple of 8 slots
- * and at most 128 query heads per K/V head run on the tensor cores, the probabilities
+ * BF16 queries over a BF16 cache with head_dim 64 or 128, pages of a multiple of 8 slots, heads
+ * adjacent within a slot or whole heads within a page, and at most 128 query heads per K/V
+ * head run on the tensor cores, the probabilities
  * rounded to BF16 for the product with V (FP32 sums); every other case runs in FP32.
  * The work is cut over the keys of all sequences by their lengths on the device, and
  * parts of one sequence are joined by a second launch in a fixed order: the same call gives the

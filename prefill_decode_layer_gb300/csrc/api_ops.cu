@@ -124,7 +124,7 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
     if ((double)batch->width * kv->page_size / 64 * ((double)batch->max_new * n_heads / 4 + kv->n_kv_heads) > 2e9)
         return DS4G_EINVAL;
     const int64_t row = (int64_t)n_heads * kv->head_dim;
-    if (!q || !out || !al16(q) || !al16(out) || !stride_ok(q_stride, row, dtype) || !stride_ok(out_stride, row, dtype))
+    if (!q || !out || q == out || !al16(q) || !al16(out) || !stride_ok(q_stride, row, dtype) || !stride_ok(out_stride, row, dtype))
         return DS4G_EINVAL;
     if (!workspace || ((uintptr_t)workspace & 255u)) return DS4G_EINVAL;
     if (workspace_bytes < ds4g_paged_attention_workspace_bytes(kv, batch, n_heads)) return DS4G_ESIZE;

@@ -2,9 +2,38 @@
 // and host-side entry points of their kernel files (internal to the library).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace ds4g {
+
+// What is set once per device (function attributes last as
+// long as the device's context, so one call per kernel and device sets them).  Setting one
+// twice, from two threads, does no harm.
+struct PerDevice {
+    std::atomic<bool> done[64];
+    bool needs(int &dev) const
+    {
+        if (cudaGetDevice(&dev) || dev < 0 || dev >= 64) return dev = -1, true;
+        return !done[dev].load(std::memory_order_acquire);
+    }
+    void set(int dev)
+    {
+        if (dev >= 0) done[dev].store(true, std::memory_order_release);
+    }
+};
+// Let a kernel use `smem` bytes of dynamic shared memory (and clusters of 16), once per device.
+template <typename K> inline cudaError_t allow_once(PerDevice &once, K kernel, size_t smem, bool wide_cluster = false)
+{
+    int dev = -1;
+    if (!once.needs(dev)) return cudaSuccess;
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (!e && wide_cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (!e) once.set(dev);
+    return e;
+}
 
 // A cache's pages, copied into kernel arguments (strides in elements).
 struct PagedKV {

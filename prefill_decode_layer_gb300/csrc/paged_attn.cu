@@ -501,14 +501,13 @@ static cudaError_t simt(AttnArgs &a, int nsm, cudaStream_t st)
 {
     auto kernel = k_paged_attn<TQ, TKV, LPK, D, R, KB>;
     const size_t smem = pa_smem(R, a.kv.head_dim);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e) return e;
-    }
+    static PerDevice once;
+    cudaError_t e = allow_once(once, kernel, pa_smem(R, 256));
+    if (e) return e;
     a.rows = R;
     const int resident = (R * D <= 16 ? 2 : 1) * nsm;
     const int grid = paged_attn_grid(a, kPaKeys, resident < kAttnMaxCtas ? resident : kAttnMaxCtas);
-    cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kPaThreads), smem, st, a);
+    e = launch_pdl(kernel, dim3(grid), dim3(kPaThreads), smem, st, a);
     if (!e && !a.whole) e = join<TQ, kAttnRowsSimt, kAttnMaxCtas>(a, grid, nsm, st);
     return e;
 }

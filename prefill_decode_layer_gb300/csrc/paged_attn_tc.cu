@@ -684,8 +684,9 @@ cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm)
     if (!e) e = tc::make_map_bf16_nd(&vm, a.kv.v, 5, cd, cs, cb);
     if (e) return e;
     const int grid = paged_attn_grid(a, kTcKeys, nsm < kAttnMaxCtasTc ? nsm : kAttnMaxCtasTc);
+    static PerDevice once[2];
     auto kernel = hd == 64 ? k_paged_attn_tc<64> : k_paged_attn_tc<128>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    e = allow_once(once[hd == 64], kernel, kTcSmem);
     if (!e) e = launch_pdl(kernel, dim3(grid), dim3(kTcThreads), (size_t)smem, st, qm, km, vm, a, g);
     if (!e && !a.whole) e = paged_join_tc(a, grid, nsm, st);
     return e;

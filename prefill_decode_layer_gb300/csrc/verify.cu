@@ -365,13 +365,11 @@ static int row_cluster(int n, int rows, int few)
 static int row_chunk(int n, int c) { return ((n + c - 1) / c + 3) & ~3; }
 
 template <typename A>
-static cudaError_t launch_rows(void (*kernel)(A), int clusters, int cluster, int threads, size_t smem, cudaStream_t st,
-                               const A &a)
+static cudaError_t launch_rows(PerDevice &once, void (*kernel)(A), int clusters, int cluster, int threads, size_t smem,
+                               cudaStream_t st, const A &a)
 {
-    cudaError_t e = cudaSuccess;
-    if (cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (!e && smem > 48 * 1024)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the largest buffer that any row takes, and clusters of 16)
+    const cudaError_t e = allow_once(once, kernel, smem ? kRowHold * kRowTile * 4 : 0, true);
     if (e) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)clusters * cluster);
@@ -441,10 +439,12 @@ cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float
     if (vec && a.chunk <= kRowHold * kRowTile) {
         // more rows than the GPU holds clusters take turns
         const int most = probs_resident(c, nsm);
-        return launch_rows(k_probs, rows < most ? rows : most, c, kRowThreads, (size_t)a.chunk * 4, st, a);
+        static PerDevice once;
+        return launch_rows(once, k_probs, rows < most ? rows : most, c, kRowThreads, (size_t)a.chunk * 4, st, a);
     }
-    return vec ? launch_rows(k_probs_any<true>, rows, c, kRowThreads, 0, st, a)
-               : launch_rows(k_probs_any<false>, rows, c, kRowThreads, 0, st, a);
+    static PerDevice once[2];
+    return vec ? launch_rows(once[1], k_probs_any<true>, rows, c, kRowThreads, 0, st, a)
+               : launch_rows(once[0], k_probs_any<false>, rows, c, kRowThreads, 0, st, a);
 }
 
 // ------------------------------------------------------------------ verification
@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
     pdl_trigger();
 
     // ---- the accepted drafts
-    const int nd = a.n_drafts ? min(max(a.n_drafts[b], 0), D) : D;
+    // (a draft is looked up whether or not the count, which comes with it, includes it)
+    const int asked = a.n_drafts ? a.n_drafts[b] : D;
     const int *drafts = a.drafts + (long long)b * D;
     const unsigned *u24 = a.u24 + (long long)b * (D + 1);
     const float *pseq = a.p + (long long)b * a.ps;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
     if (threadIdx.x < kMaxDrafts) {
         const int i = threadIdx.x;
         bool ok = false;
-        if (i < nd) {
+        if (i < D) {
             const int d = drafts[i];
             if (d >= 0 && d < a.n) {
                 const float pd = unit_prob(pseq[i * a.pstride + d]);
@@ -507,6 +508,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
         if (lane == 0) s_ok[warp] = m;
     }
     __syncthreads();
+    const int nd = min(max(asked, 0), D);
     int k = 0;
     while (k < nd && (s_ok[k >> 5] >> (k & 31) & 1u)) ++k;
     const bool rejected = k < nd;
@@ -635,12 +637,13 @@ cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st, int ns
     const VerifyKArgs ka = {a, row_chunk(a.n, c)};
     bool vec = vec_ok(a.p, a.ps) && vec_ok(a.p, a.pstride);
     if (a.q) vec = vec && vec_ok(a.q, a.qs) && vec_ok(a.q, a.qstride);
-    const bool few = n_seqs * c <= nsm;
+    const bool few = (long long)n_seqs * c <= nsm;
+    static PerDevice once[4];
     if (few)
-        return vec ? launch_rows(k_verify<true, 512>, n_seqs, c, 512, 0, st, ka)
-                   : launch_rows(k_verify<false, 512>, n_seqs, c, 512, 0, st, ka);
-    return vec ? launch_rows(k_verify<true, 256>, n_seqs, c, 256, 0, st, ka)
-               : launch_rows(k_verify<false, 256>, n_seqs, c, 256, 0, st, ka);
+        return vec ? launch_rows(once[0], k_verify<true, 512>, n_seqs, c, 512, 0, st, ka)
+                   : launch_rows(once[1], k_verify<false, 512>, n_seqs, c, 512, 0, st, ka);
+    return vec ? launch_rows(once[2], k_verify<true, 256>, n_seqs, c, 256, 0, st, ka)
+               : launch_rows(once[3], k_verify<false, 256>, n_seqs, c, 256, 0, st, ka);
 }
 
 }  // namespace ds4g

@@ -413,7 +413,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _call(name: str, index: int, stream, *args) -> None:
     """One call of the library on CUDA device `index`, on `stream` (None: that device's
     current stream)."""
-    _require(index >= 0, name)
+    if index < 0:   # a CPU tensor
+        raise Ds4gError(EINVAL, name)
     f = getattr(_lib or lib(), name)
     st = _raw_stream(index) if stream is None else stream.cuda_stream
     if index == torch.cuda.current_device():
@@ -450,7 +451,8 @@ class PagedBatch:
                  max_new: int = 1):
         n = length.numel()
         _require(table.dim() == 2 and table.shape[0] == n and table.dtype == torch.int32 and
-                 (table.shape[1] <= 1 or table.stride(1) == 1) and length.dtype == torch.int32 and
+                 (table.shape[1] <= 1 or table.stride(1) == 1) and
+                 (n <= 1 or table.stride(0) >= table.shape[1]) and length.dtype == torch.int32 and
                  length.is_contiguous() and table.device == length.device, "PagedBatch")
         _require(start is None or (start.dtype == torch.int32 and start.numel() == n + 1 and
                                    start.is_contiguous() and start.device == length.device), "PagedBatch")
@@ -458,7 +460,7 @@ class PagedBatch:
         width = table.shape[1]
         self.struct = PagedBatchStruct(table.data_ptr(), length.data_ptr(),
                                        start.data_ptr() if start is not None else None, n, n, max_new,
-                                       width, max(table.stride(0), width) if n > 1 else width)
+                                       width, table.stride(0) if n > 1 else width)
         self.ref = C.addressof(self.struct)
 
 
@@ -558,19 +560,27 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor | None, drafts: torch.Tensor, 
     """ds4g_verify_draft: p [n_seqs][max_drafts + 1][n_vocab] and q [n_seqs][max_drafts][n_vocab]
     (or None) f32; drafts [n_seqs][max_drafts], u24 [n_seqs][max_drafts + 1], accepted [n_seqs], tokens
     [n_seqs][max_drafts + 1] and n_drafts [n_seqs] (or None) int32."""
-    shape, what, index = p.shape, "verify_draft", p.get_device()
+    shape, what, index, i32 = p.shape, "verify_draft", p.get_device(), torch.int32
     _require(len(shape) == 3 and p.dtype is torch.float32, what)
     b, d1, v = shape
     d = d1 - 1
-
-    def ints(t, *shape):
-        if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == index):
-            raise Ds4gError(EINVAL, what)
-        return t.data_ptr()
+    per_draft, per_number = (b, d), (b, d1)
+    if not (drafts.dtype is i32 and drafts.shape == per_draft and drafts.is_contiguous() and
+            u24.dtype is i32 and u24.shape == per_number and u24.is_contiguous() and
+            tokens.dtype is i32 and tokens.shape == per_number and tokens.is_contiguous() and
+            accepted.dtype is i32 and accepted.shape == (b,) and accepted.is_contiguous() and
+            drafts.get_device() == u24.get_device() == tokens.get_device() == accepted.get_device() == index):
+        raise Ds4gError(EINVAL, what)
+    n_ptr = None
+    if n_drafts is not None:
+        _require(n_drafts.dtype is i32 and n_drafts.shape == (b,) and n_drafts.is_contiguous() and
+                 n_drafts.get_device() == index, what)
+        n_ptr = n_drafts.data_ptr()
 
     def strides(t, rows):   # of a sequence and of a position; a dimension of one element has any stride
         s = t.stride()
-        _require(v <= 1 or s[2] == 1, what)
+        if not (v <= 1 or s[2] == 1):
+            raise Ds4gError(EINVAL, what)
         pos = s[1] if rows > 1 else v
         return (s[0] if b > 1 else max(v, rows * pos)), pos
 
@@ -580,6 +590,5 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor | None, drafts: torch.Tensor, 
         _require(q.dtype is torch.float32 and q.shape == (b, d, v) and q.get_device() == index, what)
         qa = q.data_ptr()
         qs, qp = strides(q, d)
-    _call("ds4g_verify_draft", index, stream, p.data_ptr(), ps, pp, qa, qs, qp, ints(drafts, b, d),
-          ints(n_drafts, b) if n_drafts is not None else None, ints(u24, b, d1), b, d, v, ints(accepted, b),
-          ints(tokens, b, d1))
+    _call("ds4g_verify_draft", index, stream, p.data_ptr(), ps, pp, qa, qs, qp, drafts.data_ptr(), n_ptr,
+          u24.data_ptr(), b, d, v, accepted.data_ptr(), tokens.data_ptr())

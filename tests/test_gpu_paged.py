@@ -154,7 +154,8 @@ LENGTHS = [1, 127, 128, 129, 5, 640, 0, 64, 255, 1000]
 @pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F32, F32), (F32, BF16), (BF16, F32)])
 @pytest.mark.parametrize("kv_heads,heads,dim,page", [(1, 64, 128, 64), (8, 32, 128, 16), (2, 8, 64, 48), (4, 4, 64, 8),
                                                      (1, 128, 128, 128), (3, 15, 128, 24), (1, 8, 32, 16),
-                                                     (2, 6, 40, 7), (1, 3, 256, 1), (2, 10, 96, 32)])
+                                                     (2, 6, 40, 7), (1, 3, 256, 1), (2, 10, 96, 32), (2, 16, 128, 256),
+                                                     (2, 8, 64, 192)])
 def test_attention_one_token(dtype, cache, kv_heads, heads, dim, page):
     p = paged_inputs(LENGTHS, [1] * len(LENGTHS), kv_heads, dim, page, cache, seed=dim + heads)
     fill_slots(p, seed=2)

@@ -75,7 +75,7 @@ def test_attention_refuses(lib):
     assert attention(lib, None, b) == EINVAL and attention(lib, kv, None) == EINVAL
     for bad in (dict(q=None), dict(q=8), dict(out=None), dict(out=4100), dict(qs=511), dict(os=64), dict(heads=0),
                 dict(heads=7), dict(dtype=9), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-1.0), dict(ws=None),
-                dict(ws=4096 + 128)):
+                dict(ws=4096 + 128), dict(out=4096)):
         assert attention(lib, kv, b, **bad) == EINVAL, bad
     assert attention(lib, kv, b, n=need - 1) == ESIZE
     assert lib.ds4g_paged_attention_status(None, None) == EINVAL
@@ -120,7 +120,7 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         with pytest.raises(E):
             pdl.PagedKV(a, b)
     for args in ((table.long(), length), (table, length.long()), (table[:2], length), (table, length, length),
-                 (table.t().contiguous().t(), length), (table, torch.zeros(6, dtype=torch.int32)[::2])):
+                 (table.t().contiguous().t(), length), (table[:1].expand(3, 2), length), (table, torch.zeros(6, dtype=torch.int32)[::2])):
         with pytest.raises(E):
             pdl.PagedBatch(*args)
     with pytest.raises(E):

@@ -210,7 +210,7 @@ cudaError_t paged_append(const AppendArgs &a, int in_dtype, int kv_dtype, cudaSt
     while (tpc < kApTokens && a.s.n_tokens / (2 * tpc) >= 4 * nsm) tpc *= 2;
     const int gx = (a.s.n_tokens + tpc - 1) / tpc;
     int gy = 1;
-    while ((long long)gx * gy < 8 * nsm && gy * groups < heads * tpc) ++gy;
+    while ((long long)gx * gy < 4 * nsm && gy * groups < heads * tpc) ++gy;
     const int per_thread = (heads * tpc + groups * gy - 1) / (groups * gy);
     return in_dtype == DS4G_BF16 ? append_from<bf16>(a, kv_dtype, dim3(gx, gy), tpc, per_thread, st)
                                  : append_from<float>(a, kv_dtype, dim3(gx, gy), tpc, per_thread, st);

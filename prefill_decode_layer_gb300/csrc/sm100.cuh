@@ -94,6 +94,32 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Store 8 bytes into the shared memory of any CTA of the cluster (`dst`, `bar`: shared::cluster
+// addresses in that CTA), counted as 8 bytes on its mbarrier.  Unlike a cluster barrier it orders
+// nothing else: the thread's global stores need not have landed.
+__device__ __forceinline__ void st_async_u64(uint32_t dst, unsigned long long v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(dst), "l"(v),
+                 "r"(bar)
+                 : "memory");
+}
+// mbar_wait for data that other CTAs of the cluster stored.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *b, uint32_t parity)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(b)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > kWaitCycles) return false;
+    }
+}
+
 // ------------------------------------------------------------------ bulk and tensor copies
 
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar,

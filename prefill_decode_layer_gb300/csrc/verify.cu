@@ -130,9 +130,10 @@ __device__ __forceinline__ float rebase(float m, float M, float c_hi, float c_lo
 __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant__ ProbsArgs a)
 {
     extern __shared__ __align__(16) float s_x[];   // the chunk: logits, then weights
-    __shared__ float2 s_red[kRowWarps], s_ms[2];
-    __shared__ unsigned long long s_red64[kRowWarps], s_key[2];
-    __shared__ uint64_t s_bar;
+    __shared__ float2 s_red[kRowWarps];
+    __shared__ unsigned long long s_red64[kRowWarps];
+    __shared__ unsigned long long s_all[2][8];   // what every CTA of the cluster has found, by row parity
+    __shared__ uint64_t s_bar, s_all_bar[2];
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = (int)rank * a.chunk, len = min(a.n, c0 + a.chunk) - c0;   // (len <= 0: a CTA without tokens)
@@ -141,9 +142,11 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
     constexpr int kBatch = kRowHold / 2;   // vectors a thread holds at a time
     if (threadIdx.x == 0) {
         mbar_init(&s_bar, 1);
+        mbar_init(&s_all_bar[0], 1);
+        mbar_init(&s_all_bar[1], 1);
         mbar_fence_init();
     }
-    __syncthreads();
+    cluster_sync_all();   // the barriers exist in every CTA
     pdl_wait();
     pdl_trigger();
     auto fetch = [&](int row) {   // thread 0
@@ -153,11 +156,24 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
     int row = blockIdx.x / size;
     if (threadIdx.x == 0 && row < a.rows) fetch(row);
     volatile int never = 0;
+    // Warp 0 sends the CTA's word of this row to every CTA of the cluster; each thread returns
+    // with word `lane` of the cluster's.  (A cluster barrier in its place waits for the stores of
+    // the row before.)  A row's words are overwritten two rows later, by CTAs that have all words
+    // of the row between, which this CTA sends after its threads have read these.
+    auto exchange = [&](unsigned long long mine, int turn, bool &landed) {
+        const int par = turn & 1;
+        if (warp == 0) {
+            if (lane == 0) mbar_expect_tx(&s_all_bar[par], size * 8);
+            if (lane < (int)size)
+                st_async_u64(cluster_map(&s_all[par][rank], lane), mine, cluster_map(&s_all_bar[par], lane));
+        }
+        landed = mbar_wait_cluster(&s_all_bar[par], (turn >> 1) & 1u) && landed;
+        return lane < (int)size ? s_all[par][lane] : 0ull;
+    };
     for (int turn = 0; row < a.rows; row += clusters, ++turn) {
         const float *z = a.z + row * a.zs + c0;
         float *p = a.p + row * a.ps + c0;
-        const int par = turn & 1;   // a row's shared pair is read by the others until the next row's exists
-        const bool landed = mbar_wait(&s_bar, turn & 1u, &never);   // if the wait gave up, the row becomes NaN
+        bool landed = mbar_wait(&s_bar, turn & 1u, &never);   // if the wait gave up, the row becomes NaN
         auto load4 = [&](int i) {   // the last one to three tokens of a row are not part of the copy
             return i + 3 < bulk ? *reinterpret_cast<const float4 *>(s_x + i) : row_load4<false>(z, i, len, -INFINITY);
         };
@@ -176,13 +192,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
             if (lane == 0) s_red64[warp] = best;
             __syncthreads();   // (also: the buffer is free)
             if (threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
-            if (warp == 0) {
-                best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
-                if (lane == 0) s_key[par] = best;
-            }
-            cluster_sync_all();   // (in place: every CTA has read its part of the row)
-            best = lane < (int)size ? ld_cluster_u64(&s_key[par], lane) : 0ull;
-            const int win = key_id(warp_max64(best)) - c0;
+            if (warp == 0) best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
+            const int win = key_id(warp_max64(exchange(best, turn, landed))) - c0;
 #pragma unroll
             for (int j = 0; j < kRowHold; ++j)
                 if (at(j) < len)
@@ -230,14 +241,11 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
             const float2 v = lane < kRowWarps ? s_red[lane] : make_float2(-INFINITY, 0.f);
             M = warp_max(v.x);
             ws = warp_sum(v.y * rebase(v.x, M, a.c_hi, a.c_lo));
-            if (lane == 0) s_ms[par] = make_float2(M, ws);
         }
-        cluster_sync_all();
-        float2 v = make_float2(-INFINITY, 0.f);
-        if (lane < (int)size) {
-            const unsigned long long w = ld_cluster_u64(reinterpret_cast<const unsigned long long *>(&s_ms[par]), lane);
-            v = make_float2(__uint_as_float((unsigned)w), __uint_as_float((unsigned)(w >> 32)));
-        }
+        const unsigned long long word =
+            exchange((unsigned long long)__float_as_uint(ws) << 32 | __float_as_uint(M), turn, landed);
+        const float2 v = lane < (int)size ? make_float2(__uint_as_float((unsigned)word), __uint_as_float((unsigned)(word >> 32)))
+                                          : make_float2(-INFINITY, 0.f);
         M = warp_max(v.x);
         const float total = warp_sum(v.y * rebase(v.x, M, a.c_hi, a.c_lo));
         const float inv = !landed ? NAN : total > 0.f ? 1.f / total : 0.f;
@@ -352,12 +360,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
     cluster_sync_all();   // no CTA leaves while another may still read its shared memory
 }
 
-// CTAs of a row's cluster: as many as keep 2048 tokens each, at most 8, or 16 (more than the
-// portable size) for up to `few` rows: one verification of 129280 tokens takes 7.9 us on 16
-// CTAs and 9.5 on 8, nine take 10.4 and 9.7; a row of probabilities is no faster on 16.
-static int row_cluster(int n, int rows, int few)
+// CTAs of a row's cluster.  Probabilities: as few as hold the row, doubled while the rows leave
+// SMs idle and 2048 tokens a CTA remain (4000 rows of 10000 tokens run 2.4 times as fast on one
+// CTA each as on four).  Verification: as many as keep 2048 tokens each, at most 8, or 16 (more
+// than the portable size) for up to four sequences: one of 129280 tokens takes 7.9 us on 16
+// CTAs and 9.5 on 8, nine take 10.4 and 9.7.
+static int probs_cluster(int n, int rows, int nsm)
 {
-    const int most = rows <= few ? kMaxCluster : 8;
+    int c = 1;
+    while (c < 8 && n > c * kRowHold * kRowTile) c *= 2;
+    while (c < 8 && n >= 2 * c * kRowTile && (long long)rows * c < nsm) c *= 2;
+    return c;
+}
+static int verify_cluster(int n, int seqs)
+{
+    const int most = seqs <= 4 ? kMaxCluster : 8;
     int c = 1;
     while (c < most && n >= 2 * c * kRowTile) c *= 2;
     return c;
@@ -428,7 +445,7 @@ cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float
                        long long os, cudaStream_t st, int nsm)
 {
     if (rows == 0) return cudaSuccess;
-    const int c = row_cluster(n, rows, 0);
+    const int c = probs_cluster(n, rows, nsm);
     ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), rows, 0.f, 0.f, temperature <= 0.f};
     if (!a.greedy) {
         const double cc = 1.4426950408889634 / (double)temperature;
@@ -633,7 +650,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
 cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st, int nsm)
 {
     if (n_seqs == 0) return cudaSuccess;
-    const int c = row_cluster(a.n, n_seqs, 4);
+    const int c = verify_cluster(a.n, n_seqs);
     const VerifyKArgs ka = {a, row_chunk(a.n, c)};
     bool vec = vec_ok(a.p, a.ps) && vec_ok(a.p, a.pstride);
     if (a.q) vec = vec && vec_ok(a.q, a.qs) && vec_ok(a.q, a.qstride);

@@ -55,24 +55,36 @@ __device__ __forceinline__ uint32_t cluster_size()
     return r;
 }
 
-// Values i .. i + 3 of a row of n (absent ones: `none`).
-template <bool VEC>
-__device__ __forceinline__ float4 row_load4(const float *row, int i, int n, float none)
+// A warp's 128 consecutive tokens from t0, four per lane: adjacent ones where the row is 16-byte
+// aligned (VEC), else every 32nd, so that a warp's loads and stores stay whole lines.
+template <bool VEC> __device__ __forceinline__ int row_token(int t0, int lane, int e)
 {
-    if (VEC && i + 3 < n) return *reinterpret_cast<const float4 *>(row + i);
-    return make_float4(i < n ? row[i] : none, i + 1 < n ? row[i + 1] : none, i + 2 < n ? row[i + 2] : none,
-                       i + 3 < n ? row[i + 3] : none);
+    return VEC ? t0 + 4 * lane + e : t0 + 32 * e + lane;
 }
-template <bool VEC> __device__ __forceinline__ void row_store4(float *row, int i, int n, const float4 &v)
+// This lane's four of them, of a row of n (absent ones: `none`).
+template <bool VEC> __device__ __forceinline__ float4 row_load4(const float *row, int t0, int lane, int n, float none)
 {
-    if (VEC && i + 3 < n) {
-        *reinterpret_cast<float4 *>(row + i) = v;
+    if (VEC && t0 + 4 * lane + 3 < n) return *reinterpret_cast<const float4 *>(row + t0 + 4 * lane);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = row_token<VEC>(t0, lane, e);
+        v[e] = i < n ? row[i] : none;
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+template <bool VEC> __device__ __forceinline__ void row_store4(float *row, int t0, int lane, int n, const float4 &x)
+{
+    if (VEC && t0 + 4 * lane + 3 < n) {
+        *reinterpret_cast<float4 *>(row + t0 + 4 * lane) = x;
         return;
     }
-    if (i < n) row[i] = v.x;
-    if (i + 1 < n) row[i + 1] = v.y;
-    if (i + 2 < n) row[i + 2] = v.z;
-    if (i + 3 < n) row[i + 3] = v.w;
+    const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = row_token<VEC>(t0, lane, e);
+        if (i < n) row[i] = v[e];
+    }
 }
 
 // 2^((z - m) c), c = c_hi + c_lo.  The rounding of the product is carried to the result, so
@@ -110,11 +122,16 @@ __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v)
     for (int o = 16; o > 0; o >>= 1) v = max64(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// Values i .. i + 3 of the row that is 1 at id `win`.
-__device__ __forceinline__ float4 one_hot4(int i, int win)
+// Values i, i + step, .. of the row that is 1 at id `win`.
+__device__ __forceinline__ float4 one_hot4(int i, int step, int win)
 {
-    return make_float4(i == win ? 1.f : 0.f, i + 1 == win ? 1.f : 0.f, i + 2 == win ? 1.f : 0.f,
-                       i + 3 == win ? 1.f : 0.f);
+    return make_float4(i == win ? 1.f : 0.f, i + step == win ? 1.f : 0.f, i + 2 * step == win ? 1.f : 0.f,
+                       i + 3 * step == win ? 1.f : 0.f);
+}
+__device__ __forceinline__ unsigned long long arg_key4(const float4 &v, int i, int step)
+{
+    return max64(max64(arg_key(v.x, i), arg_key(v.y, i + step)),
+                 max64(arg_key(v.z, i + 2 * step), arg_key(v.w, i + 3 * step)));
 }
 __device__ __forceinline__ int key_id(unsigned long long k) { return k ? (int)(0xffffffffu - (unsigned)(k & 0xffffffffull)) : -1; }
 
@@ -125,8 +142,10 @@ __device__ __forceinline__ float rebase(float m, float M, float c_hi, float c_lo
     return m == M ? 1.f : exp_scaled(m, M, c_hi, c_lo);
 }
 
-// Rows 16-byte aligned, chunks of at most kRowHold rounds: cluster i of the grid takes rows i,
-// i + clusters, ..
+// Chunks of at most kRowHold rounds; cluster i of the grid takes rows i, i + clusters, ..  A row
+// that begins `mis` floats behind a 16-byte boundary (as the rows of an odd vocabulary do) is taken
+// as one that begins at the boundary, whose first `mis` values are not there; its result
+// begins as far behind one.
 __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant__ ProbsArgs a)
 {
     extern __shared__ __align__(16) float s_x[];   // the chunk: logits, then weights
@@ -136,8 +155,23 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
     __shared__ uint64_t s_bar, s_all_bar[2];
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = (int)rank * a.chunk, len = min(a.n, c0 + a.chunk) - c0;   // (len <= 0: a CTA without tokens)
-    const int bulk = max(len, 0) & ~3;                                       // what the copy brings
+    const int c0 = (int)rank * a.chunk;
+    // of this CTA's chunk of a row: values [lo, len) are there, [bf, be) comes by the copy
+    struct Span {
+        const float *z;   // the chunk, 16-byte aligned
+        int mis, lo, len, bf, be;
+    };
+    auto span = [&](int row) {
+        Span s;
+        const float *z = a.z + row * a.zs;
+        s.mis = (int)((uintptr_t)z >> 2 & 3u);
+        s.z = z - s.mis + c0;
+        s.lo = max(s.mis - c0, 0);
+        s.len = min(a.n + s.mis - c0, a.chunk);   // (none: a CTA without tokens)
+        s.bf = (s.lo + 3) & ~3;
+        s.be = max(s.len, 0) & ~3;
+        return s;
+    };
     const int clusters = gridDim.x / size;
     constexpr int kBatch = kRowHold / 2;   // vectors a thread holds at a time
     if (threadIdx.x == 0) {
@@ -150,8 +184,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
     pdl_wait();
     pdl_trigger();
     auto fetch = [&](int row) {   // thread 0
-        mbar_expect_tx(&s_bar, (uint32_t)bulk * 4);
-        if (bulk) bulk_g2s(s_x, a.z + row * a.zs + c0, (uint32_t)bulk * 4, &s_bar, policy_evict_first());
+        const Span s = span(row);
+        const int n = max(s.be - s.bf, 0);
+        mbar_expect_tx(&s_bar, (uint32_t)n * 4);
+        if (n) bulk_g2s(s_x + s.bf, s.z + s.bf, (uint32_t)n * 4, &s_bar, policy_evict_first());
     };
     int row = blockIdx.x / size;
     if (threadIdx.x == 0 && row < a.rows) fetch(row);
@@ -171,11 +207,26 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
         return lane < (int)size ? s_all[par][lane] : 0ull;
     };
     for (int turn = 0; row < a.rows; row += clusters, ++turn) {
-        const float *z = a.z + row * a.zs + c0;
-        float *p = a.p + row * a.ps + c0;
+        const Span sp = span(row);
+        const int lo = sp.lo, len = sp.len, id0 = c0 - sp.mis;   // id of the chunk's value 0
+        float *p = a.p + row * a.ps + id0;
         bool landed = mbar_wait(&s_bar, turn & 1u, &never);   // if the wait gave up, the row becomes NaN
-        auto load4 = [&](int i) {   // the last one to three tokens of a row are not part of the copy
-            return i + 3 < bulk ? *reinterpret_cast<const float4 *>(s_x + i) : row_load4<false>(z, i, len, -INFINITY);
+        auto load4 = [&](int i) {   // (values that the copy does not bring: at most three at each end of a row)
+            if (i >= sp.bf && i < sp.be) return *reinterpret_cast<const float4 *>(s_x + i);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = i + e >= lo && i + e < len ? sp.z[i + e] : -INFINITY;
+            return make_float4(v[0], v[1], v[2], v[3]);
+        };
+        auto store4 = [&](int i, const float4 &x) {
+            if (i >= lo && i + 3 < len) {
+                *reinterpret_cast<float4 *>(p + i) = x;
+                return;
+            }
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e >= lo && i + e < len) p[i + e] = v[e];
         };
         auto at = [&](int j) { return (j * kRowThreads + (int)threadIdx.x) * 4; };
         if (a.greedy) {   // one at the largest logit, lowest id on ties
@@ -185,19 +236,18 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
                 const int i = at(j);
                 if (i >= len) break;
                 const float4 v = load4(i);
-                best = max64(best, max64(max64(arg_key(v.x, c0 + i), arg_key(v.y, c0 + i + 1)),
-                                         max64(arg_key(v.z, c0 + i + 2), arg_key(v.w, c0 + i + 3))));
+                best = max64(best, arg_key4(v, id0 + i, 1));
             }
             best = warp_max64(best);
             if (lane == 0) s_red64[warp] = best;
             __syncthreads();   // (also: the buffer is free)
             if (threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
             if (warp == 0) best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
-            const int win = key_id(warp_max64(exchange(best, turn, landed))) - c0;
+            const int win = key_id(warp_max64(exchange(best, turn, landed))) - id0;   // (none: below 0, or a value that is not there)
 #pragma unroll
             for (int j = 0; j < kRowHold; ++j)
                 if (at(j) < len)
-                    row_store4<true>(p, at(j), len, landed ? one_hot4(at(j), win) : make_float4(NAN, NAN, NAN, NAN));
+                    store4(at(j), landed ? one_hot4(at(j), 1, win) : make_float4(NAN, NAN, NAN, NAN));
             continue;
         }
         // ---- weights against the maximum of each batch of the thread
@@ -256,7 +306,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
             if (i >= len) break;
             const float4 w = *reinterpret_cast<const float4 *>(s_x + i);
             const float g = f[j / kBatch];
-            row_store4<true>(p, i, len, make_float4(w.x * g, w.y * g, w.z * g, w.w * g));
+            store4(i, make_float4(w.x * g, w.y * g, w.z * g, w.w * g));
         }
         fence_proxy_async_smem();   // this thread's accesses of the buffer, before the next copy's
         __syncthreads();
@@ -280,19 +330,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
     float *p = a.p + row * a.ps;
     pdl_wait();
     pdl_trigger();
-    auto at = [&](int j) { return c0 + (j * kRowThreads + (int)threadIdx.x) * 4; };
+    auto at = [&](int j) { return c0 + (j * kRowThreads + 32 * warp) * 4; };   // the warp's 128 tokens of round j
     float4 x[kRowHold];
 #pragma unroll
-    for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), c1, -INFINITY);
+    for (int j = 0; j < kRowHold; ++j) x[j] = row_load4<VEC>(z, at(j), lane, c1, -INFINITY);
     if (a.greedy) {
         unsigned long long best = 0ull;
-        auto look4 = [&](const float4 &v, int i) {   // (absent tokens are -inf)
-            best = max64(best, max64(max64(arg_key(v.x, i), arg_key(v.y, i + 1)),
-                                     max64(arg_key(v.z, i + 2), arg_key(v.w, i + 3))));
+        auto look4 = [&](const float4 &v, int t0) {   // (absent tokens are -inf)
+            best = max64(best, arg_key4(v, row_token<VEC>(t0, lane, 0), VEC ? 1 : 32));
         };
 #pragma unroll
         for (int j = 0; j < kRowHold; ++j) look4(x[j], at(j));
-        for (int j = kRowHold; j < rounds; ++j) look4(row_load4<VEC>(z, at(j), c1, -INFINITY), at(j));
+        for (int j = kRowHold; j < rounds; ++j) look4(row_load4<VEC>(z, at(j), lane, c1, -INFINITY), at(j));
         best = warp_max64(best);
         if (lane == 0) s_red64[warp] = best;
         __syncthreads();
@@ -302,7 +351,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
         }
         cluster_sync_all();   // (in place: every CTA has read its part of the row)
         const int win = key_id(warp_max64(lane < (int)size ? ld_cluster_u64(&s_key, lane) : 0ull));
-        for (int j = 0; j < rounds; ++j) row_store4<VEC>(p, at(j), c1, one_hot4(at(j), win));
+        for (int j = 0; j < rounds; ++j)
+            row_store4<VEC>(p, at(j), lane, c1, one_hot4(row_token<VEC>(at(j), lane, 0), VEC ? 1 : 32, win));
         cluster_sync_all();   // no CTA leaves while another may still read its shared memory
         return;
     }
@@ -310,7 +360,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
 #pragma unroll
     for (int j = 0; j < kRowHold; ++j) mx = fmaxf(fmaxf(mx, fmaxf(x[j].x, x[j].y)), fmaxf(x[j].z, x[j].w));
     for (int j = kRowHold; j < rounds; ++j) {
-        const float4 v = row_load4<VEC>(z, at(j), c1, -INFINITY);
+        const float4 v = row_load4<VEC>(z, at(j), lane, c1, -INFINITY);
         mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
     }
     mx = warp_max(mx);
@@ -338,7 +388,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
         sum += (x[j].x + x[j].y) + (x[j].z + x[j].w);
     }
     for (int j = kRowHold; j < rounds; ++j) {
-        const float4 v = weight4(row_load4<VEC>(z, at(j), c1, -INFINITY));
+        const float4 v = weight4(row_load4<VEC>(z, at(j), lane, c1, -INFINITY));
         sum += (v.x + v.y) + (v.z + v.w);
     }
     sum = warp_sum(sum);
@@ -352,11 +402,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
     sum = warp_sum(lane < (int)size ? ld_cluster_f32(&s_sum, lane) : 0.f);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     auto store = [&](int j, const float4 &v) {
-        row_store4<VEC>(p, at(j), c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        row_store4<VEC>(p, at(j), lane, c1, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
     };
 #pragma unroll
     for (int j = 0; j < kRowHold; ++j) store(j, x[j]);
-    for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), c1, -INFINITY)));
+    for (int j = kRowHold; j < rounds; ++j) store(j, weight4(row_load4<VEC>(z, at(j), lane, c1, -INFINITY)));
     cluster_sync_all();   // no CTA leaves while another may still read its shared memory
 }
 
@@ -445,21 +495,24 @@ cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float
                        long long os, cudaStream_t st, int nsm)
 {
     if (rows == 0) return cudaSuccess;
-    const int c = probs_cluster(n, rows, nsm);
-    ProbsArgs a = {logits, out, ls, os, n, row_chunk(n, c), rows, 0.f, 0.f, temperature <= 0.f};
+    // rows that begin anywhere need up to three values more
+    const bool vec = vec_ok(logits, ls) && vec_ok(out, os);
+    const bool alike = (((uintptr_t)logits ^ (uintptr_t)out) & 15u) == 0 && ((ls ^ os) & 3) == 0;
+    const int room = vec ? n : n + 3, c = probs_cluster(room, rows, nsm);
+    ProbsArgs a = {logits, out, ls, os, n, row_chunk(room, c), rows, 0.f, 0.f, temperature <= 0.f};
     if (!a.greedy) {
         const double cc = 1.4426950408889634 / (double)temperature;
         a.c_hi = (float)(cc < 3e38 ? cc : 3e38);
         a.c_lo = cc < 3e38 ? (float)(cc - (double)a.c_hi) : 0.f;
     }
-    const bool vec = vec_ok(logits, ls) && vec_ok(out, os);
-    if (vec && a.chunk <= kRowHold * kRowTile) {
+    if (alike && a.chunk <= kRowHold * kRowTile) {
         // more rows than the GPU holds clusters take turns
-        const int most = probs_resident(c, nsm);
         static PerDevice once;
+        const int most = probs_resident(c, nsm);
         return launch_rows(once, k_probs, rows < most ? rows : most, c, kRowThreads, (size_t)a.chunk * 4, st, a);
     }
     static PerDevice once[2];
+    a.chunk = row_chunk(n, c);
     return vec ? launch_rows(once[1], k_probs_any<true>, rows, c, kRowThreads, 0, st, a)
                : launch_rows(once[0], k_probs_any<false>, rows, c, kRowThreads, 0, st, a);
 }
@@ -536,14 +589,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
     // ---- the weights of tokens i .. i + 3 as integers; alone: those of p
     const int c0 = (int)rank * args.chunk, c1 = min(a.n, c0 + args.chunk);
     const int rounds = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0;
-    auto weights4 = [&](const float4 &p, const float4 &q, int i, bool alone, unsigned (&hi)[4], unsigned (&lo)[4]) {
+    // (t0: the warp's 128 tokens)
+    auto weights4 = [&](const float4 &p, const float4 &q, int t0, bool alone, unsigned (&hi)[4], unsigned (&lo)[4]) {
         const float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float v = unit_prob(pv[e]);
             if (!alone) {
                 v = fmaxf(v - unit_prob(qv[e]), 0.f);
-                if (i + e == gone) v = 0.f;
+                if (row_token<VEC>(t0, lane, e) == gone) v = 0.f;
             }
             weight_q(v, hi[e], lo[e]);
         }
@@ -559,16 +613,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
             float4 p[4], q[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int i = c0 + ((j0 + u) * NT + (int)threadIdx.x) * 4;
-                p[u] = j0 + u < rounds ? row_load4<VEC>(prow, i, c1, 0.f) : zero4;
-                q[u] = j0 + u < rounds && with_q ? row_load4<VEC>(qrow, i, c1, 0.f) : zero4;
+                const int t0 = c0 + ((j0 + u) * NT + 32 * warp) * 4;
+                p[u] = j0 + u < rounds ? row_load4<VEC>(prow, t0, lane, c1, 0.f) : zero4;
+                q[u] = j0 + u < rounds && with_q ? row_load4<VEC>(qrow, t0, lane, c1, 0.f) : zero4;
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (j0 + u >= rounds) break;
-                const int i = c0 + ((j0 + u) * NT + (int)threadIdx.x) * 4;
+                const int t0 = c0 + ((j0 + u) * NT + 32 * warp) * 4;
                 unsigned h4[4], l4[4];
-                weights4(p[u], q[u], i, alone, h4, l4);
+                weights4(p[u], q[u], t0, alone, h4, l4);
                 // 128 tokens: both halves stay below 2^28
                 const unsigned lo = __reduce_add_sync(0xffffffffu, (l4[0] + l4[1]) + (l4[2] + l4[3]));
                 const unsigned hi = __reduce_add_sync(0xffffffffu, (h4[0] + h4[1]) + (h4[2] + h4[3]));
@@ -630,20 +684,35 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
     int seg = src * per;
     while (left > s_seg[seg]) left -= s_seg[seg++];   // ends: the lane's segments reach it
     const int j = seg / kWarps, w0 = seg - j * kWarps;
-    const int i = c0 + (j * NT + w0 * 32 + lane) * 4;
+    const int t0 = c0 + (j * NT + w0 * 32) * 4;
     unsigned h4[4], l4[4];
-    weights4(row_load4<VEC>(prow, i, c1, 0.f), qrow && !alone ? row_load4<VEC>(qrow, i, c1, 0.f) : zero4, i, alone, h4, l4);
+    weights4(row_load4<VEC>(prow, t0, lane, c1, 0.f), qrow && !alone ? row_load4<VEC>(qrow, t0, lane, c1, 0.f) : zero4, t0,
+             alone, h4, l4);
     unsigned long long w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = ((unsigned long long)h4[e] << 20) + l4[e];
-    sum = (w[0] + w[1]) + (w[2] + w[3]);
-    incl = scan(sum);
-    const int hit = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;
-    if (lane == hit) {
-        unsigned long long run = incl - sum;
-        int e = 0;
-        while (e < 3 && run + w[e] < left) run += w[e++];
-        out[k] = i + e;
+    if (VEC) {   // in vocabulary order: lane by lane
+        sum = (w[0] + w[1]) + (w[2] + w[3]);
+        incl = scan(sum);
+        const int hit = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;
+        if (lane == hit) {
+            unsigned long long run = incl - sum;
+            int e = 0;
+            while (e < 3 && run + w[e] < left) run += w[e++];
+            out[k] = row_token<VEC>(t0, lane, e);
+        }
+        return;
+    }
+    unsigned long long run = 0ull;   // 32 tokens by 32
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        incl = run + scan(w[e]);
+        const unsigned reach = __ballot_sync(0xffffffffu, incl >= left);
+        if (reach) {
+            if (lane == __ffs(reach) - 1) out[k] = row_token<VEC>(t0, lane, e);
+            return;
+        }
+        run = __shfl_sync(0xffffffffu, incl, 31);
     }
 }
 

@@ -51,9 +51,14 @@ def test_probs_extremes():
 
 def test_probs_strides_and_in_place():
     buf = randn((5, 40003), torch.float32, 6, 2.0)
-    a = check_probs(buf[:, 1:30000], 0.8)       # rows that start off a 16-byte boundary
-    b = check_probs(buf[:, 1:30000].contiguous(), 0.8)
-    assert torch.equal(a, b)
+    check_probs(buf[:, 1:30000], 0.8)           # rows and results at different places of a 16-byte line
+    check_probs(buf[:, 1:30000].contiguous(), 0.8)
+    for at in (1, 2, 3):                        # at the same one
+        check_probs(buf[:, at:at + 30000], 0.8, out=torch.full_like(buf, float("nan"))[:, at:at + 30000])
+        check_probs(buf[:, at:at + 30000], 0.0, out=torch.full_like(buf, float("nan"))[:, at:at + 30000])
+    wide = torch.full((5, 40003), 7.0, device="cuda")
+    check_probs(buf[:, 5:20006], 0.8, out=wide[:, 9:20010])
+    assert (wide[:, :9] == 7).all() and (wide[:, 20010:] == 7).all()   # nothing beside the rows
     for n in (40000, 29999):
         z = buf[:, :n].contiguous()
         want = torch.empty_like(z)

@@ -611,11 +611,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const __grid_constant_
         unsigned long long wsum = 0ull;
         for (int j0 = 0; j0 < rounds; j0 += 4) {
             float4 p[4], q[4];
+            const int first = c0 + (j0 * NT + 32 * warp) * 4;   // the warp's tokens of the four rounds
+            if (VEC && first + 3 * kTile + 128 <= c1) {          // all there: eight loads without a branch
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int t0 = c0 + ((j0 + u) * NT + 32 * warp) * 4;
-                p[u] = j0 + u < rounds ? row_load4<VEC>(prow, t0, lane, c1, 0.f) : zero4;
-                q[u] = j0 + u < rounds && with_q ? row_load4<VEC>(qrow, t0, lane, c1, 0.f) : zero4;
+                for (int u = 0; u < 4; ++u)
+                    p[u] = *reinterpret_cast<const float4 *>(prow + first + u * kTile + 4 * lane);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    q[u] = with_q ? *reinterpret_cast<const float4 *>(qrow + first + u * kTile + 4 * lane) : zero4;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int t0 = first + u * kTile;
+                    p[u] = j0 + u < rounds ? row_load4<VEC>(prow, t0, lane, c1, 0.f) : zero4;
+                    q[u] = j0 + u < rounds && with_q ? row_load4<VEC>(qrow, t0, lane, c1, 0.f) : zero4;
+                }
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {

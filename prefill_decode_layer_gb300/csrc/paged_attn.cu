@@ -488,11 +488,15 @@ static long long most_tiles(const AttnArgs &a, int kt)
     }
     return keys > 0 ? (keys + kt - 1) / kt : 1;
 }
+// Items stay whole where cutting them gains less than the join costs (about 3 us, two or three
+// units): up to four units (one sequence of 384 positions: 9.5 us whole, 10.4 cut; 64 with 8 K/V
+// heads 31 and 42), and up to eight where the items alone occupy a quarter of the CTAs (8 x 8
+// heads of 768 positions: 12.4 and 14.4 us; one sequence: 12.8 and 11.1).
 int paged_attn_grid(AttnArgs &a, int kt, int most)
 {
-    const long long tiles = most_tiles(a, kt);
-    a.whole = tiles <= 2;
-    const long long u = most_items(a) * (a.whole ? 1 : tiles);
+    const long long tiles = most_tiles(a, kt), items = most_items(a);
+    a.whole = tiles <= 4 || (tiles <= 8 && items * 4 >= most);
+    const long long u = items * (a.whole ? 1 : tiles);
     return (int)(u < most ? u : most);
 }
 

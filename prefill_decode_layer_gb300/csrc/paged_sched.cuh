@@ -9,9 +9,8 @@
 // of an item that others share goes to the workspace as a part (row maxima, row sums,
 // unnormalised rows), and k_paged_join adds the parts in CTA order.  A CTA has at most
 // two parts: of the item it begins in (slot 2c) and of the one it ends in (slot 2c + 1).
-// Where no item can have more than two units (a short window or table), items are not cut
-// and the unit of the division is the item: a second launch for the join would cost more than
-// the second unit.
+// Where no item can have more than a few units (a short window or table), items are not cut
+// and the unit of the division is the item (a.whole).
 #pragma once
 
 #include "paged.h"

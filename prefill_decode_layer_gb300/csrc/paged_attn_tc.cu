@@ -560,10 +560,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool has0 = kb - ka >= 2 || (kb - ka == 1 && ((u0 + ka) & 1u) == 0);
                 const bool has1 = kb - ka >= 2 || (kb - ka == 1 && ((u0 + ka) & 1u) == 1);
                 const float mm = fmaxf(a0.x, a1.x), ref = mm == -INFINITY ? 0.f : mm;
-                const float f0 = exp2f(a0.x - ref), f1 = exp2f(a1.x - ref);
+                float f0, f1;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f0) : "f"(a0.x - ref));
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f1) : "f"(a1.x - ref));
                 const float sum = f0 * a0.y + f1 * a1.y;
                 const bool part = it.part >= 0;
-                const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                if (!part) {   // the output's scale goes into the streams' factors
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    f0 *= inv;
+                    f1 *= inv;
+                }
                 const size_t at = (size_t)it.part * a.rows + r;
                 if (part && mine && s == 0) {
                     float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + at * 2;
@@ -596,9 +602,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int e = 0; e < 4; ++e) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                w[y] = pack_bf16x2(__float2bfloat16_rn(o[8 * e + 2 * y] * inv),
-                                                   __float2bfloat16_rn(o[8 * e + 2 * y + 1] * inv));
+                            for (int y = 0; y < 4; ++y) {
+                                const __nv_bfloat162 pk = __floats2bfloat162_rn(o[8 * e + 2 * y], o[8 * e + 2 * y + 1]);
+                                w[y] = *reinterpret_cast<const uint32_t *>(&pk);
+                            }
                             *reinterpret_cast<uint4 *>(dst + d + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }

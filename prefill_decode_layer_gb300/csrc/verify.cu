@@ -14,8 +14,8 @@
 // way out.  Three CTAs fit an SM, so that the copies of some overlap the arithmetic of others
 // (with the chunk in registers two fit, and 56 of a GPC's 57 places against 32 of 38: 94 us
 // for 320 rows of 129280).  k_probs_any holds the chunk in registers and reads what a larger
-// vocabulary has beyond again: for rows that are not 16-byte aligned and vocabularies above
-// 131072.
+// vocabulary has beyond again: for rows that begin elsewhere in a 16-byte line than their
+// results, and vocabularies above 262144.
 //
 // k_verify: draft i is accepted while u_i q_i(d_i) < p_i(d_i) (exact: products of two
 // 24-bit numbers in FP64), which every CTA of the cluster evaluates for itself.  The
@@ -145,13 +145,15 @@ __device__ __forceinline__ float rebase(float m, float M, float c_hi, float c_lo
 // Chunks of at most kRowHold rounds; cluster i of the grid takes rows i, i + clusters, ..  A row
 // that begins `mis` floats behind a 16-byte boundary (as the rows of an odd vocabulary do) is taken
 // as one that begins at the boundary, whose first `mis` values are not there; its result
-// begins as far behind one.
-__global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant__ ProbsArgs a)
+// begins as far behind one.  Threads: 512, or 128 for short rows (twelve CTAs an SM).
+template <int NT>
+__global__ void __launch_bounds__(NT, 3 * kRowThreads / NT) k_probs(const __grid_constant__ ProbsArgs a)
 {
+    constexpr int kWarps = NT / 32;
     extern __shared__ __align__(16) float s_x[];   // the chunk: logits, then weights
-    __shared__ float2 s_red[kRowWarps];
-    __shared__ unsigned long long s_red64[kRowWarps];
-    __shared__ unsigned long long s_all[2][8];   // what every CTA of the cluster has found, by row parity
+    __shared__ float2 s_red[kWarps];
+    __shared__ unsigned long long s_red64[kWarps];
+    __shared__ unsigned long long s_all[2][kMaxCluster];   // what every CTA of the cluster has found, by row parity
     __shared__ uint64_t s_bar, s_all_bar[2];
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
             for (int e = 0; e < 4; ++e)
                 if (i + e >= lo && i + e < len) p[i + e] = v[e];
         };
-        auto at = [&](int j) { return (j * kRowThreads + (int)threadIdx.x) * 4; };
+        auto at = [&](int j) { return (j * NT + (int)threadIdx.x) * 4; };
         if (a.greedy) {   // one at the largest logit, lowest id on ties
             unsigned long long best = 0ull;
 #pragma unroll
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
             if (lane == 0) s_red64[warp] = best;
             __syncthreads();   // (also: the buffer is free)
             if (threadIdx.x == 0 && row + clusters < a.rows) fetch(row + clusters);
-            if (warp == 0) best = warp_max64(lane < kRowWarps ? s_red64[lane] : 0ull);
+            if (warp == 0) best = warp_max64(lane < kWarps ? s_red64[lane] : 0ull);
             const int win = key_id(warp_max64(exchange(best, turn, landed))) - id0;   // (none: below 0, or a value that is not there)
 #pragma unroll
             for (int j = 0; j < kRowHold; ++j)
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) k_probs(const __grid_constant_
         if (lane == 0) s_red[warp] = make_float2(wm, ws);
         __syncthreads();
         if (warp == 0) {
-            const float2 v = lane < kRowWarps ? s_red[lane] : make_float2(-INFINITY, 0.f);
+            const float2 v = lane < kWarps ? s_red[lane] : make_float2(-INFINITY, 0.f);
             M = warp_max(v.x);
             ws = warp_sum(v.y * rebase(v.x, M, a.c_hi, a.c_lo));
         }
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_probs_any(const __grid_const
 static int probs_cluster(int n, int rows, int nsm)
 {
     int c = 1;
-    while (c < 8 && n > c * kRowHold * kRowTile) c *= 2;
+    while (c < kMaxCluster && n > c * kRowHold * kRowTile) c *= 2;
     while (c < 8 && n >= 2 * c * kRowTile && (long long)rows * c < nsm) c *= 2;
     return c;
 }
@@ -435,8 +437,8 @@ template <typename A>
 static cudaError_t launch_rows(PerDevice &once, void (*kernel)(A), int clusters, int cluster, int threads, size_t smem,
                                cudaStream_t st, const A &a)
 {
-    // (the largest buffer that any row takes, and clusters of 16)
-    const cudaError_t e = allow_once(once, kernel, smem ? kRowHold * kRowTile * 4 : 0, true);
+    // (probs_go allows its buffer; clusters of 16)
+    const cudaError_t e = allow_once(once, kernel, 0, true);
     if (e) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)clusters * cluster);
@@ -456,39 +458,39 @@ static cudaError_t launch_rows(PerDevice &once, void (*kernel)(A), int clusters,
 
 static bool vec_ok(const void *p, long long s) { return ((uintptr_t)p & 15u) == 0 && (s & 3) == 0; }
 
-// Clusters of c CTAs of k_probs, each with the largest buffer, that the current device holds at
+// Clusters of c CTAs of k_probs<NT>, each with the largest buffer, that the current device holds at
 // once (asked for once per device and size: whole clusters lie in one GPC, so that fewer fit
 // than the SMs alone say).
-static int probs_resident(int c, int nsm)
+template <int NT> static cudaError_t probs_go(const ProbsArgs &a, int c, int nsm, cudaStream_t st)
 {
+    static PerDevice once;
     static std::atomic<int> known[64][5];
-    int dev = 0;
-    if (cudaGetDevice(&dev)) return 1;
-    int k = 0;
+    constexpr int smem = kRowHold * NT * 16;
+    cudaError_t e = allow_once(once, k_probs<NT>, smem, true);
+    int dev = 0, k = 0, n = 0;
+    if (!e) e = cudaGetDevice(&dev);
+    if (e) return e;
     while ((1 << k) < c) ++k;
-    const bool keep = dev >= 0 && dev < 64 && k < 5;
-    if (keep) {
-        const int n = known[dev][k].load(std::memory_order_relaxed);
-        if (n) return n;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep) n = known[dev][k].load(std::memory_order_relaxed);
+    if (!n) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(nsm / c + 1) * c);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)c, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, k_probs<NT>, &cfg) || n < 1) {
+            cudaGetLastError();
+            n = nsm / c > 0 ? nsm / c : 1;
+        }
+        if (keep) known[dev][k].store(n, std::memory_order_relaxed);
     }
-    const int smem = kRowHold * kRowTile * 4;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(nsm / c + 1) * c);
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)c, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(k_probs, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ||
-        cudaOccupancyMaxActiveClusters(&n, k_probs, &cfg) || n < 1) {
-        cudaGetLastError();
-        n = nsm / c > 0 ? nsm / c : 1;
-    }
-    if (keep) known[dev][k].store(n, std::memory_order_relaxed);
-    return n;
+    // more rows than the GPU holds clusters take turns
+    return launch_rows(once, k_probs<NT>, a.rows < n ? a.rows : n, c, NT, (size_t)a.chunk * 4, st, a);
 }
 
 cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,
@@ -505,12 +507,9 @@ cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float
         a.c_hi = (float)(cc < 3e38 ? cc : 3e38);
         a.c_lo = cc < 3e38 ? (float)(cc - (double)a.c_hi) : 0.f;
     }
-    if (alike && a.chunk <= kRowHold * kRowTile) {
-        // more rows than the GPU holds clusters take turns
-        static PerDevice once;
-        const int most = probs_resident(c, nsm);
-        return launch_rows(once, k_probs, rows < most ? rows : most, c, kRowThreads, (size_t)a.chunk * 4, st, a);
-    }
+    // short rows: a CTA of 128 threads holds 4096 values (3700 rows of 2700 tokens: 53 us with 512)
+    if (alike && c == 1 && a.chunk <= kRowHold * 128 * 4) return probs_go<128>(a, c, nsm, st);
+    if (alike && a.chunk <= kRowHold * kRowTile) return probs_go<kRowThreads>(a, c, nsm, st);
     static PerDevice once[2];
     a.chunk = row_chunk(n, c);
     return vec ? launch_rows(once[1], k_probs_any<true>, rows, c, kRowThreads, 0, st, a)

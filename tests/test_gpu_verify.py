@@ -10,7 +10,7 @@ from paged_ref import paged_inputs, randn, ref_attention, ref_probs, ref_verify
 
 pytestmark = pytest.mark.gpu
 
-VOCABS = [1, 3, 100, 1000, 4095, 4097, 8193, 50257, 129280, 131073]
+VOCABS = [1, 3, 100, 1000, 4095, 4097, 8193, 50257, 129280, 131073, 262141, 262145]
 
 
 # ------------------------------------------------------------------ probabilities

@@ -20,7 +20,7 @@ namespace ds4g {
 // Most CTAs of the two forms (the workspace holds two parts for each).
 constexpr int kAttnMaxCtas = 320;      // FP32 form: two CTAs per SM (a multiple of 64)
 constexpr int kAttnMaxCtasTc = 160;    // tensor-core form: one
-constexpr int kAttnRowsSimt = 8;       // query rows of an FP32 row tile
+constexpr int kAttnRowsSimt = 4;       // query rows of an FP32 row tile
 
 struct PagedItem {
     int seq, head;          // sequence, K/V head

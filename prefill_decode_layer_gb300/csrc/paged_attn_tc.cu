@@ -388,10 +388,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool active = 32 * wq < it.n_rows;   // the warp has rows
             const int row = it.row0 + r, tok = row / a.group, hd = row - tok * a.group;
             const bool mine = r < it.n_rows;
-            const int pos = mine ? it.pos0 + tok : -1;          // -1: sees no key
+            const int pos = mine ? max(it.pos0 + tok, -1) : -1;   // -1: sees no key
             const int see_lo = max(it.lo, pos - win + 1), see_hi = min(pos, it.hi - 1);
             // keys that some rows of the tile see and others do not
-            const int pos_a = it.pos0 + it.tok_a, pos_b = it.pos0 + it.tok_b;
+            const int pos_a = max(it.pos0 + it.tok_a, -1), pos_b = max(it.pos0 + it.tok_b, -1);
+            const int win_a = max(pos_a - win + 1, 0), win_b = max(pos_b - win + 1, 0);
             float m = -INFINITY, l = 0.f;
             bool first = true;
             for (int k = (int)((s ^ u0) & 1u); k < units; k += 2) {
@@ -484,10 +485,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 // ---- V rows of the tile that no row, or not every row, may take as they are
                 const bool edge = ((beg | end) & 15) != 0 && end > beg;
-                // columns only some rows see: (pos_a, pos_b], and (pos_a - win, pos_b - win]
+                // columns only some rows see: keys pos_a + 1 .. pos_b, and win_a .. win_b - 1
                 const int h0 = max(pos_a + 1 - base, beg), h1 = min(pos_b + 1 - base, end);
-                const int g0 = a.window > 0 ? max(pos_a - win + 1 - base, beg) : 0;
-                const int g1 = a.window > 0 ? min(pos_b - win + 1 - base, end) : 0;
+                const int g0 = max(win_a - base, beg), g1 = min(win_b - base, end);
                 if (ok && (edge || h0 < h1 || g0 < g1)) {
                     unsigned char *vt = ring + vp.slot * kTile;
                     ok = warp_wait(&x.full[vp.slot], vp.phase);
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     };
                     add(pos_a + 1, pos_b + 1);
                     // a key of both ranges is added once
-                    if (a.window > 0) add(pos_a - win + 1, min(pos_b - win + 1, pos_a + 1));
+                    add(win_a, min(win_b, pos_a + 1));
                 }
             }
             tc_fence_before();

@@ -92,7 +92,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs &a, int b, int kt)
     w.n_new = n;
     w.pos0 = len - n;
     w.hi = min(len, cap);
-    w.lo = a.window > 0 ? min(max(w.pos0 - a.window + 1, 0), w.hi) : 0;
+    // (a token before position 0 sees no key; any window of 32 bits stays in range)
+    w.lo = a.window > 0 ? min(max(max(w.pos0, 0) - a.window + 1, 0), w.hi) : 0;
     const int t = w.hi > w.lo ? (w.hi + kt - 1) / kt - w.lo / kt : 1;   // one empty unit still writes zeros
     w.tiles = t;
     w.row_tiles = a.rows >= a.s.max_new * a.group ? min(n, 1) : (n * a.group + a.rows - 1) / a.rows;
@@ -228,7 +229,7 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     const int tok_a = w.row_tiles == 1 ? 0 : it.row0 / a.group;
     const int tok_b = w.row_tiles == 1 ? w.n_new - 1 : (it.row0 + it.n_rows - 1) / a.group;
     it.hi = min(w.hi, w.pos0 + tok_b + 1);
-    it.lo = a.window > 0 ? max(w.lo, w.pos0 + tok_a - a.window + 1) : w.lo;
+    it.lo = a.window > 0 ? max(w.lo, max(w.pos0 + tok_a, 0) - a.window + 1) : w.lo;
     it.tok_a = tok_a;
     it.tok_b = tok_b;
     it.t0 = tile0 + x;

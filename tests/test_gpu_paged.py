@@ -180,6 +180,14 @@ def test_attention_window_of_one_token(window):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [3, 2 ** 31 - 1])
+def test_attention_window_with_tokens_before_position_0(dtype, window):
+    p = paged_inputs([3, 150, 0], [7, 4, 2], 2, 64, 16, dtype, seed=22)   # positions -4 .. 2; 146 ..; -2, -1
+    fill_slots(p, 23)
+    check_attention(p, 8, dtype, window=window)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_missing_pages_and_empty_rows(dtype):
     lengths = [200, 64, 300, 90, 0, 33]
     p = paged_inputs(lengths, [2, 1, 3, 1, 2, 1], 2, 64, 16, dtype, seed=8)

@@ -429,7 +429,7 @@ int32_t ds4g_sample_static(const float *logits, int n_vocab, float temperature, 
 /* The cache of one layer.  Element d of head h of slot s of page g is at
  * k[g * page_stride + s * slot_stride + h * head_stride + d] (v alike); strides in
  * elements, each a multiple of 16 bytes, the pointers 16-byte aligned.  head_dim: a
- * multiple of 8, at most 256. */
+ * multiple of 8, at most 256; at most 65536 heads. */
 typedef struct {
     void *k, *v;
     int64_t page_stride, slot_stride, head_stride;
@@ -494,7 +494,7 @@ size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_
 /* Attention of every sequence's new tokens over its cached positions (the new tokens'
  * rows already appended): token at position p attends to the positions max(0, p -
  * window + 1) .. p (window <= 0: 0 .. p), out = sum_j softmax_j(scale q . k_j) v_j, query
- * heads h * n_heads / n_kv_heads .. sharing K/V head h.  scale > 0, or 0: 1 / sqrt(head_dim).
+ * heads h * n_heads / n_kv_heads .. sharing K/V head h.  0 < scale <= 1e38, or 0: 1 / sqrt(head_dim).
  * A masked or missing key adds nothing, whatever its K and V hold; a token without any key
  * gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
  * (multiples of 16 bytes, 16-byte aligned); dtype: their type.  q and out must not
@@ -544,7 +544,7 @@ int ds4g_probs(const float *logits, int64_t logits_stride, int n_rows, int n_voc
  * rejected); u24: uint32 [n_seqs][max_drafts + 1] (the low 24 bits).
  * accepted: int32 [n_seqs], k; tokens: int32 [n_seqs][max_drafts + 1]: the accepted
  * drafts, the drawn token (-1 if p_k has no weight), then -1.  max_drafts in [0, 64];
- * n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */
+ * n_vocab <= 1048576 (DS4G_ESIZE).  The outputs overlap no input.  One launch. */
 int ds4g_verify_draft(const float *p, int64_t p_seq_stride, int64_t p_stride, const float *q, int64_t q_seq_stride,
                       int64_t q_stride, const int32_t *drafts, const int32_t *n_drafts, const uint32_t *u24,
                       int n_seqs, int max_drafts, int n_vocab, int32_t *accepted, int32_t *tokens,

@@ -10,6 +10,7 @@ using namespace ds4g;
 namespace {
 
 bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+constexpr int kMaxHeads = 65536;  // element offsets within a token's row are 32-bit
 size_t elem(int dtype) { return dtype == DS4G_BF16 ? 2 : 4; }
 bool dtype_ok(int dtype) { return dtype == DS4G_BF16 || dtype == DS4G_F32; }
 // A stride in elements of rows of at least `row` elements: whole 16-byte vectors.
@@ -18,7 +19,7 @@ bool stride_ok(int64_t s, int64_t row, int dtype) { return s >= row && s * (int6
 bool kv_ok(const ds4g_paged_kv *kv)
 {
     if (!kv || !kv->k || !kv->v || !al16(kv->k) || !al16(kv->v) || !dtype_ok(kv->dtype)) return false;
-    if (kv->n_pages < 1 || kv->page_size < 1 || kv->n_kv_heads < 1) return false;
+    if (kv->n_pages < 1 || kv->page_size < 1 || kv->n_kv_heads < 1 || kv->n_kv_heads > kMaxHeads) return false;
     if (kv->head_dim < 8 || kv->head_dim > 256 || kv->head_dim % 8) return false;
     return stride_ok(kv->page_stride, kv->head_dim, kv->dtype) && stride_ok(kv->slot_stride, kv->head_dim, kv->dtype) &&
            stride_ok(kv->head_stride, kv->head_dim, kv->dtype);
@@ -65,7 +66,7 @@ constexpr int kMaxDraftsApi = 64;
 
 bool heads_ok(const ds4g_paged_kv *kv, int n_heads)
 {
-    return n_heads >= 1 && n_heads <= 65536 && n_heads % kv->n_kv_heads == 0;
+    return n_heads >= 1 && n_heads <= kMaxHeads && n_heads % kv->n_kv_heads == 0;
 }
 
 }  // namespace
@@ -92,7 +93,7 @@ int ds4g_paged_append(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch, co
                  rope->rot_dim > kv->head_dim))
         return DS4G_EINVAL;
     if (q) {
-        if (!q_out || n_heads < 1 || n_heads > 65536 || !al16(q) || !al16(q_out)) return DS4G_EINVAL;
+        if (!q_out || n_heads < 1 || n_heads > kMaxHeads || !al16(q) || !al16(q_out)) return DS4G_EINVAL;
         const int64_t qrow = (int64_t)n_heads * kv->head_dim;
         if (!stride_ok(q_stride, qrow, dtype) || !stride_ok(q_out_stride, qrow, dtype)) return DS4G_EINVAL;
         if (q == q_out && q_stride != q_out_stride) return DS4G_EINVAL;
@@ -117,7 +118,7 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
                          void *workspace, size_t workspace_bytes, void *stream)
 {
     if (!kv_ok(kv) || !batch_ok(batch, kv) || !dtype_ok(dtype) || !heads_ok(kv, n_heads)) return DS4G_EINVAL;
-    if (!(scale >= 0.f) || scale - scale != 0.f) return DS4G_EINVAL;   // negative, NaN or infinite
+    if (!(scale >= 0.f && scale <= 1e38f)) return DS4G_EINVAL;   // (in powers of two it stays finite)
     if (batch->n_tokens == 0 || batch->n_seqs == 0) return DS4G_OK;
     if (batch->max_new > kMaxNew) return DS4G_EINVAL;
     // units of one sequence are counted in 32 bits (64 keys and 4 query rows a unit at least)

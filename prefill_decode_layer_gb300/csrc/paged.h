@@ -8,9 +8,9 @@
 
 namespace ds4g {
 
-// What is set once per device (function attributes last as
-// long as the device's context, so one call per kernel and device sets them).  Setting one
-// twice, from two threads, does no harm.
+// Whether something has been set on the current device (function attributes last as long as
+// the device's context, so they are set once per kernel and device).  Setting one twice, from
+// two threads, does no harm.
 struct PerDevice {
     std::atomic<bool> done[64];
     bool needs(int &dev) const

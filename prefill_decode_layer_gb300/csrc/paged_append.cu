@@ -125,10 +125,19 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
         if (tk < a.s.n_tokens) {
             int b = tk, first = tk, n = 1;
             if (a.s.start) {
-                // the sequence of token tk: as many sequences end at or before it
+                // the sequence of token tk: as many sequences end at or before it.  Of many, the
+                // 32nd part in which the last of them lies first (start does not fall).
+                int from = 0, left = a.s.n_seqs;
+                while (left > 256) {
+                    const int part = (left + 31) / 32, i = (lane + 1) * part;
+                    const bool ends = i <= left && a.s.start[from + i] <= tk;
+                    const int skip = __popc(__ballot_sync(0xffffffffu, ends)) * part;
+                    from += skip;
+                    left = min(part, left - skip);
+                }
                 int ended = 0;
-                for (int i = lane; i < a.s.n_seqs; i += 32) ended += a.s.start[i + 1] <= tk;
-                b = __reduce_add_sync(0xffffffffu, ended);
+                for (int i = lane; i < left; i += 32) ended += a.s.start[from + i + 1] <= tk;
+                b = from + __reduce_add_sync(0xffffffffu, ended);
                 if (b < a.s.n_seqs) {
                     first = a.s.start[b];
                     n = a.s.start[b + 1] - first;

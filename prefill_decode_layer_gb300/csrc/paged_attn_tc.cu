@@ -63,10 +63,9 @@ struct TcMisc {
     int poison[2];                                     // of item i % 2: a partly seen V row is not finite
     float2 ml[2][128];                                 // [stream][row] maximum (log2 units) and sum
 };
-static_assert(sizeof(TcMisc) <= 3072, "shared memory beside the tiles");
+static_assert(sizeof(TcMisc) <= 4096, "shared memory beside the tiles");
 
 struct TcGeometry {
-    int rows;        // query rows of an item's tile, all loaded by one box
     int q_half;      // bytes of 64 dims of the query tile
     int slots;
     int box;         // slots of a page in one copy: gcd(page_size, 128)
@@ -660,7 +659,6 @@ cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm)
 {
     const int hd = a.kv.head_dim, halves = hd / 64;
     TcGeometry g;
-    g.rows = a.rows;
     g.toks = a.rows / a.group;
     g.q_half = (a.rows + 7) / 8 * 8 * 128;
     g.box = gcd(a.kv.page_size, kTcKeys);

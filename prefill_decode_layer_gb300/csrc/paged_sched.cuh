@@ -25,7 +25,6 @@ constexpr int kAttnRowsSimt = 4;       // query rows of an FP32 row tile
 struct PagedItem {
     int seq, head;          // sequence, K/V head
     int token;              // row of the token arrays of the sequence's first new token
-    int n_new;              // its new tokens (at most max_new)
     int pos0;               // position of its first new token
     int row0, n_rows;       // query rows of the tile
     int tok_a, tok_b;       // the new tokens (of the sequence) of its first and last row
@@ -221,7 +220,6 @@ __device__ __forceinline__ void paged_next(const AttnArgs &a, int kt, PagedCurso
     it.seq = cur.seq;
     it.head = w.row_tiles == 1 ? item : item / w.row_tiles;
     it.token = w.token;
-    it.n_new = w.n_new;
     it.pos0 = w.pos0;
     it.row0 = w.row_tiles == 1 ? 0 : (item - it.head * w.row_tiles) * a.rows;
     it.n_rows = min(a.rows, w.n_new * a.group - it.row0);

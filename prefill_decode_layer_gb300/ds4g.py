@@ -527,8 +527,8 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.
                     scale: float = 0.0, window: int = 0, stream=None) -> None:
     """ds4g_paged_attention: q and out [n_tokens][n_heads][head_dim]; scale 0: 1 /
     sqrt(head_dim); window 0: every position up to the token's own."""
-    _require(q.dim() == 3 and q.dtype in _DTYPES and kv.index == batch.index == workspace.get_device(),
-             "paged_attention")
+    _require(q.dim() == 3 and q.dtype in _DTYPES and kv.index == batch.index == workspace.get_device() and
+             workspace.is_contiguous(), "paged_attention")
     n, d, dt, heads, index = _tokens(batch, q), kv.head_dim, q.dtype, q.shape[1], batch.index
     _call("ds4g_paged_attention", index, stream, kv.ref, batch.ref, q.data_ptr(),
           _rows(q, n, heads, d, dt, index, "paged_attention"), out.data_ptr(),

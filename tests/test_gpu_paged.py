@@ -108,6 +108,23 @@ def test_append_many_tokens():
             assert torch.equal(cache[table[b][pos // 64], pos % 64], x[start[b]:start[b + 1]].bfloat16())
 
 
+@pytest.mark.parametrize("seqs", [256, 257, 700, 9000])
+def test_append_finds_the_sequence_among_many(seqs):
+    new = [(i * 7919) % 5 for i in range(seqs)]   # 0 .. 4 tokens; some sequences have none
+    new[0], new[-1] = 0, 0
+    lengths = [n + i % 3 for i, n in enumerate(new)]
+    p = paged_inputs(lengths, new, 1, 8, 8, F32, seed=13, pad_rows=3)
+    n, owner = p["tokens"] - 3, torch.repeat_interleave(torch.arange(seqs), torch.tensor(new))
+    first = torch.tensor([0] + new[:-1]).cumsum(0)
+    at = torch.tensor(lengths)[owner] - torch.tensor(new)[owner] + torch.arange(n) - first[owner]
+    k = torch.arange(n + 3, dtype=F32, device="cuda")[:, None, None].expand(-1, 1, 8).contiguous()
+    want = p["k"].clone()
+    want[p["table"].cpu()[owner, 0].long(), at] = k[:n]
+    pdl.paged_append(pdl.PagedKV(p["k"], p["v"]), pdl.PagedBatch(p["table"], p["length"], p["start"], max_new=4), k, k)
+    assert torch.equal(p["k"].nan_to_num(-1.0), want.nan_to_num(-1.0))
+    assert torch.equal(p["v"].nan_to_num(-1.0), want.nan_to_num(-1.0))
+
+
 def test_rope_table_matches_the_formula():
     t = pdl.Rope.fill(70000, 64, base=10000.0)
     pos = torch.arange(70000, dtype=torch.float64, device="cuda")[:, None]

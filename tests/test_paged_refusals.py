@@ -27,7 +27,7 @@ def structs(**kw):
 
 
 BAD = [dict(k=None), dict(v=4104), dict(page_stride=4), dict(slot_stride=129), dict(head_stride=0), dict(n_pages=0),
-       dict(page_size=0), dict(n_kv_heads=0), dict(head_dim=0), dict(head_dim=12), dict(head_dim=264), dict(dtype=2),
+       dict(page_size=0), dict(n_kv_heads=0), dict(n_kv_heads=65537), dict(head_dim=0), dict(head_dim=12), dict(head_dim=264), dict(dtype=2),
        dict(table=None), dict(length=None), dict(start=None), dict(n_seqs=-1), dict(n_tokens=-1), dict(max_new=0),
        dict(width=-1), dict(table_stride=4), dict(width=2 ** 28, table_stride=2 ** 28)]
 
@@ -74,7 +74,7 @@ def test_attention_refuses(lib):
     assert need > 0
     assert attention(lib, None, b) == EINVAL and attention(lib, kv, None) == EINVAL
     for bad in (dict(q=None), dict(q=8), dict(out=None), dict(out=4100), dict(qs=511), dict(os=64), dict(heads=0),
-                dict(heads=7), dict(dtype=9), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-1.0), dict(ws=None),
+                dict(heads=7), dict(dtype=9), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(scale=-1.0), dict(ws=None),
                 dict(ws=4096 + 128), dict(out=4096)):
         assert attention(lib, kv, b, **bad) == EINVAL, bad
     assert attention(lib, kv, b, n=need - 1) == ESIZE
@@ -135,6 +135,8 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
     for args in ((q, q[:2]), (q, q.bfloat16()), (q.double(), q.double()), (q[..., :32], q[..., :32])):
         with pytest.raises(E):
             pdl.paged_attention(kv, batch, *args, ws)
+    with pytest.raises(E):
+        pdl.paged_attention(kv, batch, q, q.clone(), ws[:1].expand(1 << 30))
     z = torch.zeros(2, 10)
     for args in ((z, z.double()), (z[0], z[0]), (z, torch.zeros(10, 2).t())):
         with pytest.raises(E):

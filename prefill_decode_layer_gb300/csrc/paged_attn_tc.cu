@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     const float off = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t cc = pack_f32x2(c, c), oo = pack_f32x2(-off, -off);
+                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
                     for (int q = q0; q < q1; ++q) {
                         load(q);
@@ -468,18 +469,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float p0, p1;
-                            const float y0 = fmaf(__uint_as_float(v[2 * e]), c, -off);
-                            const float y1 = fmaf(__uint_as_float(v[2 * e + 1]), c, -off);
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y0));
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y1));
-                            sum[e & 1] += p0;
-                            sum[2 + (e & 1)] += p1;
+                            const float2 y = unpack_f32x2(fma_f32x2(
+                                pack_f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), cc, oo));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(y.x));
+                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(y.y));
+                            sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
                             const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
                             p[e] = *reinterpret_cast<const uint32_t *>(&pk);
                         }
                         tmem_st16(t_s + 16 * q, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 s0 = unpack_f32x2(sum[0]), s1 = unpack_f32x2(sum[1]);
+                    l += (s0.x + s1.x) + (s0.y + s1.y);
                     tmem_wait_st();
                 }
                 // ---- V rows of the tile that no row, or not every row, may take as they are

@@ -63,7 +63,7 @@ struct TcMisc {
     int poison[2];                                     // of item i % 2: a partly seen V row is not finite
     float2 ml[2][128];                                 // [stream][row] maximum (log2 units) and sum
 };
-static_assert(sizeof(TcMisc) <= 4096, "shared memory beside the tiles");
+static_assert(sizeof(TcMisc) <= 3 * 1024, "five tiles of 128 dims beside two query tiles of 128 rows");
 
 struct TcGeometry {
     int q_half;      // bytes of 64 dims of the query tile

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == kTcMma) {
         // ---------------- MMAs: S0 S1, then P V of each unit and the S of the unit after the next,
         // the order in which the tiles arrive
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t sbase = smem_u32(sm), rbase = smem_u32(ring);
             const uint32_t id_s = idesc_bf16_f32(128, kTcKeys), id_o = idesc_bf16_f32_bmn(128, HD);
             unsigned s_item = 0, p_item = 0, su = 0, pu = 0;   // items begun, units issued, of the two

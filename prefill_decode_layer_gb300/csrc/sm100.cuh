@@ -65,6 +65,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, volatile
     }
 }
 
+// True in one lane of a converged warp.  (Where the compiler sees that one thread runs, the
+// uniform operands of copies and MMAs need no loop over the lanes.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ CTA pairs (clusters of 2)
 
 // This CTA's rank in its cluster.

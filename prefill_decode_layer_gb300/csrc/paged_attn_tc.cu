@@ -41,8 +41,8 @@ namespace ds4g {
 
 static constexpr int kTcKeys = 128;                    // keys of a unit
 static constexpr int kTcSoft = 256;                    // softmax threads
-static constexpr int kTcThreads = kTcSoft + 64;
-static constexpr int kTcTma = kTcSoft / 32, kTcMma = kTcTma + 1;   // their warps
+static constexpr int kTcThreads = kTcSoft + 96;
+static constexpr int kTcTma = kTcSoft / 32, kTcMma = kTcTma + 1;   // warps of the copies and of stream 0's MMAs
 static constexpr int kTcMaxSlots = 8;
 static constexpr int kTcItems = 4;                     // items ahead of the softmax at most
 static constexpr int kTcSmem = 227 * 1024;
@@ -122,8 +122,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (i < n) {
             int count = 1;
             if (bars + i == &x.p_full[0] || bars + i == &x.p_full[1]) count = 4;
+            else if (bars + i == &x.q_empty[0] || bars + i == &x.q_empty[1]) count = 2;
+            else if (bars + i == &x.o_done || bars + i == &x.done) count = 2;
             else if (bars + i == &x.o_free) count = kTcSoft / 32;
-            else if (bars + i >= x.item_empty && bars + i < x.item_empty + kTcItems) count = 1 + kTcSoft / 32;
+            else if (bars + i >= x.item_empty && bars + i < x.item_empty + kTcItems) count = 2 + kTcSoft / 32;
             mbar_init(bars + i, count);
         } else if (i == n) {
             x.abort_flag = 0;
@@ -152,25 +154,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         reinterpret_cast<int *>(a.ws + lay.status)[blockIdx.x] = DS4G_ETIMEOUT;
     };
     // stream s: scores (then P) at column 128 s, O at 256 + 128 s
-    // a place in the ring: tile idx lies in slot idx % slots, in the phase (idx / slots) % 2 of its
-    // barriers (kept up to date: a division at every poll cost more than the MMAs)
+    // Each stream has half of the slots as a ring of its own (who waits for the tiles of a ring must see
+    // every phase of its barriers: a parity tells no more than two apart).  It holds K V K V .. of the
+    // stream's units; tile i lies in slot i % ring, in the phase (i / ring) % 2 of its barriers
+    // (kept up to date: a division at every poll cost more than the MMAs).
     struct Place {
         unsigned slot, phase;
     };
-    const unsigned slots = (unsigned)geo.slots;
-    auto ahead = [&](Place &p, unsigned by) {   // by <= slots
-        p.slot += by;
-        if (p.slot >= slots) {
-            p.slot -= slots;
+    const unsigned ring_slots = (unsigned)geo.slots / 2;
+    auto next_unit = [&](Place &p) {   // two tiles on (a ring has two slots or more)
+        p.slot += 2;
+        if (p.slot >= ring_slots) {
+            p.slot -= ring_slots;
             p.phase ^= 1u;
         }
     };
-    // The ring holds the tiles in the order of their use, K0 K1 V0 K2 V1 K3 V2 .. (V of a unit is
-    // needed a softmax after its K): K V K V kept two slots waiting through each softmax, and
-    // the next K came late (2600 cycles a unit for 1400 of HBM time).
-    const Place k_first = {0, 0}, v_first = {2, 0};                              // tiles 0 and 2
-    auto k_next = [&](Place &p, unsigned u) { ahead(p, u == 0 ? 1 : 2); };       // from unit u's
-    auto v_next = [&](Place &p) { ahead(p, 2); };
+    const Place k_first = {0, 0}, v_first = {1, 0};
 
     if (warp == kTcTma) {
         // ---------------- items, page look-ups, copies
@@ -192,8 +191,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool load;
             uint32_t bytes;   // of the whole tile
         };
-        auto copy = [&](const Place &p, const CUtensorMap *map, const Box &b) {
-            const unsigned sl = p.slot;
+        auto copy = [&](const Place &p, unsigned stream, const CUtensorMap *map, const Box &b) {
+            const unsigned sl = stream * ring_slots + p.slot;
             if (!warp_wait(&x.empty[sl], p.phase ^ 1u)) return false;
             if (lane == 0) mbar_expect_tx(&x.full[sl], b.bytes);
             if (lane == (int)sl) used = (int)p.phase;
@@ -247,101 +246,110 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // a page that is not there: out of bounds, read as zeros
                 b.at = page < 0 ? geo.none : page * geo.page_mul + head * geo.head_mul;
                 if (lane == 0) x.there[u % 8] = there;   // read once the scores are there
-                ok = copy(kp, &kmap, b);
-                k_next(kp, u);
+                // (both streams' rings are at the same place)
+                ok = copy(kp, u & 1, &kmap, b);
+                if (u & 1) next_unit(kp);
                 if (ok && u > 0) {
-                    ok = copy(vp, &vmap, prev);
-                    v_next(vp);
+                    ok = copy(vp, (u - 1) & 1, &vmap, prev);
+                    if (!(u & 1)) next_unit(vp);
                 }
                 prev = b;
             }
         }
-        if (ok && u > 0) ok = copy(vp, &vmap, prev);
+        if (ok && u > 0) ok = copy(vp, (u - 1) & 1, &vmap, prev);
         if (!ok) give_up();
         // nothing may be in flight when the CTA exits
         volatile int never = 0;
         if (used >= 0) mbar_wait(&x.full[lane], (uint32_t)used, &never);
         if (lane == 0)
             for (unsigned k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait(&x.q_full[k & 1], k >> 1 & 1u, &never);
-    } else if (warp == kTcMma) {
-        // ---------------- MMAs: S0 S1, then P V of each unit and the S of the unit after the next,
-        // the order in which the tiles arrive
+    } else if (warp > kTcTma) {
+        // ---------------- MMAs of stream t, units t, t + 2, ..: S of the first, then P V of each and S
+        // of the next.  (A thread for each stream: it runs no further ahead of its MMAs than a few,
+        // and with one for both the tensor cores stood idle while it went from one group to the next.)
         if (elect_one()) {
+            const unsigned t = warp - kTcMma;
             const uint32_t sbase = smem_u32(sm), rbase = smem_u32(ring);
             const uint32_t id_s = idesc_bf16_f32(128, kTcKeys), id_o = idesc_bf16_f32_bmn(128, HD);
-            unsigned s_item = 0, p_item = 0, su = 0, pu = 0;   // items begun, units issued, of the two
-            int s_left = 0;
+            const uint32_t ss = tmem + t * 128, oo = tmem + 256 + t * 128;
+            unsigned s_item = 0, p_item = 0, su = t, pu = t;   // items begun, units, of S and of P V
+            unsigned s_end = 0, p_end = 0;                     // the first unit behind the item begun last
             bool s_over = false, ok = true;
+            const unsigned slot0 = t * ring_slots;
             Place kp = k_first, vp = v_first;
-            auto next_s = [&]() {   // the next unit's scores, if there is one; false: gave up
-                if (s_over) return true;
-                if (s_left == 0) {
+            auto next_s = [&]() {   // the stream's next unit's scores, if there is one; false: gave up
+                while (!s_over && su >= s_end) {
                     if (!mbar_wait(&x.item_full[s_item % kTcItems], s_item / kTcItems & 1u, ab)) return false;
                     const PagedItem &it = x.item[s_item % kTcItems];
                     if (!it.more) {
                         s_over = true;
-                        return true;
+                        break;
                     }
-                    s_left = it.t1 - it.t0;
+                    s_end += it.t1 - it.t0;
                     if (!mbar_wait(&x.q_full[s_item & 1], s_item >> 1 & 1u, ab)) return false;
-                }
-                if (!mbar_wait(&x.full[kp.slot], kp.phase, ab)) return false;
-                tc_fence_after();
-                const uint64_t qd = sdesc_kmajor_sw128(sbase + (s_item & 1) * qbytes);
-                const uint64_t kd = sdesc_kmajor_sw128(rbase + kp.slot * kTile, H * 1024);
-                const uint32_t qh = (uint32_t)geo.q_half >> 4, acc = tmem + (su & 1) * 128;
-#pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks)
-                    tc_mma_bf16(acc, qd + (uint64_t)((ks >> 2) * qh + (ks & 3) * 2),
-                                kd + (uint64_t)((ks >> 2) * 64 + (ks & 3) * 2), id_s, ks > 0);
-                // (also: P V of the unit before the last is complete, so that its stream may rescale O)
-                tc_commit(&x.s_full[su & 1]);
-                tc_commit(&x.empty[kp.slot]);
-                k_next(kp, su);
-                ++su;
-                if (--s_left == 0) {
-                    tc_commit(&x.q_empty[s_item & 1]);
+                    if (su >= s_end) tc_commit(&x.q_empty[s_item & 1]);   // no unit of it is this stream's
                     ++s_item;
                 }
+                if (s_over) return true;
+                const unsigned slot = slot0 + kp.slot;
+                if (!mbar_wait(&x.full[slot], kp.phase, ab)) return false;
+                tc_fence_after();
+                const uint64_t qd = sdesc_kmajor_sw128(sbase + ((s_item - 1) & 1) * qbytes);
+                const uint64_t kd = sdesc_kmajor_sw128(rbase + slot * kTile, H * 1024);
+                const uint32_t qh = (uint32_t)geo.q_half >> 4;
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    tc_mma_bf16(ss, qd + (uint64_t)((ks >> 2) * qh + (ks & 3) * 2),
+                                kd + (uint64_t)((ks >> 2) * 64 + (ks & 3) * 2), id_s, ks > 0);
+                // (also: P V of the unit before is complete, so that the softmax may rescale O)
+                tc_commit(&x.s_full[t]);
+                tc_commit(&x.empty[slot]);
+                next_unit(kp);
+                su += 2;
+                if (su >= s_end) tc_commit(&x.q_empty[(s_item - 1) & 1]);
                 return true;
             };
-            int p_tile = 0, p_end = 0, p_lo = 0, p_hi = 0, p_k = 0;
-            bool fresh[2] = {true, true};   // no MMA of the item has written the stream's O
-            ok = next_s() && next_s();
-            while (ok && pu < su) {
-                if (p_tile == p_end) {   // its scores were issued, so the item is there
+            int p_tile = 0, p_lo = 0, p_hi = 0;
+            bool fresh = true;   // no MMA of the item has written the stream's O
+            ok = next_s();
+            while (ok) {
+                while (ok && pu >= p_end) {
+                    ok = mbar_wait(&x.item_full[p_item % kTcItems], p_item / kTcItems & 1u, ab);
+                    if (!ok) break;
                     const PagedItem &it = x.item[p_item % kTcItems];
-                    p_tile = it.t0;
-                    p_end = it.t1;
+                    if (!it.more) break;
+                    p_tile = it.t0 + (int)(pu - p_end);
+                    p_end += it.t1 - it.t0;
                     p_lo = it.lo;
                     p_hi = it.hi;
-                    p_k = 0;
-                    fresh[0] = fresh[1] = true;
+                    fresh = true;
+                    ok = p_item == 0 || mbar_wait(&x.o_free, (p_item - 1) & 1u, ab);
+                    if (ok && pu >= p_end) {   // no unit of it is this stream's
+                        tc_commit(&x.o_done);
+                        mbar_arrive(&x.item_empty[p_item % kTcItems]);
+                    }
+                    ++p_item;
                 }
-                const unsigned s = pu & 1;
-                ok = (p_k >= 2 || p_item == 0 || mbar_wait(&x.o_free, (p_item - 1) & 1u, ab)) &&
-                     mbar_wait(&x.full[vp.slot], vp.phase, ab) && mbar_wait(&x.p_full[s], pu >> 1 & 1u, ab);
+                if (!ok || pu >= p_end) break;
+                ok = mbar_wait(&x.full[slot0 + vp.slot], vp.phase, ab) && mbar_wait(&x.p_full[t], pu >> 1 & 1u, ab);
                 if (!ok) break;
                 tc_fence_after();
                 const int base = p_tile * kTcKeys;
                 const int k0 = (max(p_lo - base, 0)) / 16, k1 = (min(p_hi - base, kTcKeys) + 15) / 16;
-                const bool add = s ? !fresh[1] : !fresh[0];
-                if (k0 < k1) (s ? fresh[1] : fresh[0]) = false;
-                const uint64_t vd = sdesc_mnmajor_sw128(rbase + vp.slot * kTile, 1024, H * 1024);
-                const uint32_t po = tmem + s * 128, oo = tmem + 256 + s * 128;
+                const uint64_t vd = sdesc_mnmajor_sw128(rbase + (slot0 + vp.slot) * kTile, 1024, H * 1024);
 #pragma unroll
                 for (int ks = 0; ks < kTcKeys / 16; ++ks)   // 16 keys are 2 H KB of the tile
                     if (ks >= k0 && ks < k1)
-                        tc_mma_bf16_ta(oo, po + (uint32_t)ks * 8, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), id_o,
-                                       add || ks > k0);
-                tc_commit(&x.empty[vp.slot]);
-                v_next(vp);
-                ++pu;
-                ++p_k;
-                if (++p_tile == p_end) {
+                        tc_mma_bf16_ta(oo, ss + (uint32_t)ks * 8, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), id_o,
+                                       !fresh || ks > k0);
+                if (k0 < k1) fresh = false;
+                tc_commit(&x.empty[slot0 + vp.slot]);
+                next_unit(vp);
+                p_tile += 2;
+                pu += 2;
+                if (pu >= p_end) {
                     tc_commit(&x.o_done);
-                    mbar_arrive(&x.item_empty[p_item % kTcItems]);
-                    ++p_item;
+                    mbar_arrive(&x.item_empty[(p_item - 1) % kTcItems]);
                 }
                 ok = next_s();
             }
@@ -374,7 +382,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         unsigned u0 = 0;   // the CTA's units before this item
         Place vp = v_first;   // of this stream's next unit
-        if (s) v_next(vp);
         for (unsigned i = 0;; ++i) {
             bool ok = warp_wait(&x.item_full[i % kTcItems], i / kTcItems & 1u);
             if (soft_sync_any(!ok)) {
@@ -489,8 +496,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int h0 = max(pos_a + 1 - base, beg), h1 = min(pos_b + 1 - base, end);
                 const int g0 = max(win_a - base, beg), g1 = min(win_b - base, end);
                 if (ok && (edge || h0 < h1 || g0 < g1)) {
-                    unsigned char *vt = ring + vp.slot * kTile;
-                    ok = warp_wait(&x.full[vp.slot], vp.phase);
+                    const unsigned slot = s * ring_slots + vp.slot;
+                    unsigned char *vt = ring + slot * kTile;
+                    ok = warp_wait(&x.full[slot], vp.phase);
                     if (ok) {
                         const int t = threadIdx.x & 127;
                         auto chunk = [&](int key, int d16) {   // 16 bytes of dims 8 d16 .. of a V row
@@ -535,8 +543,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         fence_proxy_async_smem();   // before the MMA reads the tile
                     }
                 }
-                v_next(vp);
-                v_next(vp);
+                next_unit(vp);
                 tc_fence_before();
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(&x.p_full[s]);
@@ -669,6 +676,7 @@ cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm)
     const int tile = halves * kTcKeys * 128, qbytes = 2 * halves * g.q_half;
     g.slots = (kTcSmem - (int)sizeof(TcMisc) - qbytes) / tile;
     if (g.slots > kTcMaxSlots) g.slots = kTcMaxSlots;
+    g.slots &= ~1;   // two rings
     const int smem = qbytes + g.slots * tile + (int)sizeof(TcMisc);
 
     CUtensorMap qm, km, vm;

@@ -11,9 +11,10 @@
 // bulk copy and crosses HBM once each way.  Every thread takes 2^((z - m) c) of its values
 // against a maximum m of its own, the (m, sum) pairs are combined over the CTA and then, in
 // one exchange, over the cluster, and each thread scales its values by 2^((m - M) c) / S on the
-// way out.  Three CTAs fit an SM, so that the copies of some overlap the arithmetic of others
-// (with the chunk in registers two fit, and 56 of a GPC's 57 places against 32 of 38: 94 us
-// for 320 rows of 129280).  k_probs_any holds the chunk in registers and reads what a larger
+// way out.  Three CTAs fit an SM, so that the copies of some overlap the arithmetic of others.
+// Bound: bytes, at many rows (320 rows of 129280, 331 MB: 68 us, 0.72 of a copy's 6.78 TB/s; with
+// the chunk in registers two CTAs fit, and 56 of a GPC's 57 places against 32 of 38: 94 us); the
+// launch and two passes over a chunk at one (5.3 us).  k_probs_any holds the chunk in registers and reads what a larger
 // vocabulary has beyond again: for rows that begin elsewhere in a 16-byte line than their
 // results, and vocabularies above 262144.
 //
@@ -22,7 +23,9 @@
 // draw's weights max(p - q, 0), or p, become integers w = round(weight 2^40), as the
 // sampler's do, so that every order of summation gives the same total and the drawn
 // token does not depend on the split: sums of 128 consecutive tokens are kept in shared
-// memory, and only the segment that holds the target R is read a second time.
+// memory, and only the segment that holds the target R is read a second time.  Bound: bytes
+// at many sequences (the two rows of each that decide: 60.6 MB in 17 us, 0.53 of the copy's rate, one
+// wave of clusters), latency at one (6.8 us: the drafts' probabilities, the rows, the segment).
 #include <atomic>
 
 #include "paged.h"

@@ -466,7 +466,10 @@ static long long most_items(const AttnArgs &a);
 template <typename T, int ROWS, int CTAS>
 static cudaError_t join(const AttnArgs &a, int ctas, int nsm, cudaStream_t st)
 {
-    const int wide = most_items(a) * 8 <= ctas, grid = 4 * nsm;
+    const long long items = most_items(a), rows = (items < ctas ? items : ctas) * a.rows;   // a cut item begins in a CTA of its own
+    const int wide = items * 8 <= ctas, most = 8 * nsm;
+    const long long jobs = wide ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
+    const int grid = (int)(jobs < most ? jobs : most);
     const dim3 block(kJoinThreads);
     if (a.kv.head_dim <= 64) return launch_pdl(k_paged_join<T, ROWS, CTAS, 2>, dim3(grid), block, 0, st, a, wide);
     if (a.kv.head_dim <= 128) return launch_pdl(k_paged_join<T, ROWS, CTAS, 4>, dim3(grid), block, 0, st, a, wide);

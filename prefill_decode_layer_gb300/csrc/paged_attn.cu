@@ -495,13 +495,14 @@ static long long most_tiles(const AttnArgs &a, int kt)
     return keys > 0 ? (keys + kt - 1) / kt : 1;
 }
 // Items stay whole where cutting them gains less than the join costs (about 3 us, two or three
-// units): up to four units (one sequence of 384 positions: 9.5 us whole, 10.4 cut; 64 with 8 K/V
-// heads 31 and 42), and up to eight where the items alone occupy a quarter of the CTAs (8 x 8
-// heads of 768 positions: 12.4 and 14.4 us; one sequence: 12.8 and 11.1).
+// units): up to four units (one sequence of 384 positions: 9.0 us whole, 10.8 cut; 64 with 8 K/V
+// heads 28.8 and 37.2), and up to eight where the items alone occupy a quarter of the CTAs or
+// more, but no CTA has two (768 positions: 8 x 8 heads 11.5 us whole, 13.8 cut; one sequence 12.8 and
+// 11.1; 24 x 8 heads, in two turns, 21.6 and 20.5).
 int paged_attn_grid(AttnArgs &a, int kt, int most)
 {
     const long long tiles = most_tiles(a, kt), items = most_items(a);
-    a.whole = tiles <= 4 || (tiles <= 8 && items * 4 >= most);
+    a.whole = tiles <= 4 || (tiles <= 8 && items * 4 >= most && items <= most);
     const long long u = items * (a.whole ? 1 : tiles);
     return (int)(u < most ? u : most);
 }

@@ -495,8 +495,9 @@ size_t ds4g_paged_attention_workspace_bytes(const ds4g_paged_kv *kv, const ds4g_
  * rows already appended): token at position p attends to the positions max(0, p -
  * window + 1) .. p (window <= 0: 0 .. p), out = sum_j softmax_j(scale q . k_j) v_j, query
  * heads h * n_heads / n_kv_heads .. sharing K/V head h.  0 < scale <= 1e38, or 0: 1 / sqrt(head_dim).
- * A masked or missing key adds nothing, whatever its K and V hold; a token without any key
- * gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
+ * A masked or missing key adds nothing, whatever its K and V hold; what is not finite in the V
+ * of a key that a token sees leaves that place of its result infinite or NaN, however small
+ * the key's weight.  A token without any key gets zeros.  q, out: [n_tokens][n_heads][head_dim] with token strides in elements
  * (multiples of 16 bytes, 16-byte aligned); dtype: their type.  q and out must not
  * overlap.  max_new <= 128.
  * BF16 queries over a BF16 cache with head_dim 64 or 128, pages of a multiple of 8 slots, heads

@@ -219,14 +219,15 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
                     for (int e = 0; e < D; ++e) o[r][e] *= fr;
                 }
             }
-            const float p = see ? pa_ex2(s[0] - finite_max(m)) : 0.f;
-            l += p;
+            // (-1: masked.  A weight of 0 counts: it may meet an infinity or a NaN)
+            const float p = see ? pa_ex2(s[0] - finite_max(m)) : -1.f;
+            l += see ? p : 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int u = 0; u < KB; ++u) {
                     const float pr = __shfl_sync(lanes, p, (r * KB + u) * REP, LPK);
-                    if (pr != 0.f) {   // (NaN: yes) a masked key adds nothing, whatever its V holds
+                    if (!(pr < 0.f)) {   // (NaN: yes) a masked key adds nothing, whatever its V holds
 #pragma unroll
                         for (int e = 0; e < D; ++e) o[r][e] = fmaf(pr, v[u][e], o[r][e]);
                     }

@@ -142,3 +142,16 @@ def test_infinities_of_partly_seen_keys_survive_the_join(kv_heads, heads, dim, p
     got = check(p, q, window)
     assert (got[:2, :, 8] == float("inf")).all() and (got[1:4, :, 9] == float("-inf")).all()
     assert (got[8:, :, 9] == float("inf")).all() and got[4:8].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F32, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("kv_heads,heads,dim,page", LAYOUTS + [(1, 3, 32, 16), (1, 2, 256, 16)])
+def test_a_seen_key_counts_however_small_its_weight(dtype, cache, kv_heads, heads, dim, page):
+    """What is not finite in the V row of a key that a token sees leaves nothing finite there, in
+    whole and in cut items, beside the key with the large score and far from it."""
+    p, q = peaked(dtype, cache, [100, 3549, 3000], [1, 1, 2], [(0, 4), (1, 2000), (2, 2999)], kv_heads, heads, dim, page, 11)
+    for b, j, d in ((0, 6, 3), (0, 70, 4), (1, 2002, 3), (1, 2064, 4), (1, 3000, 5), (2, 2997, 6), (2, 0, 7)):
+        p["v"][slot(p, b, j)][:, d] = float("inf") if d % 2 else float("nan")
+    got = check(p, q, kinds=False)
+    for t, dims in ((0, (3, 4)), (1, (3, 4, 5)), (2, (6, 7)), (3, (6, 7))):
+        assert torch.equal(got[t].isfinite().all(0).cpu(), torch.tensor([d not in dims for d in range(dim)]))

@@ -42,8 +42,9 @@
  *    reports a failed launch or CUDA call, after which the session is undefined.
  *  - The operators on device buffers (ds4g_sample*, ds4g_paged_*, ds4g_probs,
  *    ds4g_verify_draft) run on the stream they are given, which belongs to the
- *    current device, and keep nothing between calls.  The last three groups do not
- *    synchronise and can be captured into a CUDA graph.  Calls that may overlap in
+ *    current device, and keep nothing between calls (but a time-out's report in the
+ *    workspace of ds4g_paged_attention).  The last three groups do not synchronise, that
+ *    report's reading apart, and can be captured into a CUDA graph.  Calls that may overlap in
  *    time need workspaces of their own.
  */
 #ifndef DS4G_H
@@ -512,10 +513,11 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
                          void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
                          void *workspace, size_t workspace_bytes, void *cuda_stream);
 
-/* Synchronise the stream and report how the last ds4g_paged_attention on this workspace
- * ended: DS4G_OK, or DS4G_ETIMEOUT if a bounded device-side wait gave up (its output is then
- * invalid). */
-int ds4g_paged_attention_status(const void *workspace, void *cuda_stream);
+/* Synchronise the stream and report whether a bounded device-side wait gave up in any
+ * ds4g_paged_attention on this workspace since the last time it was reported:
+ * DS4G_ETIMEOUT (the outputs of the calls since then are invalid; the report is cleared) or
+ * DS4G_OK, also where there was no call or none with tokens. */
+int ds4g_paged_attention_status(void *workspace, void *cuda_stream);
 
 /* ---------------------------------------------------------------- drafted tokens */
 

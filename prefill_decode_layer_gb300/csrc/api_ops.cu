@@ -137,7 +137,7 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
     return status_of(paged_attention(a, dtype, kv->dtype, static_cast<cudaStream_t>(stream), nsm));
 }
 
-int ds4g_paged_attention_status(const void *workspace, void *stream)
+int ds4g_paged_attention_status(void *workspace, void *stream)
 {
     if (!workspace || ((uintptr_t)workspace & 255u)) return DS4G_EINVAL;
     int status = DS4G_OK;

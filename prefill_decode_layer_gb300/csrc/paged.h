@@ -83,8 +83,8 @@ cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm);
 int paged_attn_grid(AttnArgs &a, int kt, int most);
 cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st);
 size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype);
-// DS4G_OK or DS4G_ETIMEOUT of the last call that used the workspace (synchronises st).
-cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status);
+// DS4G_ETIMEOUT once after calls on the workspace in which a wait gave up (synchronises st).
+cudaError_t paged_attn_status(void *ws, cudaStream_t st, int *status);
 cudaError_t paged_attention(const AttnArgs &a, int q_dtype, int kv_dtype, cudaStream_t st, int nsm);
 
 cudaError_t probs_rows(const float *logits, long long ls, int rows, int n, float temperature, float *out,

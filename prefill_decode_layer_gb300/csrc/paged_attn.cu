@@ -460,14 +460,18 @@ size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dty
     return n;
 }
 
-cudaError_t paged_attn_status(const void *ws, cudaStream_t st, int *status)
+cudaError_t paged_attn_status(void *ws, cudaStream_t st, int *status)
 {
     int word[kAttnMaxCtas];
     cudaError_t e = cudaMemcpyAsync(word, ws, sizeof(word), cudaMemcpyDeviceToHost, st);   // PartLayout::status
     if (!e) e = cudaStreamSynchronize(st);
     *status = DS4G_OK;
     for (int c = 0; !e && c < kAttnMaxCtas; ++c)
-        if (word[c] != DS4G_OK) *status = DS4G_ETIMEOUT;
+        if (word[c] == kAttnTimedOut) *status = DS4G_ETIMEOUT;
+    if (!e && *status != DS4G_OK) {   // read: the words are cleared
+        e = cudaMemsetAsync(ws, 0, sizeof(word), st);
+        if (!e) e = cudaStreamSynchronize(st);
+    }
     return e;
 }
 

@@ -29,7 +29,7 @@
 // Roles (352 threads, one CTA per SM): warps 0-3 and 4-7 softmax and output of streams 0
 // and 1; warp 8 the items, the page look-ups and the TMA copies; warps 9 and 10 (one thread
 // each) the MMAs of streams 0 and 1.  Every wait is bounded; a CTA that gives up says so in
-// its record, drains its copies and MMAs, frees its TMEM and returns.
+// its status word, drains its copies and MMAs, frees its TMEM and returns.
 //
 // Measured (with the join; fractions of a copy's 6.78 TB/s): 64 sequences of up to 8191
 // positions, 32 heads on 8 K/V heads of 128, 1.37 GB: 217-222 us, 0.91-0.93; four of up to 131072
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *ab = &x.abort_flag;
     auto give_up = [&]() {
         x.abort_flag = 1;
-        reinterpret_cast<int *>(a.ws + lay.status)[blockIdx.x] = DS4G_ETIMEOUT;
+        reinterpret_cast<int *>(a.ws + lay.status)[blockIdx.x] = kAttnTimedOut;
     };
     // stream s: scores (then P) at column 128 s, O at 256 + 128 s
     // Each stream has half of the slots as a ring of its own (who waits for the tiles of a ring must see

@@ -21,6 +21,10 @@ namespace ds4g {
 constexpr int kAttnMaxCtas = 320;      // FP32 form: two CTAs per SM (a multiple of 64)
 constexpr int kAttnMaxCtasTc = 160;    // tensor-core form: one
 constexpr int kAttnRowsSimt = 4;       // query rows of an FP32 row tile
+// Status word of a CTA in which a bounded wait gave up.  Any other word (memory that was never
+// written) says that none has, and no call clears the words: a time-out stays until it is read,
+// behind however many calls on the workspace.
+constexpr int kAttnTimedOut = 0x54494d45;
 
 struct PagedItem {
     int seq, head;          // sequence, K/V head
@@ -39,7 +43,7 @@ struct __align__(16) PagedSplit {
     int last_cta, head, token, row0;
 };
 
-// Workspace: per CTA how it ended (DS4G_OK, or DS4G_ETIMEOUT: a bounded wait gave up), the rows of
+// Workspace: per CTA whether a bounded wait gave up (kAttnTimedOut), the rows of
 // its split item (0: none begins in it) and that item's record; then the parts, [2 ctas][rows][2]
 // maxima and sums and [2 ctas][rows][head_dim] rows.
 struct PartLayout {
@@ -56,15 +60,12 @@ struct PartLayout {
 };
 static_assert(kAttnMaxCtas * 4 % 256 == 0, "the arrays of the workspace are aligned");
 
-// This CTA's words of the workspace at the start of a launch (all threads; words of CTAs that
-// the grid does not have are cleared too).
+// This CTA's count of rows in the workspace at the start of a launch (all threads; those of CTAs
+// that the grid does not have are cleared too).
 __device__ __forceinline__ void paged_begin(const AttnArgs &a, const PartLayout &lay)
 {
-    int *n_rows = reinterpret_cast<int *>(a.ws + lay.n_rows), *status = reinterpret_cast<int *>(a.ws + lay.status);
-    for (int c = blockIdx.x + gridDim.x * threadIdx.x; c < kAttnMaxCtas; c += gridDim.x * blockDim.x) {
-        n_rows[c] = 0;
-        status[c] = DS4G_OK;
-    }
+    int *n_rows = reinterpret_cast<int *>(a.ws + lay.n_rows);
+    for (int c = blockIdx.x + gridDim.x * threadIdx.x; c < kAttnMaxCtas; c += gridDim.x * blockDim.x) n_rows[c] = 0;
 }
 
 // A sequence's keys, new tokens and units.

@@ -536,12 +536,17 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.
           workspace.data_ptr(), workspace.nbytes)
 
 
+_STATUS_BYTES = 4 * 320   # of a workspace: what ds4g_paged_attention_status reads
+
+
 def paged_attention_status(workspace: torch.Tensor, stream=None) -> int:
-    """ds4g_paged_attention_status: OK or ETIMEOUT of the workspace's last call (synchronises)."""
+    """ds4g_paged_attention_status: OK, or once ETIMEOUT after calls on the workspace in which a
+    wait gave up (synchronises)."""
     index = workspace.get_device()
-    _require(index >= 0, "paged_attention_status")
-    return lib().ds4g_paged_attention_status(workspace.data_ptr(),
-                                             _raw_stream(index) if stream is None else stream.cuda_stream)
+    _require(index >= 0 and workspace.is_contiguous() and workspace.nbytes >= _STATUS_BYTES, "paged_attention_status")
+    with torch.cuda.device(index):   # (a null stream is the current device's)
+        return lib().ds4g_paged_attention_status(workspace.data_ptr(),
+                                                 _raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:

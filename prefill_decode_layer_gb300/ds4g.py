@@ -400,6 +400,11 @@ class RopeStruct(C.Structure):
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
+def _int32(n: int) -> int:
+    """n within a C int, below 0 as 0 (ctypes would take its low 32 bits)."""
+    return min(max(n, 0), 0x7fffffff)
+
+
 def _require(ok: bool, what: str) -> None:
     if not ok:
         raise Ds4gError(EINVAL, what)
@@ -459,7 +464,7 @@ class PagedBatch:
         self.table, self.length, self.start, self.index = table, length, start, length.get_device()
         width = table.shape[1]
         self.struct = PagedBatchStruct(table.data_ptr(), length.data_ptr(),
-                                       start.data_ptr() if start is not None else None, n, n, max_new,
+                                       start.data_ptr() if start is not None else None, n, n, _int32(max_new),
                                        width, table.stride(0) if n > 1 else width)
         self.ref = C.addressof(self.struct)
 
@@ -532,7 +537,7 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.
     n, d, dt, heads, index = _tokens(batch, q), kv.head_dim, q.dtype, q.shape[1], batch.index
     _call("ds4g_paged_attention", index, stream, kv.ref, batch.ref, q.data_ptr(),
           _rows(q, n, heads, d, dt, index, "paged_attention"), out.data_ptr(),
-          _rows(out, n, heads, d, dt, index, "paged_attention"), heads, _DTYPES[dt], scale, window,
+          _rows(out, n, heads, d, dt, index, "paged_attention"), heads, _DTYPES[dt], scale, _int32(window),
           workspace.data_ptr(), workspace.nbytes)
 
 

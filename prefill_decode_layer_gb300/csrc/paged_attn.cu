@@ -17,10 +17,12 @@
 // R KB, and one 2^x a lane.  The weights then go round once (a shuffle each) for O += P V in
 // registers.  The streams of an item are merged when it ends, those of a warp by shuffles, the
 // eight warps through shared memory.  Bound: the cache's bytes at few rows (two CTAs an SM keep
-// 64 KB of loads in flight), the FP32 pipes at many.  Measured: 16 sequences of up to 2000
-// positions, 8 heads on 2 of 64, FP32, 20.8 MB: 16.3 us with the join, a chain of latencies (two
-// launches, lengths, pages, keys, merge, parts); 32 sequences of 4000, 64 heads on 8 of 64: 138 us,
-// the FP32 pipes.
+// 64 KB of loads in flight), the issue of instructions at many: K and V pass once per four rows, and
+// 15 exchanges with their selects and 16 broadcasts go with the 128 FMAs of a batch.  Measured: 16
+// sequences of up to 2000 positions, 8 heads on 2 of 64, FP32, 20.8 MB: 16.3 us with the join, a
+// chain of latencies (two launches, lengths, pages, keys, merge, parts); 32 sequences of 4000, 64
+// heads on 8 of 64, 335 MB: 138 us, an instruction in 64 % of the issue slots (21 M of the 99 M are the
+// products' FMAs), 604 MB read from DRAM because both row tiles of a K/V head read it.
 #include "paged_sched.cuh"
 
 namespace ds4g {
@@ -514,7 +516,12 @@ static long long most_tiles(const AttnArgs &a, int kt)
 // units): up to four units (one sequence of 384 positions: 9.0 us whole, 10.8 cut; 64 with 8 K/V
 // heads 28.8 and 37.2), and up to eight where the items alone occupy a quarter of the CTAs or
 // more, but no CTA has two (768 positions: 8 x 8 heads 11.5 us whole, 13.8 cut; one sequence 12.8 and
-// 11.1; 24 x 8 heads, in two turns, 21.6 and 20.5).
+// 11.1; 24 x 8 heads, in two turns, 21.6 and 20.5).  The last condition gains where the items are
+// little more than one turn (8 K/V heads, 40 of 1024 39.8 -> 33.3 us, 24 of 640 20.7 -> 18.5) and loses
+// where they fill two (32 of 640 21.8 -> 23.3, of 768 23.6 -> 26.4, of 1024 28.1 -> 29.5).
+// The host knows the table's width and the window, not the lengths: under a table four times as
+// wide as the longest sequence items of three units are cut (384 positions: one sequence 8.9 -> 10.1
+// us, 64 with 8 K/V heads 27.7 -> 35.6; 100 positions, whole at four times the width, 7.6 -> 8.7 at 16).
 int paged_attn_grid(AttnArgs &a, int kt, int most)
 {
     const long long tiles = most_tiles(a, kt), items = most_items(a);

@@ -35,8 +35,11 @@
 // positions, 32 heads on 8 K/V heads of 128, 1.37 GB: 217-222 us, 0.91-0.93; four of up to 131072
 // with 64 heads on 8, 1.63 GB: 250 us, 0.96; one token of 64 heads in a window of 128: 7.8
 // us, latency (launch, page look-up, K, softmax, V); 32 sequences of up to 16994 with up to five new
-// tokens and 64 heads on one K/V head, 181 MB and 34 GFLOP: 58 us, bound by each
-// stream's chain S -> softmax -> P V (about 2000 cycles a unit against 1024 of MMAs).
+// tokens and 64 heads on one K/V head, 181 MB and 34 GFLOP: 58 us, of which 19 do not grow with the
+// length (launch, first tiles, output, join) and 32 units a CTA take 1.2 us each: 2500 cycles between
+// two units, the streams in turn, so that a stream's chain S -> softmax -> P V takes 5000, 1024 of
+// them MMAs (tensor pipe 40 % of the active cycles).  Each row tile reads K and V for itself: 64 KB a
+// unit, 322 MB in all, 222 MB of them from DRAM.
 #include <cuda.h>
 #include <stddef.h>
 
@@ -70,7 +73,9 @@ struct TcMisc {
     int poison[2];                                     // of item i % 2: a partly seen V row is not finite
     float2 ml[2][128];                                 // [stream][row] maximum (log2 units) and sum
 };
-static_assert(sizeof(TcMisc) <= 3 * 1024, "five tiles of 128 dims beside two query tiles of 128 rows");
+// (a fifth tile would fit there, but no ring of three: a stream has one K and one V tile)
+static_assert(4 * 2 * kTcKeys * 128 + 2 * 2 * 128 * 128 + sizeof(TcMisc) <= kTcSmem,
+              "two rings of two tiles of 128 dims beside two query tiles of 128 rows");
 
 struct TcGeometry {
     int q_half;      // bytes of 64 dims of the query tile

@@ -2,10 +2,11 @@
 // 端到端推理流程", 阶段四 4.3 (temperature, then the inverse-CDF draw of
 // sample_full_vocab), for many rows and for tokens that a draft proposed.
 //
-// A row of the vocabulary (0.5 MB at 129280 tokens) is the unit of work and one cluster's:
-// 8 CTAs (16 where there are few rows) take a contiguous chunk each, so that one row alone
-// already runs on 8 or 16 SMs, and combine their maxima and sums through distributed shared
-// memory; one launch, no workspace.
+// A row of the vocabulary (0.5 MB at 129280 tokens) is the unit of work and one cluster's,
+// whose CTAs take a contiguous chunk each and combine their maxima and sums through distributed
+// shared memory; one launch, no workspace.  k_probs: 1 to 8 CTAs up to 131072 tokens, as few as hold
+// the row, more where the rows leave SMs idle; 16 above.  k_verify: 1 to 8 by the vocabulary, up to
+// 16 for up to four sequences.
 //
 // k_probs: p = 2^((z - max z) log2(e) / T) / sum.  A CTA's chunk comes into shared memory by a
 // bulk copy and crosses HBM once each way.  Every thread takes 2^((z - m) c) of its values
@@ -14,9 +15,9 @@
 // way out.  Three CTAs fit an SM, so that the copies of some overlap the arithmetic of others.
 // Bound: bytes, at many rows (320 rows of 129280, 331 MB: 68 us, 0.72 of a copy's 6.78 TB/s; with
 // the chunk in registers two CTAs fit, and 56 of a GPC's 57 places against 32 of 38: 94 us); the
-// launch and two passes over a chunk at one (5.3 us).  k_probs_any holds the chunk in registers and reads what a larger
-// vocabulary has beyond again: for rows that begin elsewhere in a 16-byte line than their
-// results, and vocabularies above 262144.
+// launch and two passes over a chunk at one (5.3 us).  k_probs_any holds the chunk in registers and
+// reads what a larger vocabulary has beyond again: for rows that begin elsewhere in a 16-byte
+// line than their results, and vocabularies above 262144.
 //
 // k_verify: draft i is accepted while u_i q_i(d_i) < p_i(d_i) (exact: products of two
 // 24-bit numbers in FP64), which every CTA of the cluster evaluates for itself.  The
@@ -24,8 +25,9 @@
 // sampler's do, so that every order of summation gives the same total and the drawn
 // token does not depend on the split: sums of 128 consecutive tokens are kept in shared
 // memory, and only the segment that holds the target R is read a second time.  Bound: bytes
-// at many sequences (the two rows of each that decide: 60.6 MB in 17 us, 0.53 of the copy's rate, one
-// wave of clusters), latency at one (6.8 us: the drafts' probabilities, the rows, the segment).
+// and latency at many sequences (64 with up to 8 drafts, a row of each and the draft's where one
+// was rejected: 50.3 MB in 17 us, 0.44 of the copy's rate, one wave of clusters), latency at one (6.8
+// us: the drafts' probabilities, the rows, the segment).
 #include <atomic>
 
 #include "paged.h"

@@ -513,13 +513,102 @@ int ds4g_paged_attention(const ds4g_paged_kv *kv, const ds4g_paged_batch *batch,
                          void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
                          void *workspace, size_t workspace_bytes, void *cuda_stream);
 
+/* The cache of one layer in 8 bits: element d of head h of slot s of page g is
+ * code(k[g * page_stride + s * slot_stride + h * head_stride + d]) * k_scale[g * scale_stride +
+ * (s / block) * n_kv_heads + h] (v alike), the codes E4M3 (a sign, 4 bits of exponent, 3 behind the first;
+ * to 448, no infinities, NaN 0x7f and 0xff).  Strides in elements, those of the codes multiples of
+ * 16, their pointers 16-byte aligned.  block: slots that share a scale, a divisor of page_size.
+ * Scales lie in [2^-64, 2^64] (the attention takes others as the nearer bound, NaN as the lower). */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t scale_stride;
+    int n_pages;
+    int page_size;
+    int n_kv_heads;
+    int head_dim;
+    int block;
+} ds4g_paged_kv8;
+
+/* ds4g_paged_append to a cache in 8 bits; what it says of tokens, positions, pages and queries holds
+ * here.  Where a block's first slot is among a sequence's new tokens its scale becomes the least
+ * power of two s with |x| <= 448 s for the block's new rows x of that head (as rotated, in FP32; s
+ * 2^-64 at least, 2^64 at most).  Otherwise the block keeps its scale, or takes the s that its new rows
+ * ask for where that is larger; the rows that it holds already are then rounded again, which is exact
+ * but for values below 2^-6 of the new scale.  Codes are rounded to nearest even from x / s; values above
+ * 448 2^64 become 448, infinities and NaN become NaN and count for no scale.  Two sequences of one call must not
+ * store into the same block.  One launch. */
+int ds4g_paged_append8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *k, int64_t k_stride,
+                       const void *v, int64_t v_stride, const ds4g_rope *rope, const void *q, int64_t q_stride,
+                       void *q_out, int64_t q_out_stride, int n_heads, int dtype, void *cuda_stream);
+
+/* ds4g_paged_attention over a cache in 8 bits: the same call, workspace rules and status, K and V
+ * being the values that codes and scales stand for, in FP32. */
+size_t ds4g_paged_attention8_workspace_bytes(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, int n_heads);
+int ds4g_paged_attention8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
+                          void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
+                          void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* Pages that no sequence holds: a stack free_pages[0 .. n_free[0]) in an array of `capacity` (device). */
+typedef struct {
+    int32_t *free_pages;
+    int32_t *n_free; /* [1] */
+    int capacity;
+    int page_size;
+} ds4g_page_pool;
+
+/* Bring every sequence's length to want[b] (below 0: 0) and its table with it.  First the pages that
+ * shorter sequences no longer need go back to the pool, in the order of sequences and of their
+ * tables, the first of them on top (one that does not fit `capacity` is lost); their table entries become -1.
+ * Then longer ones take theirs from the top, in the same order, so that giving back what the
+ * last call took restores the pool.  A sequence whose pages exceed what is left after those that
+ * all sequences before it asked for, whose new tokens exceed max_tokens behind theirs, or whose want exceeds
+ * width * page_size is left as it was.  start [n_seqs + 1]: the new tokens of
+ * the sequences one behind the other, as ds4g_paged_batch takes them (none where a sequence
+ * became shorter).  slots, where not NULL, [max_tokens]: page * page_size + slot of each new token;
+ * entries behind the last one stay as they are.  table [n_seqs][table_stride], length, start, slots and the pool are
+ * device memory, read and written on the device: the pages of [0, ceil(length[b] / page_size)) of
+ * a table are its sequence's.  n_seqs <= 65536 (DS4G_ESIZE); want may not be length.  One launch. */
+int ds4g_paged_resize(const ds4g_page_pool *pool, int32_t *table, int width, int table_stride, int32_t *length,
+                      const int32_t *want, int n_seqs, int32_t *start, int64_t *slots, int max_tokens,
+                      void *cuda_stream);
+
 /* Synchronise the stream and report whether a bounded device-side wait gave up in any
- * ds4g_paged_attention on this workspace since the last time it was reported:
+ * ds4g_paged_attention or ds4g_paged_attention8 on this workspace since the last time it was reported:
  * DS4G_ETIMEOUT (the outputs of the calls since then are invalid; the report is cleared) or
  * DS4G_OK, also where there was no call or none with tokens. */
 int ds4g_paged_attention_status(void *workspace, void *cuda_stream);
 
 /* ---------------------------------------------------------------- drafted tokens */
+
+/* Edits of rows of logits (device memory; each part may be NULL).  History: ids [n_rows]
+ * [max_history] with a row stride, the first n_history[row] of a row (NULL: all), of them the
+ * first n_prompt[row] the prompt's (NULL: none), the others generated; ids outside the vocabulary count for
+ * nothing.  repetition, frequency, presence: [n_rows] (NULL: 1, 0, 0); repetition > 0.  Biases: ids
+ * and values [n_rows][max_bias] with a row stride, the first n_bias[row] (NULL: all); max_bias <= 1024.
+ * allowed: bit i % 32 of word i / 32 of a row, rows allowed_stride words apart (0: the same for all). */
+typedef struct {
+    const int32_t *history, *n_history, *n_prompt;
+    int64_t history_stride;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_ids, *n_bias;
+    const float *bias;
+    int64_t bias_stride;
+    const uint32_t *allowed;
+    int64_t allowed_stride;
+    int max_history;
+    int max_bias;
+} ds4g_logit_edits;
+
+/* Edit rows of logits before ds4g_probs or ds4g_sample ([P3] 阶段四 4.3).  For id i, in FP32 and in this
+ * order: where i is in the row's history z <- z > 0 ? z / repetition : z * repetition; where it is c > 0
+ * times in the generated part z <- z - (frequency * c + presence); z <- z + the sum of the row's
+ * biases of i (in FP64, rounded once); where i is not allowed z <- -inf, whatever it was.  logits, out: device f32
+ * [n_rows][n_vocab] with row strides in elements; out == logits is allowed with equal strides.
+ * n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */
+int ds4g_edit_logits(const float *logits, int64_t logits_stride, int n_rows, int n_vocab, const ds4g_logit_edits *edits,
+                     float *out, int64_t out_stride, void *cuda_stream);
 
 /* Probabilities that ds4g_sample draws from (without top-p), one row of logits each:
  * p = softmax(logits / temperature); temperature <= 0: 1 at the largest logit (the lowest

@@ -1,0 +1,89 @@
+// Edits of logits before a token is drawn from them (the draw of page "ds4.c 学习笔记 --
+// 端到端推理流程", 阶段四 4.3): for token i of a row, with `seen` = i is in the row's history and
+// c = how often it is in the part of it that was generated,
+//   z <- z / r if z > 0, else z r           where seen (repetition penalty r)
+//   z <- z - (f c + p [c > 0])              (frequency and presence penalties f, p)
+//   z <- z + the sum of the row's biases of i
+//   z <- -inf                               where the row's mask has a 0 for i.
+//
+// A CTA takes a slice of a row: a word a token in shared memory, in which every id of the history
+// that lies in the slice is counted (bit 31: seen; whole numbers, so that the order of the
+// atomics does not matter), then one pass over the slice's logits.  Biases follow: the thread of
+// the first entry of an id adds up all entries of it in FP64, in their order.
+// Bound: bytes (a logit read and written once, a bit of the mask), latency at one row.
+#include "paged.h"
+
+namespace ds4g {
+
+static constexpr int kEdThreads = 512;
+
+__global__ void __launch_bounds__(kEdThreads) k_edit(const __grid_constant__ EditArgs a, int slice, int slices)
+{
+    extern __shared__ uint32_t s_count[];
+    __shared__ int s_bias[kEditMaxBias];
+    const int tid = threadIdx.x;
+    const int row = blockIdx.x / slices, v0 = (blockIdx.x - row * slices) * slice, n = max(min(slice, a.n - v0), 0);
+    pdl_wait();
+    pdl_trigger();
+    const int hist = a.history ? min(max(a.n_history ? a.n_history[row] : a.max_history, 0), a.max_history) : 0;
+    const int prompt = hist && a.n_prompt ? min(max(a.n_prompt[row], 0), hist) : 0;
+    const int biases = a.bias_ids ? min(max(a.n_bias ? a.n_bias[row] : a.max_bias, 0), a.max_bias) : 0;
+    const int *ids = a.history + row * a.history_stride, *bias_ids = a.bias_ids + row * a.bias_stride;
+    if (hist) {
+        for (int i = tid; i < n; i += kEdThreads) s_count[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < hist; i += kEdThreads) {
+            const unsigned t = (unsigned)ids[i] - (unsigned)v0;
+            if (t >= (unsigned)n) continue;
+            if (i < prompt) atomicOr(&s_count[t], 0x80000000u);
+            else atomicAdd(&s_count[t], 1u);
+        }
+    }
+    for (int i = tid; i < biases; i += kEdThreads) s_bias[i] = bias_ids[i];
+    __syncthreads();
+    const float r = a.repetition ? a.repetition[row] : 1.f, f = a.frequency ? a.frequency[row] : 0.f,
+                p = a.presence ? a.presence[row] : 0.f;
+    const float *in = a.in + row * a.in_stride + v0;
+    float *out = a.out + row * a.out_stride + v0;
+    const uint32_t *allowed = a.allowed ? a.allowed + row * a.allowed_stride : nullptr;
+    auto edited = [&](float z, int i) {   // without the biases and the mask
+        const uint32_t w = hist ? s_count[i] : 0u;
+        if (w) {
+            z = z > 0.f ? __fdiv_rn(z, r) : __fmul_rn(z, r);
+            const uint32_t c = w & 0x7fffffffu;
+            if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(f, (float)c), p));
+        }
+        return z;
+    };
+    auto open = [&](int i) { return !allowed || (allowed[(v0 + i) >> 5] >> ((v0 + i) & 31) & 1u); };
+    for (int i = tid; i < n; i += kEdThreads) out[i] = open(i) ? edited(in[i], i) : -INFINITY;
+    if (!biases) return;
+    __syncthreads();
+    for (int k = tid; k < biases; k += kEdThreads) {
+        const int id = s_bias[k];
+        if (id < v0 || id >= v0 + n) continue;
+        bool first = true;
+        for (int j = 0; j < k; ++j) first = first && s_bias[j] != id;
+        if (!first) continue;
+        double sum = 0.0;
+        for (int j = k; j < biases; ++j)
+            if (s_bias[j] == id) sum += (double)a.bias[row * a.bias_stride + j];
+        const int i = id - v0;
+        if (open(i)) out[i] += (float)sum;
+    }
+}
+
+cudaError_t edit_rows(const EditArgs &a, cudaStream_t st, int nsm)
+{
+    // slices of a row: as many as give every SM two CTAs, of 1024 tokens or more
+    int slices = (a.n + 16383) / 16384;
+    while ((long long)slices * a.rows < 2 * nsm && a.n / (2 * slices) >= 1024) slices *= 2;
+    const int slice = ((a.n + slices - 1) / slices + 31) & ~31;
+    const size_t smem = a.history ? (size_t)slice * 4 : 0;
+    static PerDevice once;
+    cudaError_t e = allow_once(once, k_edit, (size_t)16416 * 4);
+    if (e) return e;
+    return launch_pdl(k_edit, dim3((unsigned)slices * a.rows), dim3(kEdThreads), smem, st, a, slice, slices);
+}
+
+}  // namespace ds4g

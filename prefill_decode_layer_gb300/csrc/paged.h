@@ -35,11 +35,24 @@ template <typename K> inline cudaError_t allow_once(PerDevice &once, K kernel, s
     return e;
 }
 
-// A cache's pages, copied into kernel arguments (strides in elements).
+// Element type of a cache in 8 bits beside DS4G_F32 and DS4G_BF16 (the C interface has a struct of its own for it).
+constexpr int kE4m3 = 2;
+struct e4m3 {
+    uint8_t bits;
+};
+// Bounds of an 8-bit cache's scales (ds4g_paged_kv8); anything else is taken as the nearer one, NaN as the lower.
+constexpr float kScaleMin = 0x1p-64f, kScaleMax = 0x1p64f;
+__device__ __forceinline__ float kv8_scale(float s) { return fminf(fmaxf(s, kScaleMin), kScaleMax); }
+
+// A cache's pages, copied into kernel arguments (strides in elements).  In 8 bits: a scale for each
+// `block` slots and head, [page][page_size / block][n_kv_heads] with `scale_stride` floats a page.
 struct PagedKV {
     const void *k, *v;
     long long page_stride, slot_stride, head_stride;
     int n_pages, page_size, n_kv_heads, head_dim;
+    const float *k_scale, *v_scale;
+    long long scale_stride;
+    int block;
 };
 
 // The sequences of a call, copied into kernel arguments.
@@ -59,6 +72,7 @@ struct AppendArgs {
     int n_heads;       // 0: no queries
 };
 cudaError_t paged_append(const AppendArgs &a, int in_dtype, int kv_dtype, cudaStream_t st, int nsm);
+cudaError_t paged_append8(const AppendArgs &a, int in_dtype, cudaStream_t st, int nsm);
 
 struct AttnArgs {
     PagedKV kv;
@@ -99,7 +113,40 @@ struct VerifyArgs {
     int *accepted, *tokens;
 };
 cudaError_t verify_rows(const VerifyArgs &a, int n_seqs, cudaStream_t st, int nsm);
-// Largest vocabulary of probs_rows and verify_rows.
+
+struct ResizeArgs {
+    int *free, *n_free;
+    int capacity, page_size;
+    int *table;
+    int width, table_stride;
+    int *length, *start;
+    const int *want;
+    int n_seqs, max_tokens;
+    long long *slots;   // or null
+};
+cudaError_t paged_resize(const ResizeArgs &a, cudaStream_t st);
+constexpr int kResizeMaxSeqs = 65536;
+
+struct EditArgs {
+    const float *in;
+    float *out;
+    long long in_stride, out_stride;
+    int rows, n;
+    const int *history, *n_history, *n_prompt;
+    long long history_stride;
+    int max_history;
+    const float *repetition, *frequency, *presence;
+    const int *bias_ids, *n_bias;
+    const float *bias;
+    long long bias_stride;
+    int max_bias;
+    const uint32_t *allowed;
+    long long allowed_stride;
+};
+cudaError_t edit_rows(const EditArgs &a, cudaStream_t st, int nsm);
+constexpr int kEditMaxBias = 1024;
+
+// Largest vocabulary of probs_rows, verify_rows and edit_rows.
 constexpr int kMaxRowVocab = 1 << 20;
 
 // api.cu's RoPE table fill: [n_pos][half] (cos, sin), angles in FP64.

@@ -23,6 +23,10 @@
 // chain of latencies (two launches, lengths, pages, keys, merge, parts); 32 sequences of 4000, 64
 // heads on 8 of 64, 335 MB: 138 us, an instruction in 64 % of the issue slots (21 M of the 99 M are the
 // products' FMAs), 604 MB read from DRAM because both row tiles of a K/V head read it.
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
 #include "paged_sched.cuh"
 
 namespace ds4g {
@@ -67,6 +71,32 @@ template <> struct Load<bf16, 8> {
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(u[i] << 16);
             x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+
+__device__ __forceinline__ void load_e4m3x2(uint32_t two, float &a, float &b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    a = f.x;
+    b = f.y;
+}
+template <int D> struct Load<e4m3, D> {   // the codes; the scales go to scores and weights
+    static __device__ __forceinline__ void run(const e4m3 *p, float (&x)[D])
+    {
+        uint32_t w[D / 4];
+        if constexpr (D == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x; w[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+            load_e4m3x2(w[i] & 0xffffu, x[4 * i], x[4 * i + 1]);
+            load_e4m3x2(w[i] >> 16, x[4 * i + 2], x[4 * i + 3]);
         }
     }
 };
@@ -163,8 +193,17 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
                 for (int u = 0; u < KB; ++u) at[u] = place(j0 + u);
             }
         };
-        long long at[KB];
+        // of an 8-bit cache: where the scales of this lane's key lie (of none: the cache's first)
+        constexpr bool kCodes = std::is_same<TKV, e4m3>::value;
+        auto scale_at = [&](int j) -> long long {
+            if (j < k0 || j >= k1) return 0;
+            const int pi = j / ps, page = table[pi];
+            if (page < 0 || page >= a.kv.n_pages) return 0;
+            return page * a.kv.scale_stride + (j - pi * ps) / a.kv.block * a.kv.n_kv_heads + it.head;
+        };
+        long long at[KB], sc = 0;
         int j0 = k0 / KB * KB + stream * KB;
+        if (kCodes && j0 < k1) sc = scale_at(j0 + my_key);
         if (j0 < k1) places(j0, at);
 #pragma unroll 1
         for (; j0 < k1; j0 += S * KB) {
@@ -180,6 +219,12 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
 #pragma unroll
             for (int u = 0; u < KB; ++u)
                 if (at[u] >= 0 && own) Load<TKV, D>::run(vc + at[u], v[u]);
+            float ks = 1.f, vs = 1.f;
+            if (kCodes) {
+                ks = kv8_scale(a.kv.k_scale[sc]);
+                vs = kv8_scale(a.kv.v_scale[sc]);
+                sc = scale_at(j0 + S * KB + my_key);
+            }
             places(j0 + S * KB, at);   // the next batch's pages, while these keys are on their way
             float s[NV];
 #pragma unroll
@@ -203,6 +248,7 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
             }
 #pragma unroll
             for (int x = REP / 2; x > 0; x >>= 1) s[0] += __shfl_xor_sync(lanes, s[0], x);
+            if (kCodes) s[0] *= ks;
             const int j = j0 + my_key;
             const bool see = there && j >= see_lo && j <= see_hi;
             float top = see ? s[0] : -INFINITY;
@@ -224,11 +270,12 @@ __global__ void __launch_bounds__(kPaThreads, R * D <= 16 ? 2 : 1) k_paged_attn(
             // (-1: masked.  A weight of 0 counts: it may meet an infinity or a NaN)
             const float p = see ? pa_ex2(s[0] - finite_max(m)) : -1.f;
             l += see ? p : 0.f;
+            const float pv = kCodes && see ? p * vs : p;   // (vs > 0: a mask stays one)
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int u = 0; u < KB; ++u) {
-                    const float pr = __shfl_sync(lanes, p, (r * KB + u) * REP, LPK);
+                    const float pr = __shfl_sync(lanes, pv, (r * KB + u) * REP, LPK);
                     if (!(pr < 0.f)) {   // (NaN: yes) a masked key adds nothing, whatever its V holds
 #pragma unroll
                         for (int e = 0; e < D; ++e) o[r][e] = fmaf(pr, v[u][e], o[r][e]);
@@ -563,6 +610,8 @@ cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaS
         a.rows = paged_attn_tc_rows(a.group, a.s.max_new);
         return paged_attn_tc(a, st, nsm);
     }
+    if (kv_dtype == kE4m3)
+        return q_dtype == DS4G_F32 ? simt_dim<float, e4m3>(a, nsm, st) : simt_dim<bf16, e4m3>(a, nsm, st);
     if (q_dtype == DS4G_F32)
         return kv_dtype == DS4G_F32 ? simt_dim<float, float>(a, nsm, st) : simt_dim<float, bf16>(a, nsm, st);
     return kv_dtype == DS4G_F32 ? simt_dim<bf16, float>(a, nsm, st) : simt_dim<bf16, bf16>(a, nsm, st);

@@ -105,6 +105,11 @@ def lib():
             "ds4g_paged_attention_workspace_bytes": ([vp, vp, i32], sz),
             "ds4g_paged_attention": ([vp, vp, vp, i64, vp, i64, i32, i32, C.c_float, i32, vp, sz, vp], i32),
             "ds4g_paged_attention_status": ([vp, vp], i32),
+            "ds4g_paged_append8": ([vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp], i32),
+            "ds4g_paged_attention8_workspace_bytes": ([vp, vp, i32], sz),
+            "ds4g_paged_attention8": ([vp, vp, vp, i64, vp, i64, i32, i32, C.c_float, i32, vp, sz, vp], i32),
+            "ds4g_paged_resize": ([vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, vp], i32),
+            "ds4g_edit_logits": ([vp, i64, i32, i32, vp, vp, i64, vp], i32),
             "ds4g_probs": ([vp, i64, i32, i32, C.c_float, vp, i64, vp], i32),
             "ds4g_verify_draft": ([vp, i64, i64, vp, i64, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp], i32),
             "ds4g_strerror": ([i32], C.c_char_p),
@@ -387,6 +392,25 @@ class PagedKVStruct(C.Structure):
                 ("dtype", C.c_int)]
 
 
+class PagedKV8Struct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("page_stride", C.c_int64), ("slot_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("scale_stride", C.c_int64), ("n_pages", C.c_int), ("page_size", C.c_int),
+                ("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("block", C.c_int)]
+
+
+class PagePoolStruct(C.Structure):
+    _fields_ = [("free_pages", C.c_void_p), ("n_free", C.c_void_p), ("capacity", C.c_int), ("page_size", C.c_int)]
+
+
+class LogitEditsStruct(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("n_history", C.c_void_p), ("n_prompt", C.c_void_p),
+                ("history_stride", C.c_int64), ("repetition", C.c_void_p), ("frequency", C.c_void_p),
+                ("presence", C.c_void_p), ("bias_ids", C.c_void_p), ("n_bias", C.c_void_p), ("bias", C.c_void_p),
+                ("bias_stride", C.c_int64), ("allowed", C.c_void_p), ("allowed_stride", C.c_int64),
+                ("max_history", C.c_int), ("max_bias", C.c_int)]
+
+
 class PagedBatchStruct(C.Structure):
     _fields_ = [("table", C.c_void_p), ("length", C.c_void_p), ("start", C.c_void_p),
                 ("n_seqs", C.c_int), ("n_tokens", C.c_int), ("max_new", C.c_int),
@@ -435,6 +459,8 @@ class PagedKV:
     """The paged K/V cache of one layer (ds4g_paged_kv): k and v [n_pages][page_size]
     [n_kv_heads][head_dim], of equal strides, the last dimension adjacent."""
 
+    calls = ("ds4g_paged_append", "ds4g_paged_attention", "ds4g_paged_attention_workspace_bytes")
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1 and
                  k.dtype == v.dtype and k.dtype in _DTYPES and k.device == v.device, "PagedKV")
@@ -443,6 +469,30 @@ class PagedKV:
         self.n_kv_heads, self.head_dim = h, d
         self.struct = PagedKVStruct(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                                     n, p, h, d, _DTYPES[k.dtype])
+        self.ref = C.addressof(self.struct)
+
+
+class PagedKV8:
+    """The paged K/V cache of one layer in 8 bits (ds4g_paged_kv8): codes k and v
+    (torch.float8_e4m3fn) as PagedKV's, and k_scale, v_scale (f32) [n_pages][blocks][n_kv_heads]
+    of equal strides, the last two dimensions adjacent; a scale is that of page_size / blocks
+    slots.  paged_append and paged_attention take either cache."""
+
+    calls = ("ds4g_paged_append8", "ds4g_paged_attention8", "ds4g_paged_attention8_workspace_bytes")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1 and
+                 k.dtype == v.dtype == torch.float8_e4m3fn and k_scale.dim() == 3 and k_scale.shape == v_scale.shape and
+                 k_scale.stride() == v_scale.stride() and k_scale.dtype == v_scale.dtype == torch.float32 and
+                 k.device == v.device == k_scale.device == v_scale.device, "PagedKV8")
+        n, p, h, d = k.shape
+        blocks, s = k_scale.shape[1], k_scale.stride()
+        _require(k_scale.shape[0] == n and k_scale.shape[2] == h and blocks > 0 and p % blocks == 0 and
+                 (h <= 1 or s[2] == 1) and (blocks <= 1 or s[1] == h), "PagedKV8")
+        self.k, self.v, self.k_scale, self.v_scale, self.index = k, v, k_scale, v_scale, k.get_device()
+        self.n_kv_heads, self.head_dim, self.block = h, d, p // blocks
+        self.struct = PagedKV8Struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0),
+                                     k.stride(1), k.stride(2), s[0] if n > 1 else blocks * h, n, p, h, d, self.block)
         self.ref = C.addressof(self.struct)
 
 
@@ -503,9 +553,9 @@ def _tokens(batch: PagedBatch, t: torch.Tensor) -> int:
     return n
 
 
-def paged_append(kv: PagedKV, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor, rope: Rope | None = None,
+def paged_append(kv: PagedKV | PagedKV8, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor, rope: Rope | None = None,
                  q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None) -> None:
-    """ds4g_paged_append: k, v [n_tokens][n_kv_heads][head_dim] into the cache's pages, the
+    """ds4g_paged_append, ds4g_paged_append8: k, v [n_tokens][n_kv_heads][head_dim] into the cache's pages, the
     keys rotated by `rope`; q [n_tokens][n_heads][head_dim] rotated into q_out (which may
     be q)."""
     n, h, d, dt, index, what = _tokens(batch, k), kv.n_kv_heads, kv.head_dim, k.dtype, batch.index, "paged_append"
@@ -514,28 +564,28 @@ def paged_append(kv: PagedKV, batch: PagedBatch, k: torch.Tensor, v: torch.Tenso
     ks, vs = _rows(k, n, h, d, dt, index, what), _rows(v, n, h, d, dt, index, what)
     rp = rope.ref if rope is not None else None
     if q is None:
-        _call("ds4g_paged_append", index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, None, 0,
+        _call(kv.calls[0], index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, None, 0,
               None, 0, 0, _DTYPES[dt])
         return
     _require(q.dim() == 3, what)
     heads = q.shape[1]
-    _call("ds4g_paged_append", index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, q.data_ptr(),
+    _call(kv.calls[0], index, stream, kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, q.data_ptr(),
           _rows(q, n, heads, d, dt, index, what), q_out.data_ptr(), _rows(q_out, n, heads, d, dt, index, what), heads,
           _DTYPES[dt])
 
 
-def paged_attention_workspace_bytes(kv: PagedKV, batch: PagedBatch, n_heads: int) -> int:
-    return lib().ds4g_paged_attention_workspace_bytes(kv.ref, batch.ref, n_heads)
+def paged_attention_workspace_bytes(kv: PagedKV | PagedKV8, batch: PagedBatch, n_heads: int) -> int:
+    return getattr(lib(), kv.calls[2])(kv.ref, batch.ref, n_heads)
 
 
-def paged_attention(kv: PagedKV, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+def paged_attention(kv: PagedKV | PagedKV8, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                     scale: float = 0.0, window: int = 0, stream=None) -> None:
-    """ds4g_paged_attention: q and out [n_tokens][n_heads][head_dim]; scale 0: 1 /
+    """ds4g_paged_attention, ds4g_paged_attention8: q and out [n_tokens][n_heads][head_dim]; scale 0: 1 /
     sqrt(head_dim); window 0: every position up to the token's own."""
     _require(q.dim() == 3 and q.dtype in _DTYPES and kv.index == batch.index == workspace.get_device() and
              workspace.is_contiguous(), "paged_attention")
     n, d, dt, heads, index = _tokens(batch, q), kv.head_dim, q.dtype, q.shape[1], batch.index
-    _call("ds4g_paged_attention", index, stream, kv.ref, batch.ref, q.data_ptr(),
+    _call(kv.calls[1], index, stream, kv.ref, batch.ref, q.data_ptr(),
           _rows(q, n, heads, d, dt, index, "paged_attention"), out.data_ptr(),
           _rows(out, n, heads, d, dt, index, "paged_attention"), heads, _DTYPES[dt], scale, _int32(window),
           workspace.data_ptr(), workspace.nbytes)
@@ -552,6 +602,100 @@ def paged_attention_status(workspace: torch.Tensor, stream=None) -> int:
     with torch.cuda.device(index):   # (a null stream is the current device's)
         return lib().ds4g_paged_attention_status(workspace.data_ptr(),
                                                  _raw_stream(index) if stream is None else stream.cuda_stream)
+
+
+class PagePool:
+    """Pages that no sequence holds (ds4g_page_pool): int32 device tensors free [capacity], a stack, and
+    n_free [1], its height."""
+
+    def __init__(self, free: torch.Tensor, n_free: torch.Tensor, page_size: int):
+        _require(free.dim() == 1 and free.dtype == n_free.dtype == torch.int32 and free.is_contiguous() and
+                 n_free.numel() == 1 and free.device == n_free.device and 0 < page_size < 2 ** 31, "PagePool")
+        self.free, self.n_free, self.page_size, self.index = free, n_free, page_size, free.get_device()
+        self.struct = PagePoolStruct(free.data_ptr(), n_free.data_ptr(), free.numel(), page_size)
+        self.ref = C.addressof(self.struct)
+
+
+def paged_resize(pool: PagePool, batch: PagedBatch, want: torch.Tensor, slots: torch.Tensor | None = None,
+                 max_tokens: int | None = None, stream=None) -> None:
+    """ds4g_paged_resize: the batch's lengths to want [n_seqs] (int32), its table and start with them, pages
+    from and to the pool; slots (int64, or None) gets the slot of every new token.  max_tokens: the new
+    tokens of all sequences at most (slots' size; without slots, any number)."""
+    s, n, what = batch.struct, batch.struct.n_seqs, "paged_resize"
+    _require(batch.start is not None and want.dtype == torch.int32 and want.numel() == n and want.is_contiguous() and
+             pool.index == batch.index == want.get_device() and (n == 0 or want.data_ptr() != s.length), what)
+    most = 2 ** 31 - 1 if max_tokens is None else _int32(max_tokens)
+    if slots is not None:
+        _require(slots.dtype == torch.int64 and slots.dim() == 1 and slots.is_contiguous() and
+                 slots.get_device() == batch.index and (max_tokens is None or max_tokens <= slots.numel()), what)
+        most = min(most, slots.numel())
+    _call("ds4g_paged_resize", batch.index, stream, pool.ref, s.table, s.width, s.table_stride, s.length,
+          want.data_ptr(), n, s.start, slots.data_ptr() if slots is not None else None, most)
+
+
+class LogitEdits:
+    """What edit_logits does to each row (ds4g_logit_edits).  Int32 device tensors history [n_rows]
+    [max_history], n_history and n_prompt [n_rows], bias_ids [n_rows][max_bias], n_bias [n_rows], allowed [n_rows]
+    or [1][at least n_vocab / 32 words]; f32 ones repetition, frequency, presence [n_rows], bias [n_rows]
+    [max_bias].  Each may be None; the tensors are kept, and read by each call as they then are."""
+
+    def __init__(self, history=None, n_history=None, n_prompt=None, repetition=None, frequency=None, presence=None,
+                 bias_ids=None, bias=None, n_bias=None, allowed=None):
+        what, i32, f32 = "LogitEdits", torch.int32, torch.float32
+        self.tensors = (history, n_history, n_prompt, repetition, frequency, presence, bias_ids, bias, n_bias, allowed)
+        there = [t for t in self.tensors if t is not None]
+        self.index = there[0].get_device() if there else None
+        _require(all(t.get_device() == self.index for t in there), what)
+        rows = []
+
+        def table(t, dtype):   # rows of adjacent values
+            _require(t.dim() == 2 and t.dtype == dtype and (t.shape[1] <= 1 or t.stride(1) == 1) and
+                     (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]), what)
+            rows.append(t.shape[0])
+            return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], t.shape[1]
+
+        def column(t, dtype):
+            if t is None:
+                return None
+            _require(t.dim() == 1 and t.dtype == dtype and t.is_contiguous(), what)
+            rows.append(t.shape[0])
+            return t.data_ptr()
+
+        s = self.struct = LogitEditsStruct()
+        if history is not None:
+            s.history, s.history_stride, s.max_history = table(history, i32)
+        else:
+            _require(all(t is None for t in (n_history, n_prompt, repetition, frequency, presence)), what)
+        _require((bias_ids is None) == (bias is None) and (bias is not None or n_bias is None), what)
+        if bias is not None:
+            s.bias_ids, s.bias_stride, s.max_bias = table(bias_ids, i32)
+            at, stride, most = table(bias, f32)
+            _require(stride == s.bias_stride and most == s.max_bias, what)
+            s.bias = at
+        s.n_history, s.n_prompt, s.n_bias = column(n_history, i32), column(n_prompt, i32), column(n_bias, i32)
+        s.repetition, s.frequency, s.presence = (column(t, f32) for t in (repetition, frequency, presence))
+        self.words = None   # of a row of the mask
+        if allowed is not None:
+            one = allowed.dim() == 2 and allowed.shape[0] == 1
+            s.allowed, s.allowed_stride, self.words = table(allowed, i32)
+            if one:   # any number of rows
+                s.allowed_stride = 0
+                rows.pop()
+        _require(len(set(rows)) <= 1, what)
+        self.rows = rows[0] if rows else None   # None: any number
+        self.ref = C.addressof(s)
+
+
+def edit_logits(logits: torch.Tensor, out: torch.Tensor, edits: LogitEdits, stream=None) -> None:
+    """ds4g_edit_logits: rows of f32 logits [n_rows][n_vocab] into out (which may be logits)."""
+    shape, zs, ps, index = logits.shape, logits.stride(), out.stride(), logits.get_device()
+    _require(len(shape) == 2 and shape == out.shape and logits.dtype is torch.float32 and out.dtype is torch.float32 and
+             index == out.get_device() and (shape[1] <= 1 or zs[1] == ps[1] == 1) and
+             (edits.index is None or edits.index == index), "edit_logits")
+    n, v = shape
+    _require((edits.rows is None or edits.rows == n) and (edits.words is None or 32 * edits.words >= v), "edit_logits")
+    _call("ds4g_edit_logits", index, stream, logits.data_ptr(), zs[0] if n > 1 else v, n, v, edits.ref,
+          out.data_ptr(), ps[0] if n > 1 else v)
 
 
 def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:

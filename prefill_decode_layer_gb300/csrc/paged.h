@@ -92,7 +92,11 @@ bool paged_attn_tc_ok(const PagedKV &kv, int group, int q_dtype, int kv_dtype);
 // Query rows per tile of the tensor-core form: whole tokens, at most 128 rows.
 int paged_attn_tc_rows(int group, int max_new);
 cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm);
-// Shared by the two forms (paged_attn.cu): CTAs of a launch over units of kt keys (and
+// The tensor-core form over a cache in 8 bits (paged_attn8_tc.cu): BF16 queries.
+bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype);
+int paged_attn8_tc_rows(int group, int max_new);
+cudaError_t paged_attn8_tc(AttnArgs &a, cudaStream_t st, int nsm);
+// Shared by the forms (paged_attn.cu): CTAs of a launch over units of kt keys (and
 // a.whole), and the join of the tensor-core form's parts.
 int paged_attn_grid(AttnArgs &a, int kt, int most);
 cudaError_t paged_join_tc(const AttnArgs &a, int ctas, int nsm, cudaStream_t st);

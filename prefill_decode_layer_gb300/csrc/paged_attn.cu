@@ -502,6 +502,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
 size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dtype)
 {
     size_t n = PartLayout(kAttnMaxCtas, kAttnRowsSimt, kv.head_dim).total;
+    if (kv_dtype == kE4m3) {
+        const size_t t = PartLayout(kAttnMaxCtasTc, paged_attn8_tc_rows(group, max_new), kv.head_dim).total;
+        return paged_attn8_tc_ok(kv, DS4G_BF16) && t > n ? t : n;
+    }
     if (paged_attn_tc_ok(kv, group, DS4G_BF16, kv_dtype)) {
         const size_t t = PartLayout(kAttnMaxCtasTc, paged_attn_tc_rows(group, max_new), kv.head_dim).total;
         n = t > n ? t : n;
@@ -609,6 +613,10 @@ cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaS
     if (paged_attn_tc_ok(a.kv, a.group, q_dtype, kv_dtype)) {
         a.rows = paged_attn_tc_rows(a.group, a.s.max_new);
         return paged_attn_tc(a, st, nsm);
+    }
+    if (kv_dtype == kE4m3 && paged_attn8_tc_ok(a.kv, q_dtype)) {
+        a.rows = paged_attn8_tc_rows(a.group, a.s.max_new);
+        return paged_attn8_tc(a, st, nsm);
     }
     if (kv_dtype == kE4m3)
         return q_dtype == DS4G_F32 ? simt_dim<float, e4m3>(a, nsm, st) : simt_dim<bf16, e4m3>(a, nsm, st);

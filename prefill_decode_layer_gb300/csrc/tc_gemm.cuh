@@ -555,6 +555,9 @@ cudaError_t make_map_bf16(CUtensorMap *m, const void *base, int rows, int cols, 
 // adjacent; strides of the others in elements), read in boxes of box[0] = 64 elements.
 cudaError_t make_map_bf16_nd(CUtensorMap *m, const void *base, int rank, const long long *dims,
                              const long long *strides, const int *box);
+// The same of bytes, in boxes of box[0] = 64 or 128 of them, with the swizzle of that many bytes or (0) none.
+cudaError_t make_map_u8_nd(CUtensorMap *m, const void *base, int rank, const long long *dims,
+                           const long long *strides, const int *box, int swizzle);
 
 template <bool GU, int WN, bool LO, class Epi, bool GA = false>
 static cudaError_t launch_wn(const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &xhi,

@@ -5,8 +5,8 @@
 // With K_j = ks_j k_j and V_j = vs_j v_j (codes k, v; scales ks, vs of key j's block), row r is
 //   out_r = sum_j p_rj v_j / sum_j p_rj / vs_j,
 //   p_rj = 2^(t_rj - m_r),  t_rj = (scale log2 e) ks_j (q_r . k_j) + log2 vs_j,
-// so that the scales are two numbers a key, and m_r (the running maximum of t_rj, less 9) bounds what
-// p_rj v_j adds to the row whatever the scales are.
+// so that the scales are two numbers a key, and m_r (the running maximum of t_rj, less an offset) bounds
+// what p_rj v_j adds to the row whatever the scales are.
 //
 // Both products have the keys on the MMA's M side, or the dims, and the query rows on its N
 // side: with the few rows of a decode step the tensor cores' time then falls with the rows, and the
@@ -15,23 +15,33 @@
 //                  (kind::f8f6f4).  A BF16 query is the sum of two E4M3 values, exactly: of
 //                  x in units of the row's power of two, hi = E4M3(x) holds 4 of its 8 bits and
 //                  16 (x - hi) the others.  The two are 2 x rows columns of one MMA;
-//   softmax        a thread owns a key and half of the rows; it adds the two halves, applies scales and
-//                  masks and writes P^T as FP16 to shared memory.  FP16 (11 bits down to 2^-23 of the
-//                  maximum, 2^-33 at least) and not E4M3, in which what is small beside the maximum,
-//                  but counts because it is much, would vanish;
-//   O^T += V^T P^T M 128 dims x N rows (kind::f16), of V's codes as FP16, which holds them exactly.
-//                  Four warps convert each tile from its bytes.
-// m_r moves only when a weight would exceed 2^15: nothing is reduced over keys in most units.
-// Row sums are kept per key and thread in FP32 and added up when the item ends.
+//   softmax        a thread owns a key and 8 or 16 rows; it adds the two halves, applies scales and
+//                  masks and writes P^T to shared memory.  m_r moves only when a weight would exceed
+//                  the largest that fits: nothing is reduced over keys in most units.  Row sums are
+//                  kept per key and thread in FP32 and added up when the item ends;
+//   O^T += V^T P^T M 128 dims x N rows, in one of two ways.
+// Up to 32 rows ("direct"): V's codes from their TMA tile as they are, and P as E4M3 too, four columns a
+// row: a weight p as hi + lo / 16 like the queries, and weights below 2^-10 of the maximum in a pair of
+// columns of their own, in units of 2^-13 (E4M3 alone has 2^-9 .. 448: many small weights beside a large one would
+// vanish).  8 bits of each weight, or 2^-32 of the largest.
+// More rows: four times the columns would cost more than V's conversion.  Four warps make FP16 of V's
+// codes (the bits of an E4M3 value, its sign in front and the other seven from bit 7 on, are FP16 for
+// 2^-8 of it, also where it is subnormal) and P is FP16 (11 bits, or 2^-34 of the largest).
 //
 // Masked places: a key outside the item's keys or in a missing page, or hidden from a row, gets the
-// weight 0; its row of V becomes zeros in the conversion.  NaN codes in V become 0 as well, and rows
-// that see such a key get their NaN when the item ends.
+// weight 0.  In units at an edge (of the item's keys, or of what some rows see) the rows of V outside the
+// item's keys are zeroed in the tile, and NaN codes of keys that only some rows see become 0; rows
+// that see such a key get their NaN when the item ends.  (In FP16 the bits of a NaN code are finite: every
+// NaN is dealt with when the item ends.)
 //
-// Roles (480 threads, one CTA per SM): warps 0-3 and 4-7 softmax and output of the two halves of
-// the rows; warps 8-11 queries, scales and V's conversion; warp 12 the items and the TMA copies;
-// warps 13 and 14 (one thread each) the MMAs of S and of O.  Every wait is bounded; a CTA that gives up
-// says so in its status word, drains its copies and MMAs, frees its TMEM and returns.
+// Roles (one CTA per SM): one to four groups of four warps, softmax and output of 8 or 16 rows each; four
+// warps for the queries' codes and V's tiles; one warp each for the items and TMA copies, the MMAs of S, the
+// MMAs of O (one thread each) and the scales.  Page look-ups and scales are fetched for 32 boxes or blocks at
+// a time, one round ahead.  Every wait is bounded; a CTA that gives up says so in its status word, drains
+// its copies and MMAs, frees its TMEM and returns.
+//
+// Code that runs once a unit is kept small (rolled loops, one place for each wait): in a first form with 32
+// rows a thread, 174 KB of instructions, a fifth of the warps' time went to fetching them.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <stddef.h>
@@ -44,18 +54,29 @@ namespace ds4g {
 
 static constexpr int kT8Keys = 128;                    // keys of a unit
 static constexpr int kT8Rows = 64;                     // query rows of a tile at most
-static constexpr int kT8Soft = 256, kT8Conv = 128;     // threads of the softmax, of the conversion
-static constexpr int kT8Threads = kT8Soft + kT8Conv + 96;
-static constexpr int kT8ConvWarp = kT8Soft / 32, kT8Tma = kT8ConvWarp + kT8Conv / 32, kT8Mma = kT8Tma + 1;
-static constexpr int kT8MaxSlots = 4;                  // tiles of K, and of V, at most
+static constexpr int kT8MaxSlots = 6;                  // tiles of K, and of V, at most
 static constexpr int kT8Items = 4;                     // items ahead of the softmax at most
-static constexpr int kT8Scales = 4;                    // units whose scales are there at most
+static constexpr int kT8Scales = 4;                    // rounds of scales that are there at most
 static constexpr int kT8Smem = 227 * 1024;
-static constexpr float kT8Off = 9.f, kT8Most = 15.f;   // log2 of the largest weight when m is set, and before it moves
+
+// What follows from the columns of query rows NR (8, 16, 32 or 64) of a kernel.
+template <int NR> struct T8 {
+    static constexpr bool direct = NR <= 32;
+    static constexpr int own = NR < 16 ? NR : 16;      // rows of a softmax thread
+    static constexpr int groups = NR / own;
+    static constexpr int soft = groups * 128;          // softmax threads
+    static constexpr int conv = groups * 4;            // warps: the first of the queries and V's tiles, then ..
+    static constexpr int tma = conv + 4, mma_s = tma + 1, mma_o = tma + 2, scale = tma + 3;
+    static constexpr int threads = (scale + 1) * 32;
+    static constexpr int s_cols = 2 * NR, o_cols = direct ? 4 * NR : NR;   // of a unit, of an item
+    static constexpr int cols = 2 * s_cols + 2 * o_cols <= 128 ? 128 : 2 * s_cols + 2 * o_cols <= 256 ? 256 : 512;
+    // log2 of the largest weight when m is set, and of the largest that fits
+    static constexpr float off = direct ? 5.f : 9.f, most = direct ? 8.f : 15.f;
+};
 
 struct T8Misc {
     uint64_t k_full[kT8MaxSlots], k_empty[kT8MaxSlots], v_full[kT8MaxSlots], v_empty[kT8MaxSlots];
-    uint64_t w_full[2], w_empty[2];                    // V tiles in FP16
+    uint64_t w_full[kT8MaxSlots], w_empty[2];          // V's tile may be used: by slot, or of unit u % 2 in FP16
     uint64_t sc_full[kT8Scales], sc_empty[kT8Scales];
     uint64_t q_full[2], q_empty[2];                    // of item i % 2
     uint64_t s_full[2], p_full[2], p_empty[2];         // of unit u % 2
@@ -64,16 +85,15 @@ struct T8Misc {
     uint64_t done[2];
     PagedItem item[kT8Items];
     PagedCursor cur;
-    long long scratch[kT8Threads / 32];
-    float2 sc[kT8Scales][kT8Keys];                     // of a unit's keys: ks scale log2 e, log2 vs (-inf: masked)
-    uint32_t valid[kT8Scales][4];                      // a bit per key of the unit
-    int poison[kT8Items];                              // a V row of the item that counts has a NaN
+    long long scratch[24];
+    float2 sc[kT8Scales][kT8Keys];                     // of a round's blocks: ks scale log2 e, log2 vs (-inf: no page)
+    int poison[kT8Items];                              // a V row of the item has a NaN that was taken out
     uint32_t tmem;
     int abort_flag;
-    __align__(16) float q_scale[kT8Items][kT8Rows];      // of an item's rows (in item_full's slot: read until item_empty)
-    __align__(16) float neg_m[kT8Rows], factor[kT8Rows];
-    float part[8][32];                                 // of a softmax warp: a value of each row
-    int pos[kT8Rows];
+    __align__(16) float q_scale[kT8Items][kT8Rows];    // of an item's rows
+    __align__(16) float neg_m[kT8Rows], factor[kT8Rows], delta[kT8Rows];
+    float part[16][16];                                // of a softmax warp: a value of each row
+    int pos[kT8Rows], set[kT8Rows];                    // of a row: its position; it has an m
     long long off[kT8Rows];                            // of a row in the output
 };
 
@@ -81,6 +101,9 @@ struct T8Geometry {
     int k_slots, v_slots;
     int box;         // slots of a page in one copy: gcd(page_size, 128)
     int page_shift;  // log2(page_size), or -1
+    // scales: one for every 2^gran keys of a unit at least (the part of the block size that divides 128), so
+    // many a unit, and the units of a round: 32 scales, or one unit where it has more
+    int gran, per_unit, round;
 };
 
 bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype)
@@ -95,52 +118,95 @@ int paged_attn8_tc_rows(int group, int max_new)
     return (rows + tiles - 1) / tiles;
 }
 
+// mbar_wait with one place for the poll (it is inlined where every unit passes).
+__device__ __forceinline__ bool t8_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag)
+{
+    long long t0 = 0;
+    for (unsigned n = 0;; ++n) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((n & 255u) == 0) {
+            const long long t = clock64();
+            if (n == 0) t0 = t;
+            else if (*abort_flag || t - t0 > kWaitCycles) return false;
+        }
+    }
+}
 __device__ __forceinline__ uint32_t t8_e4m3x2(float lo, float hi)
 {
     unsigned short r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t t8_f16x2(uint32_t codes)   // of the low two bytes
+__device__ __forceinline__ float2 t8_floats(uint32_t codes)   // of the low two bytes
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
-    return h;
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-// Barrier `id` of the n threads that use it, which tells each whether any of them says so.
-template <int N> __device__ __forceinline__ bool t8_any(int id, bool yes)
+// Two values as codes, and 16 times what the codes leave of them.
+__device__ __forceinline__ void t8_split(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = t8_e4m3x2(a, b);
+    const float2 f = t8_floats(hi);
+    lo = t8_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
+}
+// Barrier `id` of the 128 threads that use it, which tells each whether any of them says so.
+__device__ __forceinline__ bool t8_any(int id, bool yes)
 {
     uint32_t any;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n"
+        "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 128, q;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(any)
-        : "r"((uint32_t)yes), "r"(id), "n"(N)
+        : "r"((uint32_t)yes), "r"(id)
         : "memory");
     return any != 0;
 }
-template <int N> __device__ __forceinline__ void t8_sync(int id)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
-}
+__device__ __forceinline__ void t8_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float t8_ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two rows' values of an array of floats in shared memory.
+__device__ __forceinline__ ulonglong2 t8_rows4(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+
+// The least and the greatest position of an item's rows.
+__device__ __forceinline__ int2 t8_ends(const PagedItem &it)
+{
+    return make_int2(max(it.pos0 + it.tok_a, -1), max(it.pos0 + it.tok_b, -1));
+}
+// Whether some of its rows see a key of the unit from `base` that others do not.
+__device__ __forceinline__ bool t8_by_row(int2 ends, int base, int window)
+{
+    return base + kT8Keys - 1 > ends.x || (window > 0 && base <= ends.y - window);
+}
+
+// A place in a ring (kept up to date: no division at every use).
+struct T8Place {
+    unsigned slot, phase;
+    __device__ __forceinline__ void next(unsigned slots)
+    {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // HD: head_dim.  NR: columns of query rows, the tile's rows or more.
 template <int HD, int NR>
-__global__ void __launch_bounds__(kT8Threads, 1)
+__global__ void __launch_bounds__(T8<NR>::threads, 1)
     k_paged_attn8_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ AttnArgs a, const __grid_constant__ T8Geometry geo)
 {
+    using P = T8<NR>;
+    constexpr bool kDirect = P::direct;
     constexpr int H = HD / 64;                          // 128-byte blocks of an FP16 row
     constexpr uint32_t kTile = HD * kT8Keys;            // bytes of a K or V tile of codes
-    constexpr uint32_t kWide = 2 * kTile;               // of V in FP16
+    constexpr uint32_t kWide = kDirect ? 0 : 2 * kTile; // of V in FP16
     constexpr uint32_t kQ = 2 * NR * HD, kP = kT8Keys * 128;
-    constexpr uint32_t kCols = NR == 64 ? 512 : NR == 32 ? 256 : 128;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *wide = sm, *pbuf = wide + 2 * kWide, *qbuf = pbuf + 2 * kP, *kring = qbuf + 2 * kQ;
     unsigned char *vring = kring + (uint32_t)geo.k_slots * kTile;
@@ -155,17 +221,18 @@ __global__ void __launch_bounds__(kT8Threads, 1)
         auto in = [&](const uint64_t *b, int count) { return bars + i >= b && bars + i < b + count; };
         if (i < n) {
             int count = 1;
-            if (in(x.v_empty, kT8MaxSlots) || in(x.w_full, 2) || in(x.sc_full, kT8Scales) || in(x.q_full, 2)) count = kT8Conv / 32;
-            else if (in(x.sc_empty, kT8Scales) || in(x.p_full, 2) || in(x.o_free, 2)) count = kT8Soft / 32;
-            else if (in(x.item_empty, kT8Items)) count = kT8Soft / 32 + kT8Conv / 32 + 2;
+            if (in(x.w_full, kT8MaxSlots) || in(x.q_full, 2)) count = 4;
+            else if (in(x.v_empty, kT8MaxSlots)) count = kDirect ? 5 : 4;
+            else if (in(x.sc_empty, kT8Scales) || in(x.p_full, 2) || in(x.o_free, 2)) count = 4 * P::groups;
+            else if (in(x.item_empty, kT8Items)) count = 4 * P::groups + 4 + 3;
             mbar_init(bars + i, count);
         } else if (i == n) {
             x.abort_flag = 0;
         }
         mbar_fence_init();
     }
-    if (warp == kT8Mma) tmem_alloc(&x.tmem, kCols);
-    if (threadIdx.x == kT8Tma * 32) {
+    if (warp == P::mma_s) tmem_alloc(&x.tmem, P::cols);
+    if (threadIdx.x == P::tma * 32) {
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
@@ -173,45 +240,32 @@ __global__ void __launch_bounds__(kT8Threads, 1)
     pdl_trigger();
     paged_begin(a, lay);
     const bool few = a.s.n_seqs <= 32;   // the copying warp finds the CTA's share by itself
-    if (!few) paged_cursor<kT8Threads>(a, kT8Keys, &x.cur, x.scratch);
+    if (!few) paged_cursor<P::threads>(a, kT8Keys, &x.cur, x.scratch);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = x.tmem;   // S of unit u: column (u % 2) 2 NR; O of item i: 4 NR + (i % 2) NR
+    const uint32_t tmem = x.tmem, tmem_o = tmem + 2 * P::s_cols;   // S of unit u % 2; O of item i % 2
     volatile int *ab = &x.abort_flag;
     auto give_up = [&]() {
         x.abort_flag = 1;
         reinterpret_cast<int *>(a.ws + lay.status)[blockIdx.x] = kAttnTimedOut;
     };
     auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)) != 0;
-    };
-    // a place in a ring (kept up to date: no division at every use)
-    struct Place {
-        unsigned slot, phase;
-        __device__ __forceinline__ void next(unsigned slots)
-        {
-            if (++slot == slots) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        }
+        return __all_sync(0xffffffffu, t8_wait(bar, parity, ab)) != 0;
     };
 
-    if (warp == kT8Tma) {
+    if (warp == P::tma) {
         // ---------------- items, page look-ups, copies
         PagedCursor cur;
         if (few) paged_cursor_warp(a, kT8Keys, cur);
         else cur = x.cur;
         const int boxes = kT8Keys / geo.box, ps = a.kv.page_size;
         int used_k = -1, used_v = -1;   // lane i: the phase of the last load into slot i
-        Place kp = {0, 0}, vp = {0, 0};
+        T8Place kp = {0, 0}, vp = {0, 0};
         bool ok = true;
         for (unsigned i = 0; ok; ++i) {
-            if (!warp_wait(&x.item_empty[i % kT8Items], (i / kT8Items & 1u) ^ 1u)) {
-                ok = false;
-                break;
-            }
+            ok = warp_wait(&x.item_empty[i % kT8Items], (i / kT8Items & 1u) ^ 1u);
+            if (!ok) break;
             PagedItem &it = x.item[i % kT8Items];
             if (lane == 0) {
                 paged_next(a, kT8Keys, cur, lay, it);
@@ -222,37 +276,51 @@ __global__ void __launch_bounds__(kT8Threads, 1)
             if (!it.more) break;
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
             const int lo = it.lo, hi = it.hi, head = it.head, t1 = it.t1;
-            // this lane's box of tile t: whether it is copied, its page and first slot
-            int page = -1, slot = 0;
-            auto look = [&](int t) {
-                const int j = t * kT8Keys + lane * geo.box;
-                const bool load = t < t1 && lane < boxes && j < hi && j + geo.box > lo;
+            // a look-up is of 32 boxes: the lane's box of the group of tiles from tg, its page and first slot
+            const int group = 32 / boxes, my_tile = lane / boxes, my_box = lane - my_tile * boxes;
+            int page = -1, slot = 0, at = 0, from = 0, in_group = group;
+            uint32_t loads = 0;
+            bool load = false;
+            auto look = [&](int tg) {
+                const int j = (tg + my_tile) * kT8Keys + my_box * geo.box;
+                load = tg + my_tile < t1 && j < hi && j + geo.box > lo;
                 if (load) {
                     const int p = geo.page_shift >= 0 ? j >> geo.page_shift : j / ps;
                     slot = j - p * ps;
                     page = table[p];
                 }
-                return load;
             };
-            bool load = look(it.t0);
-            for (int t = it.t0; ok && t < t1; ++t) {
-                // a page that is not there: out of bounds, read as zeros
-                const int at = page < 0 || page >= a.kv.n_pages ? a.kv.n_pages : page, from = slot;
-                const bool mine = load;
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * geo.box * HD;
-                load = look(t + 1);   // on its way while the slots become free
-                auto copy = [&](uint64_t *full, uint64_t *empty, Place &p, unsigned slots, unsigned char *ring, const CUtensorMap *map,
-                                int &used) {
-                    if (!warp_wait(&empty[p.slot], p.phase ^ 1u)) return false;
-                    if (lane == 0) mbar_expect_tx(&full[p.slot], bytes);
-                    if (lane == (int)p.slot) used = (int)p.phase;
+            // (two look-ups before the first tile, then one at the first tile of every group)
+#pragma unroll 1
+            for (int t = it.t0 - group; ok && t < t1; ++t, ++in_group) {
+                if (in_group == group) {
+                    // a page that is not there: out of bounds, read as zeros
+                    at = page < 0 || page >= a.kv.n_pages ? a.kv.n_pages : page;
+                    from = slot;
+                    loads = __ballot_sync(0xffffffffu, load);
+                    look(t + group);   // on its way meanwhile
+                    in_group = 0;
+                    if (t < it.t0) {
+                        t = it.t0 - 1;
+                        in_group = group - 1;
+                        continue;
+                    }
+                }
+                const uint32_t tile = loads & ((1u << boxes) - 1u) << (in_group * boxes);
+                const uint32_t bytes = (uint32_t)__popc(tile) * geo.box * HD;
+#pragma unroll 1
+                for (int v = 0; ok && v < 2; ++v) {   // K, then V
+                    T8Place &p = v ? vp : kp;
+                    uint64_t *full = (v ? x.v_full : x.k_full) + p.slot;
+                    ok = warp_wait((v ? x.v_empty : x.k_empty) + p.slot, p.phase ^ 1u);
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(full, bytes);
+                    if (lane == (int)p.slot) (v ? used_v : used_k) = (int)p.phase;
                     __syncwarp();
-                    if (mine) tma_load_4d(ring + p.slot * kTile + lane * geo.box * HD, map, 0, from, head, at, &full[p.slot]);
-                    p.next(slots);
-                    return true;
-                };
-                ok = copy(x.k_full, x.k_empty, kp, geo.k_slots, kring, &kmap, used_k) &&
-                     copy(x.v_full, x.v_empty, vp, geo.v_slots, vring, &vmap, used_v);
+                    if (tile >> lane & 1u)
+                        tma_load_4d((v ? vring : kring) + p.slot * kTile + my_box * geo.box * HD, v ? &vmap : &kmap, 0, from, head, at, full);
+                    p.next(v ? geo.v_slots : geo.k_slots);
+                }
             }
         }
         if (!ok) give_up();
@@ -260,27 +328,27 @@ __global__ void __launch_bounds__(kT8Threads, 1)
         volatile int never = 0;
         if (used_k >= 0) mbar_wait(&x.k_full[lane], (uint32_t)used_k, &never);
         if (used_v >= 0) mbar_wait(&x.v_full[lane], (uint32_t)used_v, &never);
-    } else if (warp == kT8Mma) {
+    } else if (warp == P::mma_s) {
         // ---------------- S of every unit, up to two ahead of its softmax
         if (elect_one()) {
-            const uint32_t id = idesc_e4m3_f32(kT8Keys, 2 * NR);
+            const uint32_t id = idesc_e4m3_f32(kT8Keys, P::s_cols);
             unsigned u = 0, item = 0;
             int left = 0;
-            Place kp = {0, 0};
+            T8Place kp = {0, 0};
             bool ok = true;
             while (ok) {
                 if (left == 0) {
-                    ok = mbar_wait(&x.item_full[item % kT8Items], item / kT8Items & 1u, ab);
+                    ok = t8_wait(&x.item_full[item % kT8Items], item / kT8Items & 1u, ab);
                     if (!ok) break;
                     const PagedItem &it = x.item[item % kT8Items];
                     if (!it.more) break;
                     left = it.t1 - it.t0;
                     mbar_arrive(&x.item_empty[item % kT8Items]);
-                    ok = mbar_wait(&x.q_full[item & 1], item >> 1 & 1u, ab);
+                    ok = t8_wait(&x.q_full[item & 1], item >> 1 & 1u, ab);
                     ++item;
                 }
-                ok = ok && (u < 2 || mbar_wait(&x.p_full[u & 1], ((u - 2) >> 1) & 1u, ab)) &&   // S of unit u - 2 has been read
-                     mbar_wait(&x.k_full[kp.slot], kp.phase, ab);
+                ok = ok && (u < 2 || t8_wait(&x.p_full[u & 1], ((u - 2) >> 1) & 1u, ab)) &&   // S of unit u - 2 has been read
+                     t8_wait(&x.k_full[kp.slot], kp.phase, ab);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t ka = smem_u32(kring) + kp.slot * kTile, qa = smem_u32(qbuf) + ((item - 1) & 1) * kQ;
@@ -288,7 +356,7 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                 const uint64_t qd = HD == 128 ? sdesc_kmajor_sw128(qa) : sdesc_kmajor_sw64(qa);
 #pragma unroll
                 for (int ks = 0; ks < HD / 32; ++ks)
-                    tc_mma_e4m3(tmem + (u & 1) * 2 * NR, kd + (uint64_t)(ks * 2), qd + (uint64_t)(ks * 2), id, ks > 0);
+                    tc_mma_e4m3(tmem + (u & 1) * P::s_cols, kd + (uint64_t)(ks * 2), qd + (uint64_t)(ks * 2), id, ks > 0);
                 tc_commit(&x.s_full[u & 1]);
                 tc_commit(&x.k_empty[kp.slot]);
                 kp.next(geo.k_slots);
@@ -300,38 +368,61 @@ __global__ void __launch_bounds__(kT8Threads, 1)
             tc_commit(&x.done[0]);
             mbar_wait(&x.done[0], 0, &never);
         }
-    } else if (warp == kT8Mma + 1) {
+    } else if (warp == P::mma_o) {
         // ---------------- O of every unit
         if (elect_one()) {
-            const uint32_t id = idesc_f16_f32_mn(128, NR);
+            const uint32_t id = kDirect ? idesc_e4m3_f32_mn(128, P::o_cols) : idesc_f16_f32_mn(128, P::o_cols);
             unsigned u = 0, item = 0;
-            int left = 0;
+            int left = 0, base = 0, lo = 0, hi = 0;
+            int2 ends = make_int2(0, 0);
+            T8Place vp = {0, 0};
             bool ok = true, fresh = true;
             while (ok) {
                 if (left == 0) {
-                    ok = mbar_wait(&x.item_full[item % kT8Items], item / kT8Items & 1u, ab);
+                    ok = t8_wait(&x.item_full[item % kT8Items], item / kT8Items & 1u, ab);
                     if (!ok) break;
                     const PagedItem &it = x.item[item % kT8Items];
                     if (!it.more) break;
                     left = it.t1 - it.t0;
+                    base = it.t0 * kT8Keys;
+                    lo = it.lo;
+                    hi = it.hi;
+                    ends = t8_ends(it);
                     mbar_arrive(&x.item_empty[item % kT8Items]);
-                    ok = item < 2 || mbar_wait(&x.o_free[item & 1], ((item - 2) >> 1) & 1u, ab);
+                    ok = item < 2 || t8_wait(&x.o_free[item & 1], ((item - 2) >> 1) & 1u, ab);
                     fresh = true;
                     ++item;
                 }
-                ok = ok && mbar_wait(&x.w_full[u & 1], u >> 1 & 1u, ab) && mbar_wait(&x.p_full[u & 1], u >> 1 & 1u, ab);
-                if (!ok) break;
-                tc_fence_after();
-                // (64 dims: rows 64 .. 127 of the MMA repeat or run past the others, and are not read)
-                const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(wide) + (u & 1) * kWide, 1024, H * 1024);
-                const uint64_t pd = sdesc_mnmajor_sw128(smem_u32(pbuf) + (u & 1) * kP, 1024, 1024);
+                const uint32_t d = tmem_o + ((item - 1) & 1) * P::o_cols, pa = smem_u32(pbuf) + (u & 1) * kP;
+                if (kDirect) {
+                    const bool edge = base < lo || base + kT8Keys > hi || t8_by_row(ends, base, a.window);
+                    ok = ok && t8_wait(&x.v_full[vp.slot], vp.phase, ab) &&
+                         (!edge || t8_wait(&x.w_full[vp.slot], vp.phase, ab)) && t8_wait(&x.p_full[u & 1], u >> 1 & 1u, ab);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // (64 dims: rows 64 .. 127 of the MMA run on into what lies behind, and are not read)
+                    const uint32_t va = smem_u32(vring) + vp.slot * kTile;
+                    const uint64_t vd = HD == 128 ? sdesc_mnmajor_sw128(va, 1024, 1024) : sdesc_mnmajor_sw64(va, 512, 512);
+                    const uint64_t pd = sdesc_mnmajor_sw128(pa, 1024, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kT8Keys / 16; ++ks)
-                    tc_mma_bf16(tmem + 4 * NR + ((item - 1) & 1) * NR, vd + (uint64_t)(ks * 2 * H * 1024 >> 4),
-                                pd + (uint64_t)(ks * 2 * 1024 >> 4), id, !fresh || ks > 0);
+                    for (int ks = 0; ks < kT8Keys / 32; ++ks)
+                        tc_mma_e4m3(d, vd + (uint64_t)(ks * 32 * HD >> 4), pd + (uint64_t)(ks * 32 * 128 >> 4), id, !fresh || ks > 0);
+                    tc_commit(&x.v_empty[vp.slot]);
+                } else {
+                    ok = ok && t8_wait(&x.w_full[u & 1], u >> 1 & 1u, ab) && t8_wait(&x.p_full[u & 1], u >> 1 & 1u, ab);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = sdesc_mnmajor_sw128(smem_u32(wide) + (u & 1) * kWide, 1024, H * 1024);
+                    const uint64_t pd = sdesc_mnmajor_sw128(pa, 1024, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < kT8Keys / 16; ++ks)
+                        tc_mma_bf16(d, vd + (uint64_t)(ks * 2 * H * 1024 >> 4), pd + (uint64_t)(ks * 2 * 1024 >> 4), id, !fresh || ks > 0);
+                    tc_commit(&x.w_empty[u & 1]);
+                }
                 fresh = false;
-                tc_commit(&x.w_empty[u & 1]);
                 tc_commit(&x.p_empty[u & 1]);
+                vp.next(geo.v_slots);
+                base += kT8Keys;
                 ++u;
                 --left;
             }
@@ -340,328 +431,414 @@ __global__ void __launch_bounds__(kT8Threads, 1)
             tc_commit(&x.done[1]);
             mbar_wait(&x.done[1], 0, &never);
         }
-    } else if (warp >= kT8ConvWarp) {
-        // ---------------- queries to pairs of codes; scales of every unit; V to FP16
-        const int t = threadIdx.x - kT8Soft, cw = t >> 5, ps = a.kv.page_size;
+    } else if (warp == P::scale) {
+        // ---------------- scales, 32 a step: fetched while those before them are stored, their pages a step earlier
+        const int ps = a.kv.page_size, unit_shift = 7 - geo.gran, steps = geo.per_unit > 32 ? geo.per_unit / 32 : 1;   // of a round
+        unsigned n = 0;   // rounds stored
+        bool ok = true;
+        for (unsigned i = 0; ok; ++i) {
+            ok = warp_wait(&x.item_full[i % kT8Items], i / kT8Items & 1u);
+            if (!ok) break;
+            const PagedItem &it = x.item[i % kT8Items];
+            if (!it.more) break;
+            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, head = it.head;
+            const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.item_empty[i % kT8Items]);
+            const int all = (units + geo.round - 1) / geo.round * steps;
+            int page = -1, next_slot = 0;
+            float k = 0.f, v = 0.f;
+#pragma unroll 1
+            for (int s = -2, in_round = 0; ok && s < all; ++s) {
+                if (s >= 0) {
+                    if (in_round == 0) ok = warp_wait(&x.sc_empty[n % kT8Scales], (n / kT8Scales & 1u) ^ 1u);
+                    x.sc[n % kT8Scales][in_round * 32 + lane] =
+                        make_float2(fminf(k * a.scale_log2, 3.402823466e38f), v > 0.f ? log2f(v) : -INFINITY);
+                    if (++in_round == steps) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&x.sc_full[n % kT8Scales]);
+                        in_round = 0;
+                        ++n;
+                    }
+                }
+                k = v = 0.f;   // (no page)
+                if (page >= 0 && page < a.kv.n_pages) {
+                    const long long at = page * a.kv.scale_stride + next_slot / a.kv.block * a.kv.n_kv_heads + head;
+                    k = kv8_scale(a.kv.k_scale[at]);
+                    v = kv8_scale(a.kv.v_scale[at]);
+                }
+                // the first key of this lane's scale of step s + 2
+                page = -1;
+                const int f = (s + 2) * 32 + lane, unit = f >> unit_shift;
+                const int j = (tile0 + unit) * kT8Keys + ((f & (geo.per_unit - 1)) << geo.gran);
+                if (unit < units && j < hi && j + (1 << geo.gran) > lo) {
+                    const int p = geo.page_shift >= 0 ? j >> geo.page_shift : j / ps;
+                    next_slot = j - p * ps;
+                    page = table[p];
+                }
+            }
+        }
+        if (!ok) give_up();
+    } else if (warp >= P::conv) {
+        // ---------------- queries to pairs of codes; V's tiles
+        const int t = threadIdx.x - P::soft, bar = 1 + P::groups;
         const bf16 *qp = static_cast<const bf16 *>(a.q);
-        unsigned u0 = 0;   // units before this item
-        Place vp = {0, 0};
+        unsigned u = 0;
+        T8Place vp = {0, 0};
         for (unsigned i = 0;; ++i) {
             bool ok = warp_wait(&x.item_full[i % kT8Items], i / kT8Items & 1u);
-            if (t8_any<kT8Conv>(3, !ok)) {
+            if (t8_any(bar, !ok)) {
                 give_up();
                 break;
             }
             const PagedItem &it = x.item[i % kT8Items];
             if (!it.more) break;
-            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, head = it.head;
-            const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
-            // queries: LPR threads a row, 8 dims each
-            constexpr int LPR = HD / 8, RPP = kT8Conv / LPR, PASSES = NR / RPP > 0 ? NR / RPP : 1;
-            const int sub = t % LPR;
-            uint4 qw[PASSES];
+            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, n_rows = it.n_rows;
+            const int2 ends = t8_ends(it);
+            // queries: LPR threads a row, 8 dims each, two rows a thread at a time
+            constexpr int LPR = HD / 8, RPP = 128 / LPR;
+            constexpr int PASSES = NR > RPP ? NR / RPP : 1, BATCH = PASSES < 2 ? PASSES : 2;
+            const int sub = t % LPR, r_first = t / LPR;
+            uint4 qw[BATCH];
+            auto fetch = [&](int p0) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int r = p * RPP + t / LPR;
-                qw[p] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < it.n_rows) {
-                    const int row = it.row0 + r, tok = row / a.group, hd = row - tok * a.group;
-                    qw[p] = *reinterpret_cast<const uint4 *>(qp + (long long)(it.token + tok) * a.q_stride +
-                                                             (head * a.group + hd) * HD + sub * 8);
+                for (int p = 0; p < BATCH; ++p) {
+                    const int r = (p0 + p) * RPP + r_first;
+                    qw[p] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < n_rows) {
+                        const int row = it.row0 + r, tok = row / a.group, hd = row - tok * a.group;
+                        qw[p] = *reinterpret_cast<const uint4 *>(qp + (long long)(it.token + tok) * a.q_stride +
+                                                                 (it.head * a.group + hd) * HD + sub * 8);
+                    }
                 }
-            }
-            // this thread's key of unit k: its page (-1: masked), its scales
-            auto page_of = [&](int k) {
-                const int j = (tile0 + k) * kT8Keys + t;
-                if (k >= units || j < lo || j >= hi) return -1;
-                const int p = table[geo.page_shift >= 0 ? j >> geo.page_shift : j / ps];
-                return p < a.kv.n_pages ? p : -1;
             };
-            struct Scales {
-                float k, v;
-                bool there;
-            };
-            auto scales = [&](int page, int k) {
-                Scales s = {1.f, 1.f, page >= 0};
-                if (page >= 0) {
-                    const int j = (tile0 + k) * kT8Keys + t;
-                    const int slot = geo.page_shift >= 0 ? j & (ps - 1) : j % ps;
-                    const long long at = page * a.kv.scale_stride + slot / a.kv.block * a.kv.n_kv_heads + head;
-                    s.k = a.kv.k_scale[at];
-                    s.v = a.kv.v_scale[at];
-                }
-                return s;
-            };
-            auto publish = [&](const Scales &s, int k) {
-                const unsigned u = u0 + k, slot = u % kT8Scales;
-                ok = ok && warp_wait(&x.sc_empty[slot], (u / kT8Scales & 1u) ^ 1u);
-                const float kc = fminf(kv8_scale(s.k) * a.scale_log2, 3.402823466e38f);
-                x.sc[slot][t] = make_float2(kc, s.there ? log2f(kv8_scale(s.v)) : -INFINITY);
-                const uint32_t bits = __ballot_sync(0xffffffffu, s.there);
-                if (lane == 0) x.valid[slot][cw] = bits;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&x.sc_full[slot]);
-            };
-            int page = page_of(0);
-            Scales next = scales(page, 0);
-            page = page_of(1);
+            fetch(0);
             ok = ok && warp_wait(&x.q_empty[i & 1], (i >> 1 & 1u) ^ 1u);
             unsigned char *q8 = qbuf + (i & 1) * kQ;
+#pragma unroll 1
+            for (int p0 = 0; p0 < PASSES; p0 += BATCH) {
+                uint4 w4[BATCH];
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int r = p * RPP + t / LPR;
-                const uint32_t w[4] = {qw[p].x, qw[p].y, qw[p].z, qw[p].w};
-                float y[8], top = 0.f;
+                for (int p = 0; p < BATCH; ++p) w4[p] = qw[p];
+                fetch(p0 + BATCH);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[2 * e] = __uint_as_float(w[e] << 16);
-                    y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                }
+                for (int p = 0; p < BATCH; ++p) {
+                    const int r = (p0 + p) * RPP + r_first;
+                    const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
+                    float y[8], top = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = fabsf(y[e]) <= 3.402823466e38f ? fmaxf(top, fabsf(y[e])) : top;
+                    for (int e = 0; e < 4; ++e) {
+                        y[2 * e] = __uint_as_float(w[e] << 16);
+                        y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                    }
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // the least power of two s with top <= 448 s
-                const uint32_t b = __float_as_uint(top);
-                const int ex = top > 0.f ? max((int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u), -126) : 0;
-                const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-                uint32_t hi2[4], lo2[4];
+                    for (int e = 0; e < 8; ++e) top = fabsf(y[e]) <= 3.402823466e38f ? fmaxf(top, fabsf(y[e])) : top;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y0 = fmaf(y[2 * e], 0.f, y[2 * e] * inv), y1 = fmaf(y[2 * e + 1], 0.f, y[2 * e + 1] * inv);   // (inf: NaN)
-                    hi2[e] = t8_e4m3x2(y0, y1);
-                    const uint32_t h = t8_f16x2(hi2[e]);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                    lo2[e] = t8_e4m3x2((y0 - f.x) * 16.f, (y1 - f.y) * 16.f);
-                }
-                if (r < NR) {   // (64 dims and 16 rows: one pass)
-                    auto place = [&](int row) {   // of this thread's 8 bytes, in the swizzled tile
-                        if (HD == 128) return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8);
-                        return (uint32_t)((row >> 3) * 512 + (row & 7) * 64 + (((sub >> 1) ^ ((row >> 1) & 3)) << 4) + (sub & 1) * 8);
-                    };
-                    *reinterpret_cast<uint2 *>(q8 + place(r)) = make_uint2(hi2[0] | hi2[1] << 16, hi2[2] | hi2[3] << 16);
-                    *reinterpret_cast<uint2 *>(q8 + place(NR + r)) = make_uint2(lo2[0] | lo2[1] << 16, lo2[2] | lo2[3] << 16);
-                    if (sub == 0) x.q_scale[i % kT8Items][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // the least power of two s with top <= 448 s
+                    const uint32_t b = __float_as_uint(top);
+                    const int ex = top > 0.f ? max((int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u), -126) : 0;
+                    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)   // (inf: NaN)
+                        t8_split(fmaf(y[2 * e], 0.f, y[2 * e] * inv), fmaf(y[2 * e + 1], 0.f, y[2 * e + 1] * inv), h[e], l[e]);
+                    if (r < NR) {   // (64 dims and 8 rows: half of the threads)
+                        auto place = [&](int row) {   // of this thread's 8 bytes, in the swizzled tile
+                            if (HD == 128) return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8);
+                            return (uint32_t)((row >> 3) * 512 + (row & 7) * 64 + (((sub >> 1) ^ ((row >> 1) & 3)) << 4) + (sub & 1) * 8);
+                        };
+                        *reinterpret_cast<uint2 *>(q8 + place(r)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                        *reinterpret_cast<uint2 *>(q8 + place(NR + r)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+                        if (sub == 0) x.q_scale[i % kT8Items][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+                    }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.q_full[i & 1]);
-            publish(next, 0);
-            next = scales(page, 1);
-            page = page_of(2);
-            for (int k = 0; k < units; ++k) {
-                const unsigned u = u0 + k;
-                if (k + 1 < units) publish(next, k + 1);
-                t8_sync<kT8Conv>(3);   // the valid keys of unit k are known
-                next = scales(page, k + 2);   // on their way meanwhile
-                page = page_of(k + 3);
-                ok = ok && warp_wait(&x.v_full[vp.slot], vp.phase) && warp_wait(&x.w_empty[u & 1], (u >> 1 & 1u) ^ 1u);
-                const unsigned char *src = vring + vp.slot * kTile;
-                unsigned char *dst = wide + (u & 1) * kWide;
-                constexpr int CPK = HD / 16, KPP = kT8Conv / CPK, TURNS = kT8Keys / KPP;   // 16-byte chunks of a key; keys of a turn
-                const int c = t % CPK;
-                uint4 in[TURNS];
+#pragma unroll 1
+            for (int k = 0; k < units; ++k, ++u) {
+                const int base = (tile0 + k) * kT8Keys;
+                ok = ok && warp_wait(&x.v_full[vp.slot], vp.phase);
+                unsigned char *src = vring + vp.slot * kTile;
+                if (kDirect) {
+                    const bool by_row = t8_by_row(ends, base, a.window);
+                    if (by_row || base < lo || base + kT8Keys > hi) {
+                        // 16 bytes at a time, whole rows: their order in a row does not matter
+#pragma unroll 1
+                        for (int c = t; c < (int)kTile / 16; c += 128) {
+                            const int j = base + c / (HD / 16);
+                            uint4 *at = reinterpret_cast<uint4 *>(src) + c;
+                            if (j < lo || j >= hi) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (by_row && (j > ends.x || (a.window > 0 && j <= ends.y - a.window))) {
+                                uint4 w4 = *at;
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&w4), any = 0u;
 #pragma unroll
-                for (int y = 0; y < TURNS; ++y)
-                    in[y] = *reinterpret_cast<const uint4 *>(src + (uint32_t)(y * KPP + t / CPK) * HD + c * 16);
-#pragma unroll
-                for (int y = 0; y < TURNS; ++y) {
-                    const int key = y * KPP + t / CPK;
-                    uint32_t w[4] = {in[y].x, in[y].y, in[y].z, in[y].w};
-                    if (!(x.valid[u % kT8Scales][key >> 5] >> (key & 31) & 1u)) w[0] = w[1] = w[2] = w[3] = 0u;
-                    uint32_t bad[4], any = 0u;   // NaN codes: 0x7f in the low seven bits
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        bad[e] = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        any |= bad[e];
+                                for (int e = 0; e < 4; ++e) {   // NaN codes: 0x7f in the low seven bits
+                                    const uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                    w[e] &= ~((nan >> 7) * 0xffu);
+                                    any |= nan;
+                                }
+                                if (any) {
+                                    *at = w4;
+                                    x.poison[i % kT8Items] = 1;
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
                     }
-                    if (any) {
-                        x.poison[i % kT8Items] = 1;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] &= ~((bad[e] >> 7) * 0xffu);
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&x.w_full[vp.slot]);
+                        mbar_arrive(&x.v_empty[vp.slot]);
                     }
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[2 * e] = t8_f16x2(w[e]);
-                        h[2 * e + 1] = t8_f16x2(w[e] >> 16);
-                    }
+                } else {
+                    ok = ok && warp_wait(&x.w_empty[u & 1], (u >> 1 & 1u) ^ 1u);
+                    unsigned char *dst = wide + (u & 1) * kWide;
+                    constexpr int CPK = HD / 16, KPP = 128 / CPK, TURNS = kT8Keys / KPP;   // 16-byte chunks of a key; keys of a turn
+                    const int c = t % CPK;
                     // rows of 128 bytes (64 dims), the second halves beside the first by groups of 8 keys; of
                     // the two 16-byte chunks the threads of the second half store the odd one first (banks)
-                    const int half = c >> 2, c2 = (c & 3) * 2;
-                    unsigned char *row = dst + (uint32_t)(key >> 3) * (H * 1024) + half * 1024 + (key & 7) * 128;
-                    const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
-                    const bool odd = half != 0;
-                    *reinterpret_cast<uint4 *>(row + (((c2 + odd) ^ (key & 7)) << 4)) = odd ? h1 : h0;
-                    *reinterpret_cast<uint4 *>(row + (((c2 + !odd) ^ (key & 7)) << 4)) = odd ? h0 : h1;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&x.w_full[u & 1]);
-                    mbar_arrive(&x.v_empty[vp.slot]);
+                    const int half = c >> 2, c2 = (c & 3) * 2, odd = half;
+                    uint32_t nan = 0u;   // a bit a turn
+#pragma unroll 1
+                    for (int y0 = 0; y0 < TURNS; y0 += 4) {
+                        uint4 in[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            in[y] = *reinterpret_cast<const uint4 *>(src + (uint32_t)((y0 + y) * KPP + t / CPK) * HD + c * 16);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int key = (y0 + y) * KPP + t / CPK;
+                            const uint32_t w[4] = {in[y].x, in[y].y, in[y].z, in[y].w};
+                            uint32_t bad = 0u, h[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                bad |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
+                                // a byte to the front of its half, then all but the sign to the right
+                                const uint32_t p = __byte_perm(w[e], 0u, 0x1404), q = __byte_perm(w[e], 0u, 0x3424);
+                                h[2 * e] = (p & 0x80008000u) | (p >> 1 & 0x3f803f80u);
+                                h[2 * e + 1] = (q & 0x80008000u) | (q >> 1 & 0x3f803f80u);
+                            }
+                            if (bad & 0x80808080u) nan |= 1u << (y0 + y);
+                            unsigned char *row = dst + (uint32_t)(key >> 3) * (H * 1024) + half * 1024 + (key & 7) * 128;
+                            const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
+                            *reinterpret_cast<uint4 *>(row + (((c2 + odd) ^ (key & 7)) << 4)) = odd ? h1 : h0;
+                            *reinterpret_cast<uint4 *>(row + (((c2 + 1 - odd) ^ (key & 7)) << 4)) = odd ? h0 : h1;
+                        }
+                    }
+                    while (nan) {   // of the item's keys?
+                        const int j = base + (__ffs(nan) - 1) * KPP + t / CPK;
+                        if (j >= lo && j < hi) x.poison[i % kT8Items] = 1;
+                        nan &= nan - 1;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&x.w_full[u & 1]);
+                        mbar_arrive(&x.v_empty[vp.slot]);
+                    }
                 }
                 vp.next(geo.v_slots);
             }
-            u0 += units;
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.item_empty[i % kT8Items]);
             if (!ok) give_up();
         }
     } else {
-        // ---------------- softmax and output: rows r0 .. r0 + NRH - 1; thread: key of S, dim of O
-        constexpr int NRH = NR / 2, CH = NRH < 16 ? NRH : 16;   // rows of a read of TMEM
-        const int g = warp >> 2, wq = warp & 3, key = 32 * wq + lane, r0 = g * NRH, bar = 1 + g, tg = threadIdx.x & 127;
+        // ---------------- softmax and output: rows r0 .. r0 + OWN - 1; thread: key of S, dim of O
+        constexpr int OWN = P::own;
+        const int g = warp >> 2, wq = warp & 3, key = 32 * wq + lane, r0 = g * OWN, bar = 1 + g, tg = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const int win = a.window > 0 ? a.window : 0x7fffffff;
         bf16 *out = static_cast<bf16 *>(a.out);
-        auto load = [&](uint32_t at, uint32_t (&v)[CH]) {
-            if constexpr (CH == 16) tmem_ld16_async(at, v);
-            else tmem_ld8_async(at, v);
-        };
-        unsigned u0 = 0;   // units before this item
+        const float *nm = x.neg_m + r0;
+        const int *pos = x.pos + r0;
+        unsigned u = 0, nr = 0;   // units, rounds of scales
         for (unsigned i = 0;; ++i) {
             bool ok = warp_wait(&x.item_full[i % kT8Items], i / kT8Items & 1u);
-            if (t8_any<128>(bar, !ok)) {
+            if (t8_any(bar, !ok)) {
                 give_up();
                 break;
             }
             const PagedItem &it = x.item[i % kT8Items];
             if (!it.more) break;
-            const int units = it.t1 - it.t0, tile0 = it.t0, n_rows = it.n_rows;
+            const int units = it.t1 - it.t0, n_rows = it.n_rows, lo = it.lo, hi = it.hi;
             const bool active = n_rows > r0;
-            // the least and the greatest position of the tile's rows
-            const int pos_a = max(it.pos0 + it.tok_a, -1), pos_b = max(it.pos0 + it.tok_b, -1);
-            if (tg < NRH) {   // (rows that are not there are taken as the last one)
+            const int2 ends = t8_ends(it);
+            if (tg < OWN) {   // (rows that are not there are taken as the last one)
                 const int r = r0 + tg, row = it.row0 + min(r, n_rows - 1), tok = row / a.group, hd = row - tok * a.group;
                 x.pos[r] = max(it.pos0 + tok, -1);
                 x.off[r] = (long long)(it.token + tok) * a.out_stride + (it.head * a.group + hd) * HD;
-                x.neg_m[r] = INFINITY;
+                x.neg_m[r] = 0.f;
+                x.set[r] = 0;
             }
-            t8_sync<128>(bar);
-            const float *qs = x.q_scale[i % kT8Items] + r0, *nm = x.neg_m + r0;
-            const int *pos = x.pos + r0;
-            const uint32_t t_o = tmem + lanes + 4 * NR + (i & 1) * NR + r0;
-            uint64_t l[NRH / 2];
+            t8_sync(bar);
+            const float *qs = x.q_scale[i % kT8Items] + r0;
+            const uint32_t t_o = tmem_o + lanes + (i & 1) * P::o_cols + (kDirect ? 4 : 1) * r0;
+            uint64_t l[OWN / 2];
 #pragma unroll
-            for (int e = 0; e < NRH / 2; ++e) l[e] = 0ull;
+            for (int e = 0; e < OWN / 2; ++e) l[e] = 0ull;
+            bool unset = true;   // some row has no m
+            int base = it.t0 * kT8Keys, in_round = 0;
 #pragma unroll 1
-            for (int k = 0; k < units; ++k) {
-                const unsigned u = u0 + k;
-                ok = ok && warp_wait(&x.sc_full[u % kT8Scales], u / kT8Scales & 1u);
-                const float2 sc = x.sc[u % kT8Scales][key];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&x.sc_empty[u % kT8Scales]);
+            for (int k = 0; k < units; ++k, ++u, base += kT8Keys) {
+                if (in_round == 0) ok = ok && warp_wait(&x.sc_full[nr % kT8Scales], nr / kT8Scales & 1u);
+                const float2 sc = x.sc[nr % kT8Scales][in_round * geo.per_unit + (key >> geo.gran)];
+                if (++in_round == geo.round || k == units - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x.sc_empty[nr % kT8Scales]);
+                    in_round = 0;
+                    ++nr;
+                }
                 ok = ok && warp_wait(&x.s_full[u & 1], u >> 1 & 1u);
                 if (active) {
                     tc_fence_after();
-                    const int base = (tile0 + k) * kT8Keys, j = base + key;
-                    const bool there = sc.y > -INFINITY;
-                    // whether some rows see a key of the unit that others do not
-                    const bool by_row = base + kT8Keys - 1 > pos_a || (a.window > 0 && base <= pos_b - win);
-                    const bool mask = by_row || !__all_sync(0xffffffffu, there);
-                    const uint32_t t_s = tmem + lanes + (u & 1) * 2 * NR + r0;
+                    const int j = base + key;
+                    const bool there = j >= lo && j < hi && sc.y > -INFINITY;
+                    const bool by_row = t8_by_row(ends, base, a.window);
+                    const uint32_t t_s = tmem + lanes + (u & 1) * P::s_cols + r0;
                     const uint64_t kc = pack_f32x2(sc.x, sc.x), lv = pack_f32x2(sc.y, sc.y), sixteenth = pack_f32x2(0.0625f, 0.0625f);
-                    float y[NRH];
-                    // t_rj, or with `less` t_rj - m_r
-                    auto scores = [&](bool less) {
+                    float y[OWN];   // t_rj - m_r
+                    {
+                        uint32_t h[OWN], s[OWN];
+                        if constexpr (OWN == 16) {
+                            tmem_ld16_async(t_s, h);
+                            tmem_ld16_async(t_s + NR, s);
+                        } else {
+                            tmem_ld8_async(t_s, h);
+                            tmem_ld8_async(t_s + NR, s);
+                        }
+                        tmem_wait_ld<OWN>(h);
+                        tmem_wait_ld<OWN>(s);
 #pragma unroll
-                        for (int q = 0; q < NRH; q += CH) {
-                            uint32_t hi[CH], lo[CH];
-                            load(t_s + q, hi);
-                            load(t_s + NR + q, lo);
-                            tmem_wait_ld<CH>(hi);
-                            tmem_wait_ld<CH>(lo);
+                        for (int e = 0; e < OWN; e += 4) {
+                            const ulonglong2 q4 = t8_rows4(qs + e), m4 = t8_rows4(nm + e);
 #pragma unroll
-                            for (int e = 0; e < CH; e += 2) {
-                                const uint64_t f = mul_f32x2(kc, *reinterpret_cast<const uint64_t *>(qs + q + e));
-                                const uint64_t s = fma_f32x2(pack_f32x2(__uint_as_float(lo[e]), __uint_as_float(lo[e + 1])), sixteenth,
-                                                             pack_f32x2(__uint_as_float(hi[e]), __uint_as_float(hi[e + 1])));
-                                const uint64_t add = less ? add_f32x2(lv, *reinterpret_cast<const uint64_t *>(nm + q + e)) : lv;
-                                const float2 v = unpack_f32x2(fma_f32x2(s, f, add));
-                                y[q + e] = v.x;
-                                y[q + e + 1] = v.y;
+                            for (int z = 0; z < 4; z += 2) {
+                                const uint64_t f = mul_f32x2(kc, z ? q4.y : q4.x), b = add_f32x2(lv, z ? m4.y : m4.x);
+                                const uint64_t w = fma_f32x2(pack_f32x2(__uint_as_float(s[e + z]), __uint_as_float(s[e + z + 1])), sixteenth,
+                                                             pack_f32x2(__uint_as_float(h[e + z]), __uint_as_float(h[e + z + 1])));
+                                const float2 v = unpack_f32x2(fma_f32x2(w, f, b));
+                                y[e + z] = v.x;
+                                y[e + z + 1] = v.y;
                             }
                         }
-                        if (mask) {
-#pragma unroll
-                            for (int e = 0; e < NRH; ++e) {
-                                const int p = pos[e];
-                                const bool see = there && (!by_row || (j <= p && j > p - win));
-                                y[e] = see ? y[e] : -INFINITY;
-                            }
-                        }
-                    };
-                    bool move = k == 0;
-                    if (k > 0) {
-                        scores(true);
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < NRH; ++e) top = fmaxf(top, y[e]);
-                        move = t8_any<128>(bar, top > kT8Most);
                     }
-                    if (move) {   // some row's weights outgrow its m
-                        scores(false);
+                    if (by_row || !__all_sync(0xffffffffu, there)) {
+                        uint32_t see = 0u;   // a bit a row
+                        if (there) {
+                            see = 0xffffu;
+                            if (by_row) {
+                                see = 0u;
+#pragma unroll 1
+                                for (int e = 0; e < OWN; ++e) {
+                                    const int p = pos[e];
+                                    see |= (uint32_t)(j <= p && j > p - win) << e;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < OWN; ++e) y[e] = see >> e & 1u ? y[e] : -INFINITY;
+                    }
+                    float top = y[0];
+#pragma unroll
+                    for (int e = 1; e < OWN; ++e) top = fmaxf(top, y[e]);
+                    if (t8_any(bar, unset || top > P::most)) {   // some row's weights outgrow its m, or it has none
                         int mine = 0;
 #pragma unroll
-                        for (int e = 0; e < NRH; ++e) {
+                        for (int e = 0; e < OWN; ++e) {
                             // the largest over the warp's keys, as integers in the order of the floats (NaN as -inf)
                             const int b = __float_as_int(fmaxf(y[e], -INFINITY));
-                            const int top = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
-                            if (lane == e) mine = top;
+                            const int m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+                            if (lane == e) mine = m;
                         }
-                        if (lane < NRH) x.part[warp][lane] = __int_as_float(mine ^ (mine >> 31 & 0x7fffffff));
-                        t8_sync<128>(bar);
-                        if (tg < NRH) {
-                            const int w0 = g * 4;
-                            const float top = fmaxf(fmaxf(x.part[w0][tg], x.part[w0 + 1][tg]), fmaxf(x.part[w0 + 2][tg], x.part[w0 + 3][tg]));
-                            const float old = -x.neg_m[r0 + tg];   // -inf: none yet
-                            const bool up = top > -INFINITY && (k == 0 || top > old + kT8Most);
-                            x.factor[r0 + tg] = up ? t8_ex2(old - (top - kT8Off)) : 1.f;
-                            if (up) x.neg_m[r0 + tg] = kT8Off - top;
+                        if (lane < OWN) x.part[warp][lane] = __int_as_float(mine ^ (mine >> 31 & 0x7fffffff));
+                        t8_sync(bar);
+                        bool none = false;
+                        if (tg < OWN) {
+                            const int w0 = g * 4, r = r0 + tg;
+                            const float m = fmaxf(fmaxf(x.part[w0][tg], x.part[w0 + 1][tg]), fmaxf(x.part[w0 + 2][tg], x.part[w0 + 3][tg]));
+                            const bool set = x.set[r] != 0, up = m > -INFINITY && (!set || m > P::most);
+                            const float d = up ? P::off - m : 0.f;
+                            none = !set && !up;
+                            x.delta[r] = d;
+                            x.factor[r] = set ? t8_ex2(d) : 1.f;   // (a row without m has no sums)
+                            x.neg_m[r] += d;
+                            if (up) x.set[r] = 1;
                         }
-                        t8_sync<128>(bar);
+                        unset = t8_any(bar, none);
                         if (k > 0) {
                             // O of the units before
                             ok = ok && warp_wait(&x.p_empty[(u - 1) & 1], ((u - 1) >> 1) & 1u);
                             tc_fence_after();
+#pragma unroll 1
+                            for (int q = 0; q < (kDirect ? 4 * OWN : OWN); q += 8) {   // (direct: eight rows have four times eight columns)
+                                uint32_t o[8];
+                                tmem_ld8_async(t_o + q, o);
+                                tmem_wait_ld<8>(o);
+                                const float *f = x.factor + r0 + (kDirect ? q >> 5 << 3 : q);
 #pragma unroll
-                            for (int q = 0; q < NRH; q += CH) {
-                                uint32_t o[CH];
-                                load(t_o + q, o);
-                                tmem_wait_ld<CH>(o);
-#pragma unroll
-                                for (int e = 0; e < CH; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * x.factor[r0 + q + e]);
-#pragma unroll
-                                for (int e = 0; e < CH; e += 8) tmem_st8(t_o + q + e, o + e);
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e]);
+                                tmem_st8(t_o + q, o);
                             }
                             tmem_wait_st();
 #pragma unroll
-                            for (int e = 0; e < NRH; e += 2)
-                                l[e / 2] = mul_f32x2(l[e / 2], *reinterpret_cast<const uint64_t *>(x.factor + r0 + e));
+                            for (int e = 0; e < OWN; e += 4) {
+                                const ulonglong2 f = t8_rows4(x.factor + r0 + e);
+                                l[e / 2] = mul_f32x2(l[e / 2], f.x);
+                                l[e / 2 + 1] = mul_f32x2(l[e / 2 + 1], f.y);
+                            }
                         }
 #pragma unroll
-                        for (int e = 0; e < NRH; ++e) {
-                            const float n = nm[e];
-                            y[e] += n == INFINITY ? 0.f : n;   // (no key yet: every score is -inf or NaN)
-                        }
+                        for (int e = 0; e < OWN; ++e) y[e] += x.delta[r0 + e];
                     }
                     const float r = there ? t8_ex2(-sc.y) : 0.f;   // 1 / vs
                     const uint64_t rr = pack_f32x2(r, r);
                     if (u >= 2) ok = ok && warp_wait(&x.p_empty[u & 1], ((u - 2) >> 1) & 1u);
                     unsigned char *prow = pbuf + (u & 1) * kP + (uint32_t)(key >> 3) * 1024 + (key & 7) * 128;
 #pragma unroll
-                    for (int q = 0; q < NRH; q += 8) {
-                        uint32_t h[4];
+                    for (int q = 0; q < OWN; q += 8) {
+                        float p[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float p0 = t8_ex2(y[q + 2 * e]), p1 = t8_ex2(y[q + 2 * e + 1]);
-                            l[q / 2 + e] = fma_f32x2(pack_f32x2(p0, p1), rr, l[q / 2 + e]);
-                            const __half2 pk = __floats2half2_rn(p0, p1);
-                            h[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                        for (int e = 0; e < 8; ++e) p[e] = t8_ex2(y[q + e]);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) l[(q + e) / 2] = fma_f32x2(pack_f32x2(p[e], p[e + 1]), rr, l[(q + e) / 2]);
+                        if (kDirect) {
+                            // columns (r / 8) 32 + 8 s + r % 8: s 0, 1 the codes of the large weights and what they
+                            // leave, 2, 3 those of the small ones, in units of 2^-13
+                            uint32_t hi4[2], lo4[2], small[2];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                uint32_t h0, h1, l0, l1, m = 0u;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (p[4 * z + e] < 0x1p-5f) {
+                                        p[4 * z + e] *= 0x1p13f;
+                                        m |= 0xffu << (8 * e);
+                                    }
+                                t8_split(p[4 * z], p[4 * z + 1], h0, l0);
+                                t8_split(p[4 * z + 2], p[4 * z + 3], h1, l1);
+                                hi4[z] = __byte_perm(h0, h1, 0x5410);
+                                lo4[z] = __byte_perm(l0, l1, 0x5410);
+                                small[z] = m;
+                            }
+                            const int c = (r0 + q) >> 2;   // 32 bytes: two of the row's 16-byte chunks
+                            *reinterpret_cast<uint4 *>(prow + ((c ^ (key & 7)) << 4)) =
+                                make_uint4(hi4[0] & ~small[0], hi4[1] & ~small[1], lo4[0] & ~small[0], lo4[1] & ~small[1]);
+                            *reinterpret_cast<uint4 *>(prow + (((c + 1) ^ (key & 7)) << 4)) =
+                                make_uint4(hi4[0] & small[0], hi4[1] & small[1], lo4[0] & small[0], lo4[1] & small[1]);
+                        } else {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 pk = __floats2half2_rn(p[2 * e], p[2 * e + 1]);
+                                h[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                            }
+                            *reinterpret_cast<uint4 *>(prow + ((((r0 + q) >> 3) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
-                        *reinterpret_cast<uint4 *>(prow + ((((r0 + q) >> 3) ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     fence_proxy_async_smem();   // before the MMA reads them
                 }
@@ -669,21 +846,21 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x.p_full[u & 1]);
             }
-            u0 += units;
-            // ---- the item's rows.  O is complete with its last unit's (waited for by both halves: neither
-            // runs ahead of the other by more than an item)
-            const unsigned last = u0 - 1;
+            // ---- the item's rows: O is complete with its last unit's.  (All groups wait for it: none
+            // runs ahead of the others by more than an item.)
+            const unsigned last = u - 1;
+            const bool part = it.part >= 0;
             if (active) {
                 // row sums over the warp's keys: at each step a lane keeps half of its rows
-                float v[NRH];
+                float v[OWN];
 #pragma unroll
-                for (int e = 0; e < NRH / 2; ++e) {
+                for (int e = 0; e < OWN / 2; ++e) {
                     const float2 f = unpack_f32x2(l[e]);
                     v[2 * e] = f.x;
                     v[2 * e + 1] = f.y;
                 }
 #pragma unroll
-                for (int n = NRH / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+                for (int n = OWN / 2, o = 16; n >= 1; n /= 2, o /= 2) {
                     const bool up = lane & o;
 #pragma unroll
                     for (int e = 0; e < n; ++e) {
@@ -691,60 +868,71 @@ __global__ void __launch_bounds__(kT8Threads, 1)
                         v[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
                     }
                 }
-                constexpr int REP = 32 / NRH;   // lanes that hold the same row
+                constexpr int REP = 32 / OWN;   // lanes that hold the same row
 #pragma unroll
                 for (int o = REP / 2; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
                 if (lane % REP == 0) x.part[warp][lane / REP] = v[0];
-                t8_sync<128>(bar);
-                const bool part = it.part >= 0;
-                if (tg < NRH) {
+                t8_sync(bar);
+                if (tg < OWN) {
                     const int w0 = g * 4, r = r0 + tg;
                     const float sum = (x.part[w0][tg] + x.part[w0 + 1][tg]) + (x.part[w0 + 2][tg] + x.part[w0 + 3][tg]);
+                    constexpr float unit = kDirect ? 1.f : 256.f;   // (V's halves are 2^-8 of its codes)
                     if (part && r < n_rows) {
                         float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + ((size_t)it.part * a.rows + r) * 2;
-                        ml[0] = -x.neg_m[r];
+                        ml[0] = x.set[r] ? -x.neg_m[r] : -INFINITY;
                         ml[1] = sum;
                     }
-                    x.factor[r] = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                    x.factor[r] = part ? unit : sum == 0.f ? 0.f : unit / sum;
                 }
-                t8_sync<128>(bar);
-                ok = ok && warp_wait(&x.p_empty[last & 1], last >> 1 & 1u);
+                t8_sync(bar);
+            }
+            ok = ok && warp_wait(&x.p_empty[last & 1], last >> 1 & 1u);
+            if (active && 32 * wq < HD) {   // thread: dim `key`
                 tc_fence_after();
-                if (32 * wq < HD) {   // thread: dim `key`
-                    uint32_t nan = 0u;   // rows that see a key whose V is NaN in this dim
-                    if (*const_cast<volatile int *>(&x.poison[i % kT8Items])) {
-                        const int j0 = max(it.lo, tile0 * kT8Keys), j1 = min(it.hi, it.t1 * kT8Keys);
+                uint32_t nan = 0u;   // rows that see a key whose V is NaN in this dim
+                if (*const_cast<volatile int *>(&x.poison[i % kT8Items])) {
+                    const int j0 = max(lo, it.t0 * kT8Keys), j1 = min(hi, it.t1 * kT8Keys);
 #pragma unroll 1
-                        for (int j = j0; j < j1; ++j) {
-                            const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
-                            if (page < 0) continue;
-                            const uint8_t code = static_cast<const uint8_t *>(a.kv.v)[page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
-                                                                                      it.head * a.kv.head_stride + key];
-                            if ((code & 0x7fu) != 0x7fu) continue;
+                    for (int j = j0; j < j1; ++j) {
+                        const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
+                        if (page < 0) continue;
+                        const uint8_t code = static_cast<const uint8_t *>(a.kv.v)[page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
+                                                                                  it.head * a.kv.head_stride + key];
+                        if ((code & 0x7fu) != 0x7fu) continue;
 #pragma unroll 1
-                            for (int e = 0; e < NRH; ++e)
-                                if (j <= pos[e] && j > pos[e] - win) nan |= 1u << e;
-                        }
-                    }
-                    float *po = reinterpret_cast<float *>(a.ws + lay.o) + ((size_t)it.part * a.rows + r0) * HD + key;
-#pragma unroll
-                    for (int q = 0; q < NRH; q += CH) {
-                        uint32_t o[CH];
-                        load(t_o + q, o);
-                        tmem_wait_ld<CH>(o);
-#pragma unroll
-                        for (int e = 0; e < CH; ++e) {
-                            const int r = r0 + q + e;
-                            if (r >= n_rows) break;
-                            float f = __uint_as_float(o[e]) * x.factor[r];
-                            if (nan >> (q + e) & 1u) f = NAN;
-                            if (part) po[(q + e) * HD] = f;
-                            else out[x.off[r] + key] = __float2bfloat16_rn(f);
-                        }
+                        for (int e = 0; e < OWN; ++e)
+                            if (j <= pos[e] && j > pos[e] - win) nan |= 1u << e;
                     }
                 }
-            } else {
-                ok = ok && warp_wait(&x.p_empty[last & 1], last >> 1 & 1u);
+                float *po = reinterpret_cast<float *>(a.ws + lay.o) + ((size_t)(part ? it.part : 0) * a.rows + r0) * HD + key;
+#pragma unroll 1
+                for (int q = 0; q < OWN; q += 8) {
+                    float f[8];
+                    if constexpr (kDirect) {
+                        uint32_t o[32];
+                        tmem_ld32_async(t_o + 4 * q, o);
+                        tmem_wait_ld32(o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = fmaf(fmaf(__uint_as_float(o[24 + e]), 0.0625f, __uint_as_float(o[16 + e])), 0x1p-13f,
+                                        fmaf(__uint_as_float(o[8 + e]), 0.0625f, __uint_as_float(o[e])));
+                    } else {
+                        uint32_t o[8];
+                        tmem_ld8_async(t_o + q, o);
+                        tmem_wait_ld<8>(o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + q + e;
+                        if (r >= n_rows) break;
+                        float v = f[e] * x.factor[r];
+                        if (nan >> (q + e) & 1u) v = NAN;
+                        if (part) po[(q + e) * HD] = v;
+                        else out[x.off[r] + key] = __float2bfloat16_rn(v);
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -757,9 +945,9 @@ __global__ void __launch_bounds__(kT8Threads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kT8Mma) {
+    if (warp == P::mma_s) {
         tc_fence_after();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc(tmem, P::cols);
     }
 }
 
@@ -768,46 +956,45 @@ __global__ void __launch_bounds__(kT8Threads, 1)
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 template <int HD, int NR>
-static cudaError_t t8_go(AttnArgs &a, T8Geometry &g, const CUtensorMap &km, const CUtensorMap &vm, int grid, cudaStream_t st)
+static cudaError_t t8_go(AttnArgs &a, T8Geometry &g, cudaStream_t st, int grid)
 {
-    const int tile = HD * kT8Keys, fixed = 2 * 2 * tile + 2 * kT8Keys * 128 + 2 * 2 * NR * HD + (int)sizeof(T8Misc);
-    static_assert(2 * 2 * HD * kT8Keys + 2 * kT8Keys * 128 + 2 * 2 * NR * HD + sizeof(T8Misc) + 4 * HD * kT8Keys <= kT8Smem,
-                  "two tiles of K and of V beside the buffers");
-    int slots = (kT8Smem - fixed) / tile;
-    if (slots > 2 * kT8MaxSlots) slots = 2 * kT8MaxSlots;
+    constexpr bool direct = T8<NR>::direct;
+    CUtensorMap km, vm;
+    const long long dims[4] = {HD, a.kv.page_size, a.kv.n_kv_heads, a.kv.n_pages};
+    const long long strides[3] = {a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
+    const int box[4] = {HD, g.box, 1, 1};
+    cudaError_t e = tc::make_map_u8_nd(&km, a.kv.k, 4, dims, strides, box, HD);
+    if (!e) e = tc::make_map_u8_nd(&vm, a.kv.v, 4, dims, strides, box, direct ? HD : 0);
+    if (e) return e;
+    constexpr int tile = HD * kT8Keys, fixed = (direct ? 0 : 4 * tile) + 2 * kT8Keys * 128 + 4 * NR * HD + (int)sizeof(T8Misc);
+    constexpr int room = (kT8Smem - fixed) / tile, slots = room > 2 * kT8MaxSlots ? 2 * kT8MaxSlots : room;
+    static_assert(slots >= 4, "two tiles of K and of V beside the buffers");
     g.k_slots = (slots + 1) / 2;
     g.v_slots = slots / 2;
     static PerDevice once;
     auto kernel = k_paged_attn8_tc<HD, NR>;
-    cudaError_t e = allow_once(once, kernel, kT8Smem);
+    e = allow_once(once, kernel, kT8Smem);
     if (e) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(kT8Threads), (size_t)(fixed + slots * tile), st, km, vm, a, g);
+    return launch_pdl(kernel, dim3(grid), dim3(T8<NR>::threads), (size_t)(fixed + slots * tile), st, km, vm, a, g);
 }
 
 cudaError_t paged_attn8_tc(AttnArgs &a, cudaStream_t st, int nsm)
 {
-    const int hd = a.kv.head_dim;
     T8Geometry g = {};
     g.box = gcd(a.kv.page_size, kT8Keys);
     g.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (1 << i == a.kv.page_size) g.page_shift = i;
-    CUtensorMap km, vm;
-    const long long dims[4] = {hd, a.kv.page_size, a.kv.n_kv_heads, a.kv.n_pages};
-    const long long strides[3] = {a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
-    const int box[4] = {hd, g.box, 1, 1};
-    cudaError_t e = tc::make_map_u8_nd(&km, a.kv.k, 4, dims, strides, box, hd);
-    if (!e) e = tc::make_map_u8_nd(&vm, a.kv.v, 4, dims, strides, box, 0);
-    if (e) return e;
+    g.gran = 0;
+    while (g.gran < 7 && a.kv.block % (2 << g.gran) == 0) ++g.gran;
+    g.per_unit = kT8Keys >> g.gran;
+    g.round = g.per_unit < 32 ? 32 / g.per_unit : 1;
     const int grid = paged_attn_grid(a, kT8Keys, nsm < kAttnMaxCtasTc ? nsm : kAttnMaxCtasTc);
-    if (hd == 64)
-        e = a.rows <= 16   ? t8_go<64, 16>(a, g, km, vm, grid, st)
-            : a.rows <= 32 ? t8_go<64, 32>(a, g, km, vm, grid, st)
-                           : t8_go<64, 64>(a, g, km, vm, grid, st);
-    else
-        e = a.rows <= 16   ? t8_go<128, 16>(a, g, km, vm, grid, st)
-            : a.rows <= 32 ? t8_go<128, 32>(a, g, km, vm, grid, st)
-                           : t8_go<128, 64>(a, g, km, vm, grid, st);
+    auto go = [&](auto by8, auto by16, auto by32, auto by64) {
+        return (a.rows <= 8 ? by8 : a.rows <= 16 ? by16 : a.rows <= 32 ? by32 : by64)(a, g, st, grid);
+    };
+    cudaError_t e = a.kv.head_dim == 64 ? go(t8_go<64, 8>, t8_go<64, 16>, t8_go<64, 32>, t8_go<64, 64>)
+                                        : go(t8_go<128, 8>, t8_go<128, 16>, t8_go<128, 32>, t8_go<128, 64>);
     if (!e && !a.whole) e = paged_join_tc(a, grid, nsm, st);
     return e;
 }

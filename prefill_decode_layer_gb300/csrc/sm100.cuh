@@ -319,6 +319,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
 {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);   // formats 0: E4M3
 }
+// The same with A and B stored MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32_mn(int M, int N)
+{
+    return idesc_e4m3_f32(M, N) | (1u << 15) | (1u << 16);
+}
 // Instruction descriptor of a dense kind::f16 MMA (tc_mma_bf16 issues it): F16 A and B, both stored
 // MN-major, FP32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32_mn(int M, int N)
@@ -542,6 +547,17 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t
     d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;   // swizzle: 128 bytes
+    return d;
+}
+// The same with the 64-byte swizzle: rows of 64 bytes along MN.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;   // swizzle: 64 bytes
     return d;
 }
 // Instruction descriptor as idesc_bf16_f32 with B stored MN-major (transposed).

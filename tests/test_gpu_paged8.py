@@ -44,18 +44,17 @@ def attend(p, q, window=0, scale=0.0, max_new=None, out=None, ws=None, start=Tru
 def bound_of(p, q, ref, err, mass, scale=None):
     """What the outputs may be off by: `err` of the FP32 form; in the tensor-core form also the
     queries' second halves (2^-22 of a row's largest for each dim, once more for the weights'
-    maximum), the scales' logarithms (up to 64 in FP32: 2^-18) and the weights as FP16 (2^-11 of each, or 2^-33
-    of the largest times V's)."""
+    maximum), the scales' logarithms (up to 64 in FP32: 2^-18) and the weights: 2^-8 of each (E4M3 pairs; 2^-11 as
+    FP16), or 2^-32 of the largest times the largest V that its scales allow."""
     dim = q.shape[2]
     before = err
     if q.dtype == BF16 and dim in (64, 128) and p["page"] % 8 == 0:
         scale = 1.0 / math.sqrt(dim) if scale is None else scale
-        v = values(p)
-        fine = v["k"].nan_to_num(0.0)
+        fine = values(p)["k"].nan_to_num(0.0)
         k_sum = float(fine.abs().sum(-1).max())
         ds = 2.0 ** -22 * q.double().abs().amax(-1, keepdim=True) * k_sum * scale
-        tiny = 2.0 ** -33 * float(p["length"].max()) * float(v["v"].nan_to_num(0.0).abs().max())
-        before = err + mass * (4 * ds + 2.0 ** -17 + 2.0 ** -11) + (mass > 0) * tiny
+        tiny = 2.0 ** -32 * float(p["length"].max()) * 448.0 * float(p["vs"].nan_to_num(0.0).max())
+        before = err + mass * (4 * ds + 2.0 ** -17 + 2.0 ** -8) + (mass > 0) * tiny
     return before + HALF[q.dtype] * (ref.abs() + before)
 
 
@@ -91,6 +90,14 @@ def test_attention_several_tokens_and_windows(dtype, kv_heads, heads, dim, page,
     new = [1, 5, 3, 8, 5, 2, 0, 7, 1, 4]
     p = inputs8(LENGTHS, new, kv_heads, dim, page, block, seed=dim + window, pad_rows=3)
     check_attention(p, heads, dtype, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [5, 8, 9, 16, 17, 32, 33, 48, 64, 65])
+def test_attention_of_any_number_of_rows(heads, dim):
+    p = inputs8([700, 200, 2], [1, 1, 1], 1, dim, 16, 16, seed=heads)
+    p["v8"].copy_((f32(p["v8"]) * 2.0 ** -14).to(E4M3))   # codes of 2^-9 .. 2^-6: subnormal
+    check_attention(p, heads, BF16)
 
 
 @pytest.mark.parametrize("window", [1, 2, 128, 1000000])

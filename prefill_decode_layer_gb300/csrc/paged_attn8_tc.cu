@@ -66,7 +66,7 @@ template <int NR> struct T8 {
     static constexpr int groups = NR / own;
     static constexpr int soft = groups * 128;          // softmax threads
     static constexpr int conv = groups * 4;            // warps: the first of the queries and V's tiles, then ..
-    static constexpr int tma = conv + 4, mma_s = tma + 1, mma_o = tma + 2, scale = tma + 3;
+    static constexpr int tma = conv + 4, mma_s = tma + 2, mma_o = tma + 3, scale = tma + 4;   // (tma: K's copies and the items, tma + 1: V's)
     static constexpr int threads = (scale + 1) * 32;
     static constexpr int s_cols = 2 * NR, o_cols = direct ? 4 * NR : NR;   // of a unit, of an item
     static constexpr int cols = 2 * s_cols + 2 * o_cols <= 128 ? 128 : 2 * s_cols + 2 * o_cols <= 256 ? 256 : 512;
@@ -85,7 +85,7 @@ struct T8Misc {
     uint64_t done[2];
     PagedItem item[kT8Items];
     PagedCursor cur;
-    long long scratch[24];
+    long long scratch[25];
     float2 sc[kT8Scales][kT8Keys];                     // of a round's blocks: ks scale log2 e, log2 vs (-inf: no page)
     int poison[kT8Items];                              // a V row of the item has a NaN that was taken out
     uint32_t tmem;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             if (in(x.w_full, kT8MaxSlots) || in(x.q_full, 2)) count = 4;
             else if (in(x.v_empty, kT8MaxSlots)) count = kDirect ? 5 : 4;
             else if (in(x.sc_empty, kT8Scales) || in(x.p_full, 2) || in(x.o_free, 2)) count = 4 * P::groups;
-            else if (in(x.item_empty, kT8Items)) count = 4 * P::groups + 4 + 3;
+            else if (in(x.item_empty, kT8Items)) count = 4 * P::groups + 4 + 4;
             mbar_init(bars + i, count);
         } else if (i == n) {
             x.abort_flag = 0;
@@ -254,20 +254,27 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
         return __all_sync(0xffffffffu, t8_wait(bar, parity, ab)) != 0;
     };
 
-    if (warp == P::tma) {
-        // ---------------- items, page look-ups, copies
+    if (warp == P::tma || warp == P::tma + 1) {
+        // ---------------- page look-ups and copies, of K or of V; the first of the two finds the items
+        const bool is_v = warp != P::tma;
         PagedCursor cur;
-        if (few) paged_cursor_warp(a, kT8Keys, cur);
-        else cur = x.cur;
+        if (!is_v) {
+            if (few) paged_cursor_warp(a, kT8Keys, cur);
+            else cur = x.cur;
+        }
         const int boxes = kT8Keys / geo.box, ps = a.kv.page_size;
-        int used_k = -1, used_v = -1;   // lane i: the phase of the last load into slot i
-        T8Place kp = {0, 0}, vp = {0, 0};
+        const CUtensorMap *map = is_v ? &vmap : &kmap;
+        uint64_t *full = is_v ? x.v_full : x.k_full, *empty = is_v ? x.v_empty : x.k_empty;
+        unsigned char *ring = is_v ? vring : kring;
+        const unsigned slots = is_v ? geo.v_slots : geo.k_slots;
+        int used = -1;   // lane i: the phase of the last load into slot i
+        T8Place p = {0, 0};
         bool ok = true;
         for (unsigned i = 0; ok; ++i) {
-            ok = warp_wait(&x.item_empty[i % kT8Items], (i / kT8Items & 1u) ^ 1u);
+            ok = warp_wait(is_v ? &x.item_full[i % kT8Items] : &x.item_empty[i % kT8Items], (i / kT8Items & 1u) ^ (is_v ? 0u : 1u));
             if (!ok) break;
             PagedItem &it = x.item[i % kT8Items];
-            if (lane == 0) {
+            if (!is_v && lane == 0) {
                 paged_next(a, kT8Keys, cur, lay, it);
                 x.poison[i % kT8Items] = 0;
                 mbar_arrive(&x.item_full[i % kT8Items]);
@@ -275,59 +282,60 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             __syncwarp();
             if (!it.more) break;
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
-            const int lo = it.lo, hi = it.hi, head = it.head, t1 = it.t1;
+            const int lo = it.lo, hi = it.hi, head = it.head, t0 = it.t0, t1 = it.t1;
+            if (is_v) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.item_empty[i % kT8Items]);
+            }
             // a look-up is of 32 boxes: the lane's box of the group of tiles from tg, its page and first slot
             const int group = 32 / boxes, my_tile = lane / boxes, my_box = lane - my_tile * boxes;
             int page = -1, slot = 0, at = 0, from = 0, in_group = group;
             uint32_t loads = 0;
             bool load = false;
-            auto look = [&](int tg) {
-                const int j = (tg + my_tile) * kT8Keys + my_box * geo.box;
-                load = tg + my_tile < t1 && j < hi && j + geo.box > lo;
-                if (load) {
-                    const int p = geo.page_shift >= 0 ? j >> geo.page_shift : j / ps;
-                    slot = j - p * ps;
-                    page = table[p];
-                }
-            };
             // (two look-ups before the first tile, then one at the first tile of every group)
 #pragma unroll 1
-            for (int t = it.t0 - group; ok && t < t1; ++t, ++in_group) {
+            for (int t = t0 - group; ok && t < t1; ++t, ++in_group) {
                 if (in_group == group) {
                     // a page that is not there: out of bounds, read as zeros
                     at = page < 0 || page >= a.kv.n_pages ? a.kv.n_pages : page;
                     from = slot;
                     loads = __ballot_sync(0xffffffffu, load);
-                    look(t + group);   // on its way meanwhile
+                    // the next group's, on its way meanwhile
+                    const int tile = t + group + my_tile, j = tile * kT8Keys + my_box * geo.box;
+                    load = tile < t1 && j < hi && j + geo.box > lo;
+                    if (load) {
+                        const int q = geo.page_shift >= 0 ? j >> geo.page_shift : j / ps;
+                        slot = j - q * ps;
+                        page = table[q];
+                    }
                     in_group = 0;
-                    if (t < it.t0) {
-                        t = it.t0 - 1;
+                    if (t < t0) {
+                        t = t0 - 1;
                         in_group = group - 1;
                         continue;
                     }
                 }
-                const uint32_t tile = loads & ((1u << boxes) - 1u) << (in_group * boxes);
-                const uint32_t bytes = (uint32_t)__popc(tile) * geo.box * HD;
+                ok = warp_wait(empty + p.slot, p.phase ^ 1u);
+                if (!ok) break;
+                // one lane issues them all: the compiler then sees uniform operands
+                uint32_t tile = loads >> (in_group * boxes) & ((1u << boxes) - 1u);
+                if (lane == (int)p.slot) used = (int)p.phase;
+                if (elect_one()) mbar_expect_tx(full + p.slot, (uint32_t)__popc(tile) * geo.box * HD);
+                __syncwarp();
+                unsigned char *dst = ring + p.slot * kTile;
 #pragma unroll 1
-                for (int v = 0; ok && v < 2; ++v) {   // K, then V
-                    T8Place &p = v ? vp : kp;
-                    uint64_t *full = (v ? x.v_full : x.k_full) + p.slot;
-                    ok = warp_wait((v ? x.v_empty : x.k_empty) + p.slot, p.phase ^ 1u);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(full, bytes);
-                    if (lane == (int)p.slot) (v ? used_v : used_k) = (int)p.phase;
-                    __syncwarp();
-                    if (tile >> lane & 1u)
-                        tma_load_4d((v ? vring : kring) + p.slot * kTile + my_box * geo.box * HD, v ? &vmap : &kmap, 0, from, head, at, full);
-                    p.next(v ? geo.v_slots : geo.k_slots);
+                for (; tile; tile &= tile - 1) {
+                    const int b = __ffs(tile) - 1;
+                    const int at_b = __shfl_sync(0xffffffffu, at, in_group * boxes + b), from_b = __shfl_sync(0xffffffffu, from, in_group * boxes + b);
+                    if (elect_one()) tma_load_4d(dst + b * geo.box * HD, map, 0, from_b, head, at_b, full + p.slot);
                 }
+                p.next(slots);
             }
         }
         if (!ok) give_up();
         // nothing may be in flight when the CTA exits
         volatile int never = 0;
-        if (used_k >= 0) mbar_wait(&x.k_full[lane], (uint32_t)used_k, &never);
-        if (used_v >= 0) mbar_wait(&x.v_full[lane], (uint32_t)used_v, &never);
+        if (used >= 0) mbar_wait(full + lane, (uint32_t)used, &never);
     } else if (warp == P::mma_s) {
         // ---------------- S of every unit, up to two ahead of its softmax
         if (elect_one()) {

@@ -13,8 +13,8 @@
 //
 // One CTA has the block in hand: the CTA of a "leader", the first new token of its sequence or
 // one at a block's first slot.  Warps take (head, K or V) pairs, a thread 8 dims of a row; where
-// there are fewer pairs than warps, several share a pair's rows.  Up to kHold rows a thread stay in
-// registers between the maximum and the rounding, others are read again (from L2).  The
+// there are fewer pairs than warps, several share a pair's rows.  Up to eight rows a thread (FP32: four) stay in
+// registers, as they came, between the maximum and the rounding, others are read again (from L2).  The
 // queries' rotation is other CTAs' of the same launch.
 //
 // Bound: bytes (rows read once, codes written once).
@@ -25,7 +25,6 @@
 namespace ds4g {
 
 static constexpr int kA8Tokens = 16;   // tokens of a K/V CTA at most
-static constexpr int kHold = 4;
 static constexpr int kA8Warps = kApThreads / 32;
 
 // A block that one CTA stores into: rows tok .. tok + n - 1 of the token arrays at positions pos ..
@@ -148,9 +147,7 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
             const TI *src = static_cast<const TI *>(is_k ? a.k : a.v) + head * hd + d;
             const long long ss = is_k ? a.k_stride : a.v_stride;
             const int r0 = part * rpw + row, n = some && row < rpw ? w.n : 0;
-            auto value = [&](int r, float (&x)[8]) {
-                Row8<TI> v;
-                v.load(src + (long long)(w.tok + r) * ss);
+            auto turn = [&](int r, const Row8<TI> &v, float (&x)[8]) {   // (the angles: from L1 when they are read again)
                 v.floats(x);
                 if (turns) {
                     float c[8];
@@ -158,7 +155,14 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
                     turn8_rn(x, c, d, a.rot_dim);
                 }
             };
-            float x[kHold][8], top = 0.f;
+            auto value = [&](int r, float (&x)[8]) {
+                Row8<TI> v;
+                v.load(src + (long long)(w.tok + r) * ss);
+                turn(r, v, x);
+            };
+            constexpr int kHold = 16 / sizeof(TI);
+            Row8<TI> held[kHold];
+            float top = 0.f;
             auto add = [&](const float (&y)[8]) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -169,11 +173,17 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
 #pragma unroll
             for (int h = 0; h < kHold; ++h) {
                 const int r = r0 + h * stride;
-                if (r < n) value(r, x[h]);
+                if (r < n) held[h].load(src + (long long)(w.tok + r) * ss);
             }
 #pragma unroll
-            for (int h = 0; h < kHold; ++h)
-                if (r0 + h * stride < n) add(x[h]);
+            for (int h = 0; h < kHold; ++h) {
+                const int r = r0 + h * stride;
+                float y[8];
+                if (r < n) {
+                    turn(r, held[h], y);
+                    add(y);
+                }
+            }
             for (int r = r0 + kHold * stride; r < n; r += stride) {
                 float y[8];
                 value(r, y);
@@ -208,7 +218,11 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
 #pragma unroll
             for (int h = 0; h < kHold; ++h) {
                 const int r = r0 + h * stride;
-                if (r < n) *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(x[h], s);
+                float y[8];
+                if (r < n) {
+                    turn(r, held[h], y);
+                    *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(y, s);
+                }
             }
             for (int r = r0 + kHold * stride; r < n; r += stride) {
                 float y[8];
@@ -227,7 +241,7 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
 
 // CTAs 0 .. kv_ctas - 1: blocks of K and V; the others: the queries, ny of them a token group.
 template <typename TI, int U>
-__global__ void __launch_bounds__(kApThreads) k_paged_append8(const __grid_constant__ AppendArgs a, int kv_ctas,
+__global__ void __launch_bounds__(kApThreads, 3) k_paged_append8(const __grid_constant__ AppendArgs a, int kv_ctas,
                                                               int kv_tokens, int q_tokens, int ny)
 {
     const int bx = (int)blockIdx.x - kv_ctas;

@@ -25,14 +25,12 @@
 // columns of their own, in units of 2^-13 (E4M3 alone has 2^-9 .. 448: many small weights beside a large one would
 // vanish).  8 bits of each weight, or 2^-32 of the largest.
 // More rows: four times the columns would cost more than V's conversion.  Four warps make FP16 of V's
-// codes (the bits of an E4M3 value, its sign in front and the other seven from bit 7 on, are FP16 for
-// 2^-8 of it, also where it is subnormal) and P is FP16 (11 bits, or 2^-34 of the largest).
+// codes, which holds them exactly, and P is FP16 (11 bits, or 2^-34 of the largest).
 //
 // Masked places: a key outside the item's keys or in a missing page, or hidden from a row, gets the
 // weight 0.  In units at an edge (of the item's keys, or of what some rows see) the rows of V outside the
 // item's keys are zeroed in the tile, and NaN codes of keys that only some rows see become 0; rows
-// that see such a key get their NaN when the item ends.  (In FP16 the bits of a NaN code are finite: every
-// NaN is dealt with when the item ends.)
+// that see such a key get their NaN when the item ends.
 //
 // Roles (one CTA per SM): one to four groups of four warps, softmax and output of 8 or 16 rows each; four
 // warps for the queries' codes and V's tiles; one warp each for the items and TMA copies, the MMAs of S, the
@@ -137,11 +135,29 @@ __device__ __forceinline__ uint32_t t8_e4m3x2(float lo, float hi)
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float2 t8_floats(uint32_t codes)   // of the low two bytes
+__device__ __forceinline__ uint32_t t8_f16x2(uint32_t codes)   // of the low two bytes
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
+    return h;
+}
+__device__ __forceinline__ float2 t8_floats(uint32_t codes)
+{
+    const uint32_t h = t8_f16x2(codes);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// NaN codes among four (0x7f in the low seven bits) become 0; true if there was one.
+__device__ __forceinline__ bool t8_no_nan(uint32_t &w)
+{
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    w &= ~((nan >> 7) * 0xffu);
+    return nan != 0u;
+}
+__device__ __forceinline__ float t8_max3(float a, float b, float c)
+{
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));   // (the number beside a NaN)
+    return m;
 }
 // Two values as codes, and 16 times what the codes leave of them.
 __device__ __forceinline__ void t8_split(float a, float b, uint32_t &hi, uint32_t &lo)
@@ -570,30 +586,22 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 const int base = (tile0 + k) * kT8Keys;
                 ok = ok && warp_wait(&x.v_full[vp.slot], vp.phase);
                 unsigned char *src = vring + vp.slot * kTile;
+                const bool by_row = t8_by_row(ends, base, a.window), edge = by_row || base < lo || base + kT8Keys > hi;
+                // 16 codes of key j as they may be used
+                auto mend = [&](uint4 &w4, int j) {
+                    if (j < lo || j >= hi) {
+                        w4 = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (by_row && (j > ends.x || (a.window > 0 && j <= ends.y - a.window))) {
+                        if ((int)t8_no_nan(w4.x) | (int)t8_no_nan(w4.y) | (int)t8_no_nan(w4.z) | (int)t8_no_nan(w4.w)) x.poison[i % kT8Items] = 1;
+                    }
+                };
                 if (kDirect) {
-                    const bool by_row = t8_by_row(ends, base, a.window);
-                    if (by_row || base < lo || base + kT8Keys > hi) {
-                        // 16 bytes at a time, whole rows: their order in a row does not matter
+                    if (edge) {   // whole rows: the order of their chunks does not matter
 #pragma unroll 1
                         for (int c = t; c < (int)kTile / 16; c += 128) {
-                            const int j = base + c / (HD / 16);
-                            uint4 *at = reinterpret_cast<uint4 *>(src) + c;
-                            if (j < lo || j >= hi) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (by_row && (j > ends.x || (a.window > 0 && j <= ends.y - a.window))) {
-                                uint4 w4 = *at;
-                                uint32_t *w = reinterpret_cast<uint32_t *>(&w4), any = 0u;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {   // NaN codes: 0x7f in the low seven bits
-                                    const uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                    w[e] &= ~((nan >> 7) * 0xffu);
-                                    any |= nan;
-                                }
-                                if (any) {
-                                    *at = w4;
-                                    x.poison[i % kT8Items] = 1;
-                                }
-                            }
+                            uint4 *at = reinterpret_cast<uint4 *>(src) + c, w4 = *at;
+                            mend(w4, base + c / (HD / 16));
+                            *at = w4;
                         }
                         fence_proxy_async_smem();
                     }
@@ -604,43 +612,31 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     }
                 } else {
                     ok = ok && warp_wait(&x.w_empty[u & 1], (u >> 1 & 1u) ^ 1u);
-                    unsigned char *dst = wide + (u & 1) * kWide;
                     constexpr int CPK = HD / 16, KPP = 128 / CPK, TURNS = kT8Keys / KPP;   // 16-byte chunks of a key; keys of a turn
-                    const int c = t % CPK;
+                    const int c = t % CPK, key0 = t / CPK;
                     // rows of 128 bytes (64 dims), the second halves beside the first by groups of 8 keys; of
                     // the two 16-byte chunks the threads of the second half store the odd one first (banks)
                     const int half = c >> 2, c2 = (c & 3) * 2, odd = half;
-                    uint32_t nan = 0u;   // a bit a turn
+                    unsigned char *dst = wide + (u & 1) * kWide + half * 1024;
 #pragma unroll 1
                     for (int y0 = 0; y0 < TURNS; y0 += 4) {
                         uint4 in[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            in[y] = *reinterpret_cast<const uint4 *>(src + (uint32_t)((y0 + y) * KPP + t / CPK) * HD + c * 16);
+                            in[y] = *reinterpret_cast<const uint4 *>(src + (uint32_t)((y0 + y) * KPP + key0) * HD + c * 16);
+                        if (edge) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) mend(in[y], base + (y0 + y) * KPP + key0);
+                        }
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const int key = (y0 + y) * KPP + t / CPK;
-                            const uint32_t w[4] = {in[y].x, in[y].y, in[y].z, in[y].w};
-                            uint32_t bad = 0u, h[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                bad |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
-                                // a byte to the front of its half, then all but the sign to the right
-                                const uint32_t p = __byte_perm(w[e], 0u, 0x1404), q = __byte_perm(w[e], 0u, 0x3424);
-                                h[2 * e] = (p & 0x80008000u) | (p >> 1 & 0x3f803f80u);
-                                h[2 * e + 1] = (q & 0x80008000u) | (q >> 1 & 0x3f803f80u);
-                            }
-                            if (bad & 0x80808080u) nan |= 1u << (y0 + y);
-                            unsigned char *row = dst + (uint32_t)(key >> 3) * (H * 1024) + half * 1024 + (key & 7) * 128;
-                            const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
+                            const int key = (y0 + y) * KPP + key0;
+                            unsigned char *row = dst + (uint32_t)(key >> 3) * (H * 1024) + (key & 7) * 128;
+                            const uint4 h0 = make_uint4(t8_f16x2(in[y].x), t8_f16x2(in[y].x >> 16), t8_f16x2(in[y].y), t8_f16x2(in[y].y >> 16));
+                            const uint4 h1 = make_uint4(t8_f16x2(in[y].z), t8_f16x2(in[y].z >> 16), t8_f16x2(in[y].w), t8_f16x2(in[y].w >> 16));
                             *reinterpret_cast<uint4 *>(row + (((c2 + odd) ^ (key & 7)) << 4)) = odd ? h1 : h0;
                             *reinterpret_cast<uint4 *>(row + (((c2 + 1 - odd) ^ (key & 7)) << 4)) = odd ? h0 : h1;
                         }
-                    }
-                    while (nan) {   // of the item's keys?
-                        const int j = base + (__ffs(nan) - 1) * KPP + t / CPK;
-                        if (j >= lo && j < hi) x.poison[i % kT8Items] = 1;
-                        nan &= nan - 1;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -753,7 +749,8 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     }
                     float top = y[0];
 #pragma unroll
-                    for (int e = 1; e < OWN; ++e) top = fmaxf(top, y[e]);
+                    for (int e = 1; e < OWN - 1; e += 2) top = t8_max3(top, y[e], y[e + 1]);
+                    top = fmaxf(top, y[OWN - 1]);
                     if (t8_any(bar, unset || top > P::most)) {   // some row's weights outgrow its m, or it has none
                         int mine = 0;
 #pragma unroll
@@ -884,13 +881,12 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 if (tg < OWN) {
                     const int w0 = g * 4, r = r0 + tg;
                     const float sum = (x.part[w0][tg] + x.part[w0 + 1][tg]) + (x.part[w0 + 2][tg] + x.part[w0 + 3][tg]);
-                    constexpr float unit = kDirect ? 1.f : 256.f;   // (V's halves are 2^-8 of its codes)
                     if (part && r < n_rows) {
                         float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + ((size_t)it.part * a.rows + r) * 2;
                         ml[0] = x.set[r] ? -x.neg_m[r] : -INFINITY;
                         ml[1] = sum;
                     }
-                    x.factor[r] = part ? unit : sum == 0.f ? 0.f : unit / sum;
+                    x.factor[r] = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
                 }
                 t8_sync(bar);
             }

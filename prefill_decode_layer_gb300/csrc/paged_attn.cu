@@ -388,6 +388,7 @@ template <typename T, int ROWS, int CTAS, int V>   // V: adjacent dims per lane
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ AttnArgs a, int wide)
 {
     __shared__ float s_o[kJoinWarps][32 * V], s_l[kJoinWarps];
+    __shared__ float2 s_ml[CTAS];   // of a row that is the CTA's: its parts' maxima and sums
     const int hd = a.kv.head_dim;
     const int stride = ROWS > 0 ? ROWS : a.rows;
     const PartLayout lay(CTAS, stride, hd);
@@ -437,9 +438,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
         // part i: the CTA's own tail, then the head parts of the CTAs after it
         auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride + r; };
         float mx = -INFINITY, acc[V], sum;
-        const float2 m0 = lane < parts ? ml[slot(lane)] : make_float2(-INFINITY, 0.f);
-        mx = m0.x;
-        for (int i = lane + 32; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i)].x);
+        float2 m0 = make_float2(-INFINITY, 0.f);
+        if (wide) {   // (one wait for all of them)
+            for (int i = threadIdx.x; i < parts; i += kJoinThreads) s_ml[i] = ml[slot(i)];
+            __syncthreads();
+            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, s_ml[i].x);
+        } else {
+            if (lane < parts) m0 = ml[slot(lane)];
+            mx = m0.x;
+            for (int i = lane + 32; i < parts; i += 32) mx = fmaxf(mx, ml[slot(i)].x);
+        }
         mx = warp_max(mx);
         const float ref = finite_max(mx);
         const int w0 = wide ? warp : 0, ws = wide ? kJoinWarps : 1;
@@ -447,10 +455,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
             sum = 0.f;
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = w0; i < parts; i += ws) {
                 float2 m2 = make_float2(__shfl_sync(0xffffffffu, m0.x, i & 31), __shfl_sync(0xffffffffu, m0.y, i & 31));
-                if (i >= 32) m2 = ml[slot(i)];
+                if (wide) m2 = s_ml[i];
+                else if (i >= 32) m2 = ml[slot(i)];
                 const float f = pa_ex2(m2.x - ref);
                 sum = fmaf(f, m2.y, sum);
                 if (d < hd) {

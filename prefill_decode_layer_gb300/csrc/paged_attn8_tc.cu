@@ -92,7 +92,7 @@ struct T8Misc {
     __align__(16) float neg_m[kT8Rows], factor[kT8Rows], delta[kT8Rows];
     float part[16][16];                                // of a softmax warp: a value of each row
     int pos[kT8Rows], set[kT8Rows];                    // of a row: its position; it has an m
-    long long off[kT8Rows];                            // of a row in the output
+    long long off[kT8Rows], q_off[kT8Rows];            // of a row in the output; in the queries (-1: none)
 };
 
 struct T8Geometry {
@@ -116,23 +116,35 @@ int paged_attn8_tc_rows(int group, int max_new)
     return (rows + tiles - 1) / tiles;
 }
 
-// mbar_wait with one place for the poll (it is inlined where every unit passes).
+// mbar_wait with one place for the poll (it is inlined where every unit passes), which may sleep for up to
+// 0.1 ms: warps that poll take issue slots from those that work.
 __device__ __forceinline__ bool t8_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag)
 {
     long long t0 = 0;
-    for (unsigned n = 0;; ++n) {
-        if (mbar_try_wait(b, parity)) return true;
-        if ((n & 255u) == 0) {
-            const long long t = clock64();
-            if (n == 0) t0 = t;
-            else if (*abort_flag || t - t0 > kWaitCycles) return false;
-        }
+    for (bool first = true;; first = false) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(b)), "r"(parity), "r"(100000u)
+            : "memory");
+        if (ok) return true;
+        const long long t = clock64();
+        if (first) t0 = t;
+        else if (*abort_flag || t - t0 > kWaitCycles) return false;
     }
 }
 __device__ __forceinline__ uint32_t t8_e4m3x2(float lo, float hi)
 {
     unsigned short r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t t8_e4m3x2(__half2 v)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
     return r;
 }
 __device__ __forceinline__ uint32_t t8_f16x2(uint32_t codes)   // of the low two bytes
@@ -193,10 +205,11 @@ __device__ __forceinline__ int2 t8_ends(const PagedItem &it)
 {
     return make_int2(max(it.pos0 + it.tok_a, -1), max(it.pos0 + it.tok_b, -1));
 }
-// Whether some of its rows see a key of the unit from `base` that others do not.
+// Whether some of its rows see a key of the unit from `base` that others do not.  (Rows of one token: no.  Its
+// keys are the item's.)
 __device__ __forceinline__ bool t8_by_row(int2 ends, int base, int window)
 {
-    return base + kT8Keys - 1 > ends.x || (window > 0 && base <= ends.y - window);
+    return ends.x != ends.y && (base + kT8Keys - 1 > ends.x || (window > 0 && base <= ends.y - window));
 }
 
 // A place in a ring (kept up to date: no division at every use).
@@ -333,17 +346,26 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 }
                 ok = warp_wait(empty + p.slot, p.phase ^ 1u);
                 if (!ok) break;
-                // one lane issues them all: the compiler then sees uniform operands
-                uint32_t tile = loads >> (in_group * boxes) & ((1u << boxes) - 1u);
+                // one lane issues them all (the compiler then sees uniform operands), four at a time
+                const uint32_t tile = loads >> (in_group * boxes) & ((1u << boxes) - 1u);
                 if (lane == (int)p.slot) used = (int)p.phase;
-                if (elect_one()) mbar_expect_tx(full + p.slot, (uint32_t)__popc(tile) * geo.box * HD);
-                __syncwarp();
                 unsigned char *dst = ring + p.slot * kTile;
+                const bool one = elect_one();
+                if (one) mbar_expect_tx(full + p.slot, (uint32_t)__popc(tile) * geo.box * HD);
 #pragma unroll 1
-                for (; tile; tile &= tile - 1) {
-                    const int b = __ffs(tile) - 1;
-                    const int at_b = __shfl_sync(0xffffffffu, at, in_group * boxes + b), from_b = __shfl_sync(0xffffffffu, from, in_group * boxes + b);
-                    if (elect_one()) tma_load_4d(dst + b * geo.box * HD, map, 0, from_b, head, at_b, full + p.slot);
+                for (int b = 0; b < boxes; b += 4) {
+                    int at_b[4], from_b[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        at_b[z] = __shfl_sync(0xffffffffu, at, in_group * boxes + b + z);   // (past the tile's boxes: not used)
+                        from_b[z] = __shfl_sync(0xffffffffu, from, in_group * boxes + b + z);
+                    }
+                    if (one) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            if (tile >> (b + z) & 1u)
+                                tma_load_4d(dst + (b + z) * geo.box * HD, map, 0, from_b[z], head, at_b[z], full + p.slot);
+                    }
                 }
                 p.next(slots);
             }
@@ -519,63 +541,67 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             if (!it.more) break;
             const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, n_rows = it.n_rows;
             const int2 ends = t8_ends(it);
-            // queries: LPR threads a row, 8 dims each, two rows a thread at a time
-            constexpr int LPR = HD / 8, RPP = 128 / LPR;
-            constexpr int PASSES = NR > RPP ? NR / RPP : 1, BATCH = PASSES < 2 ? PASSES : 2;
+            // queries: LPR threads a row, 8 dims each, all rows in flight
+            if (t < NR) {
+                const int row = it.row0 + t, tok = row / a.group;
+                x.q_off[t] = t < n_rows ? (long long)(it.token + tok) * a.q_stride + (it.head * a.group + row - tok * a.group) * HD : -1;
+            }
+            t8_sync(bar);
+            constexpr int LPR = HD / 8, RPP = 128 / LPR, PASSES = NR > RPP ? NR / RPP : 1;
             const int sub = t % LPR, r_first = t / LPR;
-            uint4 qw[BATCH];
-            auto fetch = [&](int p0) {
+            uint4 qw[PASSES];
 #pragma unroll
-                for (int p = 0; p < BATCH; ++p) {
-                    const int r = (p0 + p) * RPP + r_first;
-                    qw[p] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < n_rows) {
-                        const int row = it.row0 + r, tok = row / a.group, hd = row - tok * a.group;
-                        qw[p] = *reinterpret_cast<const uint4 *>(qp + (long long)(it.token + tok) * a.q_stride +
-                                                                 (it.head * a.group + hd) * HD + sub * 8);
-                    }
-                }
-            };
-            fetch(0);
+            for (int p = 0; p < PASSES; ++p) {
+                qw[p] = make_uint4(0u, 0u, 0u, 0u);
+                const int r = p * RPP + r_first;
+                const long long off = r < NR ? x.q_off[r] : -1;   // (64 dims and 8 rows: half of the threads have none)
+                if (off >= 0) qw[p] = *reinterpret_cast<const uint4 *>(qp + off + sub * 8);
+            }
             ok = ok && warp_wait(&x.q_empty[i & 1], (i >> 1 & 1u) ^ 1u);
             unsigned char *q8 = qbuf + (i & 1) * kQ;
-#pragma unroll 1
-            for (int p0 = 0; p0 < PASSES; p0 += BATCH) {
-                uint4 w4[BATCH];
 #pragma unroll
-                for (int p = 0; p < BATCH; ++p) w4[p] = qw[p];
-                fetch(p0 + BATCH);
-#pragma unroll
-                for (int p = 0; p < BATCH; ++p) {
-                    const int r = (p0 + p) * RPP + r_first;
-                    const uint32_t w[4] = {w4[p].x, w4[p].y, w4[p].z, w4[p].w};
-                    float y[8], top = 0.f;
+            for (int p = 0; p < PASSES; ++p) {
+                const int r = p * RPP + r_first;
+                const uint32_t w[4] = {qw[p].x, qw[p].y, qw[p].z, qw[p].w};
+                auto largest = [&](bool finite) {   // of the row's magnitudes, as bits; or of its finite ones
+                    uint32_t m2 = 0u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[2 * e] = __uint_as_float(w[e] << 16);
-                        y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                        uint32_t v = w[e] & 0x7fff7fffu;
+                        if (finite) {
+                            if ((v & 0xffffu) >= 0x7f80u) v &= 0xffff0000u;
+                            if (v >= 0x7f800000u) v &= 0xffffu;
+                        }
+                        m2 = __vmaxu2(m2, v);
                     }
+                    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fabsf(y[e]) <= 3.402823466e38f ? fmaxf(top, fabsf(y[e])) : top;
+                    for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    return m;
+                };
+                uint32_t top = largest(false);
+                if (__any_sync(0xffffffffu, top >= 0x7f80u)) top = largest(true);
+                // the least power of two s with top <= 448 s
+                const int ex = top ? max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126) : 0;
+                const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+                uint32_t h[4], l[4];
 #pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    // the least power of two s with top <= 448 s
-                    const uint32_t b = __float_as_uint(top);
-                    const int ex = top > 0.f ? max((int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u), -126) : 0;
-                    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    uint32_t h[4], l[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)   // (inf: NaN)
-                        t8_split(fmaf(y[2 * e], 0.f, y[2 * e] * inv), fmaf(y[2 * e + 1], 0.f, y[2 * e + 1] * inv), h[e], l[e]);
-                    if (r < NR) {   // (64 dims and 8 rows: half of the threads)
-                        auto place = [&](int row) {   // of this thread's 8 bytes, in the swizzled tile
-                            if (HD == 128) return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8);
-                            return (uint32_t)((row >> 3) * 512 + (row & 7) * 64 + (((sub >> 1) ^ ((row >> 1) & 3)) << 4) + (sub & 1) * 8);
-                        };
-                        *reinterpret_cast<uint2 *>(q8 + place(r)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-                        *reinterpret_cast<uint2 *>(q8 + place(NR + r)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-                        if (sub == 0) x.q_scale[i % kT8Items][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    // as FP16, which holds 8 bits down to 2^-17; infinities become NaN
+                    __half2 y = __floats2half2_rn(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv);
+                    y = __hfma2(y, __float2half2_rn(0.f), y);
+                    h[e] = t8_e4m3x2(y);
+                    const uint32_t f = t8_f16x2(h[e]);
+                    l[e] = t8_e4m3x2(__hmul2(__hsub2(y, *reinterpret_cast<const __half2 *>(&f)), __float2half2_rn(16.f)));
+                }
+                if (r < NR) {
+                    auto place = [&](int row) {   // of this thread's 8 bytes, in the swizzled tile
+                        if (HD == 128) return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8);
+                        return (uint32_t)((row >> 3) * 512 + (row & 7) * 64 + (((sub >> 1) ^ ((row >> 1) & 3)) << 4) + (sub & 1) * 8);
+                    };
+                    *reinterpret_cast<uint2 *>(q8 + place(r)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                    *reinterpret_cast<uint2 *>(q8 + place(NR + r)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+                    if (sub == 0) x.q_scale[i % kT8Items][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
                 }
             }
             fence_proxy_async_smem();

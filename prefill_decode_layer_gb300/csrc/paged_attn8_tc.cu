@@ -200,6 +200,27 @@ __device__ __forceinline__ float t8_ex2(float x)
 // Two rows' values of an array of floats in shared memory.
 __device__ __forceinline__ ulonglong2 t8_rows4(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
 
+// v[e] over the warp's lanes, the largest or the sum; at each step a lane keeps half of the rows, so that lane i
+// ends with row i / (32 / N), in v[0].
+template <bool MAX, int N> __device__ __forceinline__ void t8_over_warp(float (&v)[N])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            const float send = up ? v[e] : v[e + n], keep = up ? v[e + n] : v[e], got = __shfl_xor_sync(0xffffffffu, send, o);
+            v[e] = MAX ? fmaxf(keep, got) : keep + got;
+        }
+    }
+#pragma unroll
+    for (int o = 16 / N; o > 0; o >>= 1) {
+        const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+        v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+    }
+}
+
 // The least and the greatest position of an item's rows.
 __device__ __forceinline__ int2 t8_ends(const PagedItem &it)
 {
@@ -559,30 +580,42 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             }
             ok = ok && warp_wait(&x.q_empty[i & 1], (i >> 1 & 1u) ^ 1u);
             unsigned char *q8 = qbuf + (i & 1) * kQ;
+            uint32_t top[PASSES];   // a row's largest magnitude, as bits
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const uint32_t m2 = __vmaxu2(__vmaxu2(qw[p].x & 0x7fff7fffu, qw[p].y & 0x7fff7fffu),
+                                             __vmaxu2(qw[p].z & 0x7fff7fffu, qw[p].w & 0x7fff7fffu));
+                top[p] = max(m2 & 0xffffu, m2 >> 16);
+            }
+            auto over_row = [&]() {
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p) top[p] = max(top[p], __shfl_xor_sync(0xffffffffu, top[p], o));
+            };
+            over_row();
+            uint32_t all = top[0];
+#pragma unroll
+            for (int p = 1; p < PASSES; ++p) all = max(all, top[p]);
+            if (__any_sync(0xffffffffu, all >= 0x7f80u)) {   // of the finite ones
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    const uint32_t w[4] = {qw[p].x, qw[p].y, qw[p].z, qw[p].w};
+                    top[p] = 0u;
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t v = w[e >> 1] >> (e & 1) * 16 & 0x7fffu;
+                        if (v < 0x7f80u) top[p] = max(top[p], v);
+                    }
+                }
+                over_row();
+            }
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
                 const int r = p * RPP + r_first;
                 const uint32_t w[4] = {qw[p].x, qw[p].y, qw[p].z, qw[p].w};
-                auto largest = [&](bool finite) {   // of the row's magnitudes, as bits; or of its finite ones
-                    uint32_t m2 = 0u;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t v = w[e] & 0x7fff7fffu;
-                        if (finite) {
-                            if ((v & 0xffffu) >= 0x7f80u) v &= 0xffff0000u;
-                            if (v >= 0x7f800000u) v &= 0xffffu;
-                        }
-                        m2 = __vmaxu2(m2, v);
-                    }
-                    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    return m;
-                };
-                uint32_t top = largest(false);
-                if (__any_sync(0xffffffffu, top >= 0x7f80u)) top = largest(true);
                 // the least power of two s with top <= 448 s
-                const int ex = top ? max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u), -126) : 0;
+                const int ex = top[p] ? max((int)(top[p] >> 7) - 127 - 8 + ((top[p] & 0x7fu) > 0x60u), -126) : 0;
                 const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
                 uint32_t h[4], l[4];
 #pragma unroll
@@ -687,6 +720,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
         const float *nm = x.neg_m + r0;
         const int *pos = x.pos + r0;
         unsigned u = 0, nr = 0;   // units, rounds of scales
+        constexpr int REP = 32 / OWN;     // lanes that end with the same row
         for (unsigned i = 0;; ++i) {
             bool ok = warp_wait(&x.item_full[i % kT8Items], i / kT8Items & 1u);
             if (t8_any(bar, !ok)) {
@@ -778,15 +812,11 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     for (int e = 1; e < OWN - 1; e += 2) top = t8_max3(top, y[e], y[e + 1]);
                     top = fmaxf(top, y[OWN - 1]);
                     if (t8_any(bar, unset || top > P::most)) {   // some row's weights outgrow its m, or it has none
-                        int mine = 0;
+                        float v[OWN];
 #pragma unroll
-                        for (int e = 0; e < OWN; ++e) {
-                            // the largest over the warp's keys, as integers in the order of the floats (NaN as -inf)
-                            const int b = __float_as_int(fmaxf(y[e], -INFINITY));
-                            const int m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
-                            if (lane == e) mine = m;
-                        }
-                        if (lane < OWN) x.part[warp][lane] = __int_as_float(mine ^ (mine >> 31 & 0x7fffffff));
+                        for (int e = 0; e < OWN; ++e) v[e] = y[e];
+                        t8_over_warp<true>(v);   // (the number beside a NaN)
+                        if (lane % REP == 0) x.part[warp][lane / REP] = fmaxf(v[0], -INFINITY);
                         t8_sync(bar);
                         bool none = false;
                         if (tg < OWN) {
@@ -882,26 +912,14 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             const unsigned last = u - 1;
             const bool part = it.part >= 0;
             if (active) {
-                // row sums over the warp's keys: at each step a lane keeps half of its rows
-                float v[OWN];
+                float v[OWN];   // row sums
 #pragma unroll
                 for (int e = 0; e < OWN / 2; ++e) {
                     const float2 f = unpack_f32x2(l[e]);
                     v[2 * e] = f.x;
                     v[2 * e + 1] = f.y;
                 }
-#pragma unroll
-                for (int n = OWN / 2, o = 16; n >= 1; n /= 2, o /= 2) {
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int e = 0; e < n; ++e) {
-                        const float send = up ? v[e] : v[e + n], keep = up ? v[e + n] : v[e];
-                        v[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                    }
-                }
-                constexpr int REP = 32 / OWN;   // lanes that hold the same row
-#pragma unroll
-                for (int o = REP / 2; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                t8_over_warp<false>(v);
                 if (lane % REP == 0) x.part[warp][lane / REP] = v[0];
                 t8_sync(bar);
                 if (tg < OWN) {

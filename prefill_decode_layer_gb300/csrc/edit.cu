@@ -8,19 +8,19 @@
 //
 // A CTA takes a slice of a row: a word a token in shared memory, in which every id of the history
 // that lies in the slice is counted (bit 31: seen; whole numbers, so that the order of the
-// atomics does not matter), then one pass over the slice's logits.  Biases follow: the thread of
-// the first entry of an id adds up all entries of it in FP64, in their order.
+// atomics does not matter), then one pass over the slice's logits.  Biases follow: a warp adds up all entries of an
+// id in FP64, in their order.
 // Bound: bytes (a logit read and written once, a bit of the mask), latency at one row.
 #include "paged.h"
 
 namespace ds4g {
 
-static constexpr int kEdThreads = 512;
+static constexpr int kEdThreads = 256;
 static constexpr int kEdHold = 32;                          // logits of a thread
 static constexpr int kEdSlice = kEdThreads * kEdHold;       // tokens of a CTA at most
 static constexpr int kEdBatch = 8;                          // ids of a thread in flight
 
-__global__ void __launch_bounds__(kEdThreads, 2) k_edit(const __grid_constant__ EditArgs a, int slice, int slices)
+__global__ void __launch_bounds__(kEdThreads, 4) k_edit(const __grid_constant__ EditArgs a, int slice, int slices)
 {
     extern __shared__ __align__(16) uint32_t s_count[];
     __shared__ int s_bias[kEditMaxBias];
@@ -80,16 +80,20 @@ __global__ void __launch_bounds__(kEdThreads, 2) k_edit(const __grid_constant__ 
     }
     if (!biases) return;
     __syncthreads();
-    for (int k = tid; k < biases; k += kEdThreads) {
+    // a warp an entry of the slice, if no entry before it has its id
+    for (int k = tid >> 5; k < biases; k += kEdThreads / 32) {
         const int id = s_bias[k];
         if (id < v0 || id >= v0 + n) continue;
         bool first = true;
-        for (int j = 0; j < k; ++j) first = first && s_bias[j] != id;
-        if (!first) continue;
         double sum = 0.0;
-        for (int j = k; j < biases; ++j)
-            if (s_bias[j] == id) sum += (double)a.bias[row * a.bias_stride + j];
-        if (!a.allowed || (a.allowed[row * a.allowed_stride + (id >> 5)] >> (id & 31) & 1u)) out[id - v0] += (float)sum;
+        for (int j0 = 0; first && j0 < biases; j0 += 32) {
+            const int j = j0 + lane;
+            uint32_t same = __ballot_sync(0xffffffffu, j < biases && s_bias[min(j, biases - 1)] == id);
+            if (j0 <= k) first = (same & (k - j0 < 32 ? (1u << (k - j0)) - 1u : 0xffffffffu)) == 0u;
+            for (; first && same; same &= same - 1) sum += (double)a.bias[row * a.bias_stride + j0 + __ffs(same) - 1];
+        }
+        if (lane == 0 && first && (!a.allowed || (a.allowed[row * a.allowed_stride + (id >> 5)] >> (id & 31) & 1u)))
+            out[id - v0] += (float)sum;
     }
 }
 

@@ -239,13 +239,16 @@ __device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_pe
     }
 }
 
-// CTAs 0 .. kv_ctas - 1: blocks of K and V; the others: the queries, ny of them a token group.
+// kv_ctas of the grid's CTAs, evenly spread, take blocks of K and V (a chain of look-ups, which the others' copies
+// cover); the others the queries, ny of them a token group.
 template <typename TI, int U>
 __global__ void __launch_bounds__(kApThreads, 3) k_paged_append8(const __grid_constant__ AppendArgs a, int kv_ctas,
-                                                              int kv_tokens, int q_tokens, int ny)
+                                                                 int kv_tokens, int q_tokens, int ny)
 {
-    const int bx = (int)blockIdx.x - kv_ctas;
-    if (bx < 0) append_blocks<TI>(a, kv_tokens, blockIdx.x);
+    const unsigned long long n = gridDim.x, b = blockIdx.x;
+    const int before = (int)(b * kv_ctas / n), upto = (int)((b + 1) * kv_ctas / n);   // CTAs of blocks
+    const int bx = (int)b - before;
+    if (upto > before) append_blocks<TI>(a, kv_tokens, before);
     else append_rows<TI, TI, U>(a, q_tokens, bx / ny, bx % ny, ny, 0);
 }
 

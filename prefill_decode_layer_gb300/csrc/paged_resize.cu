@@ -25,9 +25,10 @@ static constexpr int kRzThreads = 512;
 static constexpr int kRzWarps = kRzThreads / 32;
 static constexpr int kRzCluster = 8;
 
-// Three sums that are scanned together.
-struct RzSums {
-    long long back, more, tokens;
+// Three sums that are scanned together (the pages of all tables fit 32 bits: checked by the host).
+struct __align__(16) RzSums {
+    int back, more;
+    long long tokens;
     __device__ __forceinline__ void add(const RzSums &o)
     {
         back += o.back;
@@ -35,18 +36,29 @@ struct RzSums {
         tokens += o.tokens;
     }
 };
-__device__ __forceinline__ RzSums rz_shfl_up(const RzSums &v, int o)
+// Inclusive prefix over the first `n` lanes of a warp (a power of two; the others' values have no meaning).
+__device__ __forceinline__ RzSums rz_scan(RzSums v, int n)
 {
-    return {__shfl_up_sync(0xffffffffu, v.back, o), __shfl_up_sync(0xffffffffu, v.more, o),
-            __shfl_up_sync(0xffffffffu, v.tokens, o)};
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o >= n) break;
+        const RzSums y = {__shfl_up_sync(0xffffffffu, v.back, o), __shfl_up_sync(0xffffffffu, v.more, o),
+                          __shfl_up_sync(0xffffffffu, v.tokens, o)};
+        if (lane >= o) v.add(y);
+    }
+    return v;
+}
+__device__ __forceinline__ RzSums rz_from_lane(const RzSums &v, int lane)
+{
+    return {__shfl_sync(0xffffffffu, v.back, lane), __shfl_sync(0xffffffffu, v.more, lane), __shfl_sync(0xffffffffu, v.tokens, lane)};
 }
 __device__ __forceinline__ RzSums rz_remote(const RzSums *p, uint32_t rank)
 {
     RzSums v;
     const uint32_t at = cluster_map(p, rank);
-    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v.back) : "r"(at) : "memory");
-    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v.more) : "r"(at + 8) : "memory");
-    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v.tokens) : "r"(at + 16) : "memory");
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.back), "=r"(v.more) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v.tokens) : "r"(at + 8) : "memory");
     return v;
 }
 
@@ -83,7 +95,7 @@ template <typename T> __device__ __forceinline__ int rz_find(const T *p, int n, 
 __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_constant__ ResizeArgs a, int share)
 {
     extern __shared__ int sm[];
-    __shared__ RzSums s_warp[kRzWarps], s_cta[2];
+    __shared__ RzSums s_warp[2][kRzWarps], s_cta[2];
     int *s_back = sm, *s_more = sm + share + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), size = gridDim.x;   // one cluster
@@ -91,36 +103,31 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
     const int per = (share + kRzThreads - 1) / kRzThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
     pdl_wait();
     pdl_trigger();
-    // Exclusive prefix of `mine` over the cluster's threads; total: over all.
-    auto scan = [&](RzSums mine, int which, RzSums &cta, RzSums &total) {
-        RzSums incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const RzSums y = rz_shfl_up(incl, o);
-            if (lane >= o) incl.add(y);
-        }
-        if (lane == 31) s_warp[warp] = incl;
+    auto sync_all = [&]() {   // of the cluster
+        if (size == 1) __syncthreads();
+        else cluster_sync_all();
+    };
+    // Exclusive prefix of `mine` over the CTA's threads; cta: before the CTA; total: over all.
+    auto scan = [&](const RzSums &mine, int which, RzSums &cta, RzSums &total) {
+        RzSums before = rz_scan(mine, 32);
+        if (lane == 31) s_warp[which][warp] = before;
         __syncthreads();
-        RzSums before = {0, 0, 0}, all = {0, 0, 0};
-#pragma unroll 1
-        for (int w = 0; w < kRzWarps; ++w) {
-            if (w < warp) before.add(s_warp[w]);
-            all.add(s_warp[w]);
+        // the warps' and the CTAs' sums, by every warp
+        const RzSums w = rz_scan(s_warp[which][lane % kRzWarps], kRzWarps);
+        total = rz_from_lane(w, kRzWarps - 1);
+        const RzSums ahead = rz_from_lane(w, max(warp - 1, 0));
+        if (warp > 0) before.add(ahead);
+        before.add({-mine.back, -mine.more, -mine.tokens});
+        cta = RzSums{0, 0, 0};
+        if (size > 1) {
+            if (tid == 0) s_cta[which] = total;
+            cluster_sync_all();
+            const RzSums c = rz_scan(rz_remote(&s_cta[which], min((uint32_t)lane, size - 1)), kRzCluster);
+            total = rz_from_lane(c, (int)size - 1);
+            const RzSums earlier = rz_from_lane(c, max((int)rank - 1, 0));
+            if (rank > 0) cta = earlier;
         }
-        if (tid == 0) s_cta[which] = all;
-        cluster_sync_all();
-        cta = total = RzSums{0, 0, 0};
-#pragma unroll 1
-        for (uint32_t r = 0; r < size; ++r) {
-            const RzSums c = rz_remote(&s_cta[which], r);
-            if (r < rank) cta.add(c);
-            total.add(c);
-        }
-        before.add(incl);
-        before.back -= mine.back;
-        before.more -= mine.more;
-        before.tokens -= mine.tokens;
-        return before;   // within the CTA; `cta`: before the CTA
+        return before;
     };
     const int n_free = min(max(*a.n_free, 0), a.capacity);
     RzSums mine = {0, 0, 0};
@@ -131,15 +138,16 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
     }
     RzSums cta, total;
     RzSums at = scan(mine, 0, cta, total);
-    const long long top = n_free + total.back, back0 = cta.back;
+    const long long top = (long long)n_free + total.back, back0 = cta.back;
     // ---- who fits; pages given back
     RzSums taken = {0, 0, 0}, run = at;
     unsigned long long fit = 0;   // of this thread's sequences (64 at most: per <= kResizeMaxSeqs / kRzThreads / cluster)
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const RzSeq s = rz_seq(a, b0 + i);
-        const long long more = max(s.need - s.held, 0), tokens = max(s.want - s.now, 0ll);
-        s_back[i] = (int)run.back;
+        const int more = max(s.need - s.held, 0);
+        const long long tokens = max(s.want - s.now, 0ll);
+        s_back[i] = run.back;
         run.add({max(s.held - s.need, 0), more, tokens});
         const bool ok = (more == 0 || cta.more + run.more <= top) && (tokens == 0 || cta.tokens + run.tokens <= a.max_tokens);
         if (ok) {
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
             fit |= 1ull << (i - i0);
         }
     }
-    if (i1 == n && i0 < i1) s_back[n] = (int)run.back;
+    if (i1 == n && i0 < i1) s_back[n] = run.back;
     if (n == 0 && tid == 0) s_back[0] = 0;
     RzSums cta2, total2;
     at = scan(taken, 1, cta2, total2);
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         if (to < a.capacity) a.free[to] = *entry;
         *entry = -1;
     }
-    cluster_sync_all();   // what was given back may be taken; the old lengths have been read by then
+    sync_all();   // what was given back may be taken
     // ---- lengths, starts, and the pages before each sequence
     {
         RzSums run2 = at;
@@ -168,11 +176,11 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         for (int i = i0; i < i1; ++i) {
             const RzSeq s = rz_seq(a, b0 + i);
             const bool ok = fit >> (i - i0) & 1ull;
-            s_more[i] = (int)run2.more;
+            s_more[i] = run2.more;
             a.start[b0 + i] = (int)(cta2.tokens + run2.tokens);
             if (ok) run2.add({0, max(s.need - s.held, 0), max(s.want - s.now, 0ll)});
         }
-        if (i1 == n && i0 < i1) s_more[n] = (int)run2.more;
+        if (i1 == n && i0 < i1) s_more[n] = run2.more;
         if (n == 0 && tid == 0) s_more[0] = 0;
         if (rank == 0 && tid == 0) {
             a.start[a.n_seqs] = (int)total2.tokens;
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         const RzSeq s = rz_seq(a, b0 + i);
         if (s.want < s.now || (fit >> (i - i0) & 1ull)) a.length[b0 + i] = (int)s.want;
     }
-    cluster_sync_all();   // tables, lengths and starts are complete
+    sync_all();   // tables, lengths and starts are complete
     if (!a.slots) return;
     const long long tokens = total2.tokens, chunk = (tokens + size - 1) / size;
     const long long t1 = min((rank + 1) * chunk, tokens);

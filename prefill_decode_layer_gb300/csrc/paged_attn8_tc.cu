@@ -116,13 +116,20 @@ int paged_attn8_tc_rows(int group, int max_new)
     return (rows + tiles - 1) / tiles;
 }
 
-// mbar_wait with one place for the poll (it is inlined where every unit passes), which may sleep for up to
-// 0.1 ms: warps that poll take issue slots from those that work.
+// mbar_wait that looks once without sleeping (a wait that is over costs 60 cycles then, and 200 with the form
+// that may sleep), and then sleeps for up to 0.1 ms at a time: warps that poll take issue slots from those that work.
 __device__ __forceinline__ bool t8_wait(uint64_t *b, uint32_t parity, volatile int *abort_flag)
 {
-    long long t0 = 0;
-    for (bool first = true;; first = false) {
-        uint32_t ok;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const long long t0 = clock64();
+    while (true) {
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
             " selp.u32 %0, 1, 0, p;\n}\n"
@@ -130,9 +137,7 @@ __device__ __forceinline__ bool t8_wait(uint64_t *b, uint32_t parity, volatile i
             : "r"(smem_u32(b)), "r"(parity), "r"(100000u)
             : "memory");
         if (ok) return true;
-        const long long t = clock64();
-        if (first) t0 = t;
-        else if (*abort_flag || t - t0 > kWaitCycles) return false;
+        if (*abort_flag || clock64() - t0 > kWaitCycles) return false;
     }
 }
 __device__ __forceinline__ uint32_t t8_e4m3x2(float lo, float hi)

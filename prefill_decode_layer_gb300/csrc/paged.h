@@ -94,7 +94,7 @@ int paged_attn_tc_rows(int group, int max_new);
 cudaError_t paged_attn_tc(AttnArgs &a, cudaStream_t st, int nsm);
 // The tensor-core form over a cache in 8 bits (paged_attn8_tc.cu): BF16 queries.
 bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype);
-int paged_attn8_tc_rows(int group, int max_new);
+int paged_attn8_tc_rows(int n_kv_heads, int group, int max_new);   // (of all K/V heads of a unit)
 cudaError_t paged_attn8_tc(AttnArgs &a, cudaStream_t st, int nsm);
 // Shared by the forms (paged_attn.cu): CTAs of a launch over units of kt keys (and
 // a.whole), and the join of the tensor-core form's parts.

@@ -525,7 +525,7 @@ size_t paged_attn_ws_bytes(const PagedKV &kv, int group, int max_new, int kv_dty
 {
     size_t n = PartLayout(kAttnMaxCtas, kAttnRowsSimt, kv.head_dim).total;
     if (kv_dtype == kE4m3) {
-        const size_t t = PartLayout(kAttnMaxCtasTc, paged_attn8_tc_rows(group, max_new), kv.head_dim).total;
+        const size_t t = PartLayout(kAttnMaxCtasTc, paged_attn8_tc_rows(kv.n_kv_heads, group, max_new), kv.head_dim).total;
         return paged_attn8_tc_ok(kv, DS4G_BF16) && t > n ? t : n;
     }
     if (paged_attn_tc_ok(kv, group, DS4G_BF16, kv_dtype)) {
@@ -637,7 +637,7 @@ cudaError_t paged_attention(const AttnArgs &in, int q_dtype, int kv_dtype, cudaS
         return paged_attn_tc(a, st, nsm);
     }
     if (kv_dtype == kE4m3 && paged_attn8_tc_ok(a.kv, q_dtype)) {
-        a.rows = paged_attn8_tc_rows(a.group, a.s.max_new);
+        a.rows = paged_attn8_tc_rows(a.kv.n_kv_heads, a.group, a.s.max_new);
         return paged_attn8_tc(a, st, nsm);
     }
     if (kv_dtype == kE4m3)

@@ -57,19 +57,21 @@ static constexpr int kT8Items = 4;                     // items ahead of the sof
 static constexpr int kT8Scales = 4;                    // rounds of scales that are there at most
 static constexpr int kT8Smem = 227 * 1024;
 
-// What follows from the columns of query rows NR (8, 16, 32 or 64) of a kernel.
-template <int NR> struct T8 {
+// What follows from the columns of query rows NR (8, 16, 32 or 64) and the K/V heads HP of a kernel's units.
+template <int NR, int HP> struct T8 {
     static constexpr bool direct = NR <= 32;
     static constexpr int own = NR < 16 ? NR : 16;      // rows of a softmax thread
-    static constexpr int groups = NR / own;
+    static constexpr int groups = HP * (NR / own);
     static constexpr int soft = groups * 128;          // softmax threads
     static constexpr int conv = groups * 4;            // warps: the first of the queries and V's tiles, then ..
     static constexpr int tma = conv + 4, mma_s = tma + 2, mma_o = tma + 3, scale = tma + 4;   // (tma: K's copies and the items, tma + 1: V's)
     static constexpr int threads = (scale + 1) * 32;
-    static constexpr int s_cols = 2 * NR, o_cols = direct ? 4 * NR : NR;   // of a unit, of an item
+    static constexpr int s_head = 2 * NR, o_head = direct ? 4 * NR : NR;   // columns of a head: of a unit, of an item
+    static constexpr int s_cols = HP * s_head, o_cols = HP * o_head;
     static constexpr int cols = 2 * s_cols + 2 * o_cols <= 128 ? 128 : 2 * s_cols + 2 * o_cols <= 256 ? 256 : 512;
     // log2 of the largest weight when m is set, and of the largest that fits
     static constexpr float off = direct ? 5.f : 9.f, most = direct ? 8.f : 15.f;
+    static_assert(HP == 1 || (direct && NR == own), "of two heads each has a group");
 };
 
 struct T8Misc {
@@ -84,14 +86,14 @@ struct T8Misc {
     PagedItem item[kT8Items];
     PagedCursor cur;
     long long scratch[25];
-    float2 sc[kT8Scales][kT8Keys];                     // of a round's blocks: ks scale log2 e, log2 vs (-inf: no page)
+    float2 sc[kT8Scales][2][kT8Keys];                  // of a round's blocks, by head: ks scale log2 e, log2 vs (-inf: no page)
     int poison[kT8Items];                              // a V row of the item has a NaN that was taken out
     uint32_t tmem;
     int abort_flag;
     __align__(16) float q_scale[kT8Items][kT8Rows];    // of an item's rows
     __align__(16) float neg_m[kT8Rows], factor[kT8Rows], delta[kT8Rows];
     float part[16][16];                                // of a softmax warp: a value of each row
-    int pos[kT8Rows], set[kT8Rows];                    // of a row: its position; it has an m
+    int pos[kT8Rows], set[kT8Rows], row[kT8Rows];      // of a row: its position; it has an m; its place among the item's
     long long off[kT8Rows], q_off[kT8Rows];            // of a row in the output; in the queries (-1: none)
 };
 
@@ -102,6 +104,7 @@ struct T8Geometry {
     // scales: one for every 2^gran keys of a unit at least (the part of the block size that divides 128), so
     // many a unit, and the units of a round: 32 scales, or one unit where it has more
     int gran, per_unit, round;
+    int group, n_heads;   // query heads of a K/V head, K/V heads (AttnArgs' are those of a unit's heads taken as one)
 };
 
 bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype)
@@ -109,11 +112,17 @@ bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype)
     return q_dtype == DS4G_BF16 && (kv.head_dim == 64 || kv.head_dim == 128) && kv.page_size % 8 == 0;
 }
 
+// K/V heads of a unit: two where their rows fit a group each.  A head's rows of a tile are 128 bytes (64) apart by all
+// heads; two heads' are read side by side, which DRAM serves better, and a unit's waits serve twice the bytes.
+int paged_attn8_tc_heads(int n_kv_heads, int group, int max_new)
+{
+    return n_kv_heads % 2 == 0 && group <= 16 && group * max_new <= 16 ? 2 : 1;
+}
 // Query rows of a tile: as few tiles as hold them, of equal size.
-int paged_attn8_tc_rows(int group, int max_new)
+int paged_attn8_tc_rows(int n_kv_heads, int group, int max_new)
 {
     const int rows = group * max_new, tiles = (rows + kT8Rows - 1) / kT8Rows;
-    return (rows + tiles - 1) / tiles;
+    return paged_attn8_tc_heads(n_kv_heads, group, max_new) * ((rows + tiles - 1) / tiles);
 }
 
 // mbar_wait that looks once without sleeping (a wait that is over costs 60 cycles then, and 200 with the form
@@ -250,18 +259,19 @@ struct T8Place {
     }
 };
 
-// HD: head_dim.  NR: columns of query rows, the tile's rows or more.
-template <int HD, int NR>
-__global__ void __launch_bounds__(T8<NR>::threads, 1)
+// HD: head_dim.  NR: columns of a head's query rows, its rows of a tile or more.  HP: K/V heads of a unit.
+template <int HD, int NR, int HP>
+__global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
     k_paged_attn8_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ AttnArgs a, const __grid_constant__ T8Geometry geo)
 {
-    using P = T8<NR>;
+    using P = T8<NR, HP>;
     constexpr bool kDirect = P::direct;
     constexpr int H = HD / 64;                          // 128-byte blocks of an FP16 row
-    constexpr uint32_t kTile = HD * kT8Keys;            // bytes of a K or V tile of codes
+    constexpr uint32_t kGroup = 8 * HD;                 // bytes of 8 keys of a head: [16 groups][HP heads][8 keys][HD] is ..
+    constexpr uint32_t kTile = HP * HD * kT8Keys;       // .. a K or V tile of codes
     constexpr uint32_t kWide = kDirect ? 0 : 2 * kTile; // of V in FP16
-    constexpr uint32_t kQ = 2 * NR * HD, kP = kT8Keys * 128;
+    constexpr uint32_t kQhead = 2 * NR * HD, kQ = HP * kQhead, kP = kT8Keys * 128;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *wide = sm, *pbuf = wide + 2 * kWide, *qbuf = pbuf + 2 * kP, *kring = qbuf + 2 * kQ;
     unsigned char *vring = kring + (uint32_t)geo.k_slots * kTile;
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             __syncwarp();
             if (!it.more) break;
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
-            const int lo = it.lo, hi = it.hi, head = it.head, t0 = it.t0, t1 = it.t1;
+            const int lo = it.lo, hi = it.hi, head = it.head * HP, t0 = it.t0, t1 = it.t1;
             if (is_v) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x.item_empty[i % kT8Items]);
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 if (in_group == group) {
                     // a page that is not there: out of bounds, read as zeros
                     at = page < 0 || page >= a.kv.n_pages ? a.kv.n_pages : page;
-                    from = slot;
+                    from = slot >> 3;
                     loads = __ballot_sync(0xffffffffu, load);
                     // the next group's, on its way meanwhile
                     const int tile = t + group + my_tile, j = tile * kT8Keys + my_box * geo.box;
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 if (lane == (int)p.slot) used = (int)p.phase;
                 unsigned char *dst = ring + p.slot * kTile;
                 const bool one = elect_one();
-                if (one) mbar_expect_tx(full + p.slot, (uint32_t)__popc(tile) * geo.box * HD);
+                if (one) mbar_expect_tx(full + p.slot, (uint32_t)__popc(tile) * geo.box * (HP * HD));
 #pragma unroll 1
                 for (int b = 0; b < boxes; b += 4) {
                     int at_b[4], from_b[4];
@@ -390,7 +400,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
                             if (tile >> (b + z) & 1u)
-                                tma_load_4d(dst + (b + z) * geo.box * HD, map, 0, from_b[z], head, at_b[z], full + p.slot);
+                                tma_load_5d(dst + (b + z) * geo.box * (HP * HD), map, 0, 0, head, from_b[z], at_b[z], full + p.slot);
                     }
                 }
                 p.next(slots);
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
     } else if (warp == P::mma_s) {
         // ---------------- S of every unit, up to two ahead of its softmax
         if (elect_one()) {
-            const uint32_t id = idesc_e4m3_f32(kT8Keys, P::s_cols);
+            const uint32_t id = idesc_e4m3_f32(kT8Keys, P::s_head);
             unsigned u = 0, item = 0;
             int left = 0;
             T8Place kp = {0, 0};
@@ -423,12 +433,15 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                      t8_wait(&x.k_full[kp.slot], kp.phase, ab);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ka = smem_u32(kring) + kp.slot * kTile, qa = smem_u32(qbuf) + ((item - 1) & 1) * kQ;
-                const uint64_t kd = HD == 128 ? sdesc_kmajor_sw128(ka) : sdesc_kmajor_sw64(ka);
-                const uint64_t qd = HD == 128 ? sdesc_kmajor_sw128(qa) : sdesc_kmajor_sw64(qa);
 #pragma unroll
-                for (int ks = 0; ks < HD / 32; ++ks)
-                    tc_mma_e4m3(tmem + (u & 1) * P::s_cols, kd + (uint64_t)(ks * 2), qd + (uint64_t)(ks * 2), id, ks > 0);
+                for (int h = 0; h < HP; ++h) {
+                    const uint32_t ka = smem_u32(kring) + kp.slot * kTile + h * kGroup, qa = smem_u32(qbuf) + ((item - 1) & 1) * kQ + h * kQhead;
+                    const uint64_t kd = HD == 128 ? sdesc_kmajor_sw128(ka, HP * kGroup) : sdesc_kmajor_sw64(ka, HP * kGroup);
+                    const uint64_t qd = HD == 128 ? sdesc_kmajor_sw128(qa, kGroup) : sdesc_kmajor_sw64(qa, kGroup);
+#pragma unroll
+                    for (int ks = 0; ks < HD / 32; ++ks)
+                        tc_mma_e4m3(tmem + (u & 1) * P::s_cols + h * P::s_head, kd + (uint64_t)(ks * 2), qd + (uint64_t)(ks * 2), id, ks > 0);
+                }
                 tc_commit(&x.s_full[u & 1]);
                 tc_commit(&x.k_empty[kp.slot]);
                 kp.next(geo.k_slots);
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
     } else if (warp == P::mma_o) {
         // ---------------- O of every unit
         if (elect_one()) {
-            const uint32_t id = kDirect ? idesc_e4m3_f32_mn(128, P::o_cols) : idesc_f16_f32_mn(128, P::o_cols);
+            const uint32_t id = kDirect ? idesc_e4m3_f32_mn(128, P::o_head) : idesc_f16_f32_mn(128, P::o_head);
             unsigned u = 0, item = 0;
             int left = 0, base = 0, lo = 0, hi = 0;
             int2 ends = make_int2(0, 0);
@@ -473,12 +486,16 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     // (64 dims: rows 64 .. 127 of the MMA run on into what lies behind, and are not read)
-                    const uint32_t va = smem_u32(vring) + vp.slot * kTile;
-                    const uint64_t vd = HD == 128 ? sdesc_mnmajor_sw128(va, 1024, 1024) : sdesc_mnmajor_sw64(va, 512, 512);
-                    const uint64_t pd = sdesc_mnmajor_sw128(pa, 1024, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < kT8Keys / 32; ++ks)
-                        tc_mma_e4m3(d, vd + (uint64_t)(ks * 32 * HD >> 4), pd + (uint64_t)(ks * 32 * 128 >> 4), id, !fresh || ks > 0);
+                    for (int h = 0; h < HP; ++h) {
+                        const uint32_t va = smem_u32(vring) + vp.slot * kTile + h * kGroup;
+                        const uint64_t vd = HD == 128 ? sdesc_mnmajor_sw128(va, 1024, HP * kGroup) : sdesc_mnmajor_sw64(va, 512, HP * kGroup);
+                        const uint64_t pd = sdesc_mnmajor_sw128(pa + h * P::o_head, 1024, 1024);   // a byte a column
+#pragma unroll
+                        for (int ks = 0; ks < kT8Keys / 32; ++ks)
+                            tc_mma_e4m3(d + h * P::o_head, vd + (uint64_t)(ks * 4 * HP * kGroup >> 4), pd + (uint64_t)(ks * 32 * 128 >> 4), id,
+                                        !fresh || ks > 0);
+                    }
                     tc_commit(&x.v_empty[vp.slot]);
                 } else {
                     ok = ok && t8_wait(&x.w_full[u & 1], u >> 1 & 1u, ab) && t8_wait(&x.p_full[u & 1], u >> 1 & 1u, ab);
@@ -513,19 +530,21 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             if (!ok) break;
             const PagedItem &it = x.item[i % kT8Items];
             if (!it.more) break;
-            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, head = it.head;
+            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, head = it.head * HP;
             const int *table = a.s.table + (long long)it.seq * a.s.table_stride;
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.item_empty[i % kT8Items]);
             const int all = (units + geo.round - 1) / geo.round * steps;
             int page = -1, next_slot = 0;
-            float k = 0.f, v = 0.f;
+            float k[HP] = {}, v[HP] = {};
 #pragma unroll 1
             for (int s = -2, in_round = 0; ok && s < all; ++s) {
                 if (s >= 0) {
                     if (in_round == 0) ok = warp_wait(&x.sc_empty[n % kT8Scales], (n / kT8Scales & 1u) ^ 1u);
-                    x.sc[n % kT8Scales][in_round * 32 + lane] =
-                        make_float2(fminf(k * a.scale_log2, 3.402823466e38f), v > 0.f ? log2f(v) : -INFINITY);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h)
+                        x.sc[n % kT8Scales][h][in_round * 32 + lane] =
+                            make_float2(fminf(k[h] * a.scale_log2, 3.402823466e38f), v[h] > 0.f ? log2f(v[h]) : -INFINITY);
                     if (++in_round == steps) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&x.sc_full[n % kT8Scales]);
@@ -533,11 +552,12 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                         ++n;
                     }
                 }
-                k = v = 0.f;   // (no page)
-                if (page >= 0 && page < a.kv.n_pages) {
-                    const long long at = page * a.kv.scale_stride + next_slot / a.kv.block * a.kv.n_kv_heads + head;
-                    k = kv8_scale(a.kv.k_scale[at]);
-                    v = kv8_scale(a.kv.v_scale[at]);
+                const bool paged = page >= 0 && page < a.kv.n_pages;
+                const long long at = paged ? page * a.kv.scale_stride + next_slot / a.kv.block * geo.n_heads + head : 0;
+#pragma unroll
+                for (int h = 0; h < HP; ++h) {
+                    k[h] = paged ? kv8_scale(a.kv.k_scale[at + h]) : 0.f;   // (0: no page)
+                    v[h] = paged ? kv8_scale(a.kv.v_scale[at + h]) : 0.f;
                 }
                 // the first key of this lane's scale of step s + 2
                 page = -1;
@@ -565,22 +585,23 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             }
             const PagedItem &it = x.item[i % kT8Items];
             if (!it.more) break;
-            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, n_rows = it.n_rows;
+            const int units = it.t1 - it.t0, lo = it.lo, hi = it.hi, tile0 = it.t0, n_rows = it.n_rows / HP;
             const int2 ends = t8_ends(it);
             // queries: LPR threads a row, 8 dims each, all rows in flight
-            if (t < NR) {
-                const int row = it.row0 + t, tok = row / a.group;
-                x.q_off[t] = t < n_rows ? (long long)(it.token + tok) * a.q_stride + (it.head * a.group + row - tok * a.group) * HD : -1;
+            if (t < HP * NR) {
+                const int h = t / NR, row = it.row0 + t % NR, tok = row / geo.group;
+                x.q_off[t] = t % NR < n_rows ? (long long)(it.token + tok) * a.q_stride + (it.head * a.group + h * geo.group + row - tok * geo.group) * HD
+                                             : -1;
             }
             t8_sync(bar);
-            constexpr int LPR = HD / 8, RPP = 128 / LPR, PASSES = NR > RPP ? NR / RPP : 1;
+            constexpr int LPR = HD / 8, RPP = 128 / LPR, ROWS = HP * NR, PASSES = ROWS > RPP ? ROWS / RPP : 1;
             const int sub = t % LPR, r_first = t / LPR;
             uint4 qw[PASSES];
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
                 qw[p] = make_uint4(0u, 0u, 0u, 0u);
                 const int r = p * RPP + r_first;
-                const long long off = r < NR ? x.q_off[r] : -1;   // (64 dims and 8 rows: half of the threads have none)
+                const long long off = r < ROWS ? x.q_off[r] : -1;   // (64 dims and 8 rows: half of the threads have none)
                 if (off >= 0) qw[p] = *reinterpret_cast<const uint4 *>(qp + off + sub * 8);
             }
             ok = ok && warp_wait(&x.q_empty[i & 1], (i >> 1 & 1u) ^ 1u);
@@ -632,13 +653,14 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     const uint32_t f = t8_f16x2(h[e]);
                     l[e] = t8_e4m3x2(__hmul2(__hsub2(y, *reinterpret_cast<const __half2 *>(&f)), __float2half2_rn(16.f)));
                 }
-                if (r < NR) {
+                if (r < ROWS) {
                     auto place = [&](int row) {   // of this thread's 8 bytes, in the swizzled tile
                         if (HD == 128) return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8);
                         return (uint32_t)((row >> 3) * 512 + (row & 7) * 64 + (((sub >> 1) ^ ((row >> 1) & 3)) << 4) + (sub & 1) * 8);
                     };
-                    *reinterpret_cast<uint2 *>(q8 + place(r)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-                    *reinterpret_cast<uint2 *>(q8 + place(NR + r)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+                    unsigned char *qh = q8 + r / NR * kQhead;   // of the row's head
+                    *reinterpret_cast<uint2 *>(qh + place(r % NR)) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                    *reinterpret_cast<uint2 *>(qh + place(NR + r % NR)) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
                     if (sub == 0) x.q_scale[i % kT8Items][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
                 }
             }
@@ -664,7 +686,8 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
 #pragma unroll 1
                         for (int c = t; c < (int)kTile / 16; c += 128) {
                             uint4 *at = reinterpret_cast<uint4 *>(src) + c, w4 = *at;
-                            mend(w4, base + c / (HD / 16));
+                            const int row = c / (HD / 16);   // (of 8 keys of one head, then of the other)
+                            mend(w4, base + row / (8 * HP) * 8 + row % 8);
                             *at = w4;
                         }
                         fence_proxy_async_smem();
@@ -719,6 +742,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
         // ---------------- softmax and output: rows r0 .. r0 + OWN - 1; thread: key of S, dim of O
         constexpr int OWN = P::own;
         const int g = warp >> 2, wq = warp & 3, key = 32 * wq + lane, r0 = g * OWN, bar = 1 + g, tg = threadIdx.x & 127;
+        const int head_row = HP > 1 ? r0 : 0;   // the first row of the group's head
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const int win = a.window > 0 ? a.window : 0x7fffffff;
         bf16 *out = static_cast<bf16 *>(a.out);
@@ -734,13 +758,15 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
             }
             const PagedItem &it = x.item[i % kT8Items];
             if (!it.more) break;
-            const int units = it.t1 - it.t0, n_rows = it.n_rows, lo = it.lo, hi = it.hi;
-            const bool active = n_rows > r0;
+            const int units = it.t1 - it.t0, n_rows = it.n_rows / HP, lo = it.lo, hi = it.hi;   // (rows of a head)
+            const bool active = n_rows > r0 - head_row;
             const int2 ends = t8_ends(it);
             if (tg < OWN) {   // (rows that are not there are taken as the last one)
-                const int r = r0 + tg, row = it.row0 + min(r, n_rows - 1), tok = row / a.group, hd = row - tok * a.group;
+                const int r = r0 + tg, row = min(r - head_row, n_rows - 1), tok = (it.row0 + row) / geo.group;
+                const int hd = (HP > 1 ? g : 0) * geo.group + it.row0 + row - tok * geo.group;
                 x.pos[r] = max(it.pos0 + tok, -1);
                 x.off[r] = (long long)(it.token + tok) * a.out_stride + (it.head * a.group + hd) * HD;
+                x.row[r] = HP > 1 ? tok * a.group + hd : row;
                 x.neg_m[r] = 0.f;
                 x.set[r] = 0;
             }
@@ -755,7 +781,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
 #pragma unroll 1
             for (int k = 0; k < units; ++k, ++u, base += kT8Keys) {
                 if (in_round == 0) ok = ok && warp_wait(&x.sc_full[nr % kT8Scales], nr / kT8Scales & 1u);
-                const float2 sc = x.sc[nr % kT8Scales][in_round * geo.per_unit + (key >> geo.gran)];
+                const float2 sc = x.sc[nr % kT8Scales][HP > 1 ? g : 0][in_round * geo.per_unit + (key >> geo.gran)];
                 if (++in_round == geo.round || k == units - 1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&x.sc_empty[nr % kT8Scales]);
@@ -768,7 +794,7 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                     const int j = base + key;
                     const bool there = j >= lo && j < hi && sc.y > -INFINITY;
                     const bool by_row = t8_by_row(ends, base, a.window);
-                    const uint32_t t_s = tmem + lanes + (u & 1) * P::s_cols + r0;
+                    const uint32_t t_s = tmem + lanes + (u & 1) * P::s_cols + head_row * 2 + r0 - head_row;
                     const uint64_t kc = pack_f32x2(sc.x, sc.x), lv = pack_f32x2(sc.y, sc.y), sixteenth = pack_f32x2(0.0625f, 0.0625f);
                     float y[OWN];   // t_rj - m_r
                     {
@@ -930,8 +956,8 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                 if (tg < OWN) {
                     const int w0 = g * 4, r = r0 + tg;
                     const float sum = (x.part[w0][tg] + x.part[w0 + 1][tg]) + (x.part[w0 + 2][tg] + x.part[w0 + 3][tg]);
-                    if (part && r < n_rows) {
-                        float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + ((size_t)it.part * a.rows + r) * 2;
+                    if (part && r - head_row < n_rows) {
+                        float *ml = reinterpret_cast<float *>(a.ws + lay.ml) + ((size_t)it.part * a.rows + x.row[r]) * 2;
                         ml[0] = x.set[r] ? -x.neg_m[r] : -INFINITY;
                         ml[1] = sum;
                     }
@@ -950,14 +976,14 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
                         const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
                         if (page < 0) continue;
                         const uint8_t code = static_cast<const uint8_t *>(a.kv.v)[page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
-                                                                                  it.head * a.kv.head_stride + key];
+                                                                                  (it.head * HP + (HP > 1 ? g : 0)) * a.kv.head_stride + key];
                         if ((code & 0x7fu) != 0x7fu) continue;
 #pragma unroll 1
                         for (int e = 0; e < OWN; ++e)
                             if (j <= pos[e] && j > pos[e] - win) nan |= 1u << e;
                     }
                 }
-                float *po = reinterpret_cast<float *>(a.ws + lay.o) + ((size_t)(part ? it.part : 0) * a.rows + r0) * HD + key;
+                float *po = reinterpret_cast<float *>(a.ws + lay.o) + (size_t)(part ? it.part : 0) * a.rows * HD + key;
 #pragma unroll 1
                 for (int q = 0; q < OWN; q += 8) {
                     float f[8];
@@ -979,10 +1005,10 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int r = r0 + q + e;
-                        if (r >= n_rows) break;
+                        if (r - head_row >= n_rows) break;
                         float v = f[e] * x.factor[r];
                         if (nan >> (q + e) & 1u) v = NAN;
-                        if (part) po[(q + e) * HD] = v;
+                        if (part) po[x.row[r] * HD] = v;
                         else out[x.off[r] + key] = __float2bfloat16_rn(v);
                     }
                 }
@@ -1008,27 +1034,37 @@ __global__ void __launch_bounds__(T8<NR>::threads, 1)
 
 static int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-template <int HD, int NR>
+template <int HD, int NR, int HP>
 static cudaError_t t8_go(AttnArgs &a, T8Geometry &g, cudaStream_t st, int grid)
 {
-    constexpr bool direct = T8<NR>::direct;
+    constexpr bool direct = T8<NR, HP>::direct;
     CUtensorMap km, vm;
-    const long long dims[4] = {HD, a.kv.page_size, a.kv.n_kv_heads, a.kv.n_pages};
-    const long long strides[3] = {a.kv.slot_stride, a.kv.head_stride, a.kv.page_stride};
-    const int box[4] = {HD, g.box, 1, 1};
-    cudaError_t e = tc::make_map_u8_nd(&km, a.kv.k, 4, dims, strides, box, HD);
-    if (!e) e = tc::make_map_u8_nd(&vm, a.kv.v, 4, dims, strides, box, direct ? HD : 0);
+    // 8 slots, then the heads, then the groups of 8 slots of a page
+    const long long dims[5] = {HD, 8, g.n_heads, a.kv.page_size / 8, a.kv.n_pages};
+    const long long strides[4] = {a.kv.slot_stride, a.kv.head_stride, 8 * a.kv.slot_stride, a.kv.page_stride};
+    const int box[5] = {HD, 8, HP, g.box / 8, 1};
+    cudaError_t e = tc::make_map_u8_nd(&km, a.kv.k, 5, dims, strides, box, HD);
+    if (!e) e = tc::make_map_u8_nd(&vm, a.kv.v, 5, dims, strides, box, direct ? HD : 0);
     if (e) return e;
-    constexpr int tile = HD * kT8Keys, fixed = (direct ? 0 : 4 * tile) + 2 * kT8Keys * 128 + 4 * NR * HD + (int)sizeof(T8Misc);
+    constexpr int tile = HP * HD * kT8Keys, fixed = (direct ? 0 : 4 * tile) + 2 * kT8Keys * 128 + 4 * HP * NR * HD + (int)sizeof(T8Misc);
     constexpr int room = (kT8Smem - fixed) / tile, slots = room > 2 * kT8MaxSlots ? 2 * kT8MaxSlots : room;
     static_assert(slots >= 4, "two tiles of K and of V beside the buffers");
     g.k_slots = (slots + 1) / 2;
     g.v_slots = slots / 2;
     static PerDevice once;
-    auto kernel = k_paged_attn8_tc<HD, NR>;
+    auto kernel = k_paged_attn8_tc<HD, NR, HP>;
     e = allow_once(once, kernel, kT8Smem);
     if (e) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(T8<NR>::threads), (size_t)(fixed + slots * tile), st, km, vm, a, g);
+    return launch_pdl(kernel, dim3(grid), dim3(T8<NR, HP>::threads), (size_t)(fixed + slots * tile), st, km, vm, a, g);
+}
+
+template <int HD> static cudaError_t t8_dim(AttnArgs &a, T8Geometry &g, int heads, cudaStream_t st, int grid)
+{
+    const int rows = a.rows / heads;
+    if (heads == 2) return rows <= 8 ? t8_go<HD, 8, 2>(a, g, st, grid) : t8_go<HD, 16, 2>(a, g, st, grid);
+    if (rows <= 8) return t8_go<HD, 8, 1>(a, g, st, grid);
+    if (rows <= 16) return t8_go<HD, 16, 1>(a, g, st, grid);
+    return rows <= 32 ? t8_go<HD, 32, 1>(a, g, st, grid) : t8_go<HD, 64, 1>(a, g, st, grid);
 }
 
 cudaError_t paged_attn8_tc(AttnArgs &a, cudaStream_t st, int nsm)
@@ -1042,12 +1078,14 @@ cudaError_t paged_attn8_tc(AttnArgs &a, cudaStream_t st, int nsm)
     while (g.gran < 7 && a.kv.block % (2 << g.gran) == 0) ++g.gran;
     g.per_unit = kT8Keys >> g.gran;
     g.round = g.per_unit < 32 ? 32 / g.per_unit : 1;
+    g.group = a.group;
+    g.n_heads = a.kv.n_kv_heads;
+    // two heads are taken as one with their query heads, for the division of the work and the join
+    const int heads = paged_attn8_tc_heads(a.kv.n_kv_heads, a.group, a.s.max_new);
+    a.group *= heads;
+    a.kv.n_kv_heads /= heads;
     const int grid = paged_attn_grid(a, kT8Keys, nsm < kAttnMaxCtasTc ? nsm : kAttnMaxCtasTc);
-    auto go = [&](auto by8, auto by16, auto by32, auto by64) {
-        return (a.rows <= 8 ? by8 : a.rows <= 16 ? by16 : a.rows <= 32 ? by32 : by64)(a, g, st, grid);
-    };
-    cudaError_t e = a.kv.head_dim == 64 ? go(t8_go<64, 8>, t8_go<64, 16>, t8_go<64, 32>, t8_go<64, 64>)
-                                        : go(t8_go<128, 8>, t8_go<128, 16>, t8_go<128, 32>, t8_go<128, 64>);
+    cudaError_t e = a.kv.head_dim == 64 ? t8_dim<64>(a, g, heads, st, grid) : t8_dim<128>(a, g, heads, st, grid);
     if (!e && !a.whole) e = paged_join_tc(a, grid, nsm, st);
     return e;
 }

@@ -1049,8 +1049,9 @@ static cudaError_t t8_go(AttnArgs &a, T8Geometry &g, cudaStream_t st, int grid)
     constexpr int tile = HP * HD * kT8Keys, fixed = (direct ? 0 : 4 * tile) + 2 * kT8Keys * 128 + 4 * HP * NR * HD + (int)sizeof(T8Misc);
     constexpr int room = (kT8Smem - fixed) / tile, slots = room > 2 * kT8MaxSlots ? 2 * kT8MaxSlots : room;
     static_assert(slots >= 4, "two tiles of K and of V beside the buffers");
-    g.k_slots = (slots + 1) / 2;
-    g.v_slots = slots / 2;
+    // the odd one is V's, whose tiles wait for the softmax (converted ones do not)
+    g.v_slots = (slots + (direct ? 1 : 0)) / 2;
+    g.k_slots = slots - g.v_slots;
     static PerDevice once;
     auto kernel = k_paged_attn8_tc<HD, NR, HP>;
     e = allow_once(once, kernel, kT8Smem);

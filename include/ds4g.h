@@ -589,8 +589,8 @@ int ds4g_paged_attention_status(void *workspace, void *cuda_stream);
 /* Edits of rows of logits (device memory; each part may be NULL).  History: ids [n_rows]
  * [max_history] with a row stride, the first n_history[row] of a row (NULL: all), of them the
  * first n_prompt[row] the prompt's (NULL: none), the others generated; ids outside the vocabulary count for
- * nothing.  repetition, frequency, presence: [n_rows] (NULL: 1, 0, 0); repetition > 0.  Biases: ids
- * and values [n_rows][max_bias] with a row stride, the first n_bias[row] (NULL: all); max_bias <= 1024.
+ * nothing.  repetition, frequency, presence: [n_rows] (NULL: 1, 0, 0); repetition > 0; max_history < 2^30.  Biases:
+ * ids and values [n_rows][max_bias] with a row stride, the first n_bias[row] (NULL: all); max_bias <= 1024.
  * allowed: bit i % 32 of word i / 32 of a row, rows allowed_stride words apart (0: the same for all). */
 typedef struct {
     const int32_t *history, *n_history, *n_prompt;
@@ -606,7 +606,7 @@ typedef struct {
 } ds4g_logit_edits;
 
 /* Edit rows of logits before ds4g_probs or ds4g_sample ([P3] 阶段四 4.3).  For id i, in FP32 and in this
- * order: where i is in the row's history z <- z > 0 ? z / repetition : z * repetition; where it is c > 0
+ * order: where i is in the row's history z <- z * (z > 0 ? 1 / repetition : repetition); where it is c > 0
  * times in the generated part z <- z - (frequency * c + presence); z <- z + the sum of the row's
  * biases of i (in FP64, rounded once); where i is not allowed z <- -inf, whatever it was.  logits, out: device f32
  * [n_rows][n_vocab] with row strides in elements; out == logits is allowed with equal strides.

@@ -238,14 +238,14 @@ int ds4g_edit_logits(const float *logits, int64_t logits_stride, int n_rows, int
     if (n_rows < 0 || n_vocab < 1 || !e) return DS4G_EINVAL;
     if (n_vocab > kMaxRowVocab) return DS4G_ESIZE;
     if (n_rows == 0) return DS4G_OK;
-    if (!logits || !out || logits_stride < n_vocab || out_stride < n_vocab || n_rows > (1 << 24)) return DS4G_EINVAL;
+    if (!logits || !out || logits_stride < n_vocab || out_stride < n_vocab || n_rows > (1 << 24)) return DS4G_EINVAL;   // (items are 32-bit)
     if (logits == out && logits_stride != out_stride) return DS4G_EINVAL;
     // (a part without entries needs no array)
     if (e->max_history < 0 || (e->max_history > 0 && !e->history) || (n_rows > 1 && e->history_stride < e->max_history))
         return DS4G_EINVAL;
     if (e->max_bias < 0 || (e->max_bias > 0 && (!e->bias_ids || !e->bias)) || (n_rows > 1 && e->bias_stride < e->max_bias))
         return DS4G_EINVAL;
-    if (e->max_bias > kEditMaxBias) return DS4G_ESIZE;
+    if (e->max_bias > kEditMaxBias || e->max_history >= 1 << 30) return DS4G_ESIZE;
     if (e->allowed && n_rows > 1 && e->allowed_stride != 0 && e->allowed_stride < (n_vocab + 31) / 32) return DS4G_EINVAL;
     const int nsm = sm_count();
     if (!nsm) return DS4G_ECUDA;

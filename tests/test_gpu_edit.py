@@ -67,8 +67,8 @@ def reference(z, e):
             words = e["allowed"][r if e["allowed"].shape[0] > 1 else 0].numpy().view(np.uint32)
             bits = (words[:, None] >> np.arange(32, dtype=np.uint32)) & 1
             z[r, bits.reshape(-1)[:vocab] == 0] = -np.inf
-    # division, product, sum, difference, the bias' rounding and its sum: six roundings of sizes up to `size`
-    return z, 6 * 2.0 ** -24 * size
+    # reciprocal, its product, product, sum, difference, the bias' rounding and its sum: seven roundings of sizes up to `size`
+    return z, 7 * 2.0 ** -24 * size
 
 
 def compare(got, ref, bound):
@@ -96,6 +96,16 @@ def test_edits(rows, vocab, history, biases, grammar):
     compare(edit(z, e), ref, bound)
     dev = z.cuda()
     compare(edit(dev, e, out=dev), ref, bound)   # in place
+
+
+@pytest.mark.parametrize("rows,vocab,history,biases,grammar", [
+    (64, 40000, 3000, 20, True), (400, 9000, 2500, 0, False), (40, 129280, 8192, 100, True), (130, 20001, 2049, 7, True)])
+def test_long_histories(rows, vocab, history, biases, grammar):
+    """Histories that several CTAs share."""
+    z, e = inputs(rows, vocab, history, biases, grammar, seed=rows)
+    e["n_history"][1], e["n_history"][2], e["n_prompt"][3] = 0, 1, 0
+    ref, bound = reference(z, e)
+    compare(edit(z, e), ref, bound)
 
 
 @pytest.mark.parametrize("left_out", ["n_history", "n_prompt", "repetition", "frequency", "presence", "n_bias"])

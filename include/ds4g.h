@@ -564,8 +564,8 @@ typedef struct {
 
 /* Bring every sequence's length to want[b] (below 0: 0) and its table with it.  First the pages that
  * shorter sequences no longer need go back to the pool, in the order of sequences and of their
- * tables, the first of them on top (one that does not fit `capacity` is lost); their table entries become -1.
- * Then longer ones take theirs from the top, in the same order, so that giving back what the
+ * tables, the first of them on top (what does not fit `capacity` is lost); their table entries become -1.
+ * Then longer ones take theirs from the top of what is in the pool then, in the same order, so that giving back what the
  * last call took restores the pool.  A sequence whose pages exceed what is left after those that
  * all sequences before it asked for, whose new tokens exceed max_tokens behind theirs, or whose want exceeds
  * width * page_size is left as it was.  start [n_seqs + 1]: the new tokens of

@@ -6,7 +6,7 @@
 // / P).  Pages behind the w_b of a shorter one go back to the pool, a stack; then the longer
 // ones take theirs from its top.  Both in the order (sequence, index in the table):
 //   the r-th page given back of R lies at n_free + R - 1 - r (the first on top),
-//   the k-th page taken comes from n_free + R - 1 - k,
+//   the k-th page taken comes from n_free + R - 1 - k (what lies beyond the stack's room is lost before),
 // so that giving back what was just taken restores the stack.  All positions are prefix sums over
 // the sequences: one of (pages back, pages wanted, tokens wanted), and, after those that do not fit
 // the pool or the token rows are refused, one of (pages taken, tokens).
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
     }
     RzSums cta, total;
     RzSums at = scan(mine, 0, cta, total);
-    const long long top = (long long)n_free + total.back, back0 = cta.back;
+    const long long full = (long long)n_free + total.back, back0 = cta.back;   // the stack's height, had it room
+    const long long top = min(full, (long long)a.capacity);
     // ---- who fits; pages given back
     RzSums taken = {0, 0, 0}, run = at;
     unsigned long long fit = 0;   // of this thread's sequences (64 at most: per <= kResizeMaxSeqs / kRzThreads / cluster)
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         const int i = rz_find(s_back, n, r);
         const RzSeq s = rz_seq(a, b0 + i);
         int *entry = a.table + (long long)(b0 + i) * a.table_stride + s.need + (r - s_back[i]);
-        const long long to = top - 1 - (back0 + r);
+        const long long to = full - 1 - (back0 + r);
         if (to < a.capacity) a.free[to] = *entry;
         *entry = -1;
     }
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         if (n == 0 && tid == 0) s_more[0] = 0;
         if (rank == 0 && tid == 0) {
             a.start[a.n_seqs] = (int)total2.tokens;
-            *a.n_free = (int)min(top - total2.more, (long long)a.capacity);
+            *a.n_free = (int)(top - total2.more);
         }
     }
     __syncthreads();
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
         const int i = rz_find(s_more, n, k);
         const RzSeq s = rz_seq(a, b0 + i);
         const long long from = top - 1 - (cta2.more + k);
-        a.table[(long long)(b0 + i) * a.table_stride + s.held + (k - s_more[i])] = from < a.capacity ? __ldcg(a.free + from) : -1;
+        a.table[(long long)(b0 + i) * a.table_stride + s.held + (k - s_more[i])] = __ldcg(a.free + from);
     }
     __syncthreads();   // every thread has read the old lengths
 #pragma unroll 1

@@ -1,5 +1,5 @@
-"""ds4g_paged_resize against the same bookkeeping with lists, and a run of serving steps that it
-drives: tables, append, attention, edited logits, probabilities and verification."""
+"""ds4g_paged_resize against the same bookkeeping with lists: lengths that go up and down, pools and token
+rows that run out, pools without room, strides, large prompts and page numbers, captured graphs."""
 import random
 
 import pytest
@@ -137,3 +137,21 @@ def test_in_a_graph_with_another_stream():
         t, length, free, start, _ = resize(*model[:2], w, model[2], 16, 400)
         assert batch.table.tolist() == t and batch.length.tolist() == length and batch.start.tolist() == start
         model = t, length, free
+
+
+@pytest.mark.parametrize("seqs", [2, 600])
+def test_pages_that_the_pool_lost_are_not_taken(seqs):
+    """Three pages given back to a pool with room for one: another sequence finds one."""
+    table = torch.full((seqs, 4), -1, dtype=torch.int32)
+    table[0] = torch.tensor([10, 11, 12, 13])
+    length = torch.zeros(seqs, dtype=torch.int32)
+    length[0] = 32
+    for more, takes in ((9, False), (8, True)):
+        pool = pool_of([], 8, capacity=1)
+        batch = pdl.PagedBatch(table.cuda(), length.cuda(), torch.zeros(seqs + 1, dtype=torch.int32, device="cuda"))
+        want = torch.zeros(seqs, dtype=torch.int32)
+        want[0], want[-1] = 8, more
+        pdl.paged_resize(pool, batch, want.cuda())
+        assert batch.table[0].tolist() == [10, -1, -1, -1] and batch.length.tolist()[:-1] == want.tolist()[:-1]
+        assert batch.table[-1].tolist() == [13 if takes else -1, -1, -1, -1]
+        assert int(batch.length[-1]) == (8 if takes else 0) and int(pool.n_free[0]) == (0 if takes else 1)

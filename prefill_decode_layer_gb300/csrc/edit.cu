@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(kEdThreads, 4) k_edit(const __grid_constant__ 
     const float r = a.repetition ? a.repetition[row] : 1.f, f = a.frequency ? a.frequency[row] : 0.f,
                 p = a.presence ? a.presence[row] : 0.f, inv = __frcp_rn(r);
     const bool counts = hist || biases;
+    asm volatile("cp.async.wait_all;" ::: "memory");   // (also where none of them counts)
     if (counts) {
         for (int i = tid * 4; i < slice; i += kEdThreads * 4) *reinterpret_cast<uint4 *>(s_word + i) = make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("cp.async.wait_all;" ::: "memory");
         if (tid == 0) s_n_found = 0;
         __syncthreads();
 #pragma unroll 1

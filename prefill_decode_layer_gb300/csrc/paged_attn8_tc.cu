@@ -970,17 +970,25 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                 tc_fence_after();
                 uint32_t nan = 0u;   // rows that see a key whose V is NaN in this dim
                 if (*const_cast<volatile int *>(&x.poison[i % kT8Items])) {
+                    // among the keys that only some rows see: those behind the first row's token, and those that left the
+                    // last one's window
                     const int j0 = max(lo, it.t0 * kT8Keys), j1 = min(hi, it.t1 * kT8Keys);
 #pragma unroll 1
-                    for (int j = j0; j < j1; ++j) {
-                        const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
-                        if (page < 0) continue;
-                        const uint8_t code = static_cast<const uint8_t *>(a.kv.v)[page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
-                                                                                  (it.head * HP + (HP > 1 ? g : 0)) * a.kv.head_stride + key];
-                        if ((code & 0x7fu) != 0x7fu) continue;
+                    for (int edge = 0; edge < 2; ++edge) {
+                        const int from = edge ? j0 : max(j0, ends.x + 1);
+                        const int upto = edge ? (a.window > 0 ? min(j1, min(ends.y - win, ends.x) + 1) : j0) : j1;
 #pragma unroll 1
-                        for (int e = 0; e < OWN; ++e)
-                            if (j <= pos[e] && j > pos[e] - win) nan |= 1u << e;
+                        for (int j = from; j < upto; ++j) {
+                            const int page = key_page(a, a.s.table + (long long)it.seq * a.s.table_stride, j);
+                            if (page < 0) continue;
+                            const uint8_t code =
+                                static_cast<const uint8_t *>(a.kv.v)[page * a.kv.page_stride + (j % a.kv.page_size) * a.kv.slot_stride +
+                                                                     (it.head * HP + (HP > 1 ? g : 0)) * a.kv.head_stride + key];
+                            if ((code & 0x7fu) != 0x7fu) continue;
+#pragma unroll 1
+                            for (int e = 0; e < OWN; ++e)
+                                if (j <= pos[e] && j > pos[e] - win) nan |= 1u << e;
+                        }
                     }
                 }
                 float *po = reinterpret_cast<float *>(a.ws + lay.o) + (size_t)(part ? it.part : 0) * a.rows * HD + key;

@@ -24,8 +24,21 @@
 // row: a weight p as hi + lo / 16 like the queries, and weights below 2^-10 of the maximum in a pair of
 // columns of their own, in units of 2^-13 (E4M3 alone has 2^-9 .. 448: many small weights beside a large one would
 // vanish).  8 bits of each weight, or 2^-32 of the largest.
-// More rows: four times the columns would cost more than V's conversion.  Four warps make FP16 of V's
-// codes, which holds them exactly, and P is FP16 (11 bits, or 2^-34 of the largest).
+// More rows: four times the columns of 64 rows, twice over, do not fit TMEM.  Four warps make FP16 of V's
+// codes, which holds them exactly, and P is FP16 (11 bits, or 2^-34 of the largest).  (With that for every number of
+// rows the batch below took 222 us, not 167, the long one 246, not 199.)
+//
+// Units of two K/V heads where their rows fit a group of softmax threads each: see paged_attn8_tc_heads.
+//
+// Bound and figures (device time, of a captured graph; the copy 6.79 TB/s):
+//   one token of 64 sequences to 8191, 32 heads on 8 (0.69 GB)       114 us   DRAM, 6.0 TB/s
+//   one token of 4 sequences to 131072, 64 heads on 8 (0.81 GB)      130 us   DRAM, 6.3 TB/s
+//   1 to 5 tokens of 32 sequences to 16994, 64 heads on 1 (92 MB)     88 us   instruction issue (0.62 of the slots:
+//     the softmax's 16 warps, V's conversion) and the chains of a unit, 2500 cycles for 128 keys and 64 rows;
+//     shared memory, 176 KB of a unit, would take 1400, the MMAs 480
+//   one token, 64 heads on 1, a window of 128                         9.7 us  latency: launch, item, page, K, softmax, O
+// The K and V tiles are most of shared memory (five of two heads, 32 KB each, at eight rows; eleven of one), so that
+// the copies run far ahead of the MMAs.
 //
 // Masked places: a key outside the item's keys or in a missing page, or hidden from a row, gets the
 // weight 0.  In units at an edge (of the item's keys, or of what some rows see) the rows of V outside the
@@ -113,7 +126,9 @@ bool paged_attn8_tc_ok(const PagedKV &kv, int q_dtype)
 }
 
 // K/V heads of a unit: two where their rows fit a group each.  A head's rows of a tile are 128 bytes (64) apart by all
-// heads; two heads' are read side by side, which DRAM serves better, and a unit's waits serve twice the bytes.
+// heads; two heads' are read side by side, which DRAM serves better, and a unit's waits serve twice the bytes.  (64
+// sequences to 8191 with 32 heads on 8: 127 us with one head a unit, 116 with two; 4 to 131072 with 64 on 8: 157, and
+// 136 to 163 on other devices, and 129.  More rows than a group's 16 would take a third and a fourth group beside them.)
 int paged_attn8_tc_heads(int n_kv_heads, int group, int max_new)
 {
     return n_kv_heads % 2 == 0 && group <= 16 && group * max_new <= 16 ? 2 : 1;
@@ -777,10 +792,15 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
 #pragma unroll
             for (int e = 0; e < OWN / 2; ++e) l[e] = 0ull;
             bool unset = true;   // some row has no m
+            // (each lane looks for itself: a vote a wait cost 1.5 us of the drafts' 90)
+            auto wait = [&](uint64_t *b, uint32_t parity) {
+                ok = ok && t8_wait(b, parity, ab);
+                __syncwarp();
+            };
             int base = it.t0 * kT8Keys, in_round = 0;
 #pragma unroll 1
             for (int k = 0; k < units; ++k, ++u, base += kT8Keys) {
-                if (in_round == 0) ok = ok && warp_wait(&x.sc_full[nr % kT8Scales], nr / kT8Scales & 1u);
+                if (in_round == 0) wait(&x.sc_full[nr % kT8Scales], nr / kT8Scales & 1u);
                 const float2 sc = x.sc[nr % kT8Scales][HP > 1 ? g : 0][in_round * geo.per_unit + (key >> geo.gran)];
                 if (++in_round == geo.round || k == units - 1) {
                     __syncwarp();
@@ -788,7 +808,7 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                     in_round = 0;
                     ++nr;
                 }
-                ok = ok && warp_wait(&x.s_full[u & 1], u >> 1 & 1u);
+                wait(&x.s_full[u & 1], u >> 1 & 1u);
                 if (active) {
                     tc_fence_after();
                     const int j = base + key;
@@ -864,7 +884,7 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                         unset = t8_any(bar, none);
                         if (k > 0) {
                             // O of the units before
-                            ok = ok && warp_wait(&x.p_empty[(u - 1) & 1], ((u - 1) >> 1) & 1u);
+                            wait(&x.p_empty[(u - 1) & 1], ((u - 1) >> 1) & 1u);
                             tc_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < (kDirect ? 4 * OWN : OWN); q += 8) {   // (direct: eight rows have four times eight columns)
@@ -889,7 +909,7 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                     }
                     const float r = there ? t8_ex2(-sc.y) : 0.f;   // 1 / vs
                     const uint64_t rr = pack_f32x2(r, r);
-                    if (u >= 2) ok = ok && warp_wait(&x.p_empty[u & 1], ((u - 2) >> 1) & 1u);
+                    if (u >= 2) wait(&x.p_empty[u & 1], ((u - 2) >> 1) & 1u);
                     unsigned char *prow = pbuf + (u & 1) * kP + (uint32_t)(key >> 3) * 1024 + (key & 7) * 128;
 #pragma unroll
                     for (int q = 0; q < OWN; q += 8) {
@@ -965,7 +985,7 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                 }
                 t8_sync(bar);
             }
-            ok = ok && warp_wait(&x.p_empty[last & 1], last >> 1 & 1u);
+            wait(&x.p_empty[last & 1], last >> 1 & 1u);
             if (active && 32 * wq < HD) {   // thread: dim `key`
                 tc_fence_after();
                 uint32_t nan = 0u;   // rows that see a key whose V is NaN in this dim

@@ -17,7 +17,10 @@
 // registers, as they came, between the maximum and the rounding, others are read again (from L2).  The
 // queries' rotation is other CTAs' of the same launch.
 //
-// Bound: bytes (rows read once, codes written once).
+// Bound: bytes (rows read once, codes written once), and latency where tokens are few: a chain of start, length,
+// page, row, maximum, scale.  Measured: four prompts of 12,414 tokens in all, 64 + 16 heads of 128 (490 MB) 95 us, 0.76 of the
+// copy's rate; 64 sequences' one token each 4.4 us; 33 sequences of FP32 rows 10.2 us.  (Without rows held between the
+// maximum and the rounding the prompts took 123 us; with the blocks' CTAs in front of the queries' 97.)
 #include <cuda_fp16.h>
 
 #include "paged_append.cuh"

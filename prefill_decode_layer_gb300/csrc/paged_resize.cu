@@ -15,7 +15,8 @@
 // shared memory, the others' through distributed shared memory, a cluster barrier where pages
 // given back may be taken and where the tables are complete.  Pages are moved one a thread, found
 // by a binary search in the CTA's prefix sums; slots likewise, divided evenly over the cluster.
-// Bound: latency (a chain of loads and barriers; a few hundred KB at most).
+// Bound: latency (a chain of loads and barriers; a few hundred KB at most).  Measured: 64 sequences with drafts 4.8 us
+// a call in one CTA, 4096 sequences of a few pages 12.4 in eight.
 #include "paged.h"
 #include "sm100.cuh"
 
@@ -221,7 +222,8 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
 
 cudaError_t paged_resize(const ResizeArgs &a, cudaStream_t st)
 {
-    // one CTA for few sequences (the cluster's barriers cost more than its threads give)
+    // One CTA where its threads have a sequence each, a cluster of eight for more: the barriers of eight cost 3 us
+    // (one CTA and eight: 64 sequences 4.9 and 7.8 us, 512 8.4 and 8.7, 1024 13.3 and 8.5, 4096 46.8 and 12.3)
     const int cluster = a.n_seqs <= kRzThreads ? 1 : kRzCluster;
     const int share = (a.n_seqs + cluster - 1) / cluster;
     static PerDevice once;

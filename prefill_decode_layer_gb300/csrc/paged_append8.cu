@@ -11,24 +11,28 @@
 // makes division by it, and by it again, exact: where s grows, the rows that the block holds
 // already, code E4M3(code old s / s), lose only what falls below E4M3's steps of 2^-9.
 //
-// One CTA has the block in hand: the CTA of a "leader", the first new token of its sequence or
-// one at a block's first slot.  Warps take (head, K or V) pairs, a thread 8 dims of a row; where
-// there are fewer pairs than warps, several share a pair's rows.  Up to eight rows a thread (FP32: four) stay in
-// registers, as they came, between the maximum and the rounding, others are read again (from L2).  The
-// queries' rotation is other CTAs' of the same launch.
+// One CTA has the rows of a block that its (head, K or V) pairs need: a CTA of the "leader", the first new token of its
+// sequence or one at a block's first slot.  A warp has one pair, a thread 8 dims of a row; so many warps share a pair
+// that its rows of a block stay in registers, as they came, between the maximum and the rounding: eight a thread (FP32:
+// four; what is more is read again, from L2).  The other pairs are other CTAs' of the same leaders, and the queries'
+// rotation that of others of the same launch.  Leaders are found first, a lane a token: what 32 sequences have for it
+// in one round of loads, then its page.
 //
-// Bound: bytes (rows read once, codes written once), and latency where tokens are few: a chain of start, length,
-// page, row, maximum, scale.  Measured: four prompts of 12,414 tokens in all, 64 + 16 heads of 128 (490 MB) 95 us, 0.76 of the
-// copy's rate; 64 sequences' one token each 4.4 us; 33 sequences of FP32 rows 10.2 us.  (Without rows held between the
-// maximum and the rounding the prompts took 123 us; with the blocks' CTAs in front of the queries' 97.)
+// Bound: bytes (rows read once, codes written once), and latency where tokens are few: a chain of start and length,
+// page, row, maximum, scale.  Measured: four prompts of 12,414 tokens in all, 64 + 16 heads of 128 (490 MB) 84 us, 0.86 of
+// the copy's rate; 64 sequences' one token each 4.1 us; 768 FP32 rows of 33 sequences 7.9 us.  (All pairs of a block by one
+// CTA, look-ups a warp a token: 95, 4.4 and 10.2 us; without rows held 123.  K and V of the prompts alone 34 us in blocks
+// of 16 and 33 of 64, for 42 and 76; the angles are a third of it, but those of two rows at once did not fit registers.)
 #include <cuda_fp16.h>
 
 #include "paged_append.cuh"
 
 namespace ds4g {
 
-static constexpr int kA8Tokens = 16;   // tokens of a K/V CTA at most
+// Tokens of a K/V CTA at most: a lane looks up each.  (32: the prompts' K and V in blocks of 64 38.8 us for 32.8.)
+static constexpr int kA8Tokens = 128;
 static constexpr int kA8Warps = kApThreads / 32;
+template <typename TI> constexpr int kA8Hold = 16 / sizeof(TI);   // rows of a thread in registers
 
 // A block that one CTA stores into: rows tok .. tok + n - 1 of the token arrays at positions pos ..
 // (n 0: none), slots `slot` .. of block `blk` of page `page`, which begin `skip` slots into the block.
@@ -65,17 +69,21 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
     return r;
 }
 
-// Codes of x / s, 8 bytes.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s)
+// Codes of x / s, 8 bytes.  odd: some x may be infinite.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, bool odd)
 {
     float y[8];
     if ((__float_as_uint(s) & 0x7fffffu) == 0) {
         const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // a power of two: exact
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, x[i] * inv);   // (0 * inf: NaN)
+        for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
     } else {   // a caller's scale that was kept
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, __fdiv_rn(x[i], s));
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    }
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], 0.f, y[i]);   // (0 * inf: NaN)
     }
     return make_uint2(to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16,
                       to_e4m3x2(y[4], y[5]) | to_e4m3x2(y[6], y[7]) << 16);
@@ -93,14 +101,44 @@ __device__ __forceinline__ void floats8(uint2 w, float (&x)[8])
     }
 }
 
-// The block that token tk leads, by one warp.
-__device__ __forceinline__ BlockWork block_work(const AppendArgs &a, int tk)
+// The blocks that the first 32 of tokens t0 .. t0 + count - 1 lead, by one warp: a lane finds its token's.
+__device__ __forceinline__ BlockWork block_work(const AppendArgs &a, int t0, int count)
 {
+    const int lane = threadIdx.x & 31, tk = t0 + lane;
+    const bool mine = lane < count && tk < a.s.n_tokens;
     BlockWork w = {};
-    if (tk >= a.s.n_tokens) return w;
-    const TokenPlace at = find_token(a.s, tk);
-    if (at.b >= a.s.n_seqs || tk < at.first) return w;
-    const long long first = (long long)a.s.length[at.b] - at.n, p = first + (tk - at.first);
+    int b = -1, begin = tk, n_new = 1, length = 0;
+    if (!a.s.start) {
+        if (mine) length = a.s.length[b = tk];
+    } else {
+        // lane i looks at sequence b0 + i: all that the tokens need of 32 sequences in one round of loads
+        int b0 = a.s.n_seqs <= 32 ? 0 : find_token(a.s, min(t0, a.s.n_tokens - 1)).b;
+        bool open = mine;
+        for (; b0 < a.s.n_seqs && __any_sync(0xffffffffu, open); b0 += 32) {
+            const int q = min(b0 + lane, a.s.n_seqs - 1);
+            const int q_begin = a.s.start[q], q_end = a.s.start[q + 1], q_length = a.s.length[q];
+            const int end = b0 + lane < a.s.n_seqs ? q_end : 0x7fffffff;
+            int c = 0;   // as many of them end at or before the token
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (__shfl_sync(0xffffffffu, end, c + o - 1) <= tk) c += o;
+            const bool found = __shfl_sync(0xffffffffu, end, c) > tk;
+            const int f = __shfl_sync(0xffffffffu, q_begin, c), e = __shfl_sync(0xffffffffu, q_end, c),
+                      l = __shfl_sync(0xffffffffu, q_length, c);
+            if (open && found) {
+                open = false;
+                if (b0 + c < a.s.n_seqs) {
+                    b = b0 + c;
+                    begin = f;
+                    n_new = e - f;
+                    length = l;
+                }
+            }
+        }
+    }
+    if (b < 0 || tk < begin) return w;
+    const TokenPlace at = {b, begin, n_new};
+    const long long first = (long long)length - at.n, p = first + (tk - at.first);
     const int block = a.kv.block, ps = a.kv.page_size;
     long long end = min(first + at.n, (long long)a.s.width * ps);   // fits 32 bits: checked by the host
     if (a.cs) end = min(end, (long long)a.n_pos);
@@ -120,152 +158,166 @@ __device__ __forceinline__ BlockWork block_work(const AppendArgs &a, int tk)
     return w;
 }
 
+// by: which of the groups of (head, K or V) pairs; share: warps of a pair.
 template <typename TI>
-__device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_per_cta, int bx)
+__device__ __forceinline__ void append_blocks(const AppendArgs &a, int tokens_per_cta, int bx, int by, int share)
 {
-    __shared__ BlockWork s_work[kA8Tokens];
+    __shared__ BlockWork s_work[kA8Tokens];   // of the CTA's leaders, in any order
+    __shared__ int s_n;
     __shared__ unsigned s_top[kA8Warps];   // of the pairs that several warps share
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    for (int i = warp; i < tokens_per_cta; i += kA8Warps) {
-        const BlockWork w = block_work(a, bx * tokens_per_cta + i);
-        if (lane == 0) s_work[i] = w;
-    }
+    BlockWork found = {};
+    if (warp * 32 < tokens_per_cta) found = block_work(a, bx * tokens_per_cta + warp * 32, tokens_per_cta - warp * 32);
     if (threadIdx.x < kA8Warps) s_top[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    const int hd = a.kv.head_dim, hv = hd >> 3, kvh = a.kv.n_kv_heads, pairs = 2 * kvh;
+    if (found.n > 0) s_work[atomicAdd(&s_n, 1)] = found;
+    __syncthreads();
+    const int leaders = s_n;
+    const int hd = a.kv.head_dim, hv = hd >> 3, kvh = a.kv.n_kv_heads;
     const int rpw = 32 / hv, row = lane / hv, d = (lane - row * hv) * 8;   // rows of a warp's step; this lane's
-    int share = 1;   // warps of a pair
-    while (2 * share * pairs <= kA8Warps) share *= 2;
-    const int part = warp % share, stride = share * rpw;
-    for (int i = 0; i < tokens_per_cta; ++i) {
+    const int part = warp % share, stride = share * rpw, r0 = part * rpw + row;
+    const int mine = warp / share, pair = by * (kA8Warps / share) + mine;
+    const bool some = pair < 2 * kvh, is_k = pair < kvh;
+    const int head = some ? is_k ? pair : pair - kvh : 0;
+    const bool turns = is_k && a.cs && d < a.rot_dim;
+    const TI *src = static_cast<const TI *>(is_k ? a.k : a.v) + head * hd + d;
+    const long long ss = is_k ? a.k_stride : a.v_stride;
+    for (int i = 0; i < leaders; ++i) {
         const BlockWork w = s_work[i];
-        if (w.n == 0) continue;
-        // (with share > 1 all pairs are in the first turn, where every warp comes to both barriers)
-        for (int pair = warp / share; pair < pairs || share > 1; pair += kA8Warps / share) {
-            const bool some = pair < pairs, is_k = pair < kvh;
-            const int head = is_k ? pair : pair - kvh;
-            const bool turns = is_k && a.cs && d < a.rot_dim;
-            const TI *src = static_cast<const TI *>(is_k ? a.k : a.v) + head * hd + d;
-            const long long ss = is_k ? a.k_stride : a.v_stride;
-            const int r0 = part * rpw + row, n = some && row < rpw ? w.n : 0;
-            auto turn = [&](int r, const Row8<TI> &v, float (&x)[8]) {   // (the angles: from L1 when they are read again)
-                v.floats(x);
-                if (turns) {
-                    float c[8];
-                    load_angles(c, a.cs + (long long)(w.pos + r) * a.rot_dim, d, a.rot_dim);
-                    turn8_rn(x, c, d, a.rot_dim);
-                }
-            };
-            auto value = [&](int r, float (&x)[8]) {
-                Row8<TI> v;
-                v.load(src + (long long)(w.tok + r) * ss);
-                turn(r, v, x);
-            };
-            constexpr int kHold = 16 / sizeof(TI);
-            Row8<TI> held[kHold];
-            float top = 0.f;
-            auto add = [&](const float (&y)[8]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float m = fabsf(y[e]);
-                    top = m <= 3.402823466e38f ? fmaxf(top, m) : top;   // (NaN: no)
-                }
-            };
-#pragma unroll
-            for (int h = 0; h < kHold; ++h) {
-                const int r = r0 + h * stride;
-                if (r < n) held[h].load(src + (long long)(w.tok + r) * ss);
+        const int n = some && row < rpw ? w.n : 0;
+        auto turn = [&](int r, const Row8<TI> &v, float (&x)[8]) {   // (the angles: from L1 when they are read again)
+            v.floats(x);
+            if (turns) {
+                float c[8];
+                load_angles(c, a.cs + (long long)(w.pos + r) * a.rot_dim, d, a.rot_dim);
+                turn8_rn(x, c, d, a.rot_dim);
             }
+        };
+        auto value = [&](int r, float (&x)[8]) {
+            Row8<TI> v;
+            v.load(src + (long long)(w.tok + r) * ss);
+            turn(r, v, x);
+        };
+        constexpr int kHold = kA8Hold<TI>;
+        Row8<TI> held[kHold];
+        unsigned top = 0u;   // magnitudes as bits, which order as they do
+        auto add = [&](const float (&y)[8]) {
 #pragma unroll
-            for (int h = 0; h < kHold; ++h) {
-                const int r = r0 + h * stride;
-                float y[8];
-                if (r < n) {
-                    turn(r, held[h], y);
-                    add(y);
-                }
-            }
-            for (int r = r0 + kHold * stride; r < n; r += stride) {
-                float y[8];
-                value(r, y);
+            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+        };
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            const int r = r0 + h * stride;
+            if (r < n) held[h].load(src + (long long)(w.tok + r) * ss);
+        }
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            const int r = r0 + h * stride;
+            float y[8];
+            if (r < n) {
+                turn(r, held[h], y);
                 add(y);
             }
-            float *scale = const_cast<float *>(is_k ? a.kv.k_scale : a.kv.v_scale) + w.page * a.kv.scale_stride +
-                           (long long)w.blk * kvh + head;
-            unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            const float old = some && !w.begun ? kv8_scale(*scale) : 0.f;
-            if (share > 1) {
-                if (lane == 0 && some) atomicMax(&s_top[pair], bits);
-                __syncthreads();
-                bits = some ? s_top[pair] : 0u;
-            } else {
-                __syncwarp();   // every lane has read the old scale
-            }
-            const float s = fmaxf(old, ask_scale(__uint_as_float(bits)));
-            if (some && part == 0 && lane == 0) *scale = s;
-            uint8_t *dst = static_cast<uint8_t *>(const_cast<void *>(is_k ? a.kv.k : a.kv.v)) +
-                           w.page * a.kv.page_stride + head * a.kv.head_stride + d;
-            if (some && row < rpw && !w.begun && s > old) {   // the rows that the block holds already
-                const float f = __fdiv_rn(old, s);
-                for (int r = r0; r < w.skip; r += stride) {
-                    uint2 *at = reinterpret_cast<uint2 *>(dst + (w.slot - w.skip + r) * a.kv.slot_stride);
-                    float y[8];
-                    floats8(*at, y);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] *= f;
-                    *at = codes8(y, 1.f);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < kHold; ++h) {
-                const int r = r0 + h * stride;
-                float y[8];
-                if (r < n) {
-                    turn(r, held[h], y);
-                    *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(y, s);
-                }
-            }
-            for (int r = r0 + kHold * stride; r < n; r += stride) {
+        }
+        for (int r = r0 + kHold * stride; r < n; r += stride) {
+            float y[8];
+            value(r, y);
+            add(y);
+        }
+        const bool odd = top >= 0x7f800000u;   // infinities or NaN: the maximum of the others
+        if (odd) {
+            top = 0u;
+#pragma unroll 1
+            for (int r = r0; r < n; r += stride) {
                 float y[8];
                 value(r, y);
-                *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(y, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const unsigned m = __float_as_uint(y[e]) & 0x7fffffffu;
+                    top = m < 0x7f800000u ? max(top, m) : top;
+                }
             }
-            if (share > 1) {
-                __syncthreads();   // the maxima have been read
-                if (lane == 0 && some && part == 0) s_top[pair] = 0u;
-                __syncthreads();
-                break;
+        }
+        __syncwarp();
+        float *scale = const_cast<float *>(is_k ? a.kv.k_scale : a.kv.v_scale) + w.page * a.kv.scale_stride +
+                       (long long)w.blk * kvh + head;
+        unsigned bits = __reduce_max_sync(0xffffffffu, top);
+        const float old = some && !w.begun ? kv8_scale(*scale) : 0.f;
+        if (share > 1) {
+            if (lane == 0 && some) atomicMax(&s_top[mine], bits);
+            __syncthreads();
+            bits = s_top[mine];
+        } else {
+            __syncwarp();   // every lane has read the old scale
+        }
+        const float s = fmaxf(old, ask_scale(__uint_as_float(bits)));
+        if (some && part == 0 && lane == 0) *scale = s;
+        uint8_t *dst = static_cast<uint8_t *>(const_cast<void *>(is_k ? a.kv.k : a.kv.v)) +
+                       w.page * a.kv.page_stride + head * a.kv.head_stride + d;
+        if (some && row < rpw && !w.begun && s > old) {   // the rows that the block holds already
+            const float f = __fdiv_rn(old, s);
+            for (int r = r0; r < w.skip; r += stride) {
+                uint2 *at = reinterpret_cast<uint2 *>(dst + (w.slot - w.skip + r) * a.kv.slot_stride);
+                float y[8];
+                floats8(*at, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= f;
+                *at = codes8(y, 1.f, false);
             }
+        }
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            const int r = r0 + h * stride;
+            float y[8];
+            if (r < n) {
+                turn(r, held[h], y);
+                *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(y, s, odd);
+            }
+        }
+        for (int r = r0 + kHold * stride; r < n; r += stride) {
+            float y[8];
+            value(r, y);
+            *reinterpret_cast<uint2 *>(dst + (w.slot + r) * a.kv.slot_stride) = codes8(y, s, odd);
+        }
+        if (share > 1) {
+            __syncthreads();   // the maxima have been read
+            if (lane == 0 && part == 0) s_top[mine] = 0u;
+            __syncthreads();
         }
     }
 }
 
 // kv_ctas of the grid's CTAs, evenly spread, take blocks of K and V (a chain of look-ups, which the others' copies
-// cover); the others the queries, ny of them a token group.
+// cover), nk of them a token group; the others the queries, ny of them a token group.
 template <typename TI, int U>
 __global__ void __launch_bounds__(kApThreads, 3) k_paged_append8(const __grid_constant__ AppendArgs a, int kv_ctas,
-                                                                 int kv_tokens, int q_tokens, int ny)
+                                                                 int kv_tokens, int nk, int share, int q_tokens, int ny)
 {
     const unsigned long long n = gridDim.x, b = blockIdx.x;
     const int before = (int)(b * kv_ctas / n), upto = (int)((b + 1) * kv_ctas / n);   // CTAs of blocks
     const int bx = (int)b - before;
-    if (upto > before) append_blocks<TI>(a, kv_tokens, before);
+    if (upto > before) append_blocks<TI>(a, kv_tokens, before / nk, before % nk, share);
     else append_rows<TI, TI, U>(a, q_tokens, bx / ny, bx % ny, ny, 0);
 }
 
-cudaError_t paged_append8(const AppendArgs &a, int in_dtype, cudaStream_t st, int nsm)
+template <typename TI> static cudaError_t append8_from(const AppendArgs &a, cudaStream_t st, int nsm)
 {
-    const int n = a.s.n_tokens, hd = a.kv.head_dim;
-    if (n == 0) return cudaSuccess;
+    const int n = a.s.n_tokens, hd = a.kv.head_dim, hv = hd >> 3, pairs = 2 * a.kv.n_kv_heads;
+    // warps of a pair: as many as hold a block's rows in registers, more where there are fewer pairs than warps; a
+    // warp has one pair
+    int share = 1;
+    while (share < kA8Warps && (share * kA8Hold<TI> * (32 / hv) < a.kv.block || 2 * share * pairs <= kA8Warps)) share *= 2;
+    const int per_cta = kA8Warps / share, nk = (pairs + per_cta - 1) / per_cta;
     int kv_tokens = 1;
-    while (kv_tokens < kA8Tokens && 2 * kv_tokens <= a.kv.block && n / (2 * kv_tokens) >= 4 * nsm) kv_tokens *= 2;
-    const int kv_ctas = (n + kv_tokens - 1) / kv_tokens;
+    while (kv_tokens < kA8Tokens && 2 * kv_tokens <= a.kv.block && (long long)n * nk / (2 * kv_tokens) >= 4 * nsm) kv_tokens *= 2;
+    const int kv_ctas = (n + kv_tokens - 1) / kv_tokens * nk;
     // the queries as the append without scales divides them
     int tpc = 1, ny = 0, gx = 0, per_thread = 0;
     if (a.n_heads) {
-        const int groups = kApThreads / (hd >> 3);
+        const int groups = kApThreads / hv;
         while (tpc < kApTokens && n / (2 * tpc) >= 4 * nsm) tpc *= 2;
         gx = (n + tpc - 1) / tpc;
         ny = 1;
@@ -273,11 +325,14 @@ cudaError_t paged_append8(const AppendArgs &a, int in_dtype, cudaStream_t st, in
         per_thread = (a.n_heads * tpc + groups * ny - 1) / (groups * ny);
     }
     const dim3 grid(kv_ctas + gx * ny), block(kApThreads);
-    auto go = [&](auto few, auto many) {
-        return launch_pdl(per_thread <= 5 ? few : many, grid, block, 0, st, a, kv_ctas, kv_tokens, tpc, ny > 0 ? ny : 1);
-    };
-    return in_dtype == DS4G_BF16 ? go(k_paged_append8<bf16, 1>, k_paged_append8<bf16, 4>)
-                                 : go(k_paged_append8<float, 1>, k_paged_append8<float, 2>);
+    auto kernel = per_thread <= 5 ? k_paged_append8<TI, 1> : k_paged_append8<TI, 8 / sizeof(TI)>;
+    return launch_pdl(kernel, grid, block, 0, st, a, kv_ctas, kv_tokens, nk, share, tpc, ny > 0 ? ny : 1);
+}
+
+cudaError_t paged_append8(const AppendArgs &a, int in_dtype, cudaStream_t st, int nsm)
+{
+    if (a.s.n_tokens == 0) return cudaSuccess;
+    return in_dtype == DS4G_BF16 ? append8_from<bf16>(a, st, nsm) : append8_from<float>(a, st, nsm);
 }
 
 }  // namespace ds4g

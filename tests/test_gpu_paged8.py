@@ -437,3 +437,64 @@ def test_attention_on_two_streams_with_their_own_workspaces():
             pdl.paged_attention(kvs[i], bs[i], qs[i], outs[i], wss[i], stream=streams[i])
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("seqs", ["few", "many"])
+def test_append_finds_every_token_among_empty_sequences(seqs):
+    """Long runs of sequences without a new token beside short and long ones: as a call for each sequence."""
+    new = {"few": [0] * 9 + [900, 0, 1, 1, 0, 33, 5] + [0] * 11 + [2500, 2],
+           "many": [0] * 60 + [900] + [0] * 45 + [1] * 100 + [7] * 33 + [0, 1] * 40 + [0] * 70 + [3000, 0, 2] + [0] * 35}[seqs]
+    p = inputs8([n + 5 * i % 90 for i, n in enumerate(new)], new, 32, 16, 32, 32, seed=91)
+    k, v = randn((p["tokens"], 32, 16), BF16, 92), randn((p["tokens"], 32, 16), BF16, 93)
+    rope = pdl.Rope.fill(4000, 16)
+    names = ("k8", "v8", "ks", "vs")
+    one = {x: p[x].clone() for x in names}
+    pdl.paged_append(cache(p), pdl.PagedBatch(p["table"], p["length"], p["start"], max_new=4000), k, v, rope)
+    at, kv = 0, pdl.PagedKV8(*(one[x] for x in names))
+    for b, n in enumerate(new):
+        if n:
+            start = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+            pdl.paged_append(kv, pdl.PagedBatch(p["table"][b:b + 1], p["length"][b:b + 1], start, max_new=4000),
+                             k[at:at + n], v[at:at + n], rope)
+        at += n
+    for x in names:
+        bits = [t.view(torch.uint8) if x in ("k8", "v8") else t.view(torch.int32) for t in (p[x], one[x])]
+        assert torch.equal(*bits), x
+
+
+def test_operators_on_two_streams_at_once():
+    """Appends, page tables and edits have no memory in common."""
+    ps = [inputs8([300, 64, 1000, 17], [4, 64, 1, 17], 2, 64, 16, 16, seed=95 + i, width_extra=2) for i in range(2)]
+    ks, vs = [randn((86, 2, 64), BF16, 97 + i) for i in range(2)], [randn((86, 2, 64), BF16, 99 + i) for i in range(2)]
+    zs = [randn((40, 30000), F32, 101 + i) for i in range(2)]
+    edits = [pdl.LogitEdits(history=torch.randint(0, 30000, (40, 3000), generator=torch.Generator().manual_seed(i)).int().cuda(),
+                            frequency=torch.full((40,), 0.5, device="cuda")) for i in range(2)]
+    names, n_pages = ("k8", "v8", "ks", "vs"), 64
+    want_len = torch.tensor([400, 7, 0, 33], dtype=torch.int32, device="cuda")
+
+    def state():
+        return [dict({x: p[x].clone() for x in names}, out=torch.zeros_like(z), slots=torch.zeros(600, dtype=torch.int64, device="cuda"),
+                     pool=pdl.PagePool(torch.arange(n_pages, dtype=torch.int32, device="cuda"), torch.full((1,), n_pages, dtype=torch.int32, device="cuda"), 16),
+                     batch=pdl.PagedBatch(torch.full((4, 30), -1, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"),
+                                          torch.zeros(5, dtype=torch.int32, device="cuda"))) for p, z in zip(ps, zs)]
+
+    def work(i, s, stream=None):
+        for _ in range(5):
+            pdl.paged_append(pdl.PagedKV8(*(s[x] for x in names)), pdl.PagedBatch(ps[i]["table"], ps[i]["length"], ps[i]["start"], max_new=64),
+                             ks[i], vs[i], stream=stream)
+            pdl.edit_logits(zs[i], s["out"], edits[i], stream=stream)
+            pdl.paged_resize(s["pool"], s["batch"], want_len, s["slots"], stream=stream)
+    alone = state()
+    for i in range(2):
+        work(i, alone[i])
+        torch.cuda.synchronize()
+    both, streams = state(), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        work(i, both[i], streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for x in names:
+            assert torch.equal(a[x].contiguous().view(torch.uint8), b[x].contiguous().view(torch.uint8))
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["slots"], b["slots"])
+        assert torch.equal(a["batch"].table, b["batch"].table) and torch.equal(a["pool"].free, b["pool"].free)

@@ -548,7 +548,8 @@ int ds4g_paged_append8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, 
  * multiple of 8 slots run on the tensor cores: the queries as pairs of E4M3 values (exact down to 2^-14 of
  * the row's largest, off by 2^-22 of it at most below), the probabilities times the V scales
  * as pairs of E4M3 values (up to 32 rows a K/V head: 2^-8 of each) or as FP16 (2^-11), of what is very small 2^-32 of the
- * largest (FP32 sums); every other case runs in FP32. */
+ * largest (FP32 sums); every other case runs in FP32.  scale times a K scale times a query's largest value has to stay
+ * below 2^126: scores beyond FP32 are not infinities but NaN. */
 size_t ds4g_paged_attention8_workspace_bytes(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, int n_heads);
 int ds4g_paged_attention8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
                           void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,

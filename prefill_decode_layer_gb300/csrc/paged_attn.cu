@@ -476,6 +476,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
                     if (i0 + b * ws >= parts) break;
                     const float f = pa_ex2(m2[b].x - ref);
                     sum = fmaf(f, m2[b].y, sum);
+                    if (f == 0.f) {   // an 8-bit cache's sums may be as large as the factor is small (2^64 a key)
+                        const float h = pa_ex2(0.5f * (m2[b].x - ref));
+                        sum = fmaf(h * m2[b].y, h, sum);
+                    }
                     if (d < hd) {
 #pragma unroll
                         for (int e = 0; e < V; ++e) acc[e] = weigh(f, x[b][e], acc[e]);

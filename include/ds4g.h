@@ -607,8 +607,9 @@ typedef struct {
 } ds4g_logit_edits;
 
 /* Edit rows of logits before ds4g_probs or ds4g_sample ([P3] 阶段四 4.3).  For id i, in FP32 and in this
- * order: where i is in the row's history z <- z * (z > 0 ? 1 / repetition : repetition); where it is c > 0
- * times in the generated part z <- z - (frequency * c + presence); z <- z + the sum of the row's
+ * order: where i is in the row's history z <- z > 0 ? z / repetition : z * repetition (the quotient rounded once, off by
+ * half a unit of its last place and 2^-20 of that at most, for repetition in [2^-60, 2^60] and quotients above 2^-100; else a
+ * product with the rounded reciprocal); where it is c > 0 times in the generated part z <- z - (frequency * c + presence); z <- z + the sum of the row's
  * biases of i (in FP64, rounded once); where i is not allowed z <- -inf, whatever it was.  logits, out: device f32
  * [n_rows][n_vocab] with row strides in elements; out == logits is allowed with equal strides.
  * n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */

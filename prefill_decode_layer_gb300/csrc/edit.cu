@@ -7,14 +7,19 @@
 //   z <- -inf                               where the row's mask has a 0 for i.
 //
 // A CTA takes a slice of a row, up to 32 logits a thread, which are on their way to registers while it looks through
-// the row's history: a word a token in shared memory says whether the token was seen (bit 31) or has a bias (bit
-// 30) and how often it was generated (whole numbers, so that the order of the atomics does not matter).  A warp
-// adds up all entries of a biased token in FP64, in their order, for the token's thread to find.
-// Bound: bytes (a logit read and written once, a bit of the mask), latency at one row (3.1 us).  Measured: 256 rows
-// of 129280, 265 MB: 43 us without histories (0.92 of the copy); with histories of 2048 to 8192 ids 66 us, with 100
-// biases as well 72: four CTAs an SM, whose chains of loads, counts and stores then leave the pipe idle.  (Eight
-// ids in flight for four 66 us for 73; a cluster of eight CTAs that shares the history and counts in each other's
-// shared memory 76; one CTA an SM with the next item's loads in registers 99.)
+// the row's history: a word a token in shared memory says whether the token was seen (bit 31) and how often it was
+// generated (whole numbers, so that the order of the atomics does not matter).  The word of a biased token (bit 30)
+// holds the place of its first entry instead, where its count and its sum of biases lie: the entries set it before the
+// history is counted, and the token's thread finds both in one look.  A token of several entries has them added up by a
+// thread in FP64, in their order.
+// Bound: bytes (a logit read and written once, a bit of the mask), latency at one row (2.9 us).  Measured: 256 rows
+// of 129280, 265 MB: 44 us without histories (0.89 of the copy); with histories of 2048 to 8192 ids 71 us, with 100
+// biases as well 75: four CTAs an SM, whose chains of loads, counts and stores then leave the pipe idle.  1024 biases
+// 53 us, side by side or not (with a search for each biased token's entry 480 to 810); each further entry of one token
+// 0.1 us of its thread.  (Four ids in flight, not eight: 7 us more; a cluster of eight CTAs that shares the history and
+// counts in each other's shared memory 10 more than that form; one CTA an SM with the next item's loads in registers 33.)
+#include <type_traits>
+
 #include "paged.h"
 #include "sm100.cuh"
 
@@ -23,7 +28,8 @@ namespace ds4g {
 static constexpr int kEdThreads = 256;
 static constexpr int kEdHold = 32, kEdHoldFew = 8;          // logits of a thread at most, and in short slices
 static constexpr int kEdBatch = 8;                          // ids of a thread in flight
-static constexpr uint32_t kEdSeen = 0x80000000u, kEdBias = 0x40000000u;
+static constexpr uint32_t kEdSeen = 0x80000000u, kEdBias = 0x40000000u, kEdTwice = 0x40000000u;   // (of a place's count)
+static_assert((kEditMaxBias & (kEditMaxBias - 1)) == 0, "a word's low bits name an entry");
 
 // A word of global memory to shared memory, complete after cp.async.wait_all.
 __device__ __forceinline__ void copy_word(void *dst, const void *src)
@@ -35,10 +41,9 @@ template <int HOLD>
 __global__ void __launch_bounds__(kEdThreads, 4) k_edit(const __grid_constant__ EditArgs a, int slice, int slices)
 {
     extern __shared__ __align__(16) uint32_t s_word[];      // of the slice's tokens
-    __shared__ int s_bias_id[kEditMaxBias];
+    __shared__ __align__(16) int s_bias_id[kEditMaxBias];
     __shared__ float s_bias[kEditMaxBias];
-    __shared__ int s_found[kEditMaxBias], s_n_found;        // the slice's biased tokens
-    __shared__ float s_sum[kEditMaxBias];
+    __shared__ uint32_t s_count[kEditMaxBias];              // at the place of a biased token's first entry
     const int tid = threadIdx.x, lane = tid & 31;
     const int row = blockIdx.x / slices, v0 = (blockIdx.x - row * slices) * slice, n = max(min(slice, a.n - v0), 0);
     pdl_wait();
@@ -86,56 +91,79 @@ __global__ void __launch_bounds__(kEdThreads, 4) k_edit(const __grid_constant__ 
     asm volatile("cp.async.wait_all;" ::: "memory");   // (also where none of them counts)
     if (counts) {
         for (int i = tid * 4; i < slice; i += kEdThreads * 4) *reinterpret_cast<uint4 *>(s_word + i) = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0) s_n_found = 0;
+        for (int k = tid; k < biases; k += kEdThreads) s_count[k] = 0u;
         __syncthreads();
+        auto slot = [&](int k) { return (unsigned)s_bias_id[k] - (unsigned)v0; };   // n or more: not in the slice
+        auto place = [&](uint32_t w) { return kEditMaxBias - 1 - (int)(w & (kEditMaxBias - 1)); };
+        bool twice = false;
+        if (biases) {
+            for (int k = tid; k < biases; k += kEdThreads)
+                if (slot(k) < (unsigned)n) atomicMax(&s_word[slot(k)], kEdBias | (unsigned)(kEditMaxBias - 1 - k));
+            __syncthreads();
+            for (int k = tid; k < biases; k += kEdThreads) {
+                if (slot(k) >= (unsigned)n) continue;
+                const int first = place(s_word[slot(k)]);
+                if (first == k) continue;
+                atomicOr(&s_count[first], kEdTwice);
+                twice = true;
+            }
+        }
+        auto count = [&](auto with_biases) {
 #pragma unroll 1
-        for (; i0 - tid < hist; fetch(i0, hist)) {
+            for (; i0 - tid < hist; fetch(i0, hist)) {
 #pragma unroll
-            for (int k = 0; k < kEdBatch; ++k) {
-                const unsigned t = (unsigned)id[k] - (unsigned)v0;
-                const int i = i0 + k * kEdThreads;
-                if (i >= hist || id[k] < 0 || t >= (unsigned)n) continue;
-                if (i >= prompt) atomicAdd(&s_word[t], 1u);
-                else atomicOr(&s_word[t], kEdSeen);
+                for (int k = 0; k < kEdBatch; ++k) {
+                    const unsigned t = (unsigned)id[k] - (unsigned)v0;
+                    const int i = i0 + k * kEdThreads;
+                    if (i >= hist || id[k] < 0 || t >= (unsigned)n) continue;
+                    uint32_t *at = &s_word[t];
+                    if (decltype(with_biases)::value && *at & kEdBias) at = &s_count[place(*at)];
+                    if (i >= prompt) atomicAdd(at, 1u);
+                    else atomicOr(at, kEdSeen);
+                }
+                i0 += kEdBatch * kEdThreads;
             }
-            i0 += kEdBatch * kEdThreads;
+        };
+        if (biases) count(std::true_type{});
+        else count(std::false_type{});
+        if (__syncthreads_or(twice)) {
+            for (int k = tid; k < biases; k += kEdThreads) {
+                if (!(s_count[k] & kEdTwice)) continue;
+                const int token = s_bias_id[k];
+                double sum = 0.0;
+#pragma unroll 2
+                for (int j = k & ~7; j < biases; j += 8) {   // (FP64 is slow here: only where an entry is the token's)
+                    const int4 u = *reinterpret_cast<const int4 *>(s_bias_id + j), v = *reinterpret_cast<const int4 *>(s_bias_id + j + 4);
+                    uint32_t same = (u.x == token) | (u.y == token) << 1 | (u.z == token) << 2 | (u.w == token) << 3 |
+                                    (v.x == token) << 4 | (v.y == token) << 5 | (v.z == token) << 6 | (v.w == token) << 7;
+                    if (biases - j < 8) same &= (1u << (biases - j)) - 1u;   // (before k none is)
+#pragma unroll 1
+                    for (; same; same &= same - 1) sum += (double)s_bias[j + __ffs(same) - 1];
+                }
+                s_bias[k] = (float)sum;   // (no other thread looks at the token's entries)
+            }
+            __syncthreads();
         }
-        // a warp an entry of the slice, if no entry before it has its id
-        for (int k = tid >> 5; k < biases; k += kEdThreads / 32) {
-            const int token = s_bias_id[k];
-            if (token < v0 || token >= v0 + n) continue;
-            bool first = true;
-            double sum = 0.0;
-            for (int j0 = 0; first && j0 < biases; j0 += 32) {
-                const int j = j0 + lane;
-                uint32_t same = __ballot_sync(0xffffffffu, j < biases && s_bias_id[min(j, biases - 1)] == token);
-                if (j0 <= k) first = (same & (k - j0 < 32 ? (1u << (k - j0)) - 1u : 0xffffffffu)) == 0u;
-                for (; first && same; same &= same - 1) sum += (double)s_bias[j0 + __ffs(same) - 1];
-            }
-            if (lane == 0 && first) {
-                const int at = atomicAdd(&s_n_found, 1);
-                s_found[at] = token - v0;
-                s_sum[at] = (float)sum;
-                atomicOr(&s_word[token - v0], kEdBias);
-            }
-        }
-        __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < HOLD; ++k) {
         const int i = k * kEdThreads + tid;
-        const uint32_t w = counts && i < n ? s_word[i] : 0u, allowed = __shfl_sync(0xffffffffu, words, k);
+        uint32_t w = counts && i < n ? s_word[i] : 0u;
+        const uint32_t allowed = __shfl_sync(0xffffffffu, words, k);
+        const bool biased = w & kEdBias;
+        float bias = 0.f;
+        if (biased) {
+            const int first = kEditMaxBias - 1 - (int)(w & (kEditMaxBias - 1));
+            w = s_count[first] & ~kEdTwice;
+            bias = s_bias[first];
+        }
         // (without branches: of 32 tokens some are in the history as a rule)
-        const float c = (float)(w & ~(kEdSeen | kEdBias));
+        const float c = (float)(w & ~kEdSeen);
         const float low = fmaxf(__fmul_rn(z[k], inv_low), -3.402823466e38f);   // (an infinite logit stays one)
         const float turned = z[k] > 0.f ? __fmaf_rn(z[k], inv, low) : __fmul_rn(z[k], r);
-        z[k] = w & ~kEdBias ? turned : z[k];
+        z[k] = w ? turned : z[k];
         z[k] = c > 0.f ? __fsub_rn(z[k], __fadd_rn(__fmul_rn(f, c), p)) : z[k];
-        if (w & kEdBias) {
-            int j = 0;
-            while (s_found[j] != i) ++j;   // (it is there)
-            z[k] += s_sum[j];
-        }
+        if (biased) z[k] += bias;
         if (i < n) out[i] = allowed >> lane & 1u ? z[k] : -INFINITY;
     }
 }

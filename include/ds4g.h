@@ -537,8 +537,10 @@ typedef struct {
  * 2^-64 at least, 2^64 at most).  Otherwise the block keeps its scale, or takes the s that its new rows
  * ask for where that is larger; the rows that it holds already are then rounded again, which is exact
  * but for values below 2^-6 of the new scale.  Codes are rounded to nearest even from x / s; values above
- * 448 2^64 become 448, infinities and NaN become NaN and count for no scale.  Two sequences of one call must not
- * store into the same block.  One launch. */
+ * 448 2^64 become 448, infinities and NaN become NaN and count for no scale.  Rows that are taken back (a length made
+ * shorter, as after rejected drafts) leave their scale in the block until a call begins it again: the rows that it held stay
+ * rounded to it, off by 2^-10 of that scale at most beside their own rounding, so that decoding with drafts is not bit-equal
+ * to decoding without.  Two sequences of one call must not store into the same block.  One launch. */
 int ds4g_paged_append8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *k, int64_t k_stride,
                        const void *v, int64_t v_stride, const ds4g_rope *rope, const void *q, int64_t q_stride,
                        void *q_out, int64_t q_out_stride, int n_heads, int dtype, void *cuda_stream);

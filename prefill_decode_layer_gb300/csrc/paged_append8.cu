@@ -313,7 +313,11 @@ template <typename TI> static cudaError_t append8_from(const AppendArgs &a, cuda
     const int per_cta = kA8Warps / share, nk = (pairs + per_cta - 1) / per_cta;
     int kv_tokens = 1;
     while (kv_tokens < kA8Tokens && 2 * kv_tokens <= a.kv.block && (long long)n * nk / (2 * kv_tokens) >= 4 * nsm) kv_tokens *= 2;
-    const int kv_ctas = (n + kv_tokens - 1) / kv_tokens * nk;
+    // many tokens of tens of thousands of heads: a grid has 2^31 - 1 CTAs at most, of which the queries take up to 2^28
+    auto ctas = [&]() { return ((long long)n + kv_tokens - 1) / kv_tokens * nk; };
+    while (kv_tokens < kA8Tokens && ctas() > (1 << 24)) kv_tokens *= 2;
+    if (ctas() > (1 << 30)) return cudaErrorInvalidValue;
+    const int kv_ctas = (int)ctas();
     // the queries as the append without scales divides them
     int tpc = 1, ny = 0, gx = 0, per_thread = 0;
     if (a.n_heads) {

@@ -914,12 +914,12 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
 #pragma unroll
                         for (int e = 0; e < OWN; ++e) y[e] += x.delta[r0 + e];
                     }
-                    const float r = there ? t8_ex2(-sc.y) : 0.f;   // 1 / vs
-                    const uint64_t rr = pack_f32x2(r, r);
                     // Row sums: p / vs.  With a small vs, 2^-64 for a block of zeros, p may underflow beside a scale of up to 2^64
                     // although p / vs counts: then 2^(t - log2 vs - m), at the largest key 2^-59 or more.  (With that and the
-                    // second factor of the sums the drafts take 91.5 us for 89.0.)
-                    const bool far = r > 0x1p24f;
+                    // second factor of the sums the drafts take 90.1 us for 89.3; the two ways as the branches of each sum 91.6.)
+                    const bool far = there && sc.y < -24.f;
+                    const float r = there && !far ? t8_ex2(-sc.y) : 0.f;   // 1 / vs
+                    const uint64_t rr = pack_f32x2(r, r);
                     if (u >= 2) wait(&x.p_empty[u & 1], ((u - 2) >> 1) & 1u);
                     unsigned char *prow = pbuf + (u & 1) * kP + (uint32_t)(key >> 3) * 1024 + (key & 7) * 128;
 #pragma unroll
@@ -927,14 +927,8 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                         float p[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) p[e] = t8_ex2(y[q + e]);
-                        if (far) {
 #pragma unroll
-                            for (int e = 0; e < 8; e += 2)
-                                l[(q + e) / 2] = add_f32x2(l[(q + e) / 2], pack_f32x2(t8_ex2(y[q + e] - sc.y), t8_ex2(y[q + e + 1] - sc.y)));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; e += 2) l[(q + e) / 2] = fma_f32x2(pack_f32x2(p[e], p[e + 1]), rr, l[(q + e) / 2]);
-                        }
+                        for (int e = 0; e < 8; e += 2) l[(q + e) / 2] = fma_f32x2(pack_f32x2(p[e], p[e + 1]), rr, l[(q + e) / 2]);
                         if (kDirect) {
                             // columns (r / 8) 32 + 8 s + r % 8: s 0, 1 the codes of the large weights and what they
                             // leave, 2, 3 those of the small ones, in units of 2^-13
@@ -970,6 +964,11 @@ __global__ void __launch_bounds__(T8<NR, HP>::threads, 1)
                         }
                     }
                     fence_proxy_async_smem();   // before the MMA reads them
+                    if (__builtin_expect(far, 0)) {
+#pragma unroll
+                        for (int e = 0; e < OWN; e += 2)
+                            l[e / 2] = add_f32x2(l[e / 2], pack_f32x2(t8_ex2(y[e] - sc.y), t8_ex2(y[e + 1] - sc.y)));
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -177,10 +177,8 @@ cudaError_t edit_rows(const EditArgs &a, cudaStream_t st, int nsm)
     const int slice = ((a.n + slices - 1) / slices + 31) & ~31;
     const size_t smem = a.history || a.bias_ids ? (size_t)slice * 4 : 0;
     const dim3 grid((unsigned)slices * a.rows), block(kEdThreads);
+    static_assert(most * 4 + kEditMaxBias * 12 <= 48 * 1024, "the words and the entries fit without an attribute");
     if (slice <= few) return launch_pdl(k_edit<kEdHoldFew>, grid, block, smem, st, a, slice, slices);
-    static PerDevice once;   // (with the static arrays more than 48 KB)
-    const cudaError_t e = allow_once(once, k_edit<kEdHold>, 64 * 1024);
-    if (e) return e;
     return launch_pdl(k_edit<kEdHold>, grid, block, smem, st, a, slice, slices);
 }
 

@@ -40,11 +40,11 @@
  *    bf16 tensors hold raw bfloat16 bits; the embedding table is IEEE binary16.
  *  - Errors leave the session unchanged unless stated otherwise; DS4G_ECUDA
  *    reports a failed launch or CUDA call, after which the session is undefined.
- *  - The operators on device buffers (ds4g_sample*, ds4g_paged_*, ds4g_probs,
- *    ds4g_verify_draft) run on the stream they are given, which belongs to the
+ *  - The operators on device buffers (ds4g_sample*, ds4g_paged_*, ds4g_edit_logits,
+ *    ds4g_probs, ds4g_verify_draft) run on the stream they are given, which belongs to the
  *    current device, and keep nothing between calls (but a time-out's report in the
- *    workspace of ds4g_paged_attention).  The last three groups do not synchronise, that
- *    report's reading apart, and can be captured into a CUDA graph.  Calls that may overlap in
+ *    workspace of ds4g_paged_attention and ds4g_paged_attention8).  All but ds4g_sample* do not
+ *    synchronise, that report's reading apart, and can be captured into a CUDA graph.  Calls that may overlap in
  *    time need workspaces of their own.
  */
 #ifndef DS4G_H
@@ -549,8 +549,8 @@ int ds4g_paged_append8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, 
  * being the values that codes and scales stand for.  BF16 queries with head_dim 64 or 128, pages of a
  * multiple of 8 slots run on the tensor cores: the queries as pairs of E4M3 values (exact down to 2^-14 of
  * the row's largest, off by 2^-22 of it at most below), the probabilities times the V scales
- * as pairs of E4M3 values (up to 32 rows a K/V head: 2^-8 of each) or as FP16 (2^-11), of what is very small 2^-32 of the
- * largest (FP32 sums); every other case runs in FP32.  scale times a K scale times a query's largest value has to stay
+ * as pairs of E4M3 values (up to 32 rows, new tokens times query heads, a K/V head: 2^-9 of each) or as FP16 (2^-11), of
+ * what is very small 2^-32 of the largest; their sums in FP32 before that rounding; every other case runs in FP32.  scale times a K scale times a query's largest value has to stay
  * below 2^126: scores beyond FP32 are not infinities but NaN. */
 size_t ds4g_paged_attention8_workspace_bytes(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, int n_heads);
 int ds4g_paged_attention8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
@@ -576,7 +576,7 @@ typedef struct {
  * became shorter).  slots, where not NULL, [max_tokens]: page * page_size + slot of each new token;
  * entries behind the last one stay as they are.  table [n_seqs][table_stride], length, start, slots and the pool are
  * device memory, read and written on the device: the pages of [0, ceil(length[b] / page_size)) of
- * a table are its sequence's.  n_seqs <= 65536 (DS4G_ESIZE); want may not be length.  One launch. */
+ * a table are its sequence's (all of them go back to the pool in turn, also an entry that is no page).  n_seqs <= 65536 (DS4G_ESIZE); want may not be length.  One launch. */
 int ds4g_paged_resize(const ds4g_page_pool *pool, int32_t *table, int width, int table_stride, int32_t *length,
                       const int32_t *want, int n_seqs, int32_t *start, int64_t *slots, int max_tokens,
                       void *cuda_stream);

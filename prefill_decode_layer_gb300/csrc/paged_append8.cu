@@ -311,6 +311,8 @@ template <typename TI> static cudaError_t append8_from(const AppendArgs &a, cuda
     int share = 1;
     while (share < kA8Warps && (share * kA8Hold<TI> * (32 / hv) < a.kv.block || 2 * share * pairs <= kA8Warps)) share *= 2;
     const int per_cta = kA8Warps / share, nk = (pairs + per_cta - 1) / per_cta;
+    // (by tokens, of which few lead a block in calls of many: of 768 FP32 rows in blocks of 16 most CTAs find none, and
+    // the grid takes two turns, 7.9 us for the chain's 4.1)
     int kv_tokens = 1;
     while (kv_tokens < kA8Tokens && 2 * kv_tokens <= a.kv.block && (long long)n * nk / (2 * kv_tokens) >= 4 * nsm) kv_tokens *= 2;
     // many tokens of tens of thousands of heads: a grid has 2^31 - 1 CTAs at most, of which the queries take up to 2^28

@@ -23,20 +23,20 @@
 // Up to 32 rows ("direct"): V's codes from their TMA tile as they are, and P as E4M3 too, four columns a
 // row: a weight p as hi + lo / 16 like the queries, and weights below 2^-10 of the maximum in a pair of
 // columns of their own, in units of 2^-13 (E4M3 alone has 2^-9 .. 448: many small weights beside a large one would
-// vanish).  8 bits of each weight, or 2^-32 of the largest.
+// vanish).  2^-9 of each weight, or 2^-32 of the largest.
 // More rows: four times the columns of 64 rows, twice over, do not fit TMEM.  Four warps make FP16 of V's
-// codes, which holds them exactly, and P is FP16 (11 bits, or 2^-34 of the largest).  (With that for every number of
+// codes, which holds them exactly, and P is FP16 (2^-11, or 2^-34 of the largest).  (With that for every number of
 // rows the batch below took 222 us, not 167, the long one 246, not 199.)
 //
 // Units of two K/V heads where their rows fit a group of softmax threads each: see paged_attn8_tc_heads.
 //
 // Bound and figures (device time, of a captured graph; the copy 6.79 TB/s):
 //   one token of 64 sequences to 8191, 32 heads on 8 (0.69 GB)       114 us   DRAM, 6.0 TB/s
-//   one token of 4 sequences to 131072, 64 heads on 8 (0.81 GB)      130 us   DRAM, 6.3 TB/s
-//   1 to 5 tokens of 32 sequences to 16994, 64 heads on 1 (92 MB)     88 us   instruction issue (0.62 of the slots:
+//   one token of 4 sequences to 131072, 64 heads on 8 (0.81 GB)      129 us   DRAM, 6.3 TB/s
+//   1 to 5 tokens of 32 sequences to 16994, 64 heads on 1 (92 MB)     90 us   instruction issue (0.61 of the slots:
 //     the softmax's 16 warps, V's conversion) and the chains of a unit, 2500 cycles for 128 keys and 64 rows;
 //     shared memory, 176 KB of a unit, would take 1400, the MMAs 480
-//   one token, 64 heads on 1, a window of 128                         9.7 us  latency: launch, item, page, K, softmax, O
+//   one token, 64 heads on 1, a window of 128                         9.8 us  latency: launch, item, page, K, softmax, O
 // The K and V tiles are most of shared memory (five of two heads, 32 KB each, at eight rows; eleven of one), so that
 // the copies run far ahead of the MMAs.
 //

@@ -15,8 +15,11 @@
 // shared memory, the others' through distributed shared memory, a cluster barrier where pages
 // given back may be taken and where the tables are complete.  Pages are moved one a thread, found
 // by a binary search in the CTA's prefix sums; slots likewise, divided evenly over the cluster.
-// Bound: latency (a chain of loads and barriers; a few hundred KB at most).  Measured: 64 sequences with drafts 4.8 us
-// a call in one CTA, 4096 sequences of a few pages 12.4 in eight.
+// Bound: latency.  Of a decode step a chain of loads and barriers: 64 sequences with drafts 4.8 us a call in one CTA, 4096
+// sequences 12.4 in eight.  Of prompts the slots: each new token looks for its sequence in the starts, in global memory,
+// and then for its length and page, by 512 threads or 4096.  4096 sequences, 256 prompts of up to 2000 among them
+// (336,374 new tokens, 2.7 MB of slots) 262 us, 45 without slots; a prompt of 131072 among 16 sequences 275, among 64 356; one of 4096 16.
+// (These with the launch and whatever waits for it; the stores alone would take half a microsecond.)
 #include "paged.h"
 #include "sm100.cuh"
 
@@ -223,7 +226,8 @@ __global__ void __launch_bounds__(kRzThreads) k_paged_resize(const __grid_consta
 cudaError_t paged_resize(const ResizeArgs &a, cudaStream_t st)
 {
     // One CTA where its threads have a sequence each, a cluster of eight for more: the barriers of eight cost 3 us
-    // (one CTA and eight: 64 sequences 4.9 and 7.8 us, 512 8.4 and 8.7, 1024 13.3 and 8.5, 4096 46.8 and 12.3)
+    // (decode steps, one CTA and eight: 64 sequences 4.9 and 7.8 us, 512 8.4 and 8.7, 1024 13.3 and 8.5, 4096 46.8 and
+    // 12.3).  Eight would gain where few sequences bring long prompts: 64 with one of 4096 tokens 15.7 and 9.7, of 131072 356 and 54.
     const int cluster = a.n_seqs <= kRzThreads ? 1 : kRzCluster;
     const int share = (a.n_seqs + cluster - 1) / cluster;
     static PerDevice once;

@@ -549,9 +549,10 @@ int ds4g_paged_append8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, 
  * being the values that codes and scales stand for.  BF16 queries with head_dim 64 or 128, pages of a
  * multiple of 8 slots run on the tensor cores: the queries as pairs of E4M3 values (exact down to 2^-14 of
  * the row's largest, off by 2^-22 of it at most below), the probabilities times the V scales
- * as pairs of E4M3 values (up to 32 rows, new tokens times query heads, a K/V head: 2^-9 of each) or as FP16 (2^-11), of
- * what is very small 2^-32 of the largest; their sums in FP32 before that rounding; every other case runs in FP32.  scale times a K scale times a query's largest value has to stay
- * below 2^126: scores beyond FP32 are not infinities but NaN. */
+ * as pairs of E4M3 values (up to 32 rows, new tokens times query heads, a K/V head: 2^-9 of each) or as FP16 (2^-11),
+ * of what is very small 2^-32 of the largest; their sums in FP32 before that rounding; every other case runs in FP32.
+ * scale times a K scale times a query's largest value has to stay below 2^126: scores beyond FP32 are not
+ * infinities but NaN. */
 size_t ds4g_paged_attention8_workspace_bytes(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, int n_heads);
 int ds4g_paged_attention8(const ds4g_paged_kv8 *kv, const ds4g_paged_batch *batch, const void *q, int64_t q_stride,
                           void *out, int64_t out_stride, int n_heads, int dtype, float scale, int window,
@@ -576,7 +577,8 @@ typedef struct {
  * became shorter).  slots, where not NULL, [max_tokens]: page * page_size + slot of each new token;
  * entries behind the last one stay as they are.  table [n_seqs][table_stride], length, start, slots and the pool are
  * device memory, read and written on the device: the pages of [0, ceil(length[b] / page_size)) of
- * a table are its sequence's (all of them go back to the pool in turn, also an entry that is no page).  n_seqs <= 65536 (DS4G_ESIZE); want may not be length.  One launch. */
+ * a table are its sequence's (all of them go back to the pool in turn, also an entry that is no page).  n_seqs <=
+ * 65536 (DS4G_ESIZE); want may not be length.  One launch. */
 int ds4g_paged_resize(const ds4g_page_pool *pool, int32_t *table, int width, int table_stride, int32_t *length,
                       const int32_t *want, int n_seqs, int32_t *start, int64_t *slots, int max_tokens,
                       void *cuda_stream);
@@ -609,10 +611,10 @@ typedef struct {
 } ds4g_logit_edits;
 
 /* Edit rows of logits before ds4g_probs or ds4g_sample ([P3] 阶段四 4.3).  For id i, in FP32 and in this
- * order: where i is in the row's history z <- z > 0 ? z / repetition : z * repetition (the quotient rounded once, off by
- * half a unit of its last place and 2^-20 of that at most, for repetition in [2^-60, 2^60] and quotients above 2^-100; else a
- * product with the rounded reciprocal); where it is c > 0 times in the generated part z <- z - (frequency * c + presence); z <- z + the sum of the row's
- * biases of i (in FP64, rounded once); where i is not allowed z <- -inf, whatever it was.  logits, out: device f32
+ * order: where i is in the row's history z <- z > 0 ? z / repetition : z * repetition (the quotient rounded once, off
+ * by half a unit of its last place and 2^-20 of that at most, for repetition in [2^-60, 2^60] and quotients above
+ * 2^-100; else a product with the rounded reciprocal); where it is c > 0 times in the generated part z <- z -
+ * (frequency * c + presence); z <- z + the sum of the row's biases of i (in FP64, rounded once); where i is not allowed z <- -inf, whatever it was.  logits, out: device f32
  * [n_rows][n_vocab] with row strides in elements; out == logits is allowed with equal strides.
  * n_vocab <= 1048576 (DS4G_ESIZE).  One launch. */
 int ds4g_edit_logits(const float *logits, int64_t logits_stride, int n_rows, int n_vocab, const ds4g_logit_edits *edits,
